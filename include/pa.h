@@ -83,7 +83,7 @@ typedef enum {
     PA_ERR_DEVICE_BOUNDS = 5   /* returned by pa_check_err_flag for a non-zero flag */
 } pa_status;
 
-typedef enum { PA_F16 = 0, PA_BF16 = 1, PA_F32 = 2, PA_FP8_E4M3 = 3 } pa_dtype;
+typedef enum { PA_F16 = 0, PA_BF16 = 1, PA_F32 = 2, PA_FP8_E4M3 = 3, PA_INT8 = 4 } pa_dtype;
 
 /* Bits OR-ed into *err_flag by the kernels. */
 #define PA_FLAG_BAD_SLOT        0x1   /* slot_mapping entry >= num_blocks * block_size */
@@ -409,6 +409,132 @@ pa_status pa_swap_blocks(const void *src_k, const void *src_v, void *dst_k, void
                          int64_t src_num_blocks, int64_t dst_num_blocks,
                          int block_size, int num_kv_heads, int head_dim, pa_dtype dtype,
                          int *err_flag, void *stream);
+
+/*
+ * ------------------------------------------------------------------------
+ * Quantised cache with a scale per token and KV head
+ * ------------------------------------------------------------------------
+ * An 8-bit cache whose scales come from the data: k_cache and v_cache hold
+ * codes (PA_FP8_E4M3 or PA_INT8), [num_blocks, block_size, num_kv_heads,
+ * head_dim], and k_scales, v_scales one float per row,
+ * [num_blocks, block_size, num_kv_heads], both reached through the same block
+ * tables.  A row (one token, one KV head) stands for code * scale.  Scales are
+ * block-major like the codes, so pa_copy_blocks and pa_swap_blocks move them
+ * too (as a PA_FP8_E4M3 cache with head_dim 4: four bytes a row); codes of
+ * either type move as PA_FP8_E4M3.
+ *
+ * head_dim 64 or 128; arithmetic in fp32.
+ *
+ * pa_quant_reshape_and_cache -- write new K/V rows, quantised.
+ *
+ * For a row x, with qmax = 448 (e4m3) or 127 (int8), in fp32:
+ *     a = max(max_i |x_i|, 2^-60),  scale = a / qmax,
+ *     code_i = round(x_i * (qmax / a))      (nearest, ties to even)
+ * so an element is off by at most half a code step.  A row of zeros gets codes
+ * 0; a row that holds an infinity or NaN gets the scale NaN and codes 0, and
+ * reads back (and attends) as NaN.
+ *
+ *   key, value   : [num_tokens, num_kv_heads, head_dim], dtype (F16 or BF16);
+ *                  rows of one token are dense, tokens key_stride (value_stride)
+ *                  elements apart: at least num_kv_heads * head_dim, a multiple
+ *                  of 8 (e.g. slices of a fused projection's output)
+ *   slot_mapping : [num_tokens] int64, as for pa_reshape_and_cache: slot < 0 is
+ *                  skipped, slot >= num_blocks * block_size skipped with
+ *                  PA_FLAG_BAD_SLOT; slots must be distinct (else the codes and
+ *                  scale of that slot are unspecified)
+ * num_tokens == 0 is a no-op.
+ */
+pa_status pa_quant_reshape_and_cache(const void *key, const void *value, int64_t key_stride, int64_t value_stride,
+                                     void *k_cache, void *v_cache, float *k_scales, float *v_scales,
+                                     const int64_t *slot_mapping, int64_t num_tokens, int64_t num_blocks,
+                                     int block_size, int num_kv_heads, int head_dim, pa_dtype dtype,
+                                     pa_dtype cache_dtype, int *err_flag, void *stream);
+
+/*
+ * pa_quant_gather -- read a quantised cache back into dense rows.
+ *
+ * Row cu_seqlens[s] + i of out_k (out_v) becomes code * scale of sequence s's
+ * position seq_starts[s] + i, for i < cu_seqlens[s + 1] - cu_seqlens[s]: the
+ * product in fp32, rounded once to out_dtype.
+ *
+ *   out_k, out_v : [num_tokens, num_kv_heads, head_dim], F16, BF16 or F32
+ *   cu_seqlens   : [num_seqs + 1] int32 (device), cu_seqlens[0] = 0,
+ *                  non-decreasing, cu_seqlens[num_seqs] <= num_tokens; rows from
+ *                  cu_seqlens[num_seqs] on are left as they were
+ *   seq_starts   : [num_seqs] int32 (device), or NULL for 0
+ * A position outside the block table (PA_FLAG_BAD_CONTEXT_LEN) or a block id
+ * outside [0, num_blocks) (PA_FLAG_BAD_BLOCK_ID) gives a zero row; cu_seqlens
+ * that break the rules set PA_FLAG_BAD_CONTEXT_LEN.  Any block_size.
+ */
+pa_status pa_quant_gather(void *out_k, void *out_v, pa_dtype out_dtype, const void *k_cache, const void *v_cache,
+                          pa_dtype cache_dtype, const float *k_scales, const float *v_scales,
+                          const int32_t *block_tables, int max_blocks_per_seq, const int32_t *cu_seqlens,
+                          const int32_t *seq_starts, int num_seqs, int64_t num_tokens, int num_kv_heads, int head_dim,
+                          int block_size, int64_t num_blocks, int *err_flag, void *stream);
+
+/*
+ * pa_quant_decode -- pa_decode over a quantised cache.
+ *
+ *     x_p = scale * k_scale_p * <query[s][h][:], Kcode_p>,
+ *     out[s][h][:] = sum_p softmax(x)_p * v_scale_p * Vcode_p
+ * with the arguments and rules of pa_decode (query F16 or BF16, out F16, BF16
+ * or F32; shapes as there, FP8 and INT8 codes alike for head_dim 64 and 128).
+ * partition_size is 0 (auto), or a multiple of 16 of at most 32 * block_size, and
+ * above 31 * block_size + 16 a multiple of block_size.
+ * partition_size 0 (auto) also splits moderate contexts when there are few
+ * sequences.  The workspace is pa_quant_decode_workspace_size(...) bytes (0
+ * when nothing is split) and needs no initial contents.  Codes and scales at
+ * positions >= context_lens[s] are never used.  Products run in binary16 (codes
+ * are exact there; each query row is first scaled by a power of two), sums and
+ * softmax in fp32.  Results do not depend on the physical block ids and are
+ * bitwise reproducible for a given partition size.
+ */
+size_t pa_quant_decode_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size,
+                                      int max_context_len, int partition_size);
+pa_status pa_quant_decode(void *out, pa_dtype out_dtype, const void *query, pa_dtype q_dtype, const void *k_cache,
+                          const void *v_cache, pa_dtype cache_dtype, const float *k_scales, const float *v_scales,
+                          const int32_t *block_tables, int max_blocks_per_seq, const int32_t *context_lens,
+                          int max_context_len, int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                          int block_size, int64_t num_blocks, float scale, int partition_size, void *workspace,
+                          size_t workspace_bytes, int *err_flag, void *stream);
+
+/*
+ * pa_decode_shared -- pa_decode for a batch whose sequences share long
+ * prefixes, each prefix computed once for all sequences of its group.
+ *
+ * The sequences of group g are cu_groups[g] .. cu_groups[g + 1] - 1, and the
+ * first shared_lens[s] tokens of each (one value per group) are the same: the
+ * K/V rows of those positions are equal whichever member's block table they
+ * are read through (a shared prompt; Page D, copy-on-write).  The whole blocks
+ * of that prefix are read once, through the first member's table, for the query
+ * rows of all members; the rest of every context, the block in which the prefix
+ * ends included, is read through the sequence's own table.  The two parts'
+ * softmax states are then joined, so the result is that of pa_decode (whose
+ * arguments and rules hold otherwise; 16-bit caches, the query's type kv_dtype).
+ *
+ *   cu_groups    : [num_groups + 1] int32 (device), cu_groups[0] = 0,
+ *                  non-decreasing, cu_groups[num_groups] = num_seqs
+ *   shared_lens  : [num_seqs] int32 (device), 0 <= shared_lens[s] <=
+ *                  context_lens[s], equal within a group; 0: nothing is shared
+ *   max_group_size, max_shared_len : host-known upper bounds of the group sizes
+ *                  and of shared_lens (<= max_context_len)
+ *   workspace    : pa_decode_shared_workspace_size(...) bytes, always needed; no
+ *                  initial contents
+ * cu_groups or shared_lens that break these rules set PA_FLAG_BAD_CONTEXT_LEN;
+ * the groups concerned are then undefined (no memory out of bounds is touched).
+ * partition_size is that of the private parts; the prefixes are cut by a rule of
+ * the library's own.
+ */
+size_t pa_decode_shared_workspace_size(int num_seqs, int num_groups, int max_group_size, int num_heads,
+                                       int num_kv_heads, int head_dim, int block_size, int max_context_len,
+                                       int max_shared_len, int partition_size);
+pa_status pa_decode_shared(void *out, pa_dtype out_dtype, const void *query, const void *k_cache, const void *v_cache,
+                           pa_dtype kv_dtype, const int32_t *block_tables, int max_blocks_per_seq,
+                           const int32_t *context_lens, int max_context_len, const int32_t *cu_groups, int num_groups,
+                           int max_group_size, const int32_t *shared_lens, int max_shared_len, int num_seqs,
+                           int num_heads, int num_kv_heads, int head_dim, int block_size, int64_t num_blocks,
+                           float scale, int partition_size, void *workspace, size_t workspace_bytes, int *err_flag,
+                           void *stream);
 
 /* Host helper: synchronously read *err_flag (device), optionally clear it,
  * and map it to PA_OK / PA_ERR_DEVICE_BOUNDS.  `flag_out` (nullable, host)

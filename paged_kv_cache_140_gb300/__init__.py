@@ -9,11 +9,17 @@ PyTorch fallback - a missing library raises.
     decode(out, query, k_cache, v_cache, block_tables, context_lens, scale, ...)
     prefill(out, query, k_cache, v_cache, block_tables, context_lens, cu_seqlens_q, scale, ...)
     copy_blocks(k_cache, v_cache, block_mapping)
+    decode_shared(out, query, k_cache, v_cache, block_tables, context_lens, cu_groups, shared_lens, scale, ...)
+    quant_reshape_and_cache(key, value, k_cache, v_cache, k_scales, v_scales, slot_mapping)
+    quant_gather(out_k, out_v, k_cache, v_cache, k_scales, v_scales, block_tables, cu_seqlens, ...)
+    quant_decode(out, query, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, scale, ...)
 
 Cache layout: ``[num_blocks, block_size, num_kv_heads, head_dim]`` per layer
 for K and for V ("LLM推理优化：vLLM PagedAttention深度解析与工程实践", §4.1).
 Caches are float16 / bfloat16, or FP8 e4m3 codes (``torch.float8_e4m3fn`` or
-``torch.uint8``) with per-tensor ``k_scale`` / ``v_scale``.
+``torch.uint8``) with per-tensor ``k_scale`` / ``v_scale``; the ``quant_*`` calls
+keep int8 or e4m3 codes with a float32 scale per token and KV head,
+``[num_blocks, block_size, num_kv_heads]``.
 """
 from __future__ import annotations
 
@@ -21,11 +27,12 @@ import ctypes
 
 from . import _lib
 from ._lib import (FLAG_BAD_BLOCK_ID, FLAG_BAD_CONTEXT_LEN, FLAG_BAD_COPY_PAIR, FLAG_BAD_SLOT,
-                   FLAG_TIMEOUT, PA_BF16, PA_F16, PA_F32, PA_FP8_E4M3, PagedAttentionError)
+                   FLAG_TIMEOUT, PA_BF16, PA_F16, PA_F32, PA_FP8_E4M3, PA_INT8, PagedAttentionError)
 
 __all__ = ["reshape_and_cache", "decode", "decode_append", "prefill", "copy_blocks", "copy_blocks_layers", "swap_blocks", "decode_workspace_size",
            "decode_partition_size", "DecodeWorkspace", "new_err_flag", "read_err_flag",
-           "PagedAttentionError", "FLAG_BAD_SLOT", "FLAG_BAD_BLOCK_ID", "FLAG_BAD_CONTEXT_LEN",
+           "quant_reshape_and_cache", "quant_gather", "quant_decode", "quant_decode_workspace_size", "decode_shared",
+           "decode_shared_workspace_size", "PagedAttentionError", "FLAG_BAD_SLOT", "FLAG_BAD_BLOCK_ID", "FLAG_BAD_CONTEXT_LEN",
            "FLAG_BAD_COPY_PAIR", "FLAG_TIMEOUT", "library_path", "StepGraph"]
 
 
@@ -313,6 +320,203 @@ def prefill(out, query, k_cache, v_cache, block_tables, context_lens, cu_seqlens
                                 _ptr(context_lens), _ptr(cu_seqlens_q), B, T, int(max_q_len), Hq, hkv, D, bs,
                                 nb, float(scale), _ptr(err_flag), _stream(query.device))
     _lib.check(st, "pa_prefill")
+
+
+# ------------------------- quantised cache, and decode with shared prefixes
+
+def _quant_code(t) -> int:
+    torch = _torch()
+    if t.dtype == torch.int8:
+        return PA_INT8
+    if t.dtype in (torch.uint8, torch.float8_e4m3fn):
+        return PA_FP8_E4M3
+    raise TypeError(f"unsupported code dtype {t.dtype}")
+
+
+def _on_one_device(first, *rest):
+    """All tensors on the current CUDA device and contiguous; names are given on a refusal."""
+    index = first[1].device.index
+    for n, t in (first, *rest):
+        if not t.is_cuda or t.device.index != index or not t.is_contiguous():
+            _cuda_contig(n, t)
+            raise ValueError(f"{n} must be on the device of {first[0]}")
+    _need(index == _torch().cuda.current_device(), "the tensors must be on the current CUDA device")
+
+
+def _scratch(workspace, nbytes: int, device):
+    """The workspace of one call: the caller's, the default one of the current
+    stream, or, while a graph is captured, one of the graph's own (so that graphs
+    never share one and none is replaced by a larger one later)."""
+    if nbytes == 0:
+        return None
+    if workspace is None:
+        torch = _torch()
+        if torch.cuda.is_current_stream_capturing():
+            return torch.empty(nbytes, dtype=torch.uint8, device=device)
+        key = (device.index, torch.cuda.current_stream(device).cuda_stream)
+        workspace = _default_ws.get(key)
+        if workspace is None:
+            workspace = _default_ws.setdefault(key, DecodeWorkspace(device))
+    if not isinstance(workspace, DecodeWorkspace):
+        _cuda_contig("workspace", workspace)
+        _need(workspace.device == device, "workspace must be on the device of the other tensors")
+        return workspace
+    return workspace.get(nbytes)
+
+
+def _quant_cache(k_cache, v_cache, k_scales, v_scales):
+    torch = _torch()
+    _need(k_cache.dim() == 4 and v_cache.shape == k_cache.shape and k_cache.dtype == v_cache.dtype,
+          "caches must be [NB, bs, Hkv, D] of one dtype")
+    _need(k_scales.dtype == torch.float32 and v_scales.dtype == torch.float32 and
+          k_scales.shape == k_cache.shape[:3] and v_scales.shape == k_scales.shape,
+          "scales must be float32 [NB, bs, Hkv]")
+    return k_cache.shape
+
+
+def quant_reshape_and_cache(key, value, k_cache, v_cache, k_scales, v_scales, slot_mapping, err_flag=None) -> None:
+    """Quantise key/value rows [T, Hkv, D] (f16 or bf16) into cache slots
+    (slot < 0: skip), one scale per token and KV head.
+
+    The caches' dtype chooses the codes: ``torch.int8``, or e4m3 for
+    ``torch.float8_e4m3fn`` / ``torch.uint8``.  key and value may be slices along
+    the last two dimensions of a wider tensor (a token's rows dense, any token
+    stride that is a multiple of 8 elements)."""
+    torch = _torch()
+    _need(key.dim() == 3 and value.shape == key.shape and key.dtype == value.dtype, "key/value must be [T, Hkv, D]")
+    T, hkv, d = key.shape
+    for n, t in (("key", key), ("value", value)):
+        _need(t.is_cuda and t.device == k_cache.device, f"{n} must be on the device of k_cache")
+        _need(t.stride(2) == 1 and (hkv == 1 or t.stride(1) == d), f"{n}: the rows of one token must be dense")
+    _on_one_device(("k_cache", k_cache), ("v_cache", v_cache), ("k_scales", k_scales), ("v_scales", v_scales),
+                   ("slot_mapping", slot_mapping))
+    nb, bs, h2, d2 = _quant_cache(k_cache, v_cache, k_scales, v_scales)
+    _need(h2 == hkv and d2 == d, "cache and key head shapes differ")
+    _need(slot_mapping.dtype == torch.int64 and slot_mapping.numel() == T, "slot_mapping must be int64 [T]")
+    row = hkv * d
+    st = _lib.load().pa_quant_reshape_and_cache(
+        key.data_ptr(), value.data_ptr(), key.stride(0) if T > 1 else row, value.stride(0) if T > 1 else row,
+        k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), slot_mapping.data_ptr(), T,
+        nb, bs, hkv, d, _dtype_code(key), _quant_code(k_cache), _ptr(err_flag), _stream(key.device))
+    _lib.check(st, "pa_quant_reshape_and_cache")
+
+
+def quant_gather(out_k, out_v, k_cache, v_cache, k_scales, v_scales, block_tables, cu_seqlens, seq_starts=None,
+                 err_flag=None) -> None:
+    """Read a quantised cache back: row ``cu_seqlens[s] + i`` of out_k/out_v
+    [T, Hkv, D] (f16, bf16 or f32) becomes sequence s's position
+    ``seq_starts[s] + i`` (``seq_starts`` None: 0).  Rows from ``cu_seqlens[-1]``
+    on are left as they were."""
+    torch = _torch()
+    more = () if seq_starts is None else (("seq_starts", seq_starts),)
+    _on_one_device(("out_k", out_k), ("out_v", out_v), ("k_cache", k_cache), ("v_cache", v_cache),
+                   ("k_scales", k_scales), ("v_scales", v_scales), ("block_tables", block_tables),
+                   ("cu_seqlens", cu_seqlens), *more)
+    nb, bs, hkv, d = _quant_cache(k_cache, v_cache, k_scales, v_scales)
+    _need(out_k.dim() == 3 and out_v.shape == out_k.shape and out_v.dtype == out_k.dtype and
+          out_k.shape[1] == hkv and out_k.shape[2] == d, "out_k/out_v must be [T, Hkv, D] of one dtype")
+    _need(block_tables.dtype == torch.int32 and block_tables.dim() == 2, "block_tables must be int32 [B, maxNB]")
+    B, maxnb = block_tables.shape
+    _need(cu_seqlens.dtype == torch.int32 and cu_seqlens.numel() == B + 1, "cu_seqlens must be int32 [B+1]")
+    _need(seq_starts is None or (seq_starts.dtype == torch.int32 and seq_starts.numel() == B),
+          "seq_starts must be int32 [B]")
+    st = _lib.load().pa_quant_gather(
+        out_k.data_ptr(), out_v.data_ptr(), _dtype_code(out_k, allow_f32=True), k_cache.data_ptr(),
+        v_cache.data_ptr(), _quant_code(k_cache), k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(),
+        maxnb, cu_seqlens.data_ptr(), _ptr(seq_starts), B, out_k.shape[0], hkv, d, bs, nb, _ptr(err_flag),
+        _stream(out_k.device))
+    _lib.check(st, "pa_quant_gather")
+
+
+def quant_decode_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context_len,
+                                partition_size=0) -> int:
+    n = _lib.load().pa_quant_decode_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim, block_size,
+                                                   max_context_len, partition_size)
+    if n == ctypes.c_size_t(-1).value:
+        raise ValueError("arguments rejected by pa_quant_decode_workspace_size")
+    return n
+
+
+def _decode_shapes(out, query, k_cache, block_tables, context_lens):
+    torch = _torch()
+    _need(query.dim() == 3 and out.shape == query.shape, "query/out must be [B, Hq, D]")
+    B, Hq, D = query.shape
+    _need(k_cache.shape[3] == D, "head_dim mismatch")
+    _need(block_tables.dtype == torch.int32 and block_tables.dim() == 2 and block_tables.shape[0] == B,
+          "block_tables must be int32 [B, maxNB]")
+    _need(context_lens.dtype == torch.int32 and context_lens.numel() == B, "context_lens must be int32 [B]")
+    return B, Hq, D
+
+
+def quant_decode(out, query, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, scale: float,
+                 max_context_len: int | None = None, partition_size: int = 0, workspace=None, err_flag=None) -> None:
+    """:func:`decode` over a quantised cache written by :func:`quant_reshape_and_cache`."""
+    _on_one_device(("query", query), ("out", out), ("k_cache", k_cache), ("v_cache", v_cache), ("k_scales", k_scales),
+                   ("v_scales", v_scales), ("block_tables", block_tables), ("context_lens", context_lens))
+    nb, bs, hkv, _ = _quant_cache(k_cache, v_cache, k_scales, v_scales)
+    B, Hq, D = _decode_shapes(out, query, k_cache, block_tables, context_lens)
+    maxnb = block_tables.shape[1]
+    if max_context_len is None:
+        max_context_len = maxnb * bs
+    buf = _scratch(workspace, quant_decode_workspace_size(B, Hq, hkv, D, bs, max_context_len, partition_size),
+                   query.device)
+    st = _lib.load().pa_quant_decode(
+        out.data_ptr(), _dtype_code(out, allow_f32=True), query.data_ptr(), _dtype_code(query), k_cache.data_ptr(),
+        v_cache.data_ptr(), _quant_code(k_cache), k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(),
+        maxnb, context_lens.data_ptr(), max_context_len, B, Hq, hkv, D, bs, nb, scale, partition_size, _ptr(buf),
+        0 if buf is None else buf.nbytes, _ptr(err_flag), _stream(query.device))
+    _lib.check(st, "pa_quant_decode")
+
+
+def decode_shared_workspace_size(num_seqs, num_groups, max_group_size, num_heads, num_kv_heads, head_dim, block_size,
+                                 max_context_len, max_shared_len, partition_size=0) -> int:
+    n = _lib.load().pa_decode_shared_workspace_size(num_seqs, num_groups, max_group_size, num_heads, num_kv_heads,
+                                                    head_dim, block_size, max_context_len, max_shared_len,
+                                                    partition_size)
+    if n == ctypes.c_size_t(-1).value:
+        raise ValueError("arguments rejected by pa_decode_shared_workspace_size")
+    return n
+
+
+def decode_shared(out, query, k_cache, v_cache, block_tables, context_lens, cu_groups, shared_lens, scale: float,
+                  max_group_size: int | None = None, max_shared_len: int | None = None,
+                  max_context_len: int | None = None, partition_size: int = 0, workspace=None, err_flag=None) -> None:
+    """:func:`decode` for a batch whose sequences share prefixes, each computed
+    once for all sequences of its group.
+
+    Group g is the sequences ``cu_groups[g] .. cu_groups[g+1]-1`` (int32 [NG+1]);
+    the first ``shared_lens[s]`` tokens (int32 [B], one value per group) hold the
+    same K/V rows in every member.  ``max_group_size`` and ``max_shared_len`` are
+    host-side bounds (defaults: the batch size and ``max_context_len``; tight
+    bounds make the call faster)."""
+    torch = _torch()
+    _on_one_device(("query", query), ("out", out), ("k_cache", k_cache), ("v_cache", v_cache),
+                   ("block_tables", block_tables), ("context_lens", context_lens), ("cu_groups", cu_groups),
+                   ("shared_lens", shared_lens))
+    _need(k_cache.dim() == 4 and v_cache.shape == k_cache.shape and k_cache.dtype == v_cache.dtype,
+          "caches must be [NB, bs, Hkv, D] of one dtype")
+    _need(k_cache.dtype == query.dtype, "caches must have the query's dtype")
+    B, Hq, D = _decode_shapes(out, query, k_cache, block_tables, context_lens)
+    nb, bs, hkv, _ = k_cache.shape
+    _need(cu_groups.dtype == torch.int32 and cu_groups.dim() == 1 and cu_groups.numel() > 0,
+          "cu_groups must be int32 [NG+1]")
+    _need(shared_lens.dtype == torch.int32 and shared_lens.numel() == B, "shared_lens must be int32 [B]")
+    ng = cu_groups.numel() - 1
+    maxnb = block_tables.shape[1]
+    if max_context_len is None:
+        max_context_len = maxnb * bs
+    if max_group_size is None:
+        max_group_size = B
+    if max_shared_len is None:
+        max_shared_len = max_context_len
+    buf = _scratch(workspace, decode_shared_workspace_size(B, ng, max_group_size, Hq, hkv, D, bs, max_context_len,
+                                                           max_shared_len, partition_size), query.device)
+    st = _lib.load().pa_decode_shared(
+        out.data_ptr(), _dtype_code(out, allow_f32=True), query.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        _dtype_code(query), block_tables.data_ptr(), maxnb, context_lens.data_ptr(), max_context_len,
+        cu_groups.data_ptr(), ng, max_group_size, shared_lens.data_ptr(), max_shared_len, B, Hq, hkv, D, bs, nb, scale,
+        partition_size, _ptr(buf), 0 if buf is None else buf.nbytes, _ptr(err_flag), _stream(query.device))
+    _lib.check(st, "pa_decode_shared")
 
 
 class StepGraph:

@@ -11,7 +11,7 @@ import os
 from . import _build
 
 PA_OK, PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED, PA_ERR_CUDA, PA_ERR_WORKSPACE, PA_ERR_DEVICE_BOUNDS = range(6)
-PA_F16, PA_BF16, PA_F32, PA_FP8_E4M3 = 0, 1, 2, 3
+PA_F16, PA_BF16, PA_F32, PA_FP8_E4M3, PA_INT8 = 0, 1, 2, 3, 4
 
 FLAG_BAD_SLOT = 0x1
 FLAG_BAD_BLOCK_ID = 0x2
@@ -34,6 +34,15 @@ SIGNATURES = {
                                _F, _I, _P, _P]),
     "pa_prefill": (_I, [_P, _I, _P, _P, _P, _I, _P, _I, _P, _P, _I, _I64, _I, _I, _I, _I, _I, _I64, _F, _P,
                         _P]),
+    "pa_quant_reshape_and_cache": (_I, [_P, _P, _I64, _I64, _P, _P, _P, _P, _P, _I64, _I64, _I, _I, _I, _I, _I, _P,
+                                        _P]),
+    "pa_quant_gather": (_I, [_P, _P, _I, _P, _P, _I, _P, _P, _P, _I, _P, _P, _I, _I64, _I, _I, _I, _I64, _P, _P]),
+    "pa_quant_decode_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I, _I]),
+    "pa_quant_decode": (_I, [_P, _I, _P, _I, _P, _P, _I, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _I64, _F, _I, _P,
+                             _SZ, _P, _P]),
+    "pa_decode_shared_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I, _I, _I, _I, _I]),
+    "pa_decode_shared": (_I, [_P, _I, _P, _P, _P, _I, _P, _I, _P, _I, _P, _I, _I, _P, _I, _I, _I, _I, _I, _I, _I64, _F,
+                              _I, _P, _SZ, _P, _P]),
     "pa_copy_blocks": (_I, [_P, _P, _P, _I64, _I64, _I, _I, _I, _I, _P, _P]),
     "pa_copy_blocks_layers": (_I, [_P, _I, _P, _I64, _I64, _I, _I, _I, _I, _P, _P]),
     "pa_swap_blocks": (_I, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _I, _I, _I, _I, _P, _P]),

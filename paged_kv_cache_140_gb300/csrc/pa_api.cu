@@ -16,6 +16,7 @@
 #include "pa_cache_ops.h"
 #include "pa_internal.h"
 #include "pa_prefill.h"
+#include "pa_split.h"
 
 #define PA_EXPORT extern "C" __attribute__((visibility("default")))
 
@@ -244,7 +245,7 @@ PA_EXPORT const char *pa_status_string(pa_status s) {
     return "unknown status";
 }
 
-PA_EXPORT int pa_version(void) { return 100; }
+PA_EXPORT int pa_version(void) { return 200; }
 
 PA_EXPORT pa_status pa_reshape_and_cache(const void *key, const void *value, void *k_cache,
                                          void *v_cache, const int64_t *slot_mapping,
@@ -644,6 +645,366 @@ PA_EXPORT pa_status pa_prefill(void *out, pa_dtype out_dtype, const void *query,
     cudaError_t e = pa::launch_prefill(p, head_dim, kv_dtype == PA_BF16, tq, tk, tv, to, smem,
                                        static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+// ------------------------- quantised cache, and decode with shared prefixes
+
+namespace {
+
+bool quant_dtype(pa_dtype d) { return d == PA_FP8_E4M3 || d == PA_INT8; }
+bool out_dtype_ok(pa_dtype d) { return d == PA_F16 || d == PA_BF16 || d == PA_F32; }
+int split_cache(pa_dtype d) {
+    return d == PA_F16 ? pa::kCacheF16 : d == PA_BF16 ? pa::kCacheBF16 : d == PA_FP8_E4M3 ? pa::kCacheE4M3 : pa::kCacheInt8;
+}
+
+// Entries (sequences, or chunks of groups) of one launch: the kernel keeps 12
+// bytes for each in shared memory; longer lists take several launches.
+constexpr int kSplitEntries = 2048;
+// Work items a launch should have so that every SM of the GPU has one or two.
+constexpr int64_t kSplitItems = 304;
+
+// Partition length, in tokens, for `lists` lists (entries x boxes of heads) of
+// at most `max_len` tokens; 0 when the request is invalid.  Lists that fill the
+// GPU by themselves are cut at 256 tokens (512 beyond 8 K), which bounds the
+// imbalance between SMs; fewer lists are cut finer, down to 128 tokens, so that
+// kSplitItems items exist.  Up to 256 tokens nothing is cut: a join costs a
+// launch of its own, more than reading 256 tokens does.
+int split_partition(int64_t lists, int max_len, int block_size, int slot_tokens, int requested) {
+    const int cap = 32 * block_size;
+    if (requested != 0) {
+        // a partition's block ids sit in the 32 lanes of a warp; one that does not
+        // start on a block boundary may reach into one block more
+        if (requested < 16 || requested % 16 != 0 || requested > cap) return 0;
+        return requested % block_size != 0 && requested > cap - block_size + 16 ? 0 : requested;
+    }
+    if (max_len <= 256 && max_len <= cap) return static_cast<int>(std::max<int64_t>(16, round_up(max_len, 16)));
+    int64_t P = max_len <= 8192 ? 256 : 512;
+    if (lists * ((max_len + P - 1) / P) < kSplitItems) {
+        P = std::min<int64_t>(P, round_up(lists * max_len / kSplitItems + 1, slot_tokens));
+        P = std::max<int64_t>(P, std::max(128, slot_tokens));
+    }
+    P = std::min<int64_t>(P, cap);
+    if (P > slot_tokens) P -= P % slot_tokens;   // whole ring slots
+    return static_cast<int>(P);
+}
+
+struct SplitPlan {
+    int log2_heads = 0, G = 1;
+    int partition = 0;           // decode and suffix entries
+    int parts = 1;               // their partials per row
+    int prefix_cols = 0;         // shared prefixes: query rows per launch entry
+    int prefix_part = 0, prefix_parts = 0;
+    int max_parts = 1;
+    size_t acc_off = 0, bytes = 0;
+};
+
+bool split_shape_ok(int num_heads, int num_kv_heads, int head_dim, int block_size) {
+    return num_heads % num_kv_heads == 0 && supported_group(num_heads / num_kv_heads) && supported_head_dim(head_dim) &&
+           supported_block_size(block_size);
+}
+
+// The cut of a call and the workspace for its partial results.  `shared`: the
+// shared blocks of up to max_shared_len tokens are computed per group.
+bool plan_split(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size, int max_context_len,
+                int partition_size, int cache, bool shared, int num_groups, int max_group_size, int max_shared_len,
+                SplitPlan &w) {
+    if (num_seqs < 0 || num_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || block_size <= 0 || max_context_len < 0)
+        return false;
+    if (!split_shape_ok(num_heads, num_kv_heads, head_dim, block_size)) return false;
+    w.G = num_heads / num_kv_heads;
+    w.log2_heads = pa::split_log2_heads(num_kv_heads);
+    const int64_t ngroups = num_kv_heads >> w.log2_heads;
+    const int slot_tokens = 16 * pa::split_slot_stages(cache, w.log2_heads);
+    w.partition = split_partition(num_seqs * ngroups, max_context_len, block_size, slot_tokens, partition_size);
+    if (w.partition == 0) return false;
+    w.parts = std::max(1, static_cast<int>((static_cast<int64_t>(max_context_len) + w.partition - 1) / w.partition));
+    w.max_parts = w.parts;
+    if (shared) {
+        if (num_groups < 0 || max_group_size < 0 || max_shared_len < 0 || max_shared_len > max_context_len) return false;
+        w.prefix_cols = w.G;
+        while (w.prefix_cols < 8 && w.prefix_cols < static_cast<int64_t>(max_group_size) * w.G) w.prefix_cols *= 2;
+        const int chunk_seqs = w.prefix_cols / w.G;
+        const int64_t chunks = (static_cast<int64_t>(max_group_size) + chunk_seqs - 1) / chunk_seqs;
+        w.prefix_part = split_partition(num_groups * chunks * ngroups, max_shared_len, block_size, slot_tokens, 0);
+        w.prefix_parts = (max_shared_len / block_size * block_size + w.prefix_part - 1) / w.prefix_part;
+        w.max_parts += w.prefix_parts;
+    }
+    if (!shared && w.max_parts <= 1) return true;
+    const int64_t rows = static_cast<int64_t>(num_seqs) * num_heads * w.max_parts;
+    w.acc_off = static_cast<size_t>(round_up(rows * 2 * 4, 256));
+    w.bytes = w.acc_off + static_cast<size_t>(rows) * head_dim * 4;
+    return true;
+}
+
+// Tensor map over a cache [NB * bs, Hkv, D] taken as (dim, token, head): boxes
+// of min(128 bytes, row) x min(16, bs) tokens x `heads` heads, swizzled by the
+// box row's width.
+bool encode_split_map(CUtensorMap *map, const void *cache, int64_t num_blocks, int block_size, int num_kv_heads,
+                      int head_dim, int es, int heads) {
+    EncodeTiledFn fn = encode_tiled();
+    if (fn == nullptr) return false;
+    const int row = std::min(128, head_dim * es);
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(num_blocks) * block_size,
+                                static_cast<cuuint64_t>(num_kv_heads)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(num_kv_heads) * head_dim * es,
+                                   static_cast<cuuint64_t>(head_dim) * es};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(row / es), static_cast<cuuint32_t>(std::min(block_size, 16)),
+                               static_cast<cuuint32_t>(heads)};
+    const cuuint32_t estr[3] = {1u, 1u, 1u};
+    return fn(map, es == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 3,
+              const_cast<void *>(cache), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              row == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// One pass of the split kernel over `entries` entries (p.mode says which).
+pa_status run_split(pa::SplitParams p, int cache, int head_dim, int cols, int entries, int max_len, const CUtensorMap &tk,
+                    const CUtensorMap &tv, const DeviceInfo &dev, cudaStream_t stream) {
+    const int64_t per_entry = static_cast<int64_t>(p.num_kv_heads >> p.log2_heads) *
+                              std::max(1, (max_len + p.partition_size - 1) / p.partition_size);
+    for (int e = 0; e < entries; e += kSplitEntries) {
+        p.e0 = e;
+        p.entries = std::min(kSplitEntries, entries - e);
+        const pa::SplitSmem need = pa::split_smem(head_dim, cols, cache, p.log2_heads, p.entries);
+        const size_t room = static_cast<size_t>(dev.smem_optin);
+        if (need.fixed + 2 * need.slot > room) return PA_ERR_UNSUPPORTED;
+        p.stages = static_cast<int>(std::min<size_t>(8, (room - need.fixed) / need.slot));
+        const size_t smem = need.fixed + p.stages * need.slot;
+        const int grid = static_cast<int>(std::min<int64_t>(dev.sms, p.entries * per_entry));
+        auto launch = cache == pa::kCacheF16    ? pa::launch_split_f16
+                      : cache == pa::kCacheBF16 ? pa::launch_split_bf16
+                      : cache == pa::kCacheE4M3 ? pa::launch_split_e4m3
+                                                : pa::launch_split_int8;
+        if (launch(p, head_dim, cols, tk, tv, grid, smem, stream) != cudaSuccess) return PA_ERR_CUDA;
+    }
+    return PA_OK;
+}
+
+// Checks shared by pa_quant_decode and pa_decode_shared; PA_OK lets them go on.
+pa_status check_split(pa_dtype out_dtype, pa_dtype q_dtype, int max_blocks_per_seq, int max_context_len, int num_seqs,
+                      int num_heads, int num_kv_heads, int head_dim, int block_size, int64_t num_blocks, float scale) {
+    if (num_seqs < 0 || num_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || block_size <= 0 || num_blocks <= 0 ||
+        max_blocks_per_seq <= 0 || max_context_len < 0)
+        return PA_ERR_INVALID_ARG;
+    if (!half_dtype(q_dtype) || !out_dtype_ok(out_dtype)) return PA_ERR_INVALID_ARG;
+    if (num_heads % num_kv_heads != 0) return PA_ERR_INVALID_ARG;
+    if (!split_shape_ok(num_heads, num_kv_heads, head_dim, block_size)) return PA_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(max_context_len) > static_cast<int64_t>(max_blocks_per_seq) * block_size)
+        return PA_ERR_INVALID_ARG;
+    if (num_blocks > INT32_MAX / block_size || num_seqs >= (1 << 27)) return PA_ERR_UNSUPPORTED;
+    if (!(scale == scale) || scale > 3.0e38f || scale < -3.0e38f) return PA_ERR_INVALID_ARG;
+    // Work is counted in 16-token stages in 32-bit arithmetic on the device,
+    // and one join warp per output row.
+    const int64_t stages = static_cast<int64_t>(num_kv_heads) * (max_context_len / 16 + 1);
+    if (stages * std::min(num_seqs, kSplitEntries) >= (int64_t{1} << 31) ||
+        static_cast<int64_t>(num_seqs) * num_heads >= (int64_t{1} << 31))
+        return PA_ERR_UNSUPPORTED;
+    return PA_OK;
+}
+
+pa::SplitParams split_params(void *out, pa_dtype out_dtype, const void *query, pa_dtype q_dtype,
+                             const int32_t *block_tables, int max_blocks_per_seq, const int32_t *context_lens,
+                             int max_context_len, int num_seqs, int num_heads, int num_kv_heads, int block_size,
+                             int64_t num_blocks, float scale, const SplitPlan &w, void *workspace, int *err_flag) {
+    pa::SplitParams p{};
+    p.out = out;
+    p.out_dtype = static_cast<int>(out_dtype);
+    p.q = static_cast<const uint16_t *>(query);
+    p.q_bf16 = q_dtype == PA_BF16;
+    p.block_tables = block_tables;
+    p.context_lens = context_lens;
+    p.max_blocks_per_seq = max_blocks_per_seq;
+    p.max_context_len = max_context_len;
+    p.num_seqs = num_seqs;
+    p.num_heads = num_heads;
+    p.num_kv_heads = num_kv_heads;
+    while ((1 << p.log2_group) < w.G) ++p.log2_group;
+    p.block_size = block_size;
+    p.num_blocks = num_blocks;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.partition_size = w.partition;
+    p.max_parts = w.max_parts;
+    if (w.bytes) {
+        p.ws_ml = static_cast<float *>(workspace);
+        p.ws_acc = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + w.acc_off);
+    }
+    p.err_flag = err_flag;
+    p.log2_heads = w.log2_heads;
+    return p;
+}
+
+}  // namespace
+
+PA_EXPORT pa_status pa_quant_reshape_and_cache(const void *key, const void *value, int64_t key_stride,
+                                               int64_t value_stride, void *k_cache, void *v_cache, float *k_scales,
+                                               float *v_scales, const int64_t *slot_mapping, int64_t num_tokens,
+                                               int64_t num_blocks, int block_size, int num_kv_heads, int head_dim,
+                                               pa_dtype dtype, pa_dtype cache_dtype, int *err_flag, void *stream) {
+    if (num_tokens < 0 || num_blocks <= 0 || block_size <= 0 || num_kv_heads <= 0 || head_dim <= 0 ||
+        !half_dtype(dtype) || !quant_dtype(cache_dtype))
+        return PA_ERR_INVALID_ARG;
+    if (!supported_head_dim(head_dim) || num_kv_heads > (1 << 20)) return PA_ERR_UNSUPPORTED;
+    const int64_t row = static_cast<int64_t>(num_kv_heads) * head_dim;
+    if (key_stride < row || value_stride < row || key_stride % 8 != 0 || value_stride % 8 != 0)
+        return PA_ERR_INVALID_ARG;
+    if (num_tokens == 0) return PA_OK;
+    if (!key || !value || !k_cache || !v_cache || !k_scales || !v_scales || !slot_mapping) return PA_ERR_INVALID_ARG;
+    if (!aligned16(key) || !aligned16(value) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_scales) ||
+        !aligned16(v_scales))
+        return PA_ERR_INVALID_ARG;
+    DeviceInfo dev;
+    if (!device_info(dev)) return PA_ERR_CUDA;
+    const cudaError_t e = pa::launch_quant_write(
+        key, value, key_stride, value_stride, k_cache, v_cache, k_scales, v_scales, slot_mapping, num_tokens,
+        num_blocks * block_size, num_kv_heads, head_dim, dtype == PA_BF16, split_cache(cache_dtype), dev.sms, err_flag,
+        static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+PA_EXPORT pa_status pa_quant_gather(void *out_k, void *out_v, pa_dtype out_dtype, const void *k_cache,
+                                    const void *v_cache, pa_dtype cache_dtype, const float *k_scales,
+                                    const float *v_scales, const int32_t *block_tables, int max_blocks_per_seq,
+                                    const int32_t *cu_seqlens, const int32_t *seq_starts, int num_seqs,
+                                    int64_t num_tokens, int num_kv_heads, int head_dim, int block_size,
+                                    int64_t num_blocks, int *err_flag, void *stream) {
+    if (num_seqs < 0 || num_tokens < 0 || num_blocks <= 0 || block_size <= 0 || num_kv_heads <= 0 || head_dim <= 0 ||
+        max_blocks_per_seq <= 0 || !out_dtype_ok(out_dtype) || !quant_dtype(cache_dtype))
+        return PA_ERR_INVALID_ARG;
+    if (!supported_head_dim(head_dim) || num_kv_heads > (1 << 20) || num_tokens > INT32_MAX) return PA_ERR_UNSUPPORTED;
+    if (num_seqs == 0 || num_tokens == 0) return PA_OK;
+    if (!out_k || !out_v || !k_cache || !v_cache || !k_scales || !v_scales || !block_tables || !cu_seqlens)
+        return PA_ERR_INVALID_ARG;
+    if (!aligned16(out_k) || !aligned16(out_v) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_scales) ||
+        !aligned16(v_scales))
+        return PA_ERR_INVALID_ARG;
+    const cudaError_t e = pa::launch_quant_gather(out_k, out_v, static_cast<int>(out_dtype), k_cache, v_cache,
+                                                  split_cache(cache_dtype), k_scales, v_scales, block_tables,
+                                                  max_blocks_per_seq, cu_seqlens, seq_starts, num_seqs, num_tokens,
+                                                  num_kv_heads, head_dim, block_size, num_blocks, err_flag,
+                                                  static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+PA_EXPORT size_t pa_quant_decode_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                                                int block_size, int max_context_len, int partition_size) {
+    SplitPlan w;
+    if (!plan_split(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context_len, partition_size,
+                    pa::kCacheInt8, false, 0, 0, 0, w))
+        return static_cast<size_t>(-1);
+    return w.bytes;
+}
+
+PA_EXPORT pa_status pa_quant_decode(void *out, pa_dtype out_dtype, const void *query, pa_dtype q_dtype,
+                                    const void *k_cache, const void *v_cache, pa_dtype cache_dtype,
+                                    const float *k_scales, const float *v_scales, const int32_t *block_tables,
+                                    int max_blocks_per_seq, const int32_t *context_lens, int max_context_len,
+                                    int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size,
+                                    int64_t num_blocks, float scale, int partition_size, void *workspace,
+                                    size_t workspace_bytes, int *err_flag, void *stream) {
+    if (!quant_dtype(cache_dtype)) return PA_ERR_INVALID_ARG;
+    const pa_status st = check_split(out_dtype, q_dtype, max_blocks_per_seq, max_context_len, num_seqs, num_heads,
+                                     num_kv_heads, head_dim, block_size, num_blocks, scale);
+    if (st != PA_OK) return st;
+    const int cache = split_cache(cache_dtype);
+    SplitPlan w;
+    if (!plan_split(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context_len, partition_size, cache,
+                    false, 0, 0, 0, w))
+        return PA_ERR_INVALID_ARG;
+    if (num_seqs == 0) return PA_OK;
+    if (!out || !query || !k_cache || !v_cache || !k_scales || !v_scales || !block_tables || !context_lens)
+        return PA_ERR_INVALID_ARG;
+    if (!aligned16(out) || !aligned16(query) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_scales) ||
+        !aligned16(v_scales))
+        return PA_ERR_INVALID_ARG;
+    if (w.bytes > 0 && (workspace == nullptr || workspace_bytes < w.bytes || !aligned16(workspace)))
+        return PA_ERR_WORKSPACE;
+    DeviceInfo dev;
+    if (!device_info(dev)) return PA_ERR_CUDA;
+    CUtensorMap tk, tv;
+    if (!encode_split_map(&tk, k_cache, num_blocks, block_size, num_kv_heads, head_dim, 1, 1 << w.log2_heads) ||
+        !encode_split_map(&tv, v_cache, num_blocks, block_size, num_kv_heads, head_dim, 1, 1 << w.log2_heads))
+        return PA_ERR_CUDA;
+    pa::SplitParams p = split_params(out, out_dtype, query, q_dtype, block_tables, max_blocks_per_seq, context_lens,
+                                     max_context_len, num_seqs, num_heads, num_kv_heads, block_size, num_blocks, scale,
+                                     w, workspace, err_flag);
+    p.k_scales = k_scales;
+    p.v_scales = v_scales;
+    p.mode = pa::kSplitDecode;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const pa_status r = run_split(p, cache, head_dim, w.G, num_seqs, max_context_len, tk, tv, dev, s);
+    if (r != PA_OK || w.max_parts <= 1) return r;
+    return pa::launch_split_merge(p, head_dim, 1, dev.sms, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+PA_EXPORT size_t pa_decode_shared_workspace_size(int num_seqs, int num_groups, int max_group_size, int num_heads,
+                                                 int num_kv_heads, int head_dim, int block_size, int max_context_len,
+                                                 int max_shared_len, int partition_size) {
+    SplitPlan w;
+    if (!plan_split(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context_len, partition_size,
+                    pa::kCacheF16, true, num_groups, max_group_size, max_shared_len, w))
+        return static_cast<size_t>(-1);
+    return w.bytes;
+}
+
+PA_EXPORT pa_status pa_decode_shared(void *out, pa_dtype out_dtype, const void *query, const void *k_cache,
+                                     const void *v_cache, pa_dtype kv_dtype, const int32_t *block_tables,
+                                     int max_blocks_per_seq, const int32_t *context_lens, int max_context_len,
+                                     const int32_t *cu_groups, int num_groups, int max_group_size,
+                                     const int32_t *shared_lens, int max_shared_len, int num_seqs, int num_heads,
+                                     int num_kv_heads, int head_dim, int block_size, int64_t num_blocks, float scale,
+                                     int partition_size, void *workspace, size_t workspace_bytes, int *err_flag,
+                                     void *stream) {
+    if (num_groups < 0 || max_group_size < 0 || max_shared_len < 0 || max_shared_len > max_context_len)
+        return PA_ERR_INVALID_ARG;
+    const pa_status st = check_split(out_dtype, kv_dtype, max_blocks_per_seq, max_context_len, num_seqs, num_heads,
+                                     num_kv_heads, head_dim, block_size, num_blocks, scale);
+    if (st != PA_OK) return st;
+    if (num_seqs > 0 && (static_cast<int64_t>(num_groups) * max_group_size < num_seqs || num_groups > num_seqs ||
+                         max_group_size > num_seqs))
+        return PA_ERR_INVALID_ARG;
+    const int cache = split_cache(kv_dtype);
+    SplitPlan w;
+    if (!plan_split(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context_len, partition_size, cache,
+                    true, num_groups, max_group_size, max_shared_len, w))
+        return PA_ERR_INVALID_ARG;
+    if (num_seqs == 0) return PA_OK;
+    if (!out || !query || !k_cache || !v_cache || !block_tables || !context_lens || !cu_groups || !shared_lens)
+        return PA_ERR_INVALID_ARG;
+    if (!aligned16(out) || !aligned16(query) || !aligned16(k_cache) || !aligned16(v_cache)) return PA_ERR_INVALID_ARG;
+    if (workspace == nullptr || workspace_bytes < w.bytes || !aligned16(workspace)) return PA_ERR_WORKSPACE;
+    DeviceInfo dev;
+    if (!device_info(dev)) return PA_ERR_CUDA;
+    CUtensorMap tk, tv;
+    if (!encode_split_map(&tk, k_cache, num_blocks, block_size, num_kv_heads, head_dim, 2, 1 << w.log2_heads) ||
+        !encode_split_map(&tv, v_cache, num_blocks, block_size, num_kv_heads, head_dim, 2, 1 << w.log2_heads))
+        return PA_ERR_CUDA;
+    pa::SplitParams p = split_params(out, out_dtype, query, kv_dtype, block_tables, max_blocks_per_seq, context_lens,
+                                     max_context_len, num_seqs, num_heads, num_kv_heads, block_size, num_blocks, scale,
+                                     w, workspace, err_flag);
+    p.shared_lens = shared_lens;
+    p.cu_groups = cu_groups;
+    p.num_groups = num_groups;
+    p.max_group_size = max_group_size;
+    p.max_shared_len = max_shared_len;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (w.prefix_parts > 0) {
+        pa::SplitParams pre = p;
+        pre.mode = pa::kSplitPrefix;
+        pre.partition_size = w.prefix_part;
+        pre.chunk_seqs = w.prefix_cols / w.G;
+        pre.chunks = (max_group_size + pre.chunk_seqs - 1) / pre.chunk_seqs;
+        if (static_cast<int64_t>(num_groups) * pre.chunks >= (int64_t{1} << 31)) return PA_ERR_UNSUPPORTED;
+        const pa_status r = run_split(pre, cache, head_dim, w.prefix_cols, num_groups * pre.chunks, max_shared_len, tk,
+                                      tv, dev, s);
+        if (r != PA_OK) return r;
+    }
+    p.mode = pa::kSplitSuffix;
+    p.part_off = w.prefix_parts;
+    p.late_wait = w.prefix_parts > 0;
+    const pa_status r = run_split(p, cache, head_dim, w.G, num_seqs, max_context_len, tk, tv, dev, s);
+    if (r != PA_OK) return r;
+    return pa::launch_split_merge(p, head_dim, std::max(1, w.prefix_part), dev.sms, s) == cudaSuccess ? PA_OK
+                                                                                                      : PA_ERR_CUDA;
 }
 
 PA_EXPORT pa_status pa_check_err_flag(int *err_flag, int clear, int *flag_out, void *stream) {

@@ -1,0 +1,106 @@
+// Host-side interface between the C ABI (pa_api.cu) and the split decode
+// kernels (pa_split_kernel.cuh, one instantiating file per cache type), their
+// merge (pa_split_merge.cu), the shared-prefix kernel (pa_shared_prefix.cu) and
+// the quantised cache's write and read-back (pa_quant_ops.cu).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace pa {
+
+// Cache element types of the split kernels.  The 8-bit ones carry one float
+// scale per token and KV head.
+constexpr int kCacheF16 = 0, kCacheBF16 = 1, kCacheE4M3 = 2, kCacheInt8 = 3;
+
+// What a launch's entries are.
+constexpr int kSplitDecode = 0;   // sequences, whole contexts; results final where one partition holds them
+constexpr int kSplitSuffix = 1;   // sequences past their shared blocks; partial results only
+constexpr int kSplitPrefix = 2;   // (group, chunk of its sequences) over the group's shared blocks; partial only
+
+struct SplitParams {
+    void *out;
+    int out_dtype;               // pa_dtype value
+    const uint16_t *q;           // [num_seqs, Hq, D]
+    int q_bf16;
+    const int32_t *block_tables; // [num_seqs, max_blocks_per_seq]
+    const int32_t *context_lens; // [num_seqs]
+    int max_blocks_per_seq;
+    int max_context_len;
+    int num_seqs;
+    int num_heads;
+    int num_kv_heads;
+    int log2_group;              // query heads per KV head
+    int block_size;
+    int64_t num_blocks;
+    float scale_log2;            // softmax scale * log2(e)
+    int partition_size;          // tokens per partition, a multiple of 16, at most 32 blocks
+    int max_parts;               // partial results per (sequence, KV head) in the workspace
+    int part_off;                // where this launch's start among them
+    float *ws_ml;                // [num_seqs * Hkv * max_parts, G, 2]  (reference, sum)
+    float *ws_acc;               // [num_seqs * Hkv * max_parts, G, D]
+    const float *k_scales;       // 8-bit caches: [num_blocks, bs, Hkv]
+    const float *v_scales;
+    int *err_flag;
+    int mode;
+    const int32_t *shared_lens;  // suffix, prefix: [num_seqs] tokens a sequence shares with its group
+    const int32_t *cu_groups;    // prefix: [num_groups + 1]
+    int num_groups;
+    int chunks, chunk_seqs;      // prefix: a group's sequences are taken chunk_seqs at a time
+    int max_group_size;
+    int max_shared_len;
+    int e0, entries;             // this launch's entries
+    int log2_heads;              // KV heads per box: 1, 2, 4 or 8
+    int stages;                  // ring depth
+    int late_wait;               // the previous kernel is the call's own prefix kernel, whose results this
+                                 // one does not read: wait for it only at the end
+};
+
+// The state a launch needs in shared memory beyond its ring, and a ring slot.
+struct SplitSmem {
+    size_t fixed, slot;
+};
+SplitSmem split_smem(int head_dim, int cols, int cache, int log2_heads, int entries);
+
+// KV heads per box: the largest power of two up to 8 that divides Hkv.
+inline int split_log2_heads(int num_kv_heads) {
+    int l = 0;
+    while (l < 3 && num_kv_heads % (2 << l) == 0) ++l;
+    return l;
+}
+
+// 16-token stages of one ring slot (a slot feeds every consumer warp once).
+int split_slot_stages(int cache, int log2_heads);
+
+// `cols`: query rows per KV head and entry (1, 2, 4 or 8).  The tensor maps
+// view the caches as (dim, token, head) with {min(128 bytes, row), min(16, bs),
+// heads} boxes.
+cudaError_t launch_split_f16(const SplitParams &p, int head_dim, int cols, const CUtensorMap &tk,
+                             const CUtensorMap &tv, int grid, size_t smem, cudaStream_t stream);
+cudaError_t launch_split_bf16(const SplitParams &p, int head_dim, int cols, const CUtensorMap &tk,
+                              const CUtensorMap &tv, int grid, size_t smem, cudaStream_t stream);
+cudaError_t launch_split_e4m3(const SplitParams &p, int head_dim, int cols, const CUtensorMap &tk,
+                              const CUtensorMap &tv, int grid, size_t smem, cudaStream_t stream);
+cudaError_t launch_split_int8(const SplitParams &p, int head_dim, int cols, const CUtensorMap &tk,
+                              const CUtensorMap &tv, int grid, size_t smem, cudaStream_t stream);
+
+// Joins partial results into output rows.  Sequence s has ceil(len / prefix_part)
+// partials of its shared blocks at index 0.. and ceil(rest / partition_size) at
+// p.part_off.. (p.mode kSplitDecode: no shared blocks, and sequences of one
+// partition are final already).
+cudaError_t launch_split_merge(const SplitParams &p, int head_dim, int prefix_part, int sms, cudaStream_t stream);
+
+// Quantising write and read-back (cache: kCacheE4M3 or kCacheInt8).
+cudaError_t launch_quant_write(const void *key, const void *value, int64_t key_stride, int64_t value_stride,
+                               void *k_cache, void *v_cache, float *k_scales, float *v_scales,
+                               const int64_t *slot_mapping, int64_t num_tokens, int64_t num_slots, int num_kv_heads,
+                               int head_dim, bool bf16, int cache, int sms, int *err_flag, cudaStream_t stream);
+
+cudaError_t launch_quant_gather(void *out_k, void *out_v, int out_dtype, const void *k_cache, const void *v_cache,
+                                int cache, const float *k_scales, const float *v_scales, const int32_t *block_tables,
+                                int max_blocks_per_seq, const int32_t *cu_seqlens, const int32_t *seq_starts,
+                                int num_seqs, int64_t num_tokens, int num_kv_heads, int head_dim, int block_size,
+                                int64_t num_blocks, int *err_flag, cudaStream_t stream);
+
+}  // namespace pa

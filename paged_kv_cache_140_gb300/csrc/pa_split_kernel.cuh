@@ -1,0 +1,916 @@
+// Split decode attention over a paged cache: 16-bit caches, and 8-bit caches
+// (e4m3 or int8 codes) with one scale per token and KV head.
+//
+// For query row q of an entry and the entry's tokens p, with code rows c_p and
+// scales k_p, v_p (1 for 16-bit caches):
+//     x_p = scale k_p <q, cK_p>,   out = sum_p softmax(x)_p v_p cV_p.
+// An entry is a sequence (its whole context, or what follows the blocks it
+// shares with its group) or a chunk of a group's sequences over their shared
+// blocks; it is cut into partitions, and the partitions' states (reference,
+// sum, weighted sum of V) are joined by pa_split_merge.cu.
+//
+// The softmax runs in base 2 with one running reference m per query row that
+// serves the sum and the V product: with s_p = log2(e) x_p,
+//     l = sum 2^(s_p - m),   acc = sum (2^(s_p - m) v_p) cV_p.
+// m follows the maximum of s_p + log2 v_p, the exponent of the weights that
+// enter the V product, so that the weights 2^(s_p - m) v_p stay at most 2^8 (m
+// moves only when exceeded by more than that) and the largest near 1 whatever
+// the scales are: they go into the product as binary16 high and low parts
+// (~22 bits), accurate relative to the largest.  2^(s_p - m) itself is then off
+// by up to 1 / v_p, which 32 bits hold for every scale the cache write makes
+// from rows below 2^60.
+//
+// 8-bit codes are exact in binary16 and the products run there; the query is
+// scaled per row by a power of two to a largest element in [1, 2) (undone on
+// the logits), so that a bfloat16 query of any size fits.
+//
+// What bounds it: reading the cache.  One producer warp brings ring slots in by
+// TMA (boxes of up to 8 KV heads: 16 rows of one physical block of each land as
+// one swizzled tile) and, for 8-bit caches, the scales by 4- or 16-byte
+// asynchronous copies that complete on the same barrier.  A slot holds one tile
+// of 16 tokens (two for 8-bit caches with 8 warps) for each consumer warp: the
+// box's heads times as many 16-token stages as make up the warps, so KV-head
+// counts that are not a multiple of 8 keep every warp busy; warps that share a
+// head keep states of their own and join them at the item's end.
+// Waits are bounded (2 s) and report PA_FLAG_TIMEOUT.
+#pragma once
+
+#include "pa_decode_common.cuh"
+#include "pa_device.cuh"
+#include "pa_split.h"
+
+namespace pa {
+
+namespace {
+
+using namespace decode_common;
+
+constexpr int kQueryRing = 2;
+
+template <int D, int C, int CT>
+struct SplitLayout {
+    static constexpr bool k8 = CT >= kCacheE4M3;
+    static constexpr int kES = k8 ? 1 : 2;
+    static constexpr int kWarps = 8;                     // consumer warps
+    static constexpr int kSub = k8 ? 2 : 1;              // stages per consumer warp and slot
+    static constexpr int kTiles = kWarps * kSub;         // (stage, head) tiles of a slot
+    static constexpr int kRowB = D * kES < 128 ? D * kES : 128;   // bytes of one box row
+    static constexpr int kHalves = D * kES / kRowB;
+    static constexpr int kKVBytes = kTiles * kStageTokens * D * kES;   // a slot's K (or V) rows
+    static constexpr int kScaleBytes = k8 ? kTiles * kStageTokens * 4 : 0;
+    static constexpr int kSlotBytes = (2 * kKVBytes + 2 * kScaleBytes + 1023) / 1024 * 1024;
+    static constexpr int kThreads = (kWarps + 1) * 32;
+    static constexpr int kMT = D / 16;
+    static constexpr int kStateBytes = kMT * 32 * 16;    // one warp's accumulators
+};
+
+// One ring slot's description.
+struct SlotMeta {
+    int seq;         // the entry's first query sequence; < 0: no more work
+    int kvh0;        // first KV head of the box
+    int part;
+    int flags;       // kFirst | kLast | kFinal, members << 8
+    int ntok;        // valid tokens from the slot's first
+    uint32_t bad;    // bit 2 i (+ 1): rows 0-7 (8-15) of the slot's stage i were not loaded
+    int pad[2];
+};
+constexpr int kFirst = 1;    // the item's first slot: load the queries, reset the state
+constexpr int kLast = 2;     // the item's last slot: write the results
+constexpr int kFinal = 4;    // the item is the whole of the sequence's context
+
+__device__ __forceinline__ void arrive(uint64_t *bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
+// This thread's earlier cp.async copies arrive once on `bar` when they land
+// (one of the barrier's expected arrivals).
+__device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ uint64_t l2_policy_evict_normal() {
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+
+__device__ __forceinline__ float fast_log2(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Four codes (bytes 0-3) as two f16 pairs.  Natural order: (0, 1), (2, 3);
+// interleaved: (0, 2), (1, 3).  An int8 code b is u - 128 for the byte
+// u = b ^ 0x80, and 0x6400 | u is binary16 1024 + u: all steps exact.
+template <int CT, bool Interleaved>
+__device__ __forceinline__ void widen(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    if constexpr (CT == kCacheE4M3) {
+        e4m3x4_to_f16x2x2(Interleaved ? prmt(w, 0x3120u) : w, lo, hi);
+    } else {
+        const uint32_t u = w ^ 0x80808080u;
+        lo = __byte_perm(u, 0x64646464u, Interleaved ? 0x4240u : 0x4140u);
+        hi = __byte_perm(u, 0x64646464u, Interleaved ? 0x4341u : 0x4342u);
+        asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(lo) : "r"(0x64806480u));
+        asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(hi) : "r"(0x64806480u));
+    }
+}
+
+// Sequence s's shared blocks; a length that is negative, above the bound or
+// beyond the sequence's context counts as none and is reported.
+__device__ __forceinline__ int shared_blocks(const SplitParams &p, int s, int ctx, bool tell) {
+    const int n = __ldg(p.shared_lens + s);
+    if (n < 0 || n > p.max_shared_len || n > ctx) {
+        if (tell) report(p.err_flag, 0x4 /* PA_FLAG_BAD_CONTEXT_LEN */);
+        return 0;
+    }
+    return n / p.block_size;
+}
+
+__device__ __forceinline__ int context_of(const SplitParams &p, int s, bool tell) {
+    const int c = __ldg(p.context_lens + s);
+    if (c < 0 || c > p.max_context_len) {
+        if (tell) report(p.err_flag, 0x4 /* PA_FLAG_BAD_CONTEXT_LEN */);
+        return 0;
+    }
+    return c;
+}
+
+// Items (entry, partition, box of heads) in that order, weighed in slots.  An
+// entry without tokens weighs nothing, except in decode mode, where it costs
+// the slot that writes its zero row.
+struct ItemCursor {
+    int e, len, nparts, part, grp, nslots;
+    uint32_t start;
+};
+
+__device__ __forceinline__ int item_slots(int len, int part, int P, int SW) {
+    const int n = len - part * P;
+    const int st = n > 0 ? (min(P, n) + kStageTokens - 1) / kStageTokens : 1;
+    return (st + SW - 1) / SW;
+}
+
+__device__ __forceinline__ uint32_t entry_weight(int len, int mode, int ngroups, int P, int SW) {
+    if (len <= 0) return mode == kSplitDecode ? static_cast<uint32_t>(ngroups) : 0u;
+    const int full = (len - 1) / P;   // partitions before the last
+    return static_cast<uint32_t>(ngroups) *
+           static_cast<uint32_t>(full * ((P / kStageTokens + SW - 1) / SW) + item_slots(len, full, P, SW));
+}
+
+template <int D, int C, int CT>
+__global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
+    paged_split_kernel(const __grid_constant__ SplitParams p, const __grid_constant__ CUtensorMap tmap_k,
+                       const __grid_constant__ CUtensorMap tmap_v) {
+    using L = SplitLayout<D, C, CT>;
+    constexpr bool k8 = L::k8;
+    constexpr bool BF16 = CT == kCacheBF16;   // MMA operand type
+    constexpr int SUB = L::kSub, W = L::kWarps, MT = L::kMT, KS = D / 16;
+    constexpr int NE = C == 1 ? 1 : 2;        // live columns per lane (columns 2t, 2t + 1)
+    using Cvt = Half2x<BF16>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                ~static_cast<uintptr_t>(1023));
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int S = p.stages, E = p.entries, Hkv = p.num_kv_heads, Hq = p.num_heads;
+    const int P = p.partition_size, bs = p.block_size, mode = p.mode, lg = p.log2_group;
+    const int H = 1 << p.log2_heads, ngroups = Hkv >> p.log2_heads;
+    const int SW = L::kTiles >> p.log2_heads;          // stages per slot
+    const int nsubs = W >> p.log2_heads;               // consumer warps per head
+    const int RB = min(bs, kStageTokens);              // rows per box
+    const int per_stage = kStageTokens / RB;           // boxes (blocks) per stage
+    const int qmember = H * D * 2 << lg;               // one sequence's query rows of a box
+    constexpr int kQEntry = C * D * 2;                 // x H: one query-ring entry
+
+    uint8_t *slots = smem;
+    uint8_t *qbuf = smem + static_cast<size_t>(S) * L::kSlotBytes;
+    uint8_t *xbuf = qbuf + kQueryRing * kQEntry * H;   // (W - H) warp states
+    float2 *xml = reinterpret_cast<float2 *>(xbuf + (W - H) * L::kStateBytes);   // [warp][8]
+    SlotMeta *meta = reinterpret_cast<SlotMeta *>(xml + W * 8);
+    uint64_t *full = reinterpret_cast<uint64_t *>(meta + S);
+    uint64_t *empty = full + S;
+    uint64_t *qfull = empty + S;
+    uint64_t *qempty = qfull + kQueryRing;
+    uint64_t *xfull = qempty + kQueryRing;             // per head: the other warps' states are written
+    uint64_t *xfree = xfull + 8;                       //           and have been read
+    uint32_t *warp_tot = reinterpret_cast<uint32_t *>(xfree + 8);
+    int *len_s = reinterpret_cast<int *>(warp_tot + 32);
+    int *aux_s = len_s + E;                            // suffix: first block; prefix: sequence | members << 27
+    uint32_t *prefix = reinterpret_cast<uint32_t *>(aux_s + E);
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S; ++i) {
+            mbar_init(&full[i], k8 ? 33 : 1);
+            mbar_init(&empty[i], W);
+        }
+        for (int i = 0; i < kQueryRing; ++i) {
+            mbar_init(&qfull[i], 1);
+            mbar_init(&qempty[i], W);
+        }
+        for (int i = 0; i < H; ++i) {
+            mbar_init(&xfull[i], max(1, nsubs - 1));
+            mbar_init(&xfree[i], 1);
+        }
+        fence_barrier_init();
+        prefetch_tensormap(&tmap_k);
+        prefetch_tensormap(&tmap_v);
+    }
+    // Launched with programmatic dependent launch.  late_wait: the previous
+    // kernel is this call's prefix kernel, which let this one start only after
+    // everything before the call had completed.
+    if (!p.late_wait) pdl_wait();
+    pdl_launch_dependents();
+    // ---- the entries' lengths ----
+    const bool tell = blockIdx.x == 0;
+    for (int i = threadIdx.x; i < E; i += blockDim.x) {
+        int len = 0, aux = 0;
+        if (mode == kSplitPrefix) {
+            const int g = (p.e0 + i) / p.chunks, ck = (p.e0 + i) % p.chunks;
+            const int q0 = __ldg(p.cu_groups + g), q1 = __ldg(p.cu_groups + g + 1);
+            if (q0 < 0 || q1 < q0 || q1 > p.num_seqs || q1 - q0 > p.max_group_size || (g == 0 && q0 != 0) ||
+                (g == p.num_groups - 1 && q1 != p.num_seqs)) {
+                if (tell) report(p.err_flag, 0x4 /* PA_FLAG_BAD_CONTEXT_LEN */);
+            } else {
+                const int s0 = q0 + ck * p.chunk_seqs, m = min(p.chunk_seqs, q1 - s0);
+                if (m > 0) {
+                    len = shared_blocks(p, q0, context_of(p, q0, false), false) * bs;
+                    aux = s0 | (m << 27);
+                    for (int k = 0; tell && k < m; ++k)   // one length for all of a group
+                        if (__ldg(p.shared_lens + s0 + k) != __ldg(p.shared_lens + q0))
+                            report(p.err_flag, 0x4 /* PA_FLAG_BAD_CONTEXT_LEN */);
+                }
+            }
+        } else {
+            len = context_of(p, p.e0 + i, tell);
+            if (mode == kSplitSuffix) {
+                aux = shared_blocks(p, p.e0 + i, len, tell);
+                len -= aux * bs;
+            }
+        }
+        len_s[i] = len;
+        aux_s[i] = aux;
+    }
+    __syncthreads();
+    {
+        // prefix[i]: slots of the entries before i
+        const int nthr = blockDim.x, nw = nthr >> 5;
+        const int per = (E + nthr - 1) / nthr;
+        const int beg = min(E, static_cast<int>(threadIdx.x) * per), end = min(E, beg + per);
+        uint32_t local = 0;
+        for (int i = beg; i < end; ++i) local += entry_weight(len_s[i], mode, ngroups, P, SW);
+        uint32_t incl = local;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t v = __shfl_up_sync(kFull, incl, o);
+            if (lane >= o) incl += v;
+        }
+        if (lane == 31) warp_tot[warp] = incl;
+        __syncthreads();
+        uint32_t run = incl - local;
+        for (int w = 0; w < warp; ++w) run += warp_tot[w];
+        for (int i = beg; i < end; ++i) {
+            prefix[i] = run;
+            run += entry_weight(len_s[i], mode, ngroups, P, SW);
+        }
+        if (threadIdx.x == 0) {
+            uint32_t tot = 0;
+            for (int w = 0; w < nw; ++w) tot += warp_tot[w];
+            prefix[E] = tot;
+        }
+        __syncthreads();
+    }
+    // This CTA takes the items whose first slot lies in its equal share.
+    const uint32_t total = prefix[E];
+    const uint32_t lo = static_cast<uint32_t>(static_cast<uint64_t>(total) * blockIdx.x / gridDim.x);
+    const uint32_t hi = static_cast<uint32_t>(static_cast<uint64_t>(total) * (blockIdx.x + 1) / gridDim.x);
+
+    if (warp == W) {
+        // ------------------------------------------------------------ producer
+        const uint64_t policy =
+            mode == kSplitPrefix && p.chunks > 1 ? l2_policy_evict_normal() : l2_policy_evict_first();
+        ItemCursor ic{};
+        auto set_entry = [&](int e) {
+            ic.e = e;
+            ic.len = len_s[e];
+            ic.nparts = ic.len > 0 ? (ic.len + P - 1) / P : 1;
+        };
+        auto set_part = [&](int part) {
+            ic.part = part;
+            ic.nslots = item_slots(ic.len, part, P, SW);
+        };
+        auto advance = [&]() {
+            ic.start += ic.nslots;
+            if (++ic.grp < ngroups) return;
+            ic.grp = 0;
+            if (ic.part + 1 < ic.nparts) {
+                set_part(ic.part + 1);
+                return;
+            }
+            int e = ic.e + 1;
+            while (e < E && prefix[e] == prefix[e + 1]) ++e;   // entries without work
+            if (e < E) {
+                set_entry(e);
+                set_part(0);
+            }
+        };
+        const bool work = lo < hi;
+        if (work) {
+            // the entry holding slot lo (the last with prefix <= lo), then its first item starting at or after lo
+            int a = 0, b = E;
+            while (b - a > 1) {
+                const int m = (a + b) >> 1;
+                if (prefix[m] <= lo) a = m; else b = m;
+            }
+            set_entry(a);
+            const uint32_t pw = static_cast<uint32_t>(ngroups) * static_cast<uint32_t>((P / kStageTokens + SW - 1) / SW);
+            const uint32_t off = lo - prefix[a];
+            set_part(min(ic.nparts - 1, static_cast<int>(off / pw)));
+            const uint32_t pstart = prefix[a] + static_cast<uint32_t>(ic.part) * pw;
+            const int grp = static_cast<int>((lo - pstart + ic.nslots - 1) / ic.nslots);
+            ic.grp = min(grp, ngroups - 1);
+            ic.start = pstart + static_cast<uint32_t>(ic.grp) * ic.nslots;
+            if (grp >= ngroups) advance();
+        }
+        int islot = 0;
+        uint32_t uses = 0, items = 0;
+        bool ok = true;
+        auto take_slot = [&]() -> int {
+            const int slot = islot;
+            if (uses >= static_cast<uint32_t>(S)) {
+                const uint32_t par = ((uses / S) - 1) & 1u;
+                if (!mbar_try_wait(&empty[slot], par) && !mbar_wait_bounded(&empty[slot], par)) {
+                    if (lane == 0) report(p.err_flag, 0x10 /* PA_FLAG_TIMEOUT */);
+                    ok = false;
+                }
+            }
+            ok = __all_sync(kFull, ok);
+            islot = (islot + 1 == S) ? 0 : islot + 1;
+            ++uses;
+            return slot;
+        };
+        while (ok && work && ic.start < hi) {
+            const int kvh0 = ic.grp << p.log2_heads;
+            int seq = p.e0 + ic.e, members = 1, row = seq, blk0 = 0;
+            if (mode == kSplitPrefix) {
+                seq = aux_s[ic.e] & 0x7ffffff;
+                members = aux_s[ic.e] >> 27;
+                row = seq - ((p.e0 + ic.e) % p.chunks) * p.chunk_seqs;   // the group's first sequence
+            } else if (mode == kSplitSuffix) {
+                blk0 = aux_s[ic.e];
+            }
+            const int t0 = ic.part * P;
+            const int ntok = max(0, min(P, ic.len - t0));
+            // the partition's block ids, one per lane
+            const int fb = t0 / bs;
+            int32_t bid = -1;
+            if (ntok > 0 && lane <= (t0 + ntok - 1) / bs - fb)
+                bid = __ldg(p.block_tables + static_cast<int64_t>(row) * p.max_blocks_per_seq + blk0 + fb + lane);
+            {
+                const int qi = static_cast<int>(items % kQueryRing);
+                if (items >= static_cast<uint32_t>(kQueryRing)) {
+                    const uint32_t par = ((items / kQueryRing) - 1) & 1u;
+                    if (!mbar_try_wait(&qempty[qi], par) && !mbar_wait_bounded(&qempty[qi], par)) {
+                        if (lane == 0) report(p.err_flag, 0x10 /* PA_FLAG_TIMEOUT */);
+                        ok = false;
+                    }
+                    ok = __all_sync(kFull, ok);
+                    if (!ok) break;
+                }
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&qfull[qi], static_cast<uint32_t>(members * qmember));
+                    for (int m = 0; m < members; ++m)
+                        bulk_load(qbuf + qi * kQEntry * H + m * qmember,
+                                  p.q + (static_cast<int64_t>(seq + m) * Hq + (kvh0 << lg)) * D,
+                                  static_cast<uint32_t>(qmember), &qfull[qi]);
+                }
+                ++items;
+                __syncwarp();
+            }
+            const int fin = mode == kSplitDecode && ic.nparts == 1 ? kFinal : 0;
+            for (int j = 0; j < ic.nslots; ++j) {
+                const int slot = take_slot();
+                if (!ok) break;
+                uint8_t *sp = slots + static_cast<size_t>(slot) * L::kSlotBytes;
+                const int tok0 = t0 + j * SW * kStageTokens;                 // the slot's first position
+                const int nt = max(0, min(SW * kStageTokens, t0 + ntok - tok0));
+                // The slot's pieces are RB rows of one block (SW * per_stage of them, at most 32), one per lane.
+                const int ptok = tok0 + lane * RB;
+                const bool has = lane < SW * per_stage && lane * RB < nt;
+                const int id = __shfl_sync(kFull, bid, has ? ptok / bs - fb : 0);
+                const bool load = has && id >= 0 && static_cast<int64_t>(id) < p.num_blocks;
+                const uint32_t loaded = __ballot_sync(kFull, load);
+                uint32_t bad = __ballot_sync(kFull, has && !load);
+                if (bad && lane == 0) report(p.err_flag, 0x2 /* PA_FLAG_BAD_BLOCK_ID */);
+                if (bad && per_stage == 1) {   // one bit per stage -> two
+                    uint32_t w = 0;
+                    for (int i = 0; i < SW; ++i) w |= ((bad >> i) & 1u) * (3u << (2 * i));
+                    bad = w;
+                }
+                const uint32_t box = static_cast<uint32_t>(RB * L::kRowB) << p.log2_heads;
+                if (lane == 0) {
+                    SlotMeta mt;
+                    mt.seq = seq;
+                    mt.kvh0 = kvh0;
+                    mt.part = ic.part;
+                    mt.flags = (j == 0 ? kFirst : 0) | (j + 1 == ic.nslots ? kLast : 0) | fin | (members << 8);
+                    mt.ntok = nt;
+                    mt.bad = bad;
+                    mt.pad[0] = mt.pad[1] = 0;
+                    meta[slot] = mt;
+                    mbar_arrive_expect_tx(&full[slot], static_cast<uint32_t>(__popc(loaded)) * box * 2u * L::kHalves);
+                }
+                __syncwarp();
+                const int z = load ? id * bs + ptok % bs : 0;               // the piece's first cache slot
+                if (load) {
+                    const int st = lane / per_stage, b = lane % per_stage;
+                    uint8_t *dst = sp + ((static_cast<size_t>(st) * kStageTokens * D * L::kES) << p.log2_heads) + b * box;
+#pragma unroll
+                    for (int h = 0; h < L::kHalves; ++h) {
+                        const uint32_t ho = h * per_stage * box;
+                        tma_load_3d(dst + ho, &tmap_k, &full[slot], h * (L::kRowB / L::kES), z, kvh0, policy);
+                        tma_load_3d(dst + L::kKVBytes + ho, &tmap_v, &full[slot], h * (L::kRowB / L::kES), z, kvh0,
+                                    policy);
+                    }
+                }
+                if constexpr (k8) {
+                    // scales, [token of the slot][head of the box], K then V
+                    const uint32_t sd = smem_addr(sp + 2 * L::kKVBytes);
+                    const int lv = p.log2_heads >= 2 ? 2 : 0;               // floats per copy: 4 or 1
+                    const int lc = p.log2_heads - lv;                       // copies per token
+                    const int n = (SW * kStageTokens) << lc;
+                    for (int i = lane; i < n; i += 32) {
+                        const int tk = i >> lc, h = (i & ((1 << lc) - 1)) << lv;
+                        const int pc = tk / RB;
+                        const int zz = __shfl_sync(kFull, z, pc);
+                        if (!((loaded >> pc) & 1u) || tk >= nt) continue;
+                        const int64_t src = static_cast<int64_t>(zz + tk % RB) * Hkv + kvh0 + h;
+                        const uint32_t dst = sd + ((tk << p.log2_heads) + h) * 4;
+                        if (lv) {
+                            cp_async16(dst, p.k_scales + src);
+                            cp_async16(dst + L::kScaleBytes, p.v_scales + src);
+                        } else {
+                            cp_async4(dst, p.k_scales + src);
+                            cp_async4(dst + L::kScaleBytes, p.v_scales + src);
+                        }
+                    }
+                    cp_async_arrive(&full[slot]);
+                }
+                __syncwarp();
+            }
+            advance();
+        }
+        // one more slot tells the consumers to stop
+        if (ok) {
+            const int slot = take_slot();
+            if (ok) {
+                if (lane == 0) {
+                    SlotMeta mt{};
+                    mt.seq = -1;
+                    meta[slot] = mt;
+                    arrive(&full[slot]);
+                }
+                if constexpr (k8) {
+                    __syncwarp();
+                    arrive(&full[slot]);
+                }
+            }
+        }
+        if (p.late_wait) pdl_wait();   // the grid does not finish before the prefix kernel
+        return;
+    }
+
+    // ---------------------------------------------------------------- consumers
+    // Warp w takes head kvh0 + w % H and, of a slot's stages, the SUB at
+    // (w / H) * SUB.  Column c of its MMAs (c < 8) is query row c % G of member
+    // c / G; columns without a query hold zero queries and are never written.
+    const int head = warp & (H - 1), sub = warp >> p.log2_heads;
+    const int g = lane >> 2, t = lane & 3;
+    const int r8 = lane & 7, j8 = lane >> 3;
+    const uint32_t slots_sa = smem_addr(slots);
+    const uint32_t box = static_cast<uint32_t>(RB * L::kRowB) << p.log2_heads;
+    const uint32_t half_off = box * per_stage;                       // next 128-byte column block
+    const uint32_t stage_off = half_off * L::kHalves;
+    const uint32_t head_off = head * RB * L::kRowB;
+    const uint32_t hi_off = per_stage == 1 ? 8 * L::kRowB : box;     // rows 8-15 of a stage
+    const uint32_t swz = L::kRowB == 128 ? r8 : (r8 >> 1) & 3;
+    const uint32_t off_k = head_off + (j8 & 1) * hi_off + r8 * L::kRowB;
+    const uint32_t off_v = head_off + (j8 >> 1) * hi_off + r8 * L::kRowB;
+    const uint64_t keep = l2_policy_evict_last();
+
+    uint32_t qf[KS][2];
+    float qs[2];                  // logit scale of columns 2t, 2t + 1
+    float acc[MT][4], m_run[2], l_run[2];
+    int cslot = 0;
+    uint32_t cphase = 0, citems = 0;
+    for (;;) {
+        const int slot = cslot;
+        uint8_t *sp = slots + static_cast<size_t>(slot) * L::kSlotBytes;
+        const uint32_t sa = slots_sa + slot * L::kSlotBytes;
+        if (!mbar_try_wait(&full[slot], cphase) && !mbar_wait_bounded(&full[slot], cphase)) {
+            if (lane == 0) report(p.err_flag, 0x10 /* PA_FLAG_TIMEOUT */);
+            return;
+        }
+        if (++cslot == S) {
+            cslot = 0;
+            cphase ^= 1u;
+        }
+        const SlotMeta m = meta[slot];
+        if (m.seq < 0) break;
+        const int members = m.flags >> 8;
+
+        if (m.flags & kFirst) {
+            const int qi = static_cast<int>(citems % kQueryRing);
+            const uint32_t qpar = (citems / kQueryRing) & 1u;
+            ++citems;
+            if (!mbar_try_wait(&qfull[qi], qpar) && !mbar_wait_bounded(&qfull[qi], qpar)) {
+                if (lane == 0) report(p.err_flag, 0x10 /* PA_FLAG_TIMEOUT */);
+                return;
+            }
+            const bool live = g < (members << lg);
+            const uint32_t *qw = reinterpret_cast<const uint32_t *>(qbuf + qi * kQEntry * H + (live ? g >> lg : 0) * qmember) +
+                                 ((head << lg) + (g & ((1 << lg) - 1))) * (D / 2);
+            if constexpr (!k8) {
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) {
+                    qf[ks][0] = live ? qw[(ks * 16 + 2 * t) >> 1] : 0u;
+                    qf[ks][1] = live ? qw[(ks * 16 + 2 * t + 8) >> 1] : 0u;
+                }
+                qs[0] = qs[1] = p.scale_log2;
+            } else {
+                // Dims in the order the widened K fragments arrive: step
+                // 2kc + hl takes dims 32kc + 4t + 2hl (+1) and the same + 16.
+                float2 f[KS][2];
+                float amax = 0.f;
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const uint32_t w = live ? qw[(32 * (ks >> 1) + 4 * t + 2 * (ks & 1) + 16 * k) >> 1] : 0u;
+                        f[ks][k] = p.q_bf16 ? Half2x<true>::to_float2(w) : Half2x<false>::to_float2(w);
+                        amax = fmaxf(amax, fmaxf(fabsf(f[ks][k].x), fabsf(f[ks][k].y)));
+                    }
+                amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
+                amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
+                // 2^e <= amax < 2^(e+1), e kept where both 2^e and 2^-e are normal
+                const uint32_t eb = min(max(__float_as_uint(amax) & 0x7f800000u, 0x00800000u), 0x7e800000u);
+                const float inv = __uint_as_float(0x7f000000u - eb);
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) qf[ks][k] = pack2<false>(f[ks][k].x * inv, f[ks][k].y * inv);
+                const float up = __uint_as_float(eb) * p.scale_log2;
+                qs[0] = __shfl_sync(kFull, up, 8 * t);        // column 2t is held by lanes of group 2t
+                qs[1] = __shfl_sync(kFull, up, 8 * t + 4);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) arrive(&qempty[qi]);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                m_run[e] = -INFINITY;
+                l_run[e] = 0.f;
+            }
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) acc[mt][0] = acc[mt][1] = acc[mt][2] = acc[mt][3] = 0.f;
+        }
+
+        const int st0 = sub * SUB;
+        const int mine = m.ntok - st0 * kStageTokens;     // my tokens of this slot
+        if (mine > 0) {
+            const bool second = SUB > 1 && mine > kStageTokens;
+            uint32_t smask[SUB];
+            float x[SUB][4], sv[SUB][2];
+            float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int hs = 0; hs < SUB; ++hs) {
+                smask[hs] = 0;
+                if (hs > 0 && !second) continue;
+                const int n = mine - hs * kStageTokens;
+                uint32_t mk = n >= kStageTokens ? 0xffffu : (1u << n) - 1u;
+                if (m.bad) {
+                    const uint32_t b = (m.bad >> (2 * (st0 + hs))) & 3u;
+                    mk &= ~(((b & 1u) ? 0xffu : 0u) | ((b & 2u) ? 0xff00u : 0u));
+                }
+                smask[hs] = mk;
+                // ---- QK: 16 tokens x 8 columns ----
+                const uint32_t ka = sa + (st0 + hs) * stage_off + off_k;
+                float c[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+                if constexpr (!k8) {
+#pragma unroll
+                    for (int ks = 0; ks < KS; ++ks) {
+                        const int ch = 2 * ks + (j8 >> 1);
+                        uint32_t a[4];
+                        ldsm_x4(a, ka + (ch >> 3) * half_off + (((ch & 7) ^ swz) << 4));
+                        mma_16816<BF16>(c[ks & 1], a, qf[ks][0], qf[ks][1]);
+                    }
+                } else {
+#pragma unroll
+                    for (int kc = 0; kc < D / 32; ++kc) {
+                        const int ch = 2 * kc + (j8 >> 1);
+                        uint32_t a[4], lo4[4], hi4[4];
+                        ldsm_x4(a, ka + ((ch ^ swz) << 4));
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) widen<CT, false>(a[i], lo4[i], hi4[i]);
+                        mma_16816<false>(c[0], lo4, qf[2 * kc][0], qf[2 * kc][1]);
+                        mma_16816<false>(c[1], hi4, qf[2 * kc + 1][0], qf[2 * kc + 1][1]);
+                    }
+                }
+                const bool v_lo = (mk >> g) & 1u, v_hi = (mk >> (g + 8)) & 1u;
+                float y_lo = 0.f, y_hi = 0.f, k_lo = 1.f, k_hi = 1.f;
+                if constexpr (k8) {
+                    // a masked token's scales may be anything: its V scale counts as 0
+                    const float *scl = reinterpret_cast<const float *>(sp + 2 * L::kKVBytes) +
+                                       (((st0 + hs) * kStageTokens + g) << p.log2_heads) + head;
+                    k_lo = scl[0];
+                    k_hi = scl[8 << p.log2_heads];
+                    sv[hs][0] = v_lo ? scl[L::kScaleBytes / 4] : 0.f;
+                    sv[hs][1] = v_hi ? scl[L::kScaleBytes / 4 + (8 << p.log2_heads)] : 0.f;
+                    y_lo = fast_log2(sv[hs][0]);
+                    y_hi = fast_log2(sv[hs][1]);
+                }
+#pragma unroll
+                for (int e = 0; e < NE; ++e) {
+                    float a = c[0][e] + c[1][e], b = c[0][2 + e] + c[1][2 + e];
+                    if constexpr (k8) {
+                        a *= k_lo * qs[e];
+                        b *= k_hi * qs[e];
+                    } else {
+                        a *= qs[e];
+                        b *= qs[e];
+                    }
+                    x[hs][e] = v_lo ? a : -INFINITY;
+                    x[hs][2 + e] = v_hi ? b : -INFINITY;
+                    if constexpr (k8)
+                        mx[e] = fmaxf(mx[e], fmaxf(x[hs][e] + y_lo, x[hs][2 + e] + y_hi));
+                    else
+                        mx[e] = fmaxf(mx[e], fmaxf(x[hs][e], x[hs][2 + e]));
+                }
+            }
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1)
+#pragma unroll
+                for (int e = 0; e < NE; ++e) mx[e] = fmaxf(mx[e], __shfl_xor_sync(kFull, mx[e], o));
+            bool nd = mx[0] > m_run[0] + 8.f;
+            if constexpr (NE == 2) nd = nd || mx[1] > m_run[1] + 8.f;
+            if (__any_sync(kFull, nd)) {
+                float al[2] = {1.f, 1.f};
+#pragma unroll
+                for (int e = 0; e < NE; ++e) {
+                    const float mn = fmaxf(m_run[e], mx[e]);
+                    al[e] = mn == -INFINITY ? 1.f : fast_exp2(m_run[e] - mn);
+                    m_run[e] = mn;
+                    l_run[e] *= al[e];
+                }
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int e = 0; e < NE; ++e) {
+                        acc[mt][e] *= al[e];
+                        acc[mt][2 + e] *= al[e];
+                    }
+            }
+            float mu[2];
+#pragma unroll
+            for (int e = 0; e < NE; ++e) mu[e] = m_run[e] == -INFINITY ? 0.f : m_run[e];
+#pragma unroll
+            for (int hs = 0; hs < SUB; ++hs) {
+                if (hs > 0 && !second) continue;
+                float w4[4];
+#pragma unroll
+                for (int e = 0; e < NE; ++e) {
+                    w4[e] = fast_exp2(x[hs][e] - mu[e]);
+                    w4[2 + e] = fast_exp2(x[hs][2 + e] - mu[e]);
+                    l_run[e] += w4[e] + w4[2 + e];
+                    if constexpr (k8) {
+                        w4[e] *= sv[hs][0];
+                        w4[2 + e] *= sv[hs][1];
+                    }
+                }
+                // weights as the PV B fragment: tokens 2t, 2t+1, 2t+8, 2t+9 of column g
+                uint32_t bhi[2], blo[2];
+                {
+                    const int srcA = 8 * t + (g >> 1), srcB = srcA + 4;
+                    float w[4];
+                    w[0] = __shfl_sync(kFull, w4[0], srcA);
+                    w[1] = __shfl_sync(kFull, w4[0], srcB);
+                    w[2] = __shfl_sync(kFull, w4[2], srcA);
+                    w[3] = __shfl_sync(kFull, w4[2], srcB);
+                    if constexpr (NE == 2) {
+                        const float o0 = __shfl_sync(kFull, w4[1], srcA), o1 = __shfl_sync(kFull, w4[1], srcB);
+                        const float o2 = __shfl_sync(kFull, w4[3], srcA), o3 = __shfl_sync(kFull, w4[3], srcB);
+                        if (g & 1) {
+                            w[0] = o0;
+                            w[1] = o1;
+                            w[2] = o2;
+                            w[3] = o3;
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        bhi[k] = pack2<BF16>(w[2 * k], w[2 * k + 1]);
+                        const float2 h = Cvt::to_float2(bhi[k]);
+                        blo[k] = pack2<BF16>(w[2 * k] - h.x, w[2 * k + 1] - h.y);
+                    }
+                }
+                const uint32_t vbase = (st0 + hs) * stage_off + L::kKVBytes;
+                // V rows that are masked are zeroed first: stale slots may hold NaN
+                // (not so int8 codes, which a zero weight always cancels)
+                if constexpr (CT != kCacheInt8) {
+                    if (smask[hs] != 0xffffu) {
+                        constexpr int kCh = L::kRowB / 16;                  // 16-byte chunks per box row
+#pragma unroll
+                        for (int k = 0; k < kStageTokens * L::kHalves * kCh / 32; ++k) {
+                            const int q16 = lane + 32 * k;
+                            const int half = q16 / (kStageTokens * kCh), row = (q16 / kCh) % kStageTokens;
+                            if (!((smask[hs] >> row) & 1u))
+                                *reinterpret_cast<uint4 *>(sp + vbase + half * half_off + head_off +
+                                                           (row >> 3) * hi_off + (row & 7) * L::kRowB + (q16 % kCh) * 16) =
+                                    make_uint4(0u, 0u, 0u, 0u);
+                        }
+                        __syncwarp();
+                    }
+                }
+                const uint32_t va = sa + vbase + off_v;
+                if constexpr (!k8) {
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        const int ch = 2 * mt + (j8 & 1);
+                        uint32_t a[4];
+                        ldsm_x4_trans(a, va + (ch >> 3) * half_off + (((ch & 7) ^ swz) << 4));
+                        mma_16816<BF16>(acc[mt], a, bhi[0], bhi[1]);
+                        mma_16816<BF16>(acc[mt], a, blo[0], blo[1]);
+                    }
+                } else {
+                    // Byte pairs (dims 2g, 2g+1) of two tokens: even dims feed
+                    // acc[2vc], odd dims acc[2vc+1].
+#pragma unroll
+                    for (int vc = 0; vc < D / 32; ++vc) {
+                        const int ch = 2 * vc + (j8 & 1);
+                        uint32_t a[4], ev[4], od[4];
+                        ldsm_x4_trans(a, va + ((ch ^ swz) << 4));
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) widen<CT, true>(a[i], ev[i], od[i]);
+                        mma_16816<false>(acc[2 * vc], ev, bhi[0], bhi[1]);
+                        mma_16816<false>(acc[2 * vc], ev, blo[0], blo[1]);
+                        mma_16816<false>(acc[2 * vc + 1], od, bhi[0], bhi[1]);
+                        mma_16816<false>(acc[2 * vc + 1], od, blo[0], blo[1]);
+                    }
+                }
+            }
+        }
+        // my reads (and zeroing) of the slot are done
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) arrive(&empty[slot]);
+
+        if (!(m.flags & kLast)) continue;
+        // ---- item end ----
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1)
+#pragma unroll
+            for (int e = 0; e < NE; ++e) l_run[e] += __shfl_xor_sync(kFull, l_run[e], o);
+        if (nsubs > 1) {
+            // join the states of the head's warps: the others hand theirs to the first
+            const uint32_t par = (citems - 1) & 1u;      // of this item
+            if (sub > 0) {
+                if (citems > 1 && !mbar_try_wait(&xfree[head], par ^ 1u) && !mbar_wait_bounded(&xfree[head], par ^ 1u)) {
+                    if (lane == 0) report(p.err_flag, 0x10 /* PA_FLAG_TIMEOUT */);
+                    return;
+                }
+                float4 *xs = reinterpret_cast<float4 *>(xbuf + (warp - H) * L::kStateBytes);
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+                    xs[mt * 32 + lane] = make_float4(acc[mt][0], acc[mt][1], acc[mt][2], acc[mt][3]);
+                if (g == 0)
+#pragma unroll
+                    for (int e = 0; e < NE; ++e) xml[warp * 8 + 2 * t + e] = make_float2(m_run[e], l_run[e]);
+                __syncwarp();
+                if (lane == 0) arrive(&xfull[head]);
+                continue;
+            }
+            if (!mbar_try_wait(&xfull[head], par) && !mbar_wait_bounded(&xfull[head], par)) {
+                if (lane == 0) report(p.err_flag, 0x10 /* PA_FLAG_TIMEOUT */);
+                return;
+            }
+            float al[2] = {1.f, 1.f};
+#pragma unroll
+            for (int e = 0; e < NE; ++e) {
+                float mn = m_run[e];
+                for (int k = 1; k < nsubs; ++k) mn = fmaxf(mn, xml[(warp + k * H) * 8 + 2 * t + e].x);
+                al[e] = m_run[e] == -INFINITY ? 1.f : fast_exp2(m_run[e] - mn);
+                m_run[e] = mn;
+                l_run[e] *= al[e];
+            }
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int e = 0; e < NE; ++e) {
+                    acc[mt][e] *= al[e];
+                    acc[mt][2 + e] *= al[e];
+                }
+            for (int k = 1; k < nsubs; ++k) {
+                const float4 *xs = reinterpret_cast<const float4 *>(xbuf + (warp + (k - 1) * H) * L::kStateBytes);
+                float be[2] = {1.f, 1.f};
+#pragma unroll
+                for (int e = 0; e < NE; ++e) {
+                    const float2 ml = xml[(warp + k * H) * 8 + 2 * t + e];
+                    be[e] = ml.x == -INFINITY ? 1.f : fast_exp2(ml.x - m_run[e]);
+                    l_run[e] += ml.y * be[e];
+                }
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    const float4 a = xs[mt * 32 + lane];
+                    acc[mt][0] = fmaf(a.x, be[0], acc[mt][0]);
+                    acc[mt][2] = fmaf(a.z, be[0], acc[mt][2]);
+                    if constexpr (NE == 2) {
+                        acc[mt][1] = fmaf(a.y, be[1], acc[mt][1]);
+                        acc[mt][3] = fmaf(a.w, be[1], acc[mt][3]);
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) arrive(&xfree[head]);
+        }
+        const int kvh = m.kvh0 + head;
+        const bool fin = (m.flags & kFinal) != 0;
+#pragma unroll
+        for (int e = 0; e < NE; ++e) {
+            const int c = 2 * t + e;
+            if (c >= (members << lg)) continue;
+            const int64_t sq = m.seq + (c >> lg);
+            const int hq = c & ((1 << lg) - 1);
+            const float sc = fin ? (l_run[e] == 0.f ? 0.f : 1.f / l_run[e]) : 1.f;
+            const int64_t r = ((sq * Hkv + kvh) * p.max_parts + p.part_off + m.part << lg) + hq;
+            if (!fin && g == 0) st_global_hint(p.ws_ml + 2 * r, make_float2(m_run[e], l_run[e]), keep);
+            const int64_t orow = fin ? (sq * Hq + (kvh << lg) + hq) * D : r * D;
+            auto put2 = [&](int d, float a, float b) {   // two consecutive elements
+                if (!fin)
+                    st_global_hint(p.ws_acc + orow + d, make_float2(a, b), keep);
+                else if (p.out_dtype == 2)
+                    *reinterpret_cast<float2 *>(static_cast<float *>(p.out) + orow + d) = make_float2(a, b);
+                else
+                    *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.out) + orow + d) =
+                        p.out_dtype == 1 ? pack2<true>(a, b) : pack2<false>(a, b);
+            };
+            auto put1 = [&](int d, float a) {
+                if (!fin)
+                    p.ws_acc[orow + d] = a;
+                else if (p.out_dtype == 2)
+                    static_cast<float *>(p.out)[orow + d] = a;
+                else
+                    static_cast<uint16_t *>(p.out)[orow + d] = p.out_dtype == 1 ? float_to_bf16_bits(a) : float_to_f16_bits(a);
+            };
+            if constexpr (k8) {
+#pragma unroll
+                for (int vc = 0; vc < D / 32; ++vc) {
+                    put2(32 * vc + 2 * g, acc[2 * vc][e] * sc, acc[2 * vc + 1][e] * sc);
+                    put2(32 * vc + 16 + 2 * g, acc[2 * vc][2 + e] * sc, acc[2 * vc + 1][2 + e] * sc);
+                }
+            } else {
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    put1(16 * mt + g, acc[mt][e] * sc);
+                    put1(16 * mt + g + 8, acc[mt][2 + e] * sc);
+                }
+            }
+        }
+    }
+}
+
+template <int D, int C, int CT>
+cudaError_t launch_split_t(const SplitParams &p, const CUtensorMap &tk, const CUtensorMap &tv, int grid, size_t smem,
+                           cudaStream_t stream) {
+    auto kern = paged_split_kernel<D, C, CT>;
+    const cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kern, dim3(grid), dim3(SplitLayout<D, C, CT>::kThreads), smem, stream, p, tk, tv);
+}
+
+template <int D, int CT>
+cudaError_t launch_split_d(const SplitParams &p, int cols, const CUtensorMap &tk, const CUtensorMap &tv, int grid,
+                           size_t smem, cudaStream_t stream) {
+    switch (cols) {
+        case 1: return launch_split_t<D, 1, CT>(p, tk, tv, grid, smem, stream);
+        case 2: return launch_split_t<D, 2, CT>(p, tk, tv, grid, smem, stream);
+        case 4: return launch_split_t<D, 4, CT>(p, tk, tv, grid, smem, stream);
+        case 8: return launch_split_t<D, 8, CT>(p, tk, tv, grid, smem, stream);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+template <int CT>
+cudaError_t launch_split_ct(const SplitParams &p, int head_dim, int cols, const CUtensorMap &tk, const CUtensorMap &tv,
+                            int grid, size_t smem, cudaStream_t stream) {
+    if (head_dim == 128) return launch_split_d<128, CT>(p, cols, tk, tv, grid, smem, stream);
+    if (head_dim == 64) return launch_split_d<64, CT>(p, cols, tk, tv, grid, smem, stream);
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+}  // namespace pa
