@@ -518,8 +518,12 @@ pa_status pa_quant_decode(void *out, pa_dtype out_dtype, const void *query, pa_d
  *                  context_lens[s], equal within a group; 0: nothing is shared
  *   max_group_size, max_shared_len : host-known upper bounds of the group sizes
  *                  and of shared_lens (<= max_context_len)
+ *   scale        : >= 0
  *   workspace    : pa_decode_shared_workspace_size(...) bytes, always needed; no
  *                  initial contents
+ * Large groups run on the tensor cores as pa_prefill does (softmax weights
+ * rounded to binary16, or split into two bfloat16 parts); there a block id out
+ * of range may leave out more of the prefix than its own tokens.
  * cu_groups or shared_lens that break these rules set PA_FLAG_BAD_CONTEXT_LEN;
  * the groups concerned are then undefined (no memory out of bounds is touched).
  * partition_size is that of the private parts; the prefixes are cut by a rule of

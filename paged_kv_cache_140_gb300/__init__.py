@@ -24,6 +24,7 @@ keep int8 or e4m3 codes with a float32 scale per token and KV head,
 from __future__ import annotations
 
 import ctypes
+import functools
 
 from . import _lib
 from ._lib import (FLAG_BAD_BLOCK_ID, FLAG_BAD_CONTEXT_LEN, FLAG_BAD_COPY_PAIR, FLAG_BAD_SLOT,
@@ -323,55 +324,84 @@ def prefill(out, query, k_cache, v_cache, block_tables, context_lens, cu_seqlens
 
 
 # ------------------------- quantised cache, and decode with shared prefixes
+#
+# These calls are made once per layer and step on small tensors, where the
+# marshalling itself counts (16 us of a 21 us write of four rows before it was
+# written this way): each looks its tensors over in one expression and explains
+# a refusal only when that fails.
 
-def _quant_code(t) -> int:
-    torch = _torch()
-    if t.dtype == torch.int8:
-        return PA_INT8
-    if t.dtype in (torch.uint8, torch.float8_e4m3fn):
-        return PA_FP8_E4M3
-    raise TypeError(f"unsupported code dtype {t.dtype}")
+class _Runtime:
+    """What the calls below need of torch and the library, looked up once."""
+
+    def __init__(self):
+        torch = _torch()
+        self.lib = _lib.load()
+        self.half = {torch.float16: PA_F16, torch.bfloat16: PA_BF16}
+        self.out = {**self.half, torch.float32: PA_F32}
+        self.codes = {torch.int8: PA_INT8, torch.uint8: PA_FP8_E4M3, torch.float8_e4m3fn: PA_FP8_E4M3}
+        self.f32, self.i32, self.i64, self.u8 = torch.float32, torch.int32, torch.int64, torch.uint8
+        self.current_device = torch.cuda.current_device
+        self.capturing = torch.cuda.is_current_stream_capturing
+        self.stream = torch._C._cuda_getCurrentRawStream
+        self.empty = torch.empty
 
 
-def _on_one_device(first, *rest):
-    """All tensors on the current CUDA device and contiguous; names are given on a refusal."""
-    index = first[1].device.index
-    for n, t in (first, *rest):
-        if not t.is_cuda or t.device.index != index or not t.is_contiguous():
-            _cuda_contig(n, t)
-            raise ValueError(f"{n} must be on the device of {first[0]}")
-    _need(index == _torch().cuda.current_device(), "the tensors must be on the current CUDA device")
+_rt = None
 
 
-def _scratch(workspace, nbytes: int, device):
+def _runtime():
+    global _rt
+    if _rt is None:
+        _rt = _Runtime()
+    return _rt
+
+
+def _refuse(tensors, message=None):
+    """Raise for the first of (name, tensor) that is not contiguous on the current
+    CUDA device, else with ``message``."""
+    for n, t in tensors:
+        _cuda_contig(n, t)
+        _need(t.get_device() == _runtime().current_device(), f"{n} must be on the current CUDA device")
+    raise ValueError(message or "tensors must be on the current CUDA device")
+
+
+def _code(table, t, what):
+    c = table.get(t.dtype)
+    if c is None:
+        raise TypeError(f"unsupported {what} dtype {t.dtype}")
+    return c
+
+
+def _scales_ok(rt, k_scales, v_scales, shape):
+    if k_scales.shape != shape or v_scales.shape != shape or k_scales.dtype != rt.f32 or v_scales.dtype != rt.f32:
+        raise ValueError("scales must be float32 [NB, bs, Hkv]")
+
+
+def _flag(err_flag, dev: int):
+    if err_flag is None:
+        return None
+    if err_flag.get_device() != dev or err_flag.element_size() != 4:
+        raise ValueError("err_flag must be an int32 tensor on the device of the others (new_err_flag)")
+    return err_flag.data_ptr()
+
+
+def _scratch(rt, workspace, nbytes: int, dev: int, stream: int):
     """The workspace of one call: the caller's, the default one of the current
     stream, or, while a graph is captured, one of the graph's own (so that graphs
     never share one and none is replaced by a larger one later)."""
     if nbytes == 0:
         return None
     if workspace is None:
-        torch = _torch()
-        if torch.cuda.is_current_stream_capturing():
-            return torch.empty(nbytes, dtype=torch.uint8, device=device)
-        key = (device.index, torch.cuda.current_stream(device).cuda_stream)
-        workspace = _default_ws.get(key)
+        if rt.capturing():
+            return rt.empty(nbytes, dtype=rt.u8, device=dev)
+        workspace = _default_ws.get((dev, stream))
         if workspace is None:
-            workspace = _default_ws.setdefault(key, DecodeWorkspace(device))
-    if not isinstance(workspace, DecodeWorkspace):
-        _cuda_contig("workspace", workspace)
-        _need(workspace.device == device, "workspace must be on the device of the other tensors")
-        return workspace
-    return workspace.get(nbytes)
-
-
-def _quant_cache(k_cache, v_cache, k_scales, v_scales):
-    torch = _torch()
-    _need(k_cache.dim() == 4 and v_cache.shape == k_cache.shape and k_cache.dtype == v_cache.dtype,
-          "caches must be [NB, bs, Hkv, D] of one dtype")
-    _need(k_scales.dtype == torch.float32 and v_scales.dtype == torch.float32 and
-          k_scales.shape == k_cache.shape[:3] and v_scales.shape == k_scales.shape,
-          "scales must be float32 [NB, bs, Hkv]")
-    return k_cache.shape
+            workspace = _default_ws.setdefault((dev, stream), DecodeWorkspace(_torch().device("cuda", dev)))
+    if isinstance(workspace, DecodeWorkspace):
+        workspace = workspace.get(nbytes)
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        _refuse((("workspace", workspace),))
+    return workspace
 
 
 def quant_reshape_and_cache(key, value, k_cache, v_cache, k_scales, v_scales, slot_mapping, err_flag=None) -> None:
@@ -382,23 +412,34 @@ def quant_reshape_and_cache(key, value, k_cache, v_cache, k_scales, v_scales, sl
     ``torch.float8_e4m3fn`` / ``torch.uint8``.  key and value may be slices along
     the last two dimensions of a wider tensor (a token's rows dense, any token
     stride that is a multiple of 8 elements)."""
-    torch = _torch()
-    _need(key.dim() == 3 and value.shape == key.shape and key.dtype == value.dtype, "key/value must be [T, Hkv, D]")
-    T, hkv, d = key.shape
-    for n, t in (("key", key), ("value", value)):
-        _need(t.is_cuda and t.device == k_cache.device, f"{n} must be on the device of k_cache")
-        _need(t.stride(2) == 1 and (hkv == 1 or t.stride(1) == d), f"{n}: the rows of one token must be dense")
-    _on_one_device(("k_cache", k_cache), ("v_cache", v_cache), ("k_scales", k_scales), ("v_scales", v_scales),
-                   ("slot_mapping", slot_mapping))
-    nb, bs, h2, d2 = _quant_cache(k_cache, v_cache, k_scales, v_scales)
-    _need(h2 == hkv and d2 == d, "cache and key head shapes differ")
-    _need(slot_mapping.dtype == torch.int64 and slot_mapping.numel() == T, "slot_mapping must be int64 [T]")
-    row = hkv * d
-    st = _lib.load().pa_quant_reshape_and_cache(
-        key.data_ptr(), value.data_ptr(), key.stride(0) if T > 1 else row, value.stride(0) if T > 1 else row,
-        k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), slot_mapping.data_ptr(), T,
-        nb, bs, hkv, d, _dtype_code(key), _quant_code(k_cache), _ptr(err_flag), _stream(key.device))
-    _lib.check(st, "pa_quant_reshape_and_cache")
+    rt = _rt or _runtime()
+    dev, shape, cache = key.get_device(), key.shape, k_cache.shape
+    if (dev != rt.current_device() or value.get_device() != dev or k_cache.get_device() != dev or
+            v_cache.get_device() != dev or k_scales.get_device() != dev or v_scales.get_device() != dev or
+            slot_mapping.get_device() != dev or not k_cache.is_contiguous() or not v_cache.is_contiguous() or
+            not k_scales.is_contiguous() or not v_scales.is_contiguous() or not slot_mapping.is_contiguous()):
+        _refuse((("k_cache", k_cache), ("v_cache", v_cache), ("k_scales", k_scales), ("v_scales", v_scales),
+                 ("slot_mapping", slot_mapping)), "key and value must be on the device of the caches")
+    if len(shape) != 3 or value.shape != shape or value.dtype != key.dtype:
+        raise ValueError("key/value must be [T, Hkv, D] of one dtype")
+    T, hkv, d = shape
+    if len(cache) != 4 or v_cache.shape != cache or v_cache.dtype != k_cache.dtype or cache[2] != hkv or cache[3] != d:
+        raise ValueError("caches must be [NB, bs, Hkv, D] of one dtype, with the rows' heads")
+    nb, bs = cache[0], cache[1]
+    _scales_ok(rt, k_scales, v_scales, (nb, bs, hkv))
+    if slot_mapping.dtype != rt.i64 or slot_mapping.numel() != T:
+        raise ValueError("slot_mapping must be int64 [T]")
+    ks, vs = key.stride(), value.stride()
+    if ks[2] != 1 or vs[2] != 1 or (hkv != 1 and (ks[1] != d or vs[1] != d)):
+        raise ValueError("key/value: the rows of one token must be dense")
+    one = T <= 1
+    st = rt.lib.pa_quant_reshape_and_cache(
+        key.data_ptr(), value.data_ptr(), hkv * d if one else ks[0], hkv * d if one else vs[0], k_cache.data_ptr(),
+        v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), slot_mapping.data_ptr(), T, nb, bs, hkv,
+        d, _code(rt.half, key, "row"), _code(rt.codes, k_cache, "cache"),
+        _flag(err_flag, dev), rt.stream(dev))
+    if st:
+        _lib.check(st, "pa_quant_reshape_and_cache")
 
 
 def quant_gather(out_k, out_v, k_cache, v_cache, k_scales, v_scales, block_tables, cu_seqlens, seq_starts=None,
@@ -407,27 +448,42 @@ def quant_gather(out_k, out_v, k_cache, v_cache, k_scales, v_scales, block_table
     [T, Hkv, D] (f16, bf16 or f32) becomes sequence s's position
     ``seq_starts[s] + i`` (``seq_starts`` None: 0).  Rows from ``cu_seqlens[-1]``
     on are left as they were."""
-    torch = _torch()
-    more = () if seq_starts is None else (("seq_starts", seq_starts),)
-    _on_one_device(("out_k", out_k), ("out_v", out_v), ("k_cache", k_cache), ("v_cache", v_cache),
-                   ("k_scales", k_scales), ("v_scales", v_scales), ("block_tables", block_tables),
-                   ("cu_seqlens", cu_seqlens), *more)
-    nb, bs, hkv, d = _quant_cache(k_cache, v_cache, k_scales, v_scales)
-    _need(out_k.dim() == 3 and out_v.shape == out_k.shape and out_v.dtype == out_k.dtype and
-          out_k.shape[1] == hkv and out_k.shape[2] == d, "out_k/out_v must be [T, Hkv, D] of one dtype")
-    _need(block_tables.dtype == torch.int32 and block_tables.dim() == 2, "block_tables must be int32 [B, maxNB]")
-    B, maxnb = block_tables.shape
-    _need(cu_seqlens.dtype == torch.int32 and cu_seqlens.numel() == B + 1, "cu_seqlens must be int32 [B+1]")
-    _need(seq_starts is None or (seq_starts.dtype == torch.int32 and seq_starts.numel() == B),
-          "seq_starts must be int32 [B]")
-    st = _lib.load().pa_quant_gather(
-        out_k.data_ptr(), out_v.data_ptr(), _dtype_code(out_k, allow_f32=True), k_cache.data_ptr(),
-        v_cache.data_ptr(), _quant_code(k_cache), k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(),
-        maxnb, cu_seqlens.data_ptr(), _ptr(seq_starts), B, out_k.shape[0], hkv, d, bs, nb, _ptr(err_flag),
-        _stream(out_k.device))
-    _lib.check(st, "pa_quant_gather")
+    rt = _rt or _runtime()
+    dev, cache, shape, table = out_k.get_device(), k_cache.shape, out_k.shape, block_tables.shape
+    if (dev != rt.current_device() or out_v.get_device() != dev or k_cache.get_device() != dev or
+            v_cache.get_device() != dev or k_scales.get_device() != dev or v_scales.get_device() != dev or
+            block_tables.get_device() != dev or cu_seqlens.get_device() != dev or not out_k.is_contiguous() or
+            not out_v.is_contiguous() or not k_cache.is_contiguous() or not v_cache.is_contiguous() or
+            not k_scales.is_contiguous() or not v_scales.is_contiguous() or not block_tables.is_contiguous() or
+            not cu_seqlens.is_contiguous()):
+        _refuse((("out_k", out_k), ("out_v", out_v), ("k_cache", k_cache), ("v_cache", v_cache), ("k_scales", k_scales),
+                 ("v_scales", v_scales), ("block_tables", block_tables), ("cu_seqlens", cu_seqlens)))
+    if len(cache) != 4 or v_cache.shape != cache or v_cache.dtype != k_cache.dtype:
+        raise ValueError("caches must be [NB, bs, Hkv, D] of one dtype")
+    nb, bs, hkv, d = cache
+    _scales_ok(rt, k_scales, v_scales, (nb, bs, hkv))
+    if len(shape) != 3 or out_v.shape != shape or out_v.dtype != out_k.dtype or shape[1] != hkv or shape[2] != d:
+        raise ValueError("out_k/out_v must be [T, Hkv, D] of one dtype")
+    if len(table) != 2 or block_tables.dtype != rt.i32:
+        raise ValueError("block_tables must be int32 [B, maxNB]")
+    B = table[0]
+    if cu_seqlens.dtype != rt.i32 or cu_seqlens.numel() != B + 1:
+        raise ValueError("cu_seqlens must be int32 [B+1]")
+    if seq_starts is not None:
+        if seq_starts.get_device() != dev or not seq_starts.is_contiguous():
+            _refuse((("seq_starts", seq_starts),))
+        if seq_starts.dtype != rt.i32 or seq_starts.numel() != B:
+            raise ValueError("seq_starts must be int32 [B]")
+    st = rt.lib.pa_quant_gather(
+        out_k.data_ptr(), out_v.data_ptr(), _code(rt.out, out_k, "output"), k_cache.data_ptr(), v_cache.data_ptr(),
+        _code(rt.codes, k_cache, "cache"), k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(), table[1],
+        cu_seqlens.data_ptr(), None if seq_starts is None else seq_starts.data_ptr(), B, shape[0], hkv, d, bs,
+        nb, _flag(err_flag, dev), rt.stream(dev))
+    if st:
+        _lib.check(st, "pa_quant_gather")
 
 
+@functools.lru_cache(maxsize=1024)
 def quant_decode_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context_len,
                                 partition_size=0) -> int:
     n = _lib.load().pa_quant_decode_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim, block_size,
@@ -437,37 +493,54 @@ def quant_decode_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim, blo
     return n
 
 
-def _decode_shapes(out, query, k_cache, block_tables, context_lens):
-    torch = _torch()
-    _need(query.dim() == 3 and out.shape == query.shape, "query/out must be [B, Hq, D]")
-    B, Hq, D = query.shape
-    _need(k_cache.shape[3] == D, "head_dim mismatch")
-    _need(block_tables.dtype == torch.int32 and block_tables.dim() == 2 and block_tables.shape[0] == B,
-          "block_tables must be int32 [B, maxNB]")
-    _need(context_lens.dtype == torch.int32 and context_lens.numel() == B, "context_lens must be int32 [B]")
-    return B, Hq, D
+def _decode_shapes(rt, out, query, cache, v_cache, block_tables, context_lens):
+    shape, table = query.shape, block_tables.shape
+    if len(shape) != 3 or out.shape != shape:
+        raise ValueError("query/out must be [B, Hq, D]")
+    if len(cache) != 4 or v_cache.shape != cache or cache[3] != shape[2]:
+        raise ValueError("caches must be [NB, bs, Hkv, D] with the query's D")
+    if len(table) != 2 or table[0] != shape[0] or block_tables.dtype != rt.i32:
+        raise ValueError("block_tables must be int32 [B, maxNB]")
+    if context_lens.dtype != rt.i32 or context_lens.numel() != shape[0]:
+        raise ValueError("context_lens must be int32 [B]")
 
 
 def quant_decode(out, query, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, scale: float,
                  max_context_len: int | None = None, partition_size: int = 0, workspace=None, err_flag=None) -> None:
     """:func:`decode` over a quantised cache written by :func:`quant_reshape_and_cache`."""
-    _on_one_device(("query", query), ("out", out), ("k_cache", k_cache), ("v_cache", v_cache), ("k_scales", k_scales),
-                   ("v_scales", v_scales), ("block_tables", block_tables), ("context_lens", context_lens))
-    nb, bs, hkv, _ = _quant_cache(k_cache, v_cache, k_scales, v_scales)
-    B, Hq, D = _decode_shapes(out, query, k_cache, block_tables, context_lens)
+    rt = _rt or _runtime()
+    dev, cache = query.get_device(), k_cache.shape
+    if (dev != rt.current_device() or out.get_device() != dev or k_cache.get_device() != dev or
+            v_cache.get_device() != dev or k_scales.get_device() != dev or v_scales.get_device() != dev or
+            block_tables.get_device() != dev or context_lens.get_device() != dev or not query.is_contiguous() or
+            not out.is_contiguous() or not k_cache.is_contiguous() or not v_cache.is_contiguous() or
+            not k_scales.is_contiguous() or not v_scales.is_contiguous() or not block_tables.is_contiguous() or
+            not context_lens.is_contiguous()):
+        _refuse((("query", query), ("out", out), ("k_cache", k_cache), ("v_cache", v_cache), ("k_scales", k_scales),
+                 ("v_scales", v_scales), ("block_tables", block_tables), ("context_lens", context_lens)))
+    _decode_shapes(rt, out, query, cache, v_cache, block_tables, context_lens)
+    if v_cache.dtype != k_cache.dtype:
+        raise ValueError("K and V caches must share a dtype")
+    B, Hq, D = query.shape
+    nb, bs, hkv, _ = cache
+    _scales_ok(rt, k_scales, v_scales, (nb, bs, hkv))
     maxnb = block_tables.shape[1]
     if max_context_len is None:
         max_context_len = maxnb * bs
-    buf = _scratch(workspace, quant_decode_workspace_size(B, Hq, hkv, D, bs, max_context_len, partition_size),
-                   query.device)
-    st = _lib.load().pa_quant_decode(
-        out.data_ptr(), _dtype_code(out, allow_f32=True), query.data_ptr(), _dtype_code(query), k_cache.data_ptr(),
-        v_cache.data_ptr(), _quant_code(k_cache), k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(),
-        maxnb, context_lens.data_ptr(), max_context_len, B, Hq, hkv, D, bs, nb, scale, partition_size, _ptr(buf),
-        0 if buf is None else buf.nbytes, _ptr(err_flag), _stream(query.device))
-    _lib.check(st, "pa_quant_decode")
+    stream = rt.stream(dev)
+    buf = _scratch(rt, workspace, quant_decode_workspace_size(B, Hq, hkv, D, bs, max_context_len, partition_size), dev,
+                   stream)
+    st = rt.lib.pa_quant_decode(
+        out.data_ptr(), _code(rt.out, out, "output"), query.data_ptr(), _code(rt.half, query, "query"),
+        k_cache.data_ptr(), v_cache.data_ptr(), _code(rt.codes, k_cache, "cache"), k_scales.data_ptr(),
+        v_scales.data_ptr(), block_tables.data_ptr(), maxnb, context_lens.data_ptr(), max_context_len, B, Hq, hkv, D, bs,
+        nb, scale, partition_size, None if buf is None else buf.data_ptr(), 0 if buf is None else buf.nbytes,
+        _flag(err_flag, dev), stream)
+    if st:
+        _lib.check(st, "pa_quant_decode")
 
 
+@functools.lru_cache(maxsize=1024)
 def decode_shared_workspace_size(num_seqs, num_groups, max_group_size, num_heads, num_kv_heads, head_dim, block_size,
                                  max_context_len, max_shared_len, partition_size=0) -> int:
     n = _lib.load().pa_decode_shared_workspace_size(num_seqs, num_groups, max_group_size, num_heads, num_kv_heads,
@@ -489,19 +562,27 @@ def decode_shared(out, query, k_cache, v_cache, block_tables, context_lens, cu_g
     same K/V rows in every member.  ``max_group_size`` and ``max_shared_len`` are
     host-side bounds (defaults: the batch size and ``max_context_len``; tight
     bounds make the call faster)."""
-    torch = _torch()
-    _on_one_device(("query", query), ("out", out), ("k_cache", k_cache), ("v_cache", v_cache),
-                   ("block_tables", block_tables), ("context_lens", context_lens), ("cu_groups", cu_groups),
-                   ("shared_lens", shared_lens))
-    _need(k_cache.dim() == 4 and v_cache.shape == k_cache.shape and k_cache.dtype == v_cache.dtype,
-          "caches must be [NB, bs, Hkv, D] of one dtype")
-    _need(k_cache.dtype == query.dtype, "caches must have the query's dtype")
-    B, Hq, D = _decode_shapes(out, query, k_cache, block_tables, context_lens)
-    nb, bs, hkv, _ = k_cache.shape
-    _need(cu_groups.dtype == torch.int32 and cu_groups.dim() == 1 and cu_groups.numel() > 0,
-          "cu_groups must be int32 [NG+1]")
-    _need(shared_lens.dtype == torch.int32 and shared_lens.numel() == B, "shared_lens must be int32 [B]")
+    rt = _rt or _runtime()
+    dev, cache = query.get_device(), k_cache.shape
+    if (dev != rt.current_device() or out.get_device() != dev or k_cache.get_device() != dev or
+            v_cache.get_device() != dev or block_tables.get_device() != dev or context_lens.get_device() != dev or
+            cu_groups.get_device() != dev or shared_lens.get_device() != dev or not query.is_contiguous() or
+            not out.is_contiguous() or not k_cache.is_contiguous() or not v_cache.is_contiguous() or
+            not block_tables.is_contiguous() or not context_lens.is_contiguous() or not cu_groups.is_contiguous() or
+            not shared_lens.is_contiguous()):
+        _refuse((("query", query), ("out", out), ("k_cache", k_cache), ("v_cache", v_cache),
+                 ("block_tables", block_tables), ("context_lens", context_lens), ("cu_groups", cu_groups),
+                 ("shared_lens", shared_lens)))
+    _decode_shapes(rt, out, query, cache, v_cache, block_tables, context_lens)
+    if k_cache.dtype != query.dtype or v_cache.dtype != query.dtype:
+        raise ValueError("caches must have the query's dtype")
+    B, Hq, D = query.shape
+    nb, bs, hkv, _ = cache
     ng = cu_groups.numel() - 1
+    if cu_groups.dtype != rt.i32 or cu_groups.dim() != 1 or ng < 0:
+        raise ValueError("cu_groups must be int32 [NG+1]")
+    if shared_lens.dtype != rt.i32 or shared_lens.numel() != B:
+        raise ValueError("shared_lens must be int32 [B]")
     maxnb = block_tables.shape[1]
     if max_context_len is None:
         max_context_len = maxnb * bs
@@ -509,14 +590,17 @@ def decode_shared(out, query, k_cache, v_cache, block_tables, context_lens, cu_g
         max_group_size = B
     if max_shared_len is None:
         max_shared_len = max_context_len
-    buf = _scratch(workspace, decode_shared_workspace_size(B, ng, max_group_size, Hq, hkv, D, bs, max_context_len,
-                                                           max_shared_len, partition_size), query.device)
-    st = _lib.load().pa_decode_shared(
-        out.data_ptr(), _dtype_code(out, allow_f32=True), query.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-        _dtype_code(query), block_tables.data_ptr(), maxnb, context_lens.data_ptr(), max_context_len,
+    stream = rt.stream(dev)
+    buf = _scratch(rt, workspace, decode_shared_workspace_size(B, ng, max_group_size, Hq, hkv, D, bs, max_context_len,
+                                                               max_shared_len, partition_size), dev, stream)
+    st = rt.lib.pa_decode_shared(
+        out.data_ptr(), _code(rt.out, out, "output"), query.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        _code(rt.half, query, "query"), block_tables.data_ptr(), maxnb, context_lens.data_ptr(), max_context_len,
         cu_groups.data_ptr(), ng, max_group_size, shared_lens.data_ptr(), max_shared_len, B, Hq, hkv, D, bs, nb, scale,
-        partition_size, _ptr(buf), 0 if buf is None else buf.nbytes, _ptr(err_flag), _stream(query.device))
-    _lib.check(st, "pa_decode_shared")
+        partition_size, None if buf is None else buf.data_ptr(), 0 if buf is None else buf.nbytes,
+        _flag(err_flag, dev), stream)
+    if st:
+        _lib.check(st, "pa_decode_shared")
 
 
 class StepGraph:

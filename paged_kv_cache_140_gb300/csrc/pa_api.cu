@@ -16,6 +16,7 @@
 #include "pa_cache_ops.h"
 #include "pa_internal.h"
 #include "pa_prefill.h"
+#include "pa_shared_prefix.h"
 #include "pa_split.h"
 
 #define PA_EXPORT extern "C" __attribute__((visibility("default")))
@@ -660,8 +661,9 @@ int split_cache(pa_dtype d) {
 // Entries (sequences, or chunks of groups) of one launch: the kernel keeps 12
 // bytes for each in shared memory; longer lists take several launches.
 constexpr int kSplitEntries = 2048;
-// Work items a launch should have so that every SM of the GPU has one or two.
-constexpr int64_t kSplitItems = 304;
+// SMs the cuts are planned for (a constant: the workspace's size does not depend
+// on the device), and the work items a launch should have, two for each.
+constexpr int64_t kSmsTarget = 152, kSplitItems = 2 * kSmsTarget;
 
 // Partition length, in tokens, for `lists` lists (entries x boxes of heads) of
 // at most `max_len` tokens; 0 when the request is invalid.  Lists that fill the
@@ -688,12 +690,41 @@ int split_partition(int64_t lists, int max_len, int block_size, int slot_tokens,
     return static_cast<int>(P);
 }
 
+// A group with more query rows per KV head than this has its prefix computed on
+// the tensor-core kernel, whose 128-row tiles read each K/V row once for up to
+// 256 query rows; up to it the split kernel reads them once for every 8.
+constexpr int kSharedSplitRows = 16;
+
+// Tokens per unit of the tensor-core prefix kernel, for `lists` lists (groups x
+// pairs x KV heads) of up to `tokens`: the cut with the least estimated time,
+// whole waves of CTAs over the GPU's SMs times the tiles of one unit (a tile
+// costs about half as much where one query tile's products, not two, wait on it)
+// plus a CTA's own start and end, worth about 5 tiles.
+int shared_unit(int64_t lists, int tokens, bool two_tiles) {
+    const int tiles = std::max(1, (tokens + pa::kSharedTile - 1) / pa::kSharedTile);
+    const double tile = two_tiles ? 1.0 : 0.6;
+    int best = tiles;
+    double best_cost = 1e30;
+    for (int per = tiles; per >= 1; per = std::min(per - 1, per * 15 / 16)) {
+        const int64_t units = lists * ((tiles + per - 1) / per);
+        const double cost = static_cast<double>((units + kSmsTarget - 1) / kSmsTarget) * (per * tile + 5.0);
+        if (cost < best_cost) {
+            best_cost = cost;
+            best = per;
+        }
+    }
+    return best * pa::kSharedTile;
+}
+
 struct SplitPlan {
     int log2_heads = 0, G = 1;
     int partition = 0;           // decode and suffix entries
     int parts = 1;               // their partials per row
-    int prefix_cols = 0;         // shared prefixes: query rows per launch entry
-    int prefix_part = 0, prefix_parts = 0;
+    bool prefix_tc = false;      // shared prefixes: on the tensor-core kernel (else the split kernel)
+    int prefix_cols = 0;         // split kernel: query rows per entry
+    int prefix_pairs = 0;        // tensor-core kernel: pairs of query tiles per group
+    int prefix_part = 0;         // tokens per prefix_per partials
+    int prefix_per = 1, prefix_parts = 0;
     int max_parts = 1;
     size_t acc_off = 0, bytes = 0;
 };
@@ -721,12 +752,22 @@ bool plan_split(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int
     w.max_parts = w.parts;
     if (shared) {
         if (num_groups < 0 || max_group_size < 0 || max_shared_len < 0 || max_shared_len > max_context_len) return false;
+        const int shared_tokens = max_shared_len / block_size * block_size;
+        const int64_t rows = static_cast<int64_t>(max_group_size) * w.G;
+        w.prefix_tc = rows > kSharedSplitRows && block_size <= pa::kSharedTile && (block_size & (block_size - 1)) == 0;
+        if (w.prefix_tc) {
+            w.prefix_pairs = static_cast<int>((rows + 2 * pa::kSharedTile - 1) / (2 * pa::kSharedTile));
+            w.prefix_part = shared_unit(static_cast<int64_t>(num_groups) * w.prefix_pairs * num_kv_heads, shared_tokens,
+                                        rows > pa::kSharedTile);
+            w.prefix_per = 2;
+        }
         w.prefix_cols = w.G;
         while (w.prefix_cols < 8 && w.prefix_cols < static_cast<int64_t>(max_group_size) * w.G) w.prefix_cols *= 2;
         const int chunk_seqs = w.prefix_cols / w.G;
         const int64_t chunks = (static_cast<int64_t>(max_group_size) + chunk_seqs - 1) / chunk_seqs;
-        w.prefix_part = split_partition(num_groups * chunks * ngroups, max_shared_len, block_size, slot_tokens, 0);
-        w.prefix_parts = (max_shared_len / block_size * block_size + w.prefix_part - 1) / w.prefix_part;
+        if (!w.prefix_tc)
+            w.prefix_part = split_partition(num_groups * chunks * ngroups, max_shared_len, block_size, slot_tokens, 0);
+        w.prefix_parts = (shared_tokens + w.prefix_part - 1) / w.prefix_part * w.prefix_per;
         w.max_parts += w.prefix_parts;
     }
     if (!shared && w.max_parts <= 1) return true;
@@ -933,7 +974,7 @@ PA_EXPORT pa_status pa_quant_decode(void *out, pa_dtype out_dtype, const void *q
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const pa_status r = run_split(p, cache, head_dim, w.G, num_seqs, max_context_len, tk, tv, dev, s);
     if (r != PA_OK || w.max_parts <= 1) return r;
-    return pa::launch_split_merge(p, head_dim, 1, dev.sms, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+    return pa::launch_split_merge(p, head_dim, 1, 1, dev.sms, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 PA_EXPORT size_t pa_decode_shared_workspace_size(int num_seqs, int num_groups, int max_group_size, int num_heads,
@@ -954,7 +995,7 @@ PA_EXPORT pa_status pa_decode_shared(void *out, pa_dtype out_dtype, const void *
                                      int num_kv_heads, int head_dim, int block_size, int64_t num_blocks, float scale,
                                      int partition_size, void *workspace, size_t workspace_bytes, int *err_flag,
                                      void *stream) {
-    if (num_groups < 0 || max_group_size < 0 || max_shared_len < 0 || max_shared_len > max_context_len)
+    if (num_groups < 0 || max_group_size < 0 || max_shared_len < 0 || max_shared_len > max_context_len || !(scale >= 0.f))
         return PA_ERR_INVALID_ARG;
     const pa_status st = check_split(out_dtype, kv_dtype, max_blocks_per_seq, max_context_len, num_seqs, num_heads,
                                      num_kv_heads, head_dim, block_size, num_blocks, scale);
@@ -987,7 +1028,20 @@ PA_EXPORT pa_status pa_decode_shared(void *out, pa_dtype out_dtype, const void *
     p.max_group_size = max_group_size;
     p.max_shared_len = max_shared_len;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (w.prefix_parts > 0) {
+    if (w.prefix_parts > 0 && w.prefix_tc) {
+        if (pa::shared_prefix_smem(head_dim) + 1024 > static_cast<size_t>(dev.smem_optin)) return PA_ERR_UNSUPPORTED;
+        const int ranges = w.prefix_parts / w.prefix_per, tile_seqs = pa::kSharedTile / w.G;
+        if (static_cast<int64_t>(num_groups) * ranges * num_kv_heads * w.prefix_pairs >= (int64_t{1} << 31))
+            return PA_ERR_UNSUPPORTED;
+        CUtensorMap tq, sk, sv;
+        if (!encode_map_128b(&tq, query, 2, head_dim, num_heads, num_seqs, w.G, tile_seqs) ||
+            !encode_map_128b(&sk, k_cache, 2, head_dim, num_kv_heads, num_blocks * block_size, 1, block_size) ||
+            !encode_map_128b(&sv, v_cache, 2, head_dim, num_kv_heads, num_blocks * block_size, 1, block_size))
+            return PA_ERR_CUDA;
+        if (pa::launch_shared_prefix(p, head_dim, kv_dtype == PA_BF16, w.prefix_pairs, w.prefix_part, ranges, tq, sk, sv,
+                                     s) != cudaSuccess)
+            return PA_ERR_CUDA;
+    } else if (w.prefix_parts > 0) {
         pa::SplitParams pre = p;
         pre.mode = pa::kSplitPrefix;
         pre.partition_size = w.prefix_part;
@@ -1003,8 +1057,9 @@ PA_EXPORT pa_status pa_decode_shared(void *out, pa_dtype out_dtype, const void *
     p.late_wait = w.prefix_parts > 0;
     const pa_status r = run_split(p, cache, head_dim, w.G, num_seqs, max_context_len, tk, tv, dev, s);
     if (r != PA_OK) return r;
-    return pa::launch_split_merge(p, head_dim, std::max(1, w.prefix_part), dev.sms, s) == cudaSuccess ? PA_OK
-                                                                                                      : PA_ERR_CUDA;
+    return pa::launch_split_merge(p, head_dim, std::max(1, w.prefix_part), w.prefix_per, dev.sms, s) == cudaSuccess
+               ? PA_OK
+               : PA_ERR_CUDA;
 }
 
 PA_EXPORT pa_status pa_check_err_flag(int *err_flag, int clear, int *flag_out, void *stream) {

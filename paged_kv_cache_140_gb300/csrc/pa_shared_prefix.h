@@ -1,0 +1,24 @@
+// Host-side interface between the C ABI (pa_api.cu) and the tensor-core kernel
+// for prefixes shared by many sequences (pa_shared_prefix.cu).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "pa_split.h"
+
+namespace pa {
+
+constexpr int kSharedTile = 128;   // query rows per tile, tokens per K/V tile
+
+size_t shared_prefix_smem(int head_dim);
+
+// Units are (group, range of unit_tokens, KV head, pair of query tiles): `pairs`
+// pairs of tiles cover max_group_size sequences, `units_per_list` ranges the
+// longest prefix.  Range r writes the partials 2 r and 2 r + 1 of its rows.
+// unit_tokens is a multiple of kSharedTile; block_size a power of two, 8 to 128.
+cudaError_t launch_shared_prefix(const SplitParams &p, int head_dim, bool bf16, int pairs, int unit_tokens,
+                                 int units_per_list, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
+                                 cudaStream_t stream);
+
+}  // namespace pa

@@ -85,11 +85,12 @@ cudaError_t launch_split_e4m3(const SplitParams &p, int head_dim, int cols, cons
 cudaError_t launch_split_int8(const SplitParams &p, int head_dim, int cols, const CUtensorMap &tk,
                               const CUtensorMap &tv, int grid, size_t smem, cudaStream_t stream);
 
-// Joins partial results into output rows.  Sequence s has ceil(len / prefix_part)
-// partials of its shared blocks at index 0.. and ceil(rest / partition_size) at
-// p.part_off.. (p.mode kSplitDecode: no shared blocks, and sequences of one
-// partition are final already).
-cudaError_t launch_split_merge(const SplitParams &p, int head_dim, int prefix_part, int sms, cudaStream_t stream);
+// Joins partial results into output rows.  Sequence s has per_part partials for
+// each prefix_part tokens of its shared blocks at index 0.. and one for each
+// partition_size of the rest at p.part_off.. (p.mode kSplitDecode: no shared
+// blocks, and sequences of one partition are final already).
+cudaError_t launch_split_merge(const SplitParams &p, int head_dim, int prefix_part, int per_part, int sms,
+                               cudaStream_t stream);
 
 // Quantising write and read-back (cache: kCacheE4M3 or kCacheInt8).
 cudaError_t launch_quant_write(const void *key, const void *value, int64_t key_stride, int64_t value_stride,

@@ -14,7 +14,7 @@ namespace {
 
 template <int D>
 __global__ void __launch_bounds__(256)
-    split_merge_kernel(const __grid_constant__ SplitParams p, int prefix_part, int wt) {
+    split_merge_kernel(const __grid_constant__ SplitParams p, int prefix_part, int per_part, int wt) {
     constexpr int DPL = D / 32;
     __shared__ float red_o[8][D];
     __shared__ float red_l[8];
@@ -32,7 +32,7 @@ __global__ void __launch_bounds__(256)
         int shared = 0;
         if (p.mode != kSplitDecode) {
             shared = shared_blocks(p, s, ctx, false) * p.block_size;
-            npre = (shared + prefix_part - 1) / prefix_part;
+            npre = (shared + prefix_part - 1) / prefix_part * per_part;
         }
         np = npre + (ctx - shared + p.partition_size - 1) / p.partition_size;
         active = np > 1 || p.mode != kSplitDecode;
@@ -56,18 +56,25 @@ __global__ void __launch_bounds__(256)
             float w = 0.f;
             if (j0 + lane < je) {
                 const float2 ml = __ldcg(reinterpret_cast<const float2 *>(p.ws_ml + 2 * row(j0 + lane)));
-                // (a state that saw no finite reference counts fully: its sum is 0, or not a number)
-                w = ml.x == -INFINITY ? 1.f : fast_exp2(ml.x - M);
+                // An empty partial (nothing was added; its row need not exist) is passed
+                // over; any other without a finite reference counts fully, its sum being
+                // no number.
+                if (ml.x == -INFINITY) {
+                    w = ml.y == 0.f ? -1.f : 1.f;
+                } else {
+                    w = fast_exp2(ml.x - M);
+                }
                 l = fmaf(ml.y, w, l);
             }
             const int cnt = min(32, je - j0);
             for (int u0 = 0; u0 < cnt; u0 += 8) {
-                float v[8][DPL];
+                float v[8][DPL], wj[8];
 #pragma unroll
                 for (int u = 0; u < 8; ++u) {
+                    wj[u] = __shfl_sync(kFull, w, (u0 + u) & 31);
 #pragma unroll
                     for (int i = 0; i < DPL; ++i) v[u][i] = 0.f;
-                    if (u0 + u < cnt) {
+                    if (u0 + u < cnt && wj[u] >= 0.f) {
                         const float *a = p.ws_acc + row(j0 + u0 + u) * D + d0;
                         if constexpr (DPL == 4) {
                             const float4 x = __ldcg(reinterpret_cast<const float4 *>(a));
@@ -79,11 +86,9 @@ __global__ void __launch_bounds__(256)
                     }
                 }
 #pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                    const float wj = __shfl_sync(kFull, w, (u0 + u) & 31);
+                for (int u = 0; u < 8; ++u)
 #pragma unroll
-                    for (int i = 0; i < DPL; ++i) o[i] = fmaf(v[u][i], wj, o[i]);
-                }
+                    for (int i = 0; i < DPL; ++i) o[i] = fmaf(v[u][i], wj[u], o[i]);
             }
         }
 #pragma unroll
@@ -133,14 +138,15 @@ int split_slot_stages(int cache, int log2_heads) {
            log2_heads;
 }
 
-cudaError_t launch_split_merge(const SplitParams &p, int head_dim, int prefix_part, int sms, cudaStream_t stream) {
+cudaError_t launch_split_merge(const SplitParams &p, int head_dim, int prefix_part, int per_part, int sms,
+                               cudaStream_t stream) {
     const int64_t rows = static_cast<int64_t>(p.num_seqs) * p.num_heads;
     // one warp per row, more while the rows leave warps idle and there is something to share out
     int wt = 1;
     while (wt < 8 && rows * wt * 2 <= static_cast<int64_t>(sms) * 16 && p.max_parts >= 8 * wt) wt *= 2;
     const int64_t blocks = (rows + 8 / wt - 1) / (8 / wt);
     auto kern = head_dim == 128 ? split_merge_kernel<128> : split_merge_kernel<64>;
-    return launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream, p, prefix_part, wt);
+    return launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream, p, prefix_part, per_part, wt);
 }
 
 }  // namespace pa

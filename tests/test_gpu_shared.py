@@ -155,6 +155,13 @@ def test_logits_that_rise_with_the_position(n):
     check(b)
 
 
+@pytest.mark.parametrize("n", [4, 60])
+def test_a_scale_of_zero_averages(n):
+    b = make([n], [200], [7] * n, 4, 2, 128, 16, "f16", seed=12)
+    b["scale"] = 0.0
+    check(b)
+
+
 def test_loose_bounds_and_partition_sizes_agree():
     b = make([3, 20, 1], [300, 513, 40], [9] * 24, 8, 4, 64, 16, "f16", seed=6)
     a = check(b)

@@ -70,13 +70,13 @@ def test_decode_refusals(lib):
 def test_shared_refusals(lib):
     from paged_kv_cache_140_gb300 import _lib as L
 
-    def dec(B=0, ng=0, mg=0, ms=50, hq=8, hkv=8, d=64, bs=16, maxnb=8, ctx=100, dt=0, odt=2, P=0):
+    def dec(B=0, ng=0, mg=0, ms=50, hq=8, hkv=8, d=64, bs=16, maxnb=8, ctx=100, dt=0, odt=2, P=0, scale=0.1):
         return lib.pa_decode_shared(NUL, odt, NUL, NUL, NUL, dt, NUL, maxnb, NUL, ctx, NUL, ng, mg, NUL, ms, B, hq, hkv,
-                                    d, bs, 64, 0.1, P, NUL, 0, NUL, NUL)
+                                    d, bs, 64, scale, P, NUL, 0, NUL, NUL)
     assert dec() == L.PA_OK
     assert dec(B=4, ng=2, mg=2) == L.PA_ERR_INVALID_ARG      # null tensors
     for kw in (dict(ms=101), dict(ms=-1), dict(ng=-1), dict(mg=-1), dict(dt=4), dict(dt=3), dict(odt=3),
-               dict(B=4, ng=1, mg=3), dict(B=4, ng=5, mg=1), dict(B=4, ng=1, mg=5), dict(P=8)):
+               dict(B=4, ng=1, mg=3), dict(B=4, ng=5, mg=1), dict(B=4, ng=1, mg=5), dict(P=8), dict(scale=-0.1), dict(scale=float("nan"))):
         assert dec(**kw) == L.PA_ERR_INVALID_ARG, kw
     for kw in (dict(hq=24), dict(d=32), dict(bs=24)):
         assert dec(**kw) == L.PA_ERR_UNSUPPORTED, kw
