@@ -423,7 +423,8 @@ pa_status pa_swap_blocks(const void *src_k, const void *src_v, void *dst_k, void
  * too (as a PA_FP8_E4M3 cache with head_dim 4: four bytes a row); codes of
  * either type move as PA_FP8_E4M3.
  *
- * head_dim 64 or 128; arithmetic in fp32.
+ * head_dim 64 or 128; arithmetic in fp32.  Scales are positive (NaN: the row is
+ * no number); attention is accurate for V rows below 2^60 in magnitude.
  *
  * pa_quant_reshape_and_cache -- write new K/V rows, quantised.
  *

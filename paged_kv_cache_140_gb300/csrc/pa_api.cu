@@ -798,9 +798,24 @@ bool encode_split_map(CUtensorMap *map, const void *cache, int64_t num_blocks, i
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Tensor map over scales [NB * bs, Hkv] (32-bit), boxes of `heads` heads x
+// min(16, bs) tokens.
+bool encode_scale_map(CUtensorMap *map, const float *scales, int64_t num_blocks, int block_size, int num_kv_heads,
+                      int heads) {
+    EncodeTiledFn fn = encode_tiled();
+    if (fn == nullptr) return false;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(num_kv_heads), static_cast<cuuint64_t>(num_blocks) * block_size};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(num_kv_heads) * 4};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(heads), static_cast<cuuint32_t>(std::min(block_size, 16))};
+    const cuuint32_t estr[2] = {1u, 1u};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<float *>(scales), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // One pass of the split kernel over `entries` entries (p.mode says which).
-pa_status run_split(pa::SplitParams p, int cache, int head_dim, int cols, int entries, int max_len, const CUtensorMap &tk,
-                    const CUtensorMap &tv, const DeviceInfo &dev, cudaStream_t stream) {
+pa_status run_split(pa::SplitParams p, int cache, int head_dim, int cols, int entries, int max_len,
+                    const pa::SplitMaps &maps, const DeviceInfo &dev, cudaStream_t stream) {
     const int64_t per_entry = static_cast<int64_t>(p.num_kv_heads >> p.log2_heads) *
                               std::max(1, (max_len + p.partition_size - 1) / p.partition_size);
     for (int e = 0; e < entries; e += kSplitEntries) {
@@ -816,7 +831,7 @@ pa_status run_split(pa::SplitParams p, int cache, int head_dim, int cols, int en
                       : cache == pa::kCacheBF16 ? pa::launch_split_bf16
                       : cache == pa::kCacheE4M3 ? pa::launch_split_e4m3
                                                 : pa::launch_split_int8;
-        if (launch(p, head_dim, cols, tk, tv, grid, smem, stream) != cudaSuccess) return PA_ERR_CUDA;
+        if (launch(p, head_dim, cols, maps, grid, smem, stream) != cudaSuccess) return PA_ERR_CUDA;
     }
     return PA_OK;
 }
@@ -961,9 +976,14 @@ PA_EXPORT pa_status pa_quant_decode(void *out, pa_dtype out_dtype, const void *q
         return PA_ERR_WORKSPACE;
     DeviceInfo dev;
     if (!device_info(dev)) return PA_ERR_CUDA;
-    CUtensorMap tk, tv;
-    if (!encode_split_map(&tk, k_cache, num_blocks, block_size, num_kv_heads, head_dim, 1, 1 << w.log2_heads) ||
-        !encode_split_map(&tv, v_cache, num_blocks, block_size, num_kv_heads, head_dim, 1, 1 << w.log2_heads))
+    const int box_heads = 1 << w.log2_heads;
+    pa::SplitMaps maps{};
+    if (!encode_split_map(&maps.k, k_cache, num_blocks, block_size, num_kv_heads, head_dim, 1, box_heads) ||
+        !encode_split_map(&maps.v, v_cache, num_blocks, block_size, num_kv_heads, head_dim, 1, box_heads))
+        return PA_ERR_CUDA;
+    if (box_heads >= 4 &&
+        (!encode_scale_map(&maps.ks, k_scales, num_blocks, block_size, num_kv_heads, box_heads) ||
+         !encode_scale_map(&maps.vs, v_scales, num_blocks, block_size, num_kv_heads, box_heads)))
         return PA_ERR_CUDA;
     pa::SplitParams p = split_params(out, out_dtype, query, q_dtype, block_tables, max_blocks_per_seq, context_lens,
                                      max_context_len, num_seqs, num_heads, num_kv_heads, block_size, num_blocks, scale,
@@ -972,7 +992,7 @@ PA_EXPORT pa_status pa_quant_decode(void *out, pa_dtype out_dtype, const void *q
     p.v_scales = v_scales;
     p.mode = pa::kSplitDecode;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const pa_status r = run_split(p, cache, head_dim, w.G, num_seqs, max_context_len, tk, tv, dev, s);
+    const pa_status r = run_split(p, cache, head_dim, w.G, num_seqs, max_context_len, maps, dev, s);
     if (r != PA_OK || w.max_parts <= 1) return r;
     return pa::launch_split_merge(p, head_dim, 1, 1, dev.sms, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
@@ -1015,9 +1035,9 @@ PA_EXPORT pa_status pa_decode_shared(void *out, pa_dtype out_dtype, const void *
     if (workspace == nullptr || workspace_bytes < w.bytes || !aligned16(workspace)) return PA_ERR_WORKSPACE;
     DeviceInfo dev;
     if (!device_info(dev)) return PA_ERR_CUDA;
-    CUtensorMap tk, tv;
-    if (!encode_split_map(&tk, k_cache, num_blocks, block_size, num_kv_heads, head_dim, 2, 1 << w.log2_heads) ||
-        !encode_split_map(&tv, v_cache, num_blocks, block_size, num_kv_heads, head_dim, 2, 1 << w.log2_heads))
+    pa::SplitMaps maps{};
+    if (!encode_split_map(&maps.k, k_cache, num_blocks, block_size, num_kv_heads, head_dim, 2, 1 << w.log2_heads) ||
+        !encode_split_map(&maps.v, v_cache, num_blocks, block_size, num_kv_heads, head_dim, 2, 1 << w.log2_heads))
         return PA_ERR_CUDA;
     pa::SplitParams p = split_params(out, out_dtype, query, kv_dtype, block_tables, max_blocks_per_seq, context_lens,
                                      max_context_len, num_seqs, num_heads, num_kv_heads, block_size, num_blocks, scale,
@@ -1048,14 +1068,14 @@ PA_EXPORT pa_status pa_decode_shared(void *out, pa_dtype out_dtype, const void *
         pre.chunk_seqs = w.prefix_cols / w.G;
         pre.chunks = (max_group_size + pre.chunk_seqs - 1) / pre.chunk_seqs;
         if (static_cast<int64_t>(num_groups) * pre.chunks >= (int64_t{1} << 31)) return PA_ERR_UNSUPPORTED;
-        const pa_status r = run_split(pre, cache, head_dim, w.prefix_cols, num_groups * pre.chunks, max_shared_len, tk,
-                                      tv, dev, s);
+        const pa_status r = run_split(pre, cache, head_dim, w.prefix_cols, num_groups * pre.chunks, max_shared_len,
+                                      maps, dev, s);
         if (r != PA_OK) return r;
     }
     p.mode = pa::kSplitSuffix;
     p.part_off = w.prefix_parts;
     p.late_wait = w.prefix_parts > 0;
-    const pa_status r = run_split(p, cache, head_dim, w.G, num_seqs, max_context_len, tk, tv, dev, s);
+    const pa_status r = run_split(p, cache, head_dim, w.G, num_seqs, max_context_len, maps, dev, s);
     if (r != PA_OK) return r;
     return pa::launch_split_merge(p, head_dim, std::max(1, w.prefix_part), w.prefix_per, dev.sms, s) == cudaSuccess
                ? PA_OK

@@ -73,17 +73,22 @@ inline int split_log2_heads(int num_kv_heads) {
 // 16-token stages of one ring slot (a slot feeds every consumer warp once).
 int split_slot_stages(int cache, int log2_heads);
 
-// `cols`: query rows per KV head and entry (1, 2, 4 or 8).  The tensor maps
-// view the caches as (dim, token, head) with {min(128 bytes, row), min(16, bs),
-// heads} boxes.
-cudaError_t launch_split_f16(const SplitParams &p, int head_dim, int cols, const CUtensorMap &tk,
-                             const CUtensorMap &tv, int grid, size_t smem, cudaStream_t stream);
-cudaError_t launch_split_bf16(const SplitParams &p, int head_dim, int cols, const CUtensorMap &tk,
-                              const CUtensorMap &tv, int grid, size_t smem, cudaStream_t stream);
-cudaError_t launch_split_e4m3(const SplitParams &p, int head_dim, int cols, const CUtensorMap &tk,
-                              const CUtensorMap &tv, int grid, size_t smem, cudaStream_t stream);
-cudaError_t launch_split_int8(const SplitParams &p, int head_dim, int cols, const CUtensorMap &tk,
-                              const CUtensorMap &tv, int grid, size_t smem, cudaStream_t stream);
+// The caches viewed as (dim, token, head), boxes {min(128 bytes, row), min(16,
+// bs), heads}; 8-bit caches with 4 or 8 heads per box: the scales as (head,
+// token), boxes {heads, min(16, bs)}.
+struct SplitMaps {
+    CUtensorMap k, v, ks, vs;
+};
+
+// `cols`: query rows per KV head and entry (1, 2, 4 or 8).
+cudaError_t launch_split_f16(const SplitParams &p, int head_dim, int cols, const SplitMaps &m, int grid, size_t smem,
+                             cudaStream_t stream);
+cudaError_t launch_split_bf16(const SplitParams &p, int head_dim, int cols, const SplitMaps &m, int grid, size_t smem,
+                              cudaStream_t stream);
+cudaError_t launch_split_e4m3(const SplitParams &p, int head_dim, int cols, const SplitMaps &m, int grid, size_t smem,
+                              cudaStream_t stream);
+cudaError_t launch_split_int8(const SplitParams &p, int head_dim, int cols, const SplitMaps &m, int grid, size_t smem,
+                              cudaStream_t stream);
 
 // Joins partial results into output rows.  Sequence s has per_part partials for
 // each prefix_part tokens of its shared blocks at index 0.. and one for each

@@ -3,9 +3,9 @@
 
 namespace pa {
 
-cudaError_t launch_split_f16(const SplitParams &p, int head_dim, int cols, const CUtensorMap &tk,
-                             const CUtensorMap &tv, int grid, size_t smem, cudaStream_t stream) {
-    return launch_split_ct<kCacheF16>(p, head_dim, cols, tk, tv, grid, smem, stream);
+cudaError_t launch_split_f16(const SplitParams &p, int head_dim, int cols, const SplitMaps &m, int grid, size_t smem,
+                             cudaStream_t stream) {
+    return launch_split_ct<kCacheF16>(p, head_dim, cols, m, grid, smem, stream);
 }
 
 }  // namespace pa

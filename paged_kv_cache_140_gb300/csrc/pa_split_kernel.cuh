@@ -35,6 +35,8 @@
 // Waits are bounded (2 s) and report PA_FLAG_TIMEOUT.
 #pragma once
 
+#include <type_traits>
+
 #include "pa_decode_common.cuh"
 #include "pa_device.cuh"
 #include "pa_split.h"
@@ -53,6 +55,10 @@ struct SplitLayout {
     static constexpr int kES = k8 ? 1 : 2;
     static constexpr int kWarps = 8;                     // consumer warps
     static constexpr int kSub = k8 ? 2 : 1;              // stages per consumer warp and slot
+    // Up to 4 query rows leave half of the products' 8 columns free: the weights'
+    // high parts take columns 0-3 and their low parts columns 4-7 (the queries are
+    // repeated there), one product in place of two.
+    static constexpr bool kPaired = C <= 4;
     static constexpr int kTiles = kWarps * kSub;         // (stage, head) tiles of a slot
     static constexpr int kRowB = D * kES < 128 ? D * kES : 128;   // bytes of one box row
     static constexpr int kHalves = D * kES / kRowB;
@@ -61,7 +67,8 @@ struct SplitLayout {
     static constexpr int kSlotBytes = (2 * kKVBytes + 2 * kScaleBytes + 1023) / 1024 * 1024;
     static constexpr int kThreads = (kWarps + 1) * 32;
     static constexpr int kMT = D / 16;
-    static constexpr int kStateBytes = kMT * 32 * 16;    // one warp's accumulators
+    static constexpr int kStateRow = D + 4;              // floats per query row of a warp's state
+    static constexpr int kStateBytes = C * kStateRow * 4;
 };
 
 // One ring slot's description.
@@ -90,8 +97,15 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+
+// 2-D tiled TMA load (scales; the other heads' scales of the same tokens share
+// its cache lines, so no early eviction).
+__device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, uint64_t *bar, int x, int y) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_addr(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar))
+        : "memory");
 }
 __device__ __forceinline__ uint64_t l2_policy_evict_normal() {
     uint64_t p;
@@ -104,6 +118,16 @@ __device__ __forceinline__ float fast_log2(float x) {
     asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+
+// Maximum that keeps a NaN.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+// V scales below this count as this (the cache write makes none below 2^-69),
+// which bounds 2^(s_p - m) to 2^78.
+constexpr float kScaleFloor = 8.470329472543003e-22f;   // 2^-70
 
 // Four codes (bytes 0-3) as two f16 pairs.  Natural order: (0, 1), (2, 3);
 // interleaved: (0, 2), (1, 3).  An int8 code b is u - 128 for the byte
@@ -165,7 +189,8 @@ __device__ __forceinline__ uint32_t entry_weight(int len, int mode, int ngroups,
 template <int D, int C, int CT>
 __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
     paged_split_kernel(const __grid_constant__ SplitParams p, const __grid_constant__ CUtensorMap tmap_k,
-                       const __grid_constant__ CUtensorMap tmap_v) {
+                       const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ CUtensorMap tmap_ks,
+                       const __grid_constant__ CUtensorMap tmap_vs) {
     using L = SplitLayout<D, C, CT>;
     constexpr bool k8 = L::k8;
     constexpr bool BF16 = CT == kCacheBF16;   // MMA operand type
@@ -201,10 +226,13 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
     int *len_s = reinterpret_cast<int *>(warp_tot + 32);
     int *aux_s = len_s + E;                            // suffix: first block; prefix: sequence | members << 27
     uint32_t *prefix = reinterpret_cast<uint32_t *>(aux_s + E);
+    // Scales of 4 or 8 heads are 16 or 32 bytes per token: boxes.  Fewer are below
+    // a box's least width: 4-byte copies by all lanes of the producer.
+    const bool scale_boxes = k8 && p.log2_heads >= 2;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < S; ++i) {
-            mbar_init(&full[i], k8 ? 33 : 1);
+            mbar_init(&full[i], k8 && !scale_boxes ? 33 : 1);
             mbar_init(&empty[i], W);
         }
         for (int i = 0; i < kQueryRing; ++i) {
@@ -411,6 +439,7 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                     bad = w;
                 }
                 const uint32_t box = static_cast<uint32_t>(RB * L::kRowB) << p.log2_heads;
+                const uint32_t sbox = scale_boxes ? static_cast<uint32_t>(RB * 4) << p.log2_heads : 0u;
                 if (lane == 0) {
                     SlotMeta mt;
                     mt.seq = seq;
@@ -421,7 +450,8 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                     mt.bad = bad;
                     mt.pad[0] = mt.pad[1] = 0;
                     meta[slot] = mt;
-                    mbar_arrive_expect_tx(&full[slot], static_cast<uint32_t>(__popc(loaded)) * box * 2u * L::kHalves);
+                    mbar_arrive_expect_tx(&full[slot],
+                                          static_cast<uint32_t>(__popc(loaded)) * 2u * (box * L::kHalves + sbox));
                 }
                 __syncwarp();
                 const int z = load ? id * bs + ptok % bs : 0;               // the piece's first cache slot
@@ -438,26 +468,24 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                 }
                 if constexpr (k8) {
                     // scales, [token of the slot][head of the box], K then V
-                    const uint32_t sd = smem_addr(sp + 2 * L::kKVBytes);
-                    const int lv = p.log2_heads >= 2 ? 2 : 0;               // floats per copy: 4 or 1
-                    const int lc = p.log2_heads - lv;                       // copies per token
-                    const int n = (SW * kStageTokens) << lc;
-                    for (int i = lane; i < n; i += 32) {
-                        const int tk = i >> lc, h = (i & ((1 << lc) - 1)) << lv;
-                        const int pc = tk / RB;
-                        const int zz = __shfl_sync(kFull, z, pc);
-                        if (!((loaded >> pc) & 1u) || tk >= nt) continue;
-                        const int64_t src = static_cast<int64_t>(zz + tk % RB) * Hkv + kvh0 + h;
-                        const uint32_t dst = sd + ((tk << p.log2_heads) + h) * 4;
-                        if (lv) {
-                            cp_async16(dst, p.k_scales + src);
-                            cp_async16(dst + L::kScaleBytes, p.v_scales + src);
-                        } else {
-                            cp_async4(dst, p.k_scales + src);
-                            cp_async4(dst + L::kScaleBytes, p.v_scales + src);
+                    uint8_t *ss = sp + 2 * L::kKVBytes;
+                    if (scale_boxes) {
+                        if (load) {
+                            tma_load_2d(ss + lane * sbox, &tmap_ks, &full[slot], kvh0, z);
+                            tma_load_2d(ss + L::kScaleBytes + lane * sbox, &tmap_vs, &full[slot], kvh0, z);
                         }
+                    } else {
+                        const int n = (SW * kStageTokens) << p.log2_heads;
+                        for (int i = lane; i < n; i += 32) {
+                            const int tk = i >> p.log2_heads, h = i & (H - 1), pc = tk / RB;
+                            const int zz = __shfl_sync(kFull, z, pc);
+                            if (!((loaded >> pc) & 1u) || tk >= nt) continue;
+                            const int64_t src = static_cast<int64_t>(zz + tk % RB) * Hkv + kvh0 + h;
+                            cp_async4(smem_addr(ss) + i * 4, p.k_scales + src);
+                            cp_async4(smem_addr(ss) + L::kScaleBytes + i * 4, p.v_scales + src);
+                        }
+                        cp_async_arrive(&full[slot]);
                     }
-                    cp_async_arrive(&full[slot]);
                 }
                 __syncwarp();
             }
@@ -473,7 +501,7 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                     meta[slot] = mt;
                     arrive(&full[slot]);
                 }
-                if constexpr (k8) {
+                if (k8 && !scale_boxes) {
                     __syncwarp();
                     arrive(&full[slot]);
                 }
@@ -504,6 +532,7 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
     uint32_t qf[KS][2];
     float qs[2];                  // logit scale of columns 2t, 2t + 1
     float acc[MT][4], m_run[2], l_run[2];
+    float mu[2];                  // the reference that weights are taken under: m_run, or 0 while there is none
     int cslot = 0;
     uint32_t cphase = 0, citems = 0;
     for (;;) {
@@ -530,9 +559,10 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                 if (lane == 0) report(p.err_flag, 0x10 /* PA_FLAG_TIMEOUT */);
                 return;
             }
-            const bool live = g < (members << lg);
-            const uint32_t *qw = reinterpret_cast<const uint32_t *>(qbuf + qi * kQEntry * H + (live ? g >> lg : 0) * qmember) +
-                                 ((head << lg) + (g & ((1 << lg) - 1))) * (D / 2);
+            const int gq = L::kPaired ? g & 3 : g;        // my column's query row
+            const bool live = gq < (members << lg);
+            const uint32_t *qw = reinterpret_cast<const uint32_t *>(qbuf + qi * kQEntry * H + (live ? gq >> lg : 0) * qmember) +
+                                 ((head << lg) + (gq & ((1 << lg) - 1))) * (D / 2);
             if constexpr (!k8) {
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks) {
@@ -572,30 +602,37 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 m_run[e] = -INFINITY;
-                l_run[e] = 0.f;
+                l_run[e] = mu[e] = 0.f;
             }
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) acc[mt][0] = acc[mt][1] = acc[mt][2] = acc[mt][3] = 0.f;
         }
 
+        // My tokens of this slot.  kWhole: every one of them counts (all but a
+        // list's last slot), compiled apart so that the common case carries no masks.
         const int st0 = sub * SUB;
-        const int mine = m.ntok - st0 * kStageTokens;     // my tokens of this slot
-        if (mine > 0) {
-            const bool second = SUB > 1 && mine > kStageTokens;
+        const int mine = m.ntok - st0 * kStageTokens;
+        auto attend = [&](auto whole_tag) {
+            constexpr bool kWhole = decltype(whole_tag)::value;
+            const bool second = kWhole || (SUB > 1 && mine > kStageTokens);
             uint32_t smask[SUB];
             float x[SUB][4], sv[SUB][2];
-            float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
             for (int hs = 0; hs < SUB; ++hs) {
-                smask[hs] = 0;
-                if (hs > 0 && !second) continue;
-                const int n = mine - hs * kStageTokens;
-                uint32_t mk = n >= kStageTokens ? 0xffffu : (1u << n) - 1u;
-                if (m.bad) {
+                smask[hs] = 0xffffu;
+                if constexpr (!kWhole) {
+                    if (hs > 0 && !second) {
+                        smask[hs] = 0;
+                        x[hs][0] = x[hs][1] = x[hs][2] = x[hs][3] = -INFINITY;
+                        sv[hs][0] = sv[hs][1] = 0.f;
+                        continue;
+                    }
+                    const int n = mine - hs * kStageTokens;
+                    uint32_t mk = n >= kStageTokens ? 0xffffu : (1u << n) - 1u;
                     const uint32_t b = (m.bad >> (2 * (st0 + hs))) & 3u;
                     mk &= ~(((b & 1u) ? 0xffu : 0u) | ((b & 2u) ? 0xff00u : 0u));
+                    smask[hs] = mk;
                 }
-                smask[hs] = mk;
                 // ---- QK: 16 tokens x 8 columns ----
                 const uint32_t ka = sa + (st0 + hs) * stage_off + off_k;
                 float c[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
@@ -619,89 +656,91 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                         mma_16816<false>(c[1], hi4, qf[2 * kc + 1][0], qf[2 * kc + 1][1]);
                     }
                 }
-                const bool v_lo = (mk >> g) & 1u, v_hi = (mk >> (g + 8)) & 1u;
-                float y_lo = 0.f, y_hi = 0.f, k_lo = 1.f, k_hi = 1.f;
+                const bool v_lo = kWhole || ((smask[hs] >> g) & 1u), v_hi = kWhole || ((smask[hs] >> (g + 8)) & 1u);
+                float k_lo = 1.f, k_hi = 1.f;
                 if constexpr (k8) {
                     // a masked token's scales may be anything: its V scale counts as 0
                     const float *scl = reinterpret_cast<const float *>(sp + 2 * L::kKVBytes) +
                                        (((st0 + hs) * kStageTokens + g) << p.log2_heads) + head;
                     k_lo = scl[0];
                     k_hi = scl[8 << p.log2_heads];
-                    sv[hs][0] = v_lo ? scl[L::kScaleBytes / 4] : 0.f;
-                    sv[hs][1] = v_hi ? scl[L::kScaleBytes / 4 + (8 << p.log2_heads)] : 0.f;
-                    y_lo = fast_log2(sv[hs][0]);
-                    y_hi = fast_log2(sv[hs][1]);
+                    sv[hs][0] = v_lo ? max_nan(scl[L::kScaleBytes / 4], kScaleFloor) : 0.f;
+                    sv[hs][1] = v_hi ? max_nan(scl[L::kScaleBytes / 4 + (8 << p.log2_heads)], kScaleFloor) : 0.f;
                 }
 #pragma unroll
                 for (int e = 0; e < NE; ++e) {
-                    float a = c[0][e] + c[1][e], b = c[0][2 + e] + c[1][2 + e];
-                    if constexpr (k8) {
-                        a *= k_lo * qs[e];
-                        b *= k_hi * qs[e];
-                    } else {
-                        a *= qs[e];
-                        b *= qs[e];
-                    }
+                    const float a = (c[0][e] + c[1][e]) * (k8 ? k_lo * qs[e] : qs[e]);
+                    const float b = (c[0][2 + e] + c[1][2 + e]) * (k8 ? k_hi * qs[e] : qs[e]);
                     x[hs][e] = v_lo ? a : -INFINITY;
                     x[hs][2 + e] = v_hi ? b : -INFINITY;
-                    if constexpr (k8)
-                        mx[e] = fmaxf(mx[e], fmaxf(x[hs][e] + y_lo, x[hs][2 + e] + y_hi));
-                    else
-                        mx[e] = fmaxf(mx[e], fmaxf(x[hs][e], x[hs][2 + e]));
                 }
             }
+            // Weights under the present reference: 2^(x - m) for the sum, times the V
+            // scale for the product.  The reference is raised only when a weight
+            // passes 2^8 (or there is none yet): one vote in the common case.
+            float pw[SUB][4], w4[SUB][4];
+            auto weigh = [&]() {
 #pragma unroll
-            for (int o = 4; o < 32; o <<= 1)
+                for (int hs = 0; hs < SUB; ++hs)
 #pragma unroll
-                for (int e = 0; e < NE; ++e) mx[e] = fmaxf(mx[e], __shfl_xor_sync(kFull, mx[e], o));
-            bool nd = mx[0] > m_run[0] + 8.f;
-            if constexpr (NE == 2) nd = nd || mx[1] > m_run[1] + 8.f;
+                    for (int e = 0; e < NE; ++e)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            pw[hs][2 * k + e] = fast_exp2(x[hs][2 * k + e] - mu[e]);
+                            w4[hs][2 * k + e] = k8 ? pw[hs][2 * k + e] * sv[hs][k] : pw[hs][2 * k + e];
+                        }
+            };
+            weigh();
+            bool nd = false;
+#pragma unroll
+            for (int e = 0; e < NE; ++e) {
+                nd = nd || m_run[e] == -INFINITY;
+#pragma unroll
+                for (int hs = 0; hs < SUB; ++hs) nd = nd || fmaxf(w4[hs][e], w4[hs][2 + e]) > 256.f;
+            }
             if (__any_sync(kFull, nd)) {
-                float al[2] = {1.f, 1.f};
 #pragma unroll
                 for (int e = 0; e < NE; ++e) {
-                    const float mn = fmaxf(m_run[e], mx[e]);
-                    al[e] = mn == -INFINITY ? 1.f : fast_exp2(m_run[e] - mn);
+                    // the largest exponent of a weight: max x + log2 of the V scale
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int hs = 0; hs < SUB; ++hs)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            mx = fmaxf(mx, k8 ? x[hs][2 * k + e] + fast_log2(sv[hs][k]) : x[hs][2 * k + e]);
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
+                    const float mn = fmaxf(m_run[e], mx);
+                    const float al = mn == -INFINITY ? 1.f : fast_exp2(m_run[e] - mn);
                     m_run[e] = mn;
-                    l_run[e] *= al[e];
-                }
+                    mu[e] = mn == -INFINITY ? 0.f : mn;
+                    l_run[e] *= al;
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                    for (int e = 0; e < NE; ++e) {
-                        acc[mt][e] *= al[e];
-                        acc[mt][2 + e] *= al[e];
+                    for (int mt = 0; mt < MT; ++mt) {
+                        acc[mt][e] *= al;
+                        acc[mt][2 + e] *= al;
                     }
+                }
+                weigh();
             }
-            float mu[2];
-#pragma unroll
-            for (int e = 0; e < NE; ++e) mu[e] = m_run[e] == -INFINITY ? 0.f : m_run[e];
 #pragma unroll
             for (int hs = 0; hs < SUB; ++hs) {
-                if (hs > 0 && !second) continue;
-                float w4[4];
+                if constexpr (!kWhole)
+                    if (hs > 0 && !second) continue;
 #pragma unroll
-                for (int e = 0; e < NE; ++e) {
-                    w4[e] = fast_exp2(x[hs][e] - mu[e]);
-                    w4[2 + e] = fast_exp2(x[hs][2 + e] - mu[e]);
-                    l_run[e] += w4[e] + w4[2 + e];
-                    if constexpr (k8) {
-                        w4[e] *= sv[hs][0];
-                        w4[2 + e] *= sv[hs][1];
-                    }
-                }
+                for (int e = 0; e < NE; ++e) l_run[e] += pw[hs][e] + pw[hs][2 + e];
                 // weights as the PV B fragment: tokens 2t, 2t+1, 2t+8, 2t+9 of column g
                 uint32_t bhi[2], blo[2];
                 {
                     const int srcA = 8 * t + (g >> 1), srcB = srcA + 4;
                     float w[4];
-                    w[0] = __shfl_sync(kFull, w4[0], srcA);
-                    w[1] = __shfl_sync(kFull, w4[0], srcB);
-                    w[2] = __shfl_sync(kFull, w4[2], srcA);
-                    w[3] = __shfl_sync(kFull, w4[2], srcB);
+                    w[0] = __shfl_sync(kFull, w4[hs][0], srcA);
+                    w[1] = __shfl_sync(kFull, w4[hs][0], srcB);
+                    w[2] = __shfl_sync(kFull, w4[hs][2], srcA);
+                    w[3] = __shfl_sync(kFull, w4[hs][2], srcB);
                     if constexpr (NE == 2) {
-                        const float o0 = __shfl_sync(kFull, w4[1], srcA), o1 = __shfl_sync(kFull, w4[1], srcB);
-                        const float o2 = __shfl_sync(kFull, w4[3], srcA), o3 = __shfl_sync(kFull, w4[3], srcB);
+                        const float o0 = __shfl_sync(kFull, w4[hs][1], srcA), o1 = __shfl_sync(kFull, w4[hs][1], srcB);
+                        const float o2 = __shfl_sync(kFull, w4[hs][3], srcA), o3 = __shfl_sync(kFull, w4[hs][3], srcB);
                         if (g & 1) {
                             w[0] = o0;
                             w[1] = o1;
@@ -714,12 +753,13 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                         bhi[k] = pack2<BF16>(w[2 * k], w[2 * k + 1]);
                         const float2 h = Cvt::to_float2(bhi[k]);
                         blo[k] = pack2<BF16>(w[2 * k] - h.x, w[2 * k + 1] - h.y);
+                        if (L::kPaired && g >= 4) bhi[k] = blo[k];
                     }
                 }
                 const uint32_t vbase = (st0 + hs) * stage_off + L::kKVBytes;
                 // V rows that are masked are zeroed first: stale slots may hold NaN
                 // (not so int8 codes, which a zero weight always cancels)
-                if constexpr (CT != kCacheInt8) {
+                if constexpr (!kWhole && CT != kCacheInt8) {
                     if (smask[hs] != 0xffffu) {
                         constexpr int kCh = L::kRowB / 16;                  // 16-byte chunks per box row
 #pragma unroll
@@ -742,7 +782,7 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                         uint32_t a[4];
                         ldsm_x4_trans(a, va + (ch >> 3) * half_off + (((ch & 7) ^ swz) << 4));
                         mma_16816<BF16>(acc[mt], a, bhi[0], bhi[1]);
-                        mma_16816<BF16>(acc[mt], a, blo[0], blo[1]);
+                        if constexpr (!L::kPaired) mma_16816<BF16>(acc[mt], a, blo[0], blo[1]);
                     }
                 } else {
                     // Byte pairs (dims 2g, 2g+1) of two tokens: even dims feed
@@ -755,13 +795,17 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) widen<CT, true>(a[i], ev[i], od[i]);
                         mma_16816<false>(acc[2 * vc], ev, bhi[0], bhi[1]);
-                        mma_16816<false>(acc[2 * vc], ev, blo[0], blo[1]);
+                        if constexpr (!L::kPaired) mma_16816<false>(acc[2 * vc], ev, blo[0], blo[1]);
                         mma_16816<false>(acc[2 * vc + 1], od, bhi[0], bhi[1]);
-                        mma_16816<false>(acc[2 * vc + 1], od, blo[0], blo[1]);
+                        if constexpr (!L::kPaired) mma_16816<false>(acc[2 * vc + 1], od, blo[0], blo[1]);
                     }
                 }
             }
-        }
+        };
+        if (mine >= SUB * kStageTokens && m.bad == 0)
+            attend(std::true_type{});
+        else if (mine > 0)
+            attend(std::false_type{});
         // my reads (and zeroing) of the slot are done
         fence_proxy_async_smem();
         __syncwarp();
@@ -769,6 +813,15 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
 
         if (!(m.flags & kLast)) continue;
         // ---- item end ----
+        if constexpr (L::kPaired) {   // the low parts' columns (c + 4: lane t + 2) onto the high parts'
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int e = 0; e < NE; ++e) {
+                    acc[mt][e] += __shfl_xor_sync(kFull, acc[mt][e], 2);
+                    acc[mt][2 + e] += __shfl_xor_sync(kFull, acc[mt][2 + e], 2);
+                }
+        }
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1)
 #pragma unroll
@@ -781,13 +834,18 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                     if (lane == 0) report(p.err_flag, 0x10 /* PA_FLAG_TIMEOUT */);
                     return;
                 }
-                float4 *xs = reinterpret_cast<float4 *>(xbuf + (warp - H) * L::kStateBytes);
+                float *xs = reinterpret_cast<float *>(xbuf + (warp - H) * L::kStateBytes);
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-                    xs[mt * 32 + lane] = make_float4(acc[mt][0], acc[mt][1], acc[mt][2], acc[mt][3]);
-                if (g == 0)
+                for (int e = 0; e < NE; ++e) {
+                    const int c = 2 * t + e;
+                    if (c >= C) continue;
 #pragma unroll
-                    for (int e = 0; e < NE; ++e) xml[warp * 8 + 2 * t + e] = make_float2(m_run[e], l_run[e]);
+                    for (int mt = 0; mt < MT; ++mt) {
+                        xs[c * L::kStateRow + 16 * mt + g] = acc[mt][e];
+                        xs[c * L::kStateRow + 16 * mt + 8 + g] = acc[mt][2 + e];
+                    }
+                    if (g == 0) xml[warp * 8 + c] = make_float2(m_run[e], l_run[e]);
+                }
                 __syncwarp();
                 if (lane == 0) arrive(&xfull[head]);
                 continue;
@@ -796,39 +854,30 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                 if (lane == 0) report(p.err_flag, 0x10 /* PA_FLAG_TIMEOUT */);
                 return;
             }
-            float al[2] = {1.f, 1.f};
 #pragma unroll
             for (int e = 0; e < NE; ++e) {
+                const int c = 2 * t + e;
+                if (c >= C) continue;
                 float mn = m_run[e];
-                for (int k = 1; k < nsubs; ++k) mn = fmaxf(mn, xml[(warp + k * H) * 8 + 2 * t + e].x);
-                al[e] = m_run[e] == -INFINITY ? 1.f : fast_exp2(m_run[e] - mn);
+                for (int k = 1; k < nsubs; ++k) mn = fmaxf(mn, xml[(warp + k * H) * 8 + c].x);
+                const float al = m_run[e] == -INFINITY ? 1.f : fast_exp2(m_run[e] - mn);
                 m_run[e] = mn;
-                l_run[e] *= al[e];
-            }
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int e = 0; e < NE; ++e) {
-                    acc[mt][e] *= al[e];
-                    acc[mt][2 + e] *= al[e];
-                }
-            for (int k = 1; k < nsubs; ++k) {
-                const float4 *xs = reinterpret_cast<const float4 *>(xbuf + (warp + (k - 1) * H) * L::kStateBytes);
-                float be[2] = {1.f, 1.f};
-#pragma unroll
-                for (int e = 0; e < NE; ++e) {
-                    const float2 ml = xml[(warp + k * H) * 8 + 2 * t + e];
-                    be[e] = ml.x == -INFINITY ? 1.f : fast_exp2(ml.x - m_run[e]);
-                    l_run[e] += ml.y * be[e];
-                }
+                l_run[e] *= al;
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
-                    const float4 a = xs[mt * 32 + lane];
-                    acc[mt][0] = fmaf(a.x, be[0], acc[mt][0]);
-                    acc[mt][2] = fmaf(a.z, be[0], acc[mt][2]);
-                    if constexpr (NE == 2) {
-                        acc[mt][1] = fmaf(a.y, be[1], acc[mt][1]);
-                        acc[mt][3] = fmaf(a.w, be[1], acc[mt][3]);
+                    acc[mt][e] *= al;
+                    acc[mt][2 + e] *= al;
+                }
+                for (int k = 1; k < nsubs; ++k) {
+                    const float *xs = reinterpret_cast<const float *>(xbuf + (warp + (k - 1) * H) * L::kStateBytes) +
+                                      c * L::kStateRow + g;
+                    const float2 ml = xml[(warp + k * H) * 8 + c];
+                    const float be = ml.x == -INFINITY ? 1.f : fast_exp2(ml.x - mn);
+                    l_run[e] = fmaf(ml.y, be, l_run[e]);
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        acc[mt][e] = fmaf(xs[16 * mt], be, acc[mt][e]);
+                        acc[mt][2 + e] = fmaf(xs[16 * mt + 8], be, acc[mt][2 + e]);
                     }
                 }
             }
@@ -882,32 +931,32 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
 }
 
 template <int D, int C, int CT>
-cudaError_t launch_split_t(const SplitParams &p, const CUtensorMap &tk, const CUtensorMap &tv, int grid, size_t smem,
-                           cudaStream_t stream) {
+cudaError_t launch_split_t(const SplitParams &p, const SplitMaps &m, int grid, size_t smem, cudaStream_t stream) {
     auto kern = paged_split_kernel<D, C, CT>;
     const cudaError_t e =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
-    return launch_pdl(kern, dim3(grid), dim3(SplitLayout<D, C, CT>::kThreads), smem, stream, p, tk, tv);
+    return launch_pdl(kern, dim3(grid), dim3(SplitLayout<D, C, CT>::kThreads), smem, stream, p, m.k, m.v, m.ks,
+                      m.vs);
 }
 
 template <int D, int CT>
-cudaError_t launch_split_d(const SplitParams &p, int cols, const CUtensorMap &tk, const CUtensorMap &tv, int grid,
-                           size_t smem, cudaStream_t stream) {
+cudaError_t launch_split_d(const SplitParams &p, int cols, const SplitMaps &m, int grid, size_t smem,
+                           cudaStream_t stream) {
     switch (cols) {
-        case 1: return launch_split_t<D, 1, CT>(p, tk, tv, grid, smem, stream);
-        case 2: return launch_split_t<D, 2, CT>(p, tk, tv, grid, smem, stream);
-        case 4: return launch_split_t<D, 4, CT>(p, tk, tv, grid, smem, stream);
-        case 8: return launch_split_t<D, 8, CT>(p, tk, tv, grid, smem, stream);
+        case 1: return launch_split_t<D, 1, CT>(p, m, grid, smem, stream);
+        case 2: return launch_split_t<D, 2, CT>(p, m, grid, smem, stream);
+        case 4: return launch_split_t<D, 4, CT>(p, m, grid, smem, stream);
+        case 8: return launch_split_t<D, 8, CT>(p, m, grid, smem, stream);
         default: return cudaErrorInvalidValue;
     }
 }
 
 template <int CT>
-cudaError_t launch_split_ct(const SplitParams &p, int head_dim, int cols, const CUtensorMap &tk, const CUtensorMap &tv,
-                            int grid, size_t smem, cudaStream_t stream) {
-    if (head_dim == 128) return launch_split_d<128, CT>(p, cols, tk, tv, grid, smem, stream);
-    if (head_dim == 64) return launch_split_d<64, CT>(p, cols, tk, tv, grid, smem, stream);
+cudaError_t launch_split_ct(const SplitParams &p, int head_dim, int cols, const SplitMaps &m, int grid, size_t smem,
+                            cudaStream_t stream) {
+    if (head_dim == 128) return launch_split_d<128, CT>(p, cols, m, grid, smem, stream);
+    if (head_dim == 64) return launch_split_d<64, CT>(p, cols, m, grid, smem, stream);
     return cudaErrorInvalidValue;
 }
 

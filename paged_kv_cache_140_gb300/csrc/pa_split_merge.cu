@@ -113,24 +113,26 @@ __global__ void __launch_bounds__(256)
     store_row<D>(p.out, p.out_dtype, (static_cast<int64_t>(s) * p.num_heads + hq) * D + d0, o);
 }
 
-template <int D>
-SplitSmem smem_for(int cols, int cache, int log2_heads, int entries) {
-    using L16 = SplitLayout<D, 8, kCacheF16>;
-    using L8 = SplitLayout<D, 8, kCacheInt8>;
+template <int D, int CT>
+SplitSmem smem_for(int cols, int log2_heads, int entries) {
+    using L = SplitLayout<D, 1, CT>;
     const int H = 1 << log2_heads;
     SplitSmem s;
-    s.fixed = 1024 + static_cast<size_t>(kQueryRing) * cols * D * 2 * H + (L16::kWarps - H) * L16::kStateBytes +
-              L16::kWarps * 8 * sizeof(float2) + (2 * kQueryRing + 16) * 8 + 32 * 4 +
-              static_cast<size_t>(entries) * 12 + 16;
-    s.slot = (cache >= kCacheE4M3 ? L8::kSlotBytes : L16::kSlotBytes) + sizeof(SlotMeta) + 16;
+    s.fixed = 1024 + static_cast<size_t>(kQueryRing) * cols * D * 2 * H +
+              static_cast<size_t>(L::kWarps - H) * cols * L::kStateBytes + L::kWarps * 8 * sizeof(float2) +
+              (2 * kQueryRing + 16) * 8 + 32 * 4 + static_cast<size_t>(entries) * 12 + 16;
+    s.slot = L::kSlotBytes + sizeof(SlotMeta) + 16;
     return s;
 }
 
 }  // namespace
 
 SplitSmem split_smem(int head_dim, int cols, int cache, int log2_heads, int entries) {
-    return head_dim == 128 ? smem_for<128>(cols, cache, log2_heads, entries)
-                           : smem_for<64>(cols, cache, log2_heads, entries);
+    if (cache >= kCacheE4M3)
+        return head_dim == 128 ? smem_for<128, kCacheInt8>(cols, log2_heads, entries)
+                               : smem_for<64, kCacheInt8>(cols, log2_heads, entries);
+    return head_dim == 128 ? smem_for<128, kCacheF16>(cols, log2_heads, entries)
+                           : smem_for<64, kCacheF16>(cols, log2_heads, entries);
 }
 
 int split_slot_stages(int cache, int log2_heads) {
