@@ -662,16 +662,17 @@ int split_cache(pa_dtype d) {
 // bytes for each in shared memory; longer lists take several launches.
 constexpr int kSplitEntries = 2048;
 // SMs the cuts are planned for (a constant: the workspace's size does not depend
-// on the device), and the work items a launch should have, two for each.
-constexpr int64_t kSmsTarget = 152, kSplitItems = 2 * kSmsTarget;
+// on the device), and the work items a launch should have, six for each (an SM's
+// share is uneven by up to one item).
+constexpr int64_t kSmsTarget = 152, kSplitItems = 6 * kSmsTarget;
 
 // Partition length, in tokens, for `lists` lists (entries x boxes of heads) of
-// at most `max_len` tokens; 0 when the request is invalid.  Lists that fill the
+// about `len` tokens at most; 0 when the request is invalid.  Lists that fill the
 // GPU by themselves are cut at 256 tokens (512 beyond 8 K), which bounds the
 // imbalance between SMs; fewer lists are cut finer, down to 128 tokens, so that
 // kSplitItems items exist.  Up to 256 tokens nothing is cut: a join costs a
 // launch of its own, more than reading 256 tokens does.
-int split_partition(int64_t lists, int max_len, int block_size, int slot_tokens, int requested) {
+int split_partition(int64_t lists, int64_t len, int block_size, int slot_tokens, int requested) {
     const int cap = 32 * block_size;
     if (requested != 0) {
         // a partition's block ids sit in the 32 lanes of a warp; one that does not
@@ -679,10 +680,10 @@ int split_partition(int64_t lists, int max_len, int block_size, int slot_tokens,
         if (requested < 16 || requested % 16 != 0 || requested > cap) return 0;
         return requested % block_size != 0 && requested > cap - block_size + 16 ? 0 : requested;
     }
-    if (max_len <= 256 && max_len <= cap) return static_cast<int>(std::max<int64_t>(16, round_up(max_len, 16)));
-    int64_t P = max_len <= 8192 ? 256 : 512;
-    if (lists * ((max_len + P - 1) / P) < kSplitItems) {
-        P = std::min<int64_t>(P, round_up(lists * max_len / kSplitItems + 1, slot_tokens));
+    if (len <= 256 && len <= cap) return static_cast<int>(std::max<int64_t>(16, round_up(len, 16)));
+    int64_t P = len <= 8192 ? 256 : 512;
+    if (lists * ((len + P - 1) / P) < kSplitItems) {
+        P = std::min<int64_t>(P, round_up(lists * len / kSplitItems + 1, slot_tokens));
         P = std::max<int64_t>(P, std::max(128, slot_tokens));
     }
     P = std::min<int64_t>(P, cap);
@@ -746,7 +747,10 @@ bool plan_split(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int
     w.log2_heads = pa::split_log2_heads(num_kv_heads);
     const int64_t ngroups = num_kv_heads >> w.log2_heads;
     const int slot_tokens = 16 * pa::split_slot_stages(cache, w.log2_heads);
-    w.partition = split_partition(num_seqs * ngroups, max_context_len, block_size, slot_tokens, partition_size);
+    // Private parts are about as long as the bounds differ (only the cut goes by
+    // that; a part may be longer).
+    const int64_t part_len = shared ? std::max(256, max_context_len - max_shared_len) : max_context_len;
+    w.partition = split_partition(num_seqs * ngroups, part_len, block_size, slot_tokens, partition_size);
     if (w.partition == 0) return false;
     w.parts = std::max(1, static_cast<int>((static_cast<int64_t>(max_context_len) + w.partition - 1) / w.partition));
     w.max_parts = w.parts;

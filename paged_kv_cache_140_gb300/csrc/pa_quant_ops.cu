@@ -38,6 +38,13 @@ __device__ __forceinline__ uint32_t int8x4(float a, float b, float c, float d) {
     return __byte_perm(__byte_perm(ia, ib, 0x0040u), __byte_perm(ic, id, 0x0040u), 0x5410u);
 }
 
+// One 32-byte store (dst on a 32-byte boundary).
+__device__ __forceinline__ void store32(void *dst, const uint32_t (&h)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(h[0]), "r"(h[1]), "r"(h[2]),
+                 "r"(h[3]), "r"(h[4]), "r"(h[5]), "r"(h[6]), "r"(h[7])
+                 : "memory");
+}
+
 struct QuantWrite {
     const uint16_t *src[2];      // key, value
     int64_t stride[2];           // elements between tokens
@@ -132,6 +139,7 @@ struct QuantGather {
     int hkv;
     int bs;
     int64_t num_blocks;
+    int wide_out;                // both outputs start on a 32-byte boundary
     int *err_flag;
 };
 
@@ -237,12 +245,16 @@ __global__ void __launch_bounds__(kThreads) quant_gather_kernel(const __grid_con
                     __stcs(o + k, make_float4(v[4 * k] * sc[u], v[4 * k + 1] * sc[u], v[4 * k + 2] * sc[u],
                                               v[4 * k + 3] * sc[u]));
             } else {
-                uint4 *o = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out[kv[u]]) + dst[u] * 16);
                 uint32_t h[8];
 #pragma unroll
                 for (int k = 0; k < 8; ++k) h[k] = pack2<OUT == 1>(v[2 * k] * sc[u], v[2 * k + 1] * sc[u]);
-                o[0] = make_uint4(h[0], h[1], h[2], h[3]);
-                o[1] = make_uint4(h[4], h[5], h[6], h[7]);
+                uint16_t *o = static_cast<uint16_t *>(p.out[kv[u]]) + dst[u] * 16;
+                if (p.wide_out) {
+                    store32(o, h);
+                } else {
+                    reinterpret_cast<uint4 *>(o)[0] = make_uint4(h[0], h[1], h[2], h[3]);
+                    reinterpret_cast<uint4 *>(o)[1] = make_uint4(h[4], h[5], h[6], h[7]);
+                }
             }
         }
     }
@@ -326,6 +338,7 @@ cudaError_t launch_quant_gather(void *out_k, void *out_v, int out_dtype, const v
     p.hkv = num_kv_heads;
     p.bs = block_size;
     p.num_blocks = num_blocks;
+    p.wide_out = ((reinterpret_cast<uintptr_t>(out_k) | reinterpret_cast<uintptr_t>(out_v)) & 31u) == 0;
     p.err_flag = err_flag;
     if (head_dim == 128)
         return cache == kCacheE4M3 ? gather_t<128, kCacheE4M3>(p, out_dtype, stream)

@@ -3,31 +3,35 @@
 //     M = max m_j,   out = sum_j 2^(m_j - M) acc_j / sum_j 2^(m_j - M) l_j,
 // partials in index order, in 32 bits, rounded once to the output type.
 //
-// Bound by reading the partials, most of which the previous kernel left in L2.
-// A row (sequence, query head) is joined by 1 to 8 warps, as many as fill the
-// GPU; each holds D / 32 columns per lane and has 8 partials in flight.
+// Bound by latency and by reading the partials, most of which the previous kernel
+// left in L2.  A row (sequence, query head) is joined by 1 to 8 warps, as many as
+// fill the GPU; a warp requests the states and rows of 8 partials at once, so that
+// up to 8 partials cost one trip to memory after the lengths, and carries a
+// running (M, l, acc) over further ones.
 #include "pa_split_kernel.cuh"
 
 namespace pa {
 
 namespace {
 
+constexpr int kBatch = 8;     // partials a warp loads at a time
+
 template <int D>
 __global__ void __launch_bounds__(256)
     split_merge_kernel(const __grid_constant__ SplitParams p, int prefix_part, int per_part, int wt) {
     constexpr int DPL = D / 32;
     __shared__ float red_o[8][D];
-    __shared__ float red_l[8];
+    __shared__ float2 red_ml[8];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int G = 1 << p.log2_group;
     const int64_t task = static_cast<int64_t>(blockIdx.x) * (8 / wt) + warp / wt;
     const int sub = warp % wt;
+    const bool row_ok = task < static_cast<int64_t>(p.num_seqs) * p.num_heads;
+    const int s = row_ok ? static_cast<int>(task / p.num_heads) : 0;
+    const int hq = row_ok ? static_cast<int>(task % p.num_heads) : 0;
+    const int G = 1 << p.log2_group, d0 = lane * DPL;
     pdl_wait();
-    bool active = task < static_cast<int64_t>(p.num_seqs) * p.num_heads;
-    int npre = 0, np = 0, s = 0, hq = 0;
-    if (active) {
-        s = static_cast<int>(task / p.num_heads);
-        hq = static_cast<int>(task % p.num_heads);
+    int npre = 0, np = 0;
+    if (row_ok) {
         const int ctx = context_of(p, s, false);
         int shared = 0;
         if (p.mode != kSplitDecode) {
@@ -35,75 +39,76 @@ __global__ void __launch_bounds__(256)
             npre = (shared + prefix_part - 1) / prefix_part * per_part;
         }
         np = npre + (ctx - shared + p.partition_size - 1) / p.partition_size;
-        active = np > 1 || p.mode != kSplitDecode;
     }
-    const int d0 = lane * DPL;
-    float l = 0.f, o[DPL];
+    const bool active = row_ok && (np > 1 || p.mode != kSplitDecode);
+    float M = -INFINITY, l = 0.f, o[DPL];
 #pragma unroll
     for (int i = 0; i < DPL; ++i) o[i] = 0.f;
     if (active) {
         // partial j: workspace row slot(j) * G + head of the group
         const int64_t base = (static_cast<int64_t>(s) * p.num_kv_heads + (hq >> p.log2_group)) * p.max_parts;
-        auto row = [&](int j) -> int64_t {
-            return ((base + (j < npre ? j : p.part_off + j - npre)) << p.log2_group) + (hq & (G - 1));
-        };
-        float mx = -INFINITY;
-        for (int j = lane; j < np; j += 32) mx = fmaxf(mx, __ldcg(p.ws_ml + 2 * row(j)));
-        const float M = warp_max(mx);
-        const int per = (np + wt - 1) / wt;
-        const int jb = min(np, sub * per), je = min(np, jb + per);
-        for (int j0 = jb; j0 < je; j0 += 32) {
-            float w = 0.f;
-            if (j0 + lane < je) {
-                const float2 ml = __ldcg(reinterpret_cast<const float2 *>(p.ws_ml + 2 * row(j0 + lane)));
-                // An empty partial (nothing was added; its row need not exist) is passed
-                // over; any other without a finite reference counts fully, its sum being
-                // no number.
-                if (ml.x == -INFINITY) {
-                    w = ml.y == 0.f ? -1.f : 1.f;
-                } else {
-                    w = fast_exp2(ml.x - M);
-                }
-                l = fmaf(ml.y, w, l);
-            }
-            const int cnt = min(32, je - j0);
-            for (int u0 = 0; u0 < cnt; u0 += 8) {
-                float v[8][DPL], wj[8];
+        for (int j0 = sub * kBatch; j0 < np; j0 += wt * kBatch) {
+            // states and rows are requested together; the row of an empty state
+            // (nothing was added) may be anything and is not used
+            float2 ml[kBatch];
+            float v[kBatch][DPL];
 #pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                    wj[u] = __shfl_sync(kFull, w, (u0 + u) & 31);
+            for (int u = 0; u < kBatch; ++u) {
+                ml[u] = make_float2(-INFINITY, 0.f);
+                const int j = j0 + u;
+                if (j < np) {
+                    const int64_t r = ((base + (j < npre ? j : p.part_off + j - npre)) << p.log2_group) + (hq & (G - 1));
+                    ml[u] = __ldcg(reinterpret_cast<const float2 *>(p.ws_ml) + r);
+                    const float *a = p.ws_acc + r * D + d0;
+                    if constexpr (DPL == 4) {
+                        const float4 x = __ldcg(reinterpret_cast<const float4 *>(a));
+                        v[u][0] = x.x; v[u][1] = x.y; v[u][2] = x.z; v[u][3] = x.w;
+                    } else {
+                        const float2 x = __ldcg(reinterpret_cast<const float2 *>(a));
+                        v[u][0] = x.x; v[u][1] = x.y;
+                    }
+                } else {
 #pragma unroll
                     for (int i = 0; i < DPL; ++i) v[u][i] = 0.f;
-                    if (u0 + u < cnt && wj[u] >= 0.f) {
-                        const float *a = p.ws_acc + row(j0 + u0 + u) * D + d0;
-                        if constexpr (DPL == 4) {
-                            const float4 x = __ldcg(reinterpret_cast<const float4 *>(a));
-                            v[u][0] = x.x; v[u][1] = x.y; v[u][2] = x.z; v[u][3] = x.w;
-                        } else {
-                            const float2 x = __ldcg(reinterpret_cast<const float2 *>(a));
-                            v[u][0] = x.x; v[u][1] = x.y;
-                        }
-                    }
                 }
+            }
+            float mb = M;
 #pragma unroll
-                for (int u = 0; u < 8; ++u)
+            for (int u = 0; u < kBatch; ++u) mb = fmaxf(mb, ml[u].x);
+            const float al = mb == -INFINITY ? 1.f : fast_exp2(M - mb);
+            M = mb;
+            l *= al;
 #pragma unroll
-                    for (int i = 0; i < DPL; ++i) o[i] = fmaf(v[u][i], wj[u], o[i]);
+            for (int i = 0; i < DPL; ++i) o[i] *= al;
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                if (ml[u].x == -INFINITY && ml[u].y == 0.f) continue;
+                // (a state without a finite reference whose sum is no number counts fully)
+                const float w = ml[u].x == -INFINITY ? 1.f : fast_exp2(ml[u].x - M);
+                l = fmaf(ml[u].y, w, l);
+#pragma unroll
+                for (int i = 0; i < DPL; ++i) o[i] = fmaf(v[u][i], w, o[i]);
             }
         }
-#pragma unroll
-        for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(kFull, l, x);
     }
     if (wt > 1) {
 #pragma unroll
         for (int i = 0; i < DPL; ++i) red_o[warp][d0 + i] = o[i];
-        if (lane == 0) red_l[warp] = l;
+        if (lane == 0) red_ml[warp] = make_float2(M, l);
         __syncthreads();
         if (sub != 0) return;
-        for (int k = 1; k < wt; ++k) {
+        float mb = M;
+        for (int k = 1; k < wt; ++k) mb = fmaxf(mb, red_ml[warp + k].x);
+        const float al = M == -INFINITY ? 1.f : fast_exp2(M - mb);
+        l *= al;
 #pragma unroll
-            for (int i = 0; i < DPL; ++i) o[i] += red_o[warp + k][d0 + i];
-            l += red_l[warp + k];
+        for (int i = 0; i < DPL; ++i) o[i] *= al;
+        for (int k = 1; k < wt; ++k) {
+            const float2 ml = red_ml[warp + k];
+            const float w = ml.x == -INFINITY ? 1.f : fast_exp2(ml.x - mb);
+            l = fmaf(ml.y, w, l);
+#pragma unroll
+            for (int i = 0; i < DPL; ++i) o[i] = fmaf(red_o[warp + k][d0 + i], w, o[i]);
         }
     }
     if (!active) return;
@@ -145,7 +150,7 @@ cudaError_t launch_split_merge(const SplitParams &p, int head_dim, int prefix_pa
     const int64_t rows = static_cast<int64_t>(p.num_seqs) * p.num_heads;
     // one warp per row, more while the rows leave warps idle and there is something to share out
     int wt = 1;
-    while (wt < 8 && rows * wt * 2 <= static_cast<int64_t>(sms) * 16 && p.max_parts >= 8 * wt) wt *= 2;
+    while (wt < 8 && rows * wt * 2 <= static_cast<int64_t>(sms) * 16 && p.max_parts > kBatch * wt) wt *= 2;
     const int64_t blocks = (rows + 8 / wt - 1) / (8 / wt);
     auto kern = head_dim == 128 ? split_merge_kernel<128> : split_merge_kernel<64>;
     return launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream, p, prefix_part, per_part, wt);

@@ -132,6 +132,37 @@ def test_gather(hkv, d, bs, out, fmt):
         assert torch.equal(got.cpu(), want), n    # one fp32 product, one rounding: the same bits
 
 
+def test_gather_into_rows_on_16_byte_boundaries():
+    """Outputs that start 16 bytes past a 32-byte boundary, and caches and rows of write that do."""
+    hkv, d, bs, L = 2, 64, 16, 21
+    bt, nb = Q.tables([L], bs, 3)
+    c = Q.quant_cache([L], bt, nb, bs, hkv, d, "int8", 5)
+
+    def off(t):
+        n = 16 // t.element_size()
+        wide = torch.empty(t.numel() + n, dtype=t.dtype, device="cuda")
+        wide[n:] = t.flatten().cuda()
+        return wide[n:].view(t.shape)
+    o = [off(torch.zeros(L, hkv, d).half()) for _ in range(2)]
+    pa.quant_gather(*o, off(c["k"]), off(c["v"]), off(c["ks"]), off(c["vs"]), bt.cuda(),
+                    torch.tensor([0, L], dtype=torch.int32).cuda())
+    sl = Q.slots_of(bt, 0, 0, L, bs)
+    for n, got in zip("kv", o):
+        assert torch.equal(got.cpu(), Q.quant_rows(c, n, sl, "int8").float().half())
+    key = torch.randn(L, hkv, d).half()
+    t = {n: off(x) for n, x in c.items()}
+    pa.quant_reshape_and_cache(off(key), off(key), t["k"], t["v"], t["ks"], t["vs"], sl.cuda())
+    codes, scales = Q.quantise(key, "int8")
+    assert torch.equal(t["v"].view(-1, hkv, d)[sl.cuda()].cpu(), codes)
+    assert torch.equal(t["vs"].view(-1, hkv)[sl.cuda()].cpu(), scales)
+    q = torch.randn(1, 4, d).half()
+    out = off(torch.zeros(1, 4, d).half())
+    pa.quant_decode(out, off(q), t["k"], t["v"], t["ks"], t["vs"], bt.cuda(), torch.tensor([L], dtype=torch.int32).cuda(),
+                    0.125)
+    ref = Q.attend(q[0], *[Q.values(codes, "int8") * scales.double()[..., None]] * 2, 0.125)
+    assert (out[0].cpu().double() - ref).abs().max() < 4e-3
+
+
 def test_gather_without_starts_and_many_sequences():
     hkv, d, bs = 1, 64, 16
     g = np.random.default_rng(0)
