@@ -520,7 +520,7 @@ pa_status pa_quant_decode(void *out, pa_dtype out_dtype, const void *query, pa_d
  *   max_group_size, max_shared_len : host-known upper bounds of the group sizes
  *                  and of shared_lens (<= max_context_len)
  *   scale        : >= 0
- *   workspace    : pa_decode_shared_workspace_size(...) bytes, always needed; no
+ *   workspace    : pa_decode_shared_workspace_size(...) bytes (may be 0); no
  *                  initial contents
  * Large groups run on the tensor cores as pa_prefill does (softmax weights
  * rounded to binary16, or split into two bfloat16 parts); there a block id out

@@ -330,15 +330,22 @@ def prefill(out, query, k_cache, v_cache, block_tables, context_lens, cu_seqlens
 # written this way): each looks its tensors over in one expression and explains
 # a refusal only when that fails.
 
+class _Codes(dict):
+    """pa_dtype codes by torch dtype; others are refused."""
+
+    def __missing__(self, dtype):
+        raise TypeError(f"unsupported dtype {dtype}")
+
+
 class _Runtime:
     """What the calls below need of torch and the library, looked up once."""
 
     def __init__(self):
         torch = _torch()
         self.lib = _lib.load()
-        self.half = {torch.float16: PA_F16, torch.bfloat16: PA_BF16}
-        self.out = {**self.half, torch.float32: PA_F32}
-        self.codes = {torch.int8: PA_INT8, torch.uint8: PA_FP8_E4M3, torch.float8_e4m3fn: PA_FP8_E4M3}
+        self.half = _Codes({torch.float16: PA_F16, torch.bfloat16: PA_BF16})
+        self.out = _Codes({**self.half, torch.float32: PA_F32})
+        self.codes = _Codes({torch.int8: PA_INT8, torch.uint8: PA_FP8_E4M3, torch.float8_e4m3fn: PA_FP8_E4M3})
         self.f32, self.i32, self.i64, self.u8 = torch.float32, torch.int32, torch.int64, torch.uint8
         self.current_device = torch.cuda.current_device
         self.capturing = torch.cuda.is_current_stream_capturing
@@ -365,21 +372,7 @@ def _refuse(tensors, message=None):
     raise ValueError(message or "tensors must be on the current CUDA device")
 
 
-def _code(table, t, what):
-    c = table.get(t.dtype)
-    if c is None:
-        raise TypeError(f"unsupported {what} dtype {t.dtype}")
-    return c
-
-
-def _scales_ok(rt, k_scales, v_scales, shape):
-    if k_scales.shape != shape or v_scales.shape != shape or k_scales.dtype != rt.f32 or v_scales.dtype != rt.f32:
-        raise ValueError("scales must be float32 [NB, bs, Hkv]")
-
-
 def _flag(err_flag, dev: int):
-    if err_flag is None:
-        return None
     if err_flag.get_device() != dev or err_flag.element_size() != 4:
         raise ValueError("err_flag must be an int32 tensor on the device of the others (new_err_flag)")
     return err_flag.data_ptr()
@@ -426,7 +419,9 @@ def quant_reshape_and_cache(key, value, k_cache, v_cache, k_scales, v_scales, sl
     if len(cache) != 4 or v_cache.shape != cache or v_cache.dtype != k_cache.dtype or cache[2] != hkv or cache[3] != d:
         raise ValueError("caches must be [NB, bs, Hkv, D] of one dtype, with the rows' heads")
     nb, bs = cache[0], cache[1]
-    _scales_ok(rt, k_scales, v_scales, (nb, bs, hkv))
+    rows = (nb, bs, hkv)
+    if k_scales.shape != rows or v_scales.shape != rows or k_scales.dtype != rt.f32 or v_scales.dtype != rt.f32:
+        raise ValueError("scales must be float32 [NB, bs, Hkv]")
     if slot_mapping.dtype != rt.i64 or slot_mapping.numel() != T:
         raise ValueError("slot_mapping must be int64 [T]")
     ks, vs = key.stride(), value.stride()
@@ -436,8 +431,8 @@ def quant_reshape_and_cache(key, value, k_cache, v_cache, k_scales, v_scales, sl
     st = rt.lib.pa_quant_reshape_and_cache(
         key.data_ptr(), value.data_ptr(), hkv * d if one else ks[0], hkv * d if one else vs[0], k_cache.data_ptr(),
         v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), slot_mapping.data_ptr(), T, nb, bs, hkv,
-        d, _code(rt.half, key, "row"), _code(rt.codes, k_cache, "cache"),
-        _flag(err_flag, dev), rt.stream(dev))
+        d, rt.half[key.dtype], rt.codes[k_cache.dtype],
+        None if err_flag is None else _flag(err_flag, dev), rt.stream(dev))
     if st:
         _lib.check(st, "pa_quant_reshape_and_cache")
 
@@ -461,7 +456,9 @@ def quant_gather(out_k, out_v, k_cache, v_cache, k_scales, v_scales, block_table
     if len(cache) != 4 or v_cache.shape != cache or v_cache.dtype != k_cache.dtype:
         raise ValueError("caches must be [NB, bs, Hkv, D] of one dtype")
     nb, bs, hkv, d = cache
-    _scales_ok(rt, k_scales, v_scales, (nb, bs, hkv))
+    rows = (nb, bs, hkv)
+    if k_scales.shape != rows or v_scales.shape != rows or k_scales.dtype != rt.f32 or v_scales.dtype != rt.f32:
+        raise ValueError("scales must be float32 [NB, bs, Hkv]")
     if len(shape) != 3 or out_v.shape != shape or out_v.dtype != out_k.dtype or shape[1] != hkv or shape[2] != d:
         raise ValueError("out_k/out_v must be [T, Hkv, D] of one dtype")
     if len(table) != 2 or block_tables.dtype != rt.i32:
@@ -475,10 +472,10 @@ def quant_gather(out_k, out_v, k_cache, v_cache, k_scales, v_scales, block_table
         if seq_starts.dtype != rt.i32 or seq_starts.numel() != B:
             raise ValueError("seq_starts must be int32 [B]")
     st = rt.lib.pa_quant_gather(
-        out_k.data_ptr(), out_v.data_ptr(), _code(rt.out, out_k, "output"), k_cache.data_ptr(), v_cache.data_ptr(),
-        _code(rt.codes, k_cache, "cache"), k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(), table[1],
+        out_k.data_ptr(), out_v.data_ptr(), rt.out[out_k.dtype], k_cache.data_ptr(), v_cache.data_ptr(),
+        rt.codes[k_cache.dtype], k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(), table[1],
         cu_seqlens.data_ptr(), None if seq_starts is None else seq_starts.data_ptr(), B, shape[0], hkv, d, bs,
-        nb, _flag(err_flag, dev), rt.stream(dev))
+        nb, None if err_flag is None else _flag(err_flag, dev), rt.stream(dev))
     if st:
         _lib.check(st, "pa_quant_gather")
 
@@ -523,7 +520,9 @@ def quant_decode(out, query, k_cache, v_cache, k_scales, v_scales, block_tables,
         raise ValueError("K and V caches must share a dtype")
     B, Hq, D = query.shape
     nb, bs, hkv, _ = cache
-    _scales_ok(rt, k_scales, v_scales, (nb, bs, hkv))
+    rows = (nb, bs, hkv)
+    if k_scales.shape != rows or v_scales.shape != rows or k_scales.dtype != rt.f32 or v_scales.dtype != rt.f32:
+        raise ValueError("scales must be float32 [NB, bs, Hkv]")
     maxnb = block_tables.shape[1]
     if max_context_len is None:
         max_context_len = maxnb * bs
@@ -531,11 +530,11 @@ def quant_decode(out, query, k_cache, v_cache, k_scales, v_scales, block_tables,
     buf = _scratch(rt, workspace, quant_decode_workspace_size(B, Hq, hkv, D, bs, max_context_len, partition_size), dev,
                    stream)
     st = rt.lib.pa_quant_decode(
-        out.data_ptr(), _code(rt.out, out, "output"), query.data_ptr(), _code(rt.half, query, "query"),
-        k_cache.data_ptr(), v_cache.data_ptr(), _code(rt.codes, k_cache, "cache"), k_scales.data_ptr(),
+        out.data_ptr(), rt.out[out.dtype], query.data_ptr(), rt.half[query.dtype],
+        k_cache.data_ptr(), v_cache.data_ptr(), rt.codes[k_cache.dtype], k_scales.data_ptr(),
         v_scales.data_ptr(), block_tables.data_ptr(), maxnb, context_lens.data_ptr(), max_context_len, B, Hq, hkv, D, bs,
         nb, scale, partition_size, None if buf is None else buf.data_ptr(), 0 if buf is None else buf.nbytes,
-        _flag(err_flag, dev), stream)
+        None if err_flag is None else _flag(err_flag, dev), stream)
     if st:
         _lib.check(st, "pa_quant_decode")
 
@@ -594,11 +593,11 @@ def decode_shared(out, query, k_cache, v_cache, block_tables, context_lens, cu_g
     buf = _scratch(rt, workspace, decode_shared_workspace_size(B, ng, max_group_size, Hq, hkv, D, bs, max_context_len,
                                                                max_shared_len, partition_size), dev, stream)
     st = rt.lib.pa_decode_shared(
-        out.data_ptr(), _code(rt.out, out, "output"), query.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-        _code(rt.half, query, "query"), block_tables.data_ptr(), maxnb, context_lens.data_ptr(), max_context_len,
+        out.data_ptr(), rt.out[out.dtype], query.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        rt.half[query.dtype], block_tables.data_ptr(), maxnb, context_lens.data_ptr(), max_context_len,
         cu_groups.data_ptr(), ng, max_group_size, shared_lens.data_ptr(), max_shared_len, B, Hq, hkv, D, bs, nb, scale,
         partition_size, None if buf is None else buf.data_ptr(), 0 if buf is None else buf.nbytes,
-        _flag(err_flag, dev), stream)
+        None if err_flag is None else _flag(err_flag, dev), stream)
     if st:
         _lib.check(st, "pa_decode_shared")
 

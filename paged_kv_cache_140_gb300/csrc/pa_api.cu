@@ -669,9 +669,9 @@ constexpr int64_t kSmsTarget = 152, kSplitItems = 6 * kSmsTarget;
 // Partition length, in tokens, for `lists` lists (entries x boxes of heads) of
 // about `len` tokens at most; 0 when the request is invalid.  Lists that fill the
 // GPU by themselves are cut at 256 tokens (512 beyond 8 K), which bounds the
-// imbalance between SMs; fewer lists are cut finer, down to 128 tokens, so that
-// kSplitItems items exist.  Up to 256 tokens nothing is cut: a join costs a
-// launch of its own, more than reading 256 tokens does.
+// imbalance between SMs; fewer lists are cut finer, down to 4 ring slots, so that
+// kSplitItems items exist.  Lists of up to 6 slots are not cut: reading a slot
+// takes an SM about a microsecond, joining partials a launch of its own.
 int split_partition(int64_t lists, int64_t len, int block_size, int slot_tokens, int requested) {
     const int cap = 32 * block_size;
     if (requested != 0) {
@@ -680,12 +680,13 @@ int split_partition(int64_t lists, int64_t len, int block_size, int slot_tokens,
         if (requested < 16 || requested % 16 != 0 || requested > cap) return 0;
         return requested % block_size != 0 && requested > cap - block_size + 16 ? 0 : requested;
     }
-    if (len <= 256 && len <= cap) return static_cast<int>(std::max<int64_t>(16, round_up(len, 16)));
     int64_t P = len <= 8192 ? 256 : 512;
     if (lists * ((len + P - 1) / P) < kSplitItems) {
         P = std::min<int64_t>(P, round_up(lists * len / kSplitItems + 1, slot_tokens));
-        P = std::max<int64_t>(P, std::max(128, slot_tokens));
+        P = std::max<int64_t>(P, 4 * slot_tokens);
     }
+    if (len <= std::min<int64_t>(cap, std::max<int64_t>(P, 6 * slot_tokens)))
+        return static_cast<int>(std::max<int64_t>(16, round_up(len, 16)));   // one partition
     P = std::min<int64_t>(P, cap);
     if (P > slot_tokens) P -= P % slot_tokens;   // whole ring slots
     return static_cast<int>(P);
@@ -717,10 +718,16 @@ int shared_unit(int64_t lists, int tokens, bool two_tiles) {
     return best * pa::kSharedTile;
 }
 
+// A batch whose shared prefixes, read again for every sequence, cost at most this
+// many more bytes of K/V is decoded in one pass that does read them again: it
+// takes one launch in place of three, and the second reads come from L2.
+constexpr int64_t kSharedWholeBytes = 8 << 20;
+
 struct SplitPlan {
     int log2_heads = 0, G = 1;
     int partition = 0;           // decode and suffix entries
     int parts = 1;               // their partials per row
+    bool whole = false;          // shared prefixes are not worth a pass of their own
     bool prefix_tc = false;      // shared prefixes: on the tensor-core kernel (else the split kernel)
     int prefix_cols = 0;         // split kernel: query rows per entry
     int prefix_pairs = 0;        // tensor-core kernel: pairs of query tiles per group
@@ -747,15 +754,20 @@ bool plan_split(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int
     w.log2_heads = pa::split_log2_heads(num_kv_heads);
     const int64_t ngroups = num_kv_heads >> w.log2_heads;
     const int slot_tokens = 16 * pa::split_slot_stages(cache, w.log2_heads);
+    if (shared) {
+        if (num_groups < 0 || max_group_size < 0 || max_shared_len < 0 || max_shared_len > max_context_len) return false;
+        const int shared_tokens = max_shared_len / block_size * block_size;
+        w.whole = static_cast<double>(std::max(0, num_seqs - num_groups)) * shared_tokens * num_kv_heads * head_dim * 4 <=
+                  kSharedWholeBytes;
+    }
     // Private parts are about as long as the bounds differ (only the cut goes by
     // that; a part may be longer).
-    const int64_t part_len = shared ? std::max(256, max_context_len - max_shared_len) : max_context_len;
+    const int64_t part_len = shared && !w.whole ? std::max(256, max_context_len - max_shared_len) : max_context_len;
     w.partition = split_partition(num_seqs * ngroups, part_len, block_size, slot_tokens, partition_size);
     if (w.partition == 0) return false;
     w.parts = std::max(1, static_cast<int>((static_cast<int64_t>(max_context_len) + w.partition - 1) / w.partition));
     w.max_parts = w.parts;
-    if (shared) {
-        if (num_groups < 0 || max_group_size < 0 || max_shared_len < 0 || max_shared_len > max_context_len) return false;
+    if (shared && !w.whole) {
         const int shared_tokens = max_shared_len / block_size * block_size;
         const int64_t rows = static_cast<int64_t>(max_group_size) * w.G;
         w.prefix_tc = rows > kSharedSplitRows && block_size <= pa::kSharedTile && (block_size & (block_size - 1)) == 0;
@@ -774,7 +786,7 @@ bool plan_split(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int
         w.prefix_parts = (shared_tokens + w.prefix_part - 1) / w.prefix_part * w.prefix_per;
         w.max_parts += w.prefix_parts;
     }
-    if (!shared && w.max_parts <= 1) return true;
+    if ((!shared || w.whole) && w.max_parts <= 1) return true;
     const int64_t rows = static_cast<int64_t>(num_seqs) * num_heads * w.max_parts;
     w.acc_off = static_cast<size_t>(round_up(rows * 2 * 4, 256));
     w.bytes = w.acc_off + static_cast<size_t>(rows) * head_dim * 4;
@@ -1036,7 +1048,8 @@ PA_EXPORT pa_status pa_decode_shared(void *out, pa_dtype out_dtype, const void *
     if (!out || !query || !k_cache || !v_cache || !block_tables || !context_lens || !cu_groups || !shared_lens)
         return PA_ERR_INVALID_ARG;
     if (!aligned16(out) || !aligned16(query) || !aligned16(k_cache) || !aligned16(v_cache)) return PA_ERR_INVALID_ARG;
-    if (workspace == nullptr || workspace_bytes < w.bytes || !aligned16(workspace)) return PA_ERR_WORKSPACE;
+    if (w.bytes > 0 && (workspace == nullptr || workspace_bytes < w.bytes || !aligned16(workspace)))
+        return PA_ERR_WORKSPACE;
     DeviceInfo dev;
     if (!device_info(dev)) return PA_ERR_CUDA;
     pa::SplitMaps maps{};
@@ -1052,6 +1065,12 @@ PA_EXPORT pa_status pa_decode_shared(void *out, pa_dtype out_dtype, const void *
     p.max_group_size = max_group_size;
     p.max_shared_len = max_shared_len;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (w.whole) {
+        p.mode = pa::kSplitWhole;
+        const pa_status r = run_split(p, cache, head_dim, w.G, num_seqs, max_context_len, maps, dev, s);
+        if (r != PA_OK || w.max_parts <= 1) return r;
+        return pa::launch_split_merge(p, head_dim, 1, 1, dev.sms, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+    }
     if (w.prefix_parts > 0 && w.prefix_tc) {
         if (pa::shared_prefix_smem(head_dim) + 1024 > static_cast<size_t>(dev.smem_optin)) return PA_ERR_UNSUPPORTED;
         const int ranges = w.prefix_parts / w.prefix_per, tile_seqs = pa::kSharedTile / w.G;

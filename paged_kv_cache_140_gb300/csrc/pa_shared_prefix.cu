@@ -4,7 +4,7 @@
 // For group g, KV head h and the n G query rows of its n sequences (G query
 // heads each), over the group's L shared tokens (whole blocks, reached through
 // its first member's block table):
-//     s_rp = scale log2(e) <q_r, K_p>,  m_r ~ max_p s_rp,
+//     s_rp = scale log2(e) <q_r, K_p>,  m_r ~ max_p s_rp - 7,
 //     l_r = sum_p 2^(s_rp - m_r),  acc_r = sum_p 2^(s_rp - m_r) V_p,
 // written as partial results that pa_split_merge.cu joins with those of the
 // sequences' private parts.  There is no causal mask: every row sees every
@@ -221,8 +221,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
     pdl_launch_dependents();
     const int q0 = __ldg(p.cu_groups + g), q1 = __ldg(p.cu_groups + g + 1);
     const bool first = pi == 0 && kvh == 0 && range == 0;
-    if (q0 < 0 || q1 < q0 || q1 > p.num_seqs || q1 - q0 > p.max_group_size || (g == 0 && q0 != 0) ||
-        (g == p.num_groups - 1 && q1 != p.num_seqs)) {
+    if (bad_group(p, g, q0, q1)) {
         if (first && threadIdx.x == 0) report(p.err_flag, PA_FLAG_BAD_CONTEXT_LEN);
         return;
     }
@@ -457,10 +456,14 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
                     a[k] = max3(a[k], __uint_as_float(v[16 * i + k]), __uint_as_float(v[16 * i + 8 + k]));
             const float mx = max3(max3(a[0], a[1], a[2]), max3(a[3], a[4], a[5]), fmaxf(a[6], a[7]));
             const float x_tile = mx * sl;
-            const bool need = x_tile > m_run + 8.f;
+            // The reference is 2^7 below the maximum it was set by and moves when that
+            // grows by more than 2^8: binary16 weights reach 2^15 and end at 2^-24,
+            // 2^-31 of the largest.
+            const bool need = x_tile > m_run + (kWeightExp + 8.f);
             if (__any_sync(kFull, need)) {
                 // O already holds tile j-1: its product preceded this tile's QK in issue order
-                const float f = need ? fast_exp2(m_run - x_tile) : 1.f;
+                const float m_new = x_tile - kWeightExp;
+                const float f = need ? fast_exp2(m_run - m_new) : 1.f;
                 if (j > 0) {
                     const uint64_t f2x = f2(f, f);
 #pragma unroll
@@ -480,7 +483,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
                 }
                 if (need) {
                     l_run *= f;
-                    m_run = x_tile;
+                    m_run = m_new;
                 }
             }
             // weights 2^(s - m) as 16-bit pairs over their own S columns

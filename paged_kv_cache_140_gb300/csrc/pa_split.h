@@ -18,6 +18,7 @@ constexpr int kCacheF16 = 0, kCacheBF16 = 1, kCacheE4M3 = 2, kCacheInt8 = 3;
 constexpr int kSplitDecode = 0;   // sequences, whole contexts; results final where one partition holds them
 constexpr int kSplitSuffix = 1;   // sequences past their shared blocks; partial results only
 constexpr int kSplitPrefix = 2;   // (group, chunk of its sequences) over the group's shared blocks; partial only
+constexpr int kSplitWhole = 3;    // as kSplitDecode, the shared blocks read through the group's first sequence
 
 struct SplitParams {
     void *out;
@@ -44,8 +45,8 @@ struct SplitParams {
     const float *v_scales;
     int *err_flag;
     int mode;
-    const int32_t *shared_lens;  // suffix, prefix: [num_seqs] tokens a sequence shares with its group
-    const int32_t *cu_groups;    // prefix: [num_groups + 1]
+    const int32_t *shared_lens;  // suffix, prefix, whole: [num_seqs] tokens a sequence shares with its group
+    const int32_t *cu_groups;    // prefix, whole: [num_groups + 1]
     int num_groups;
     int chunks, chunk_seqs;      // prefix: a group's sequences are taken chunk_seqs at a time
     int max_group_size;

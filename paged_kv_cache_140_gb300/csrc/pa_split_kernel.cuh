@@ -13,12 +13,12 @@
 // serves the sum and the V product: with s_p = log2(e) x_p,
 //     l = sum 2^(s_p - m),   acc = sum (2^(s_p - m) v_p) cV_p.
 // m follows the maximum of s_p + log2 v_p, the exponent of the weights that
-// enter the V product, so that the weights 2^(s_p - m) v_p stay at most 2^8 (m
-// moves only when exceeded by more than that) and the largest near 1 whatever
-// the scales are: they go into the product as binary16 high and low parts
-// (~22 bits), accurate relative to the largest.  2^(s_p - m) itself is then off
-// by up to 1 / v_p, which 32 bits hold for every scale the cache write makes
-// from rows below 2^60.
+// enter the V product, less 7: the largest weight 2^(s_p - m) v_p lies between
+// 2^7 and 2^15 (m is raised only when one passes 2^15) whatever the scales are.
+// They go into the product as binary16 high and low parts, ~22 bits down to
+// 2^-24, that is 2^-31 of the largest, so that even 2^15 tokens of the least
+// weight lose no more than 2^-16.  2^(s_p - m) itself is then off by up to 1 / v_p,
+// which 32 bits hold for every scale the cache write makes from rows below 2^60.
 //
 // 8-bit codes are exact in binary16 and the products run there; the query is
 // scaled per row by a power of two to a largest element in [1, 2) (undone on
@@ -119,6 +119,10 @@ __device__ __forceinline__ float fast_log2(float x) {
     return y;
 }
 
+// The largest weight is raised to this exponent, and the reference moved when
+// one passes kWeightMax (below binary16's 65504).
+constexpr float kWeightExp = 7.f, kWeightMax = 32768.f;
+
 // Maximum that keeps a NaN.
 __device__ __forceinline__ float max_nan(float a, float b) {
     float d;
@@ -126,7 +130,7 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return d;
 }
 // V scales below this count as this (the cache write makes none below 2^-69),
-// which bounds 2^(s_p - m) to 2^78.
+// which bounds 2^(s_p - m) to 2^85.
 constexpr float kScaleFloor = 8.470329472543003e-22f;   // 2^-70
 
 // Four codes (bytes 0-3) as two f16 pairs.  Natural order: (0, 1), (2, 3);
@@ -165,9 +169,16 @@ __device__ __forceinline__ int context_of(const SplitParams &p, int s, bool tell
     return c;
 }
 
+// Group bounds that break the rules: from 0, never falling, the last num_seqs,
+// groups of at most max_group_size.
+__device__ __forceinline__ bool bad_group(const SplitParams &p, int g, int q0, int q1) {
+    return q0 < 0 || q1 < q0 || q1 > p.num_seqs || q1 - q0 > p.max_group_size || (g == 0 && q0 != 0) ||
+           (g == p.num_groups - 1 && q1 != p.num_seqs);
+}
+
 // Items (entry, partition, box of heads) in that order, weighed in slots.  An
-// entry without tokens weighs nothing, except in decode mode, where it costs
-// the slot that writes its zero row.
+// entry without tokens weighs nothing, except where it costs the slot that writes
+// its zero row.
 struct ItemCursor {
     int e, len, nparts, part, grp, nslots;
     uint32_t start;
@@ -179,8 +190,11 @@ __device__ __forceinline__ int item_slots(int len, int part, int P, int SW) {
     return (st + SW - 1) / SW;
 }
 
+// Modes in which a list of one partition is the whole result.
+__device__ __forceinline__ bool final_mode(int mode) { return mode == kSplitDecode || mode == kSplitWhole; }
+
 __device__ __forceinline__ uint32_t entry_weight(int len, int mode, int ngroups, int P, int SW) {
-    if (len <= 0) return mode == kSplitDecode ? static_cast<uint32_t>(ngroups) : 0u;
+    if (len <= 0) return final_mode(mode) ? static_cast<uint32_t>(ngroups) : 0u;
     const int full = (len - 1) / P;   // partitions before the last
     return static_cast<uint32_t>(ngroups) *
            static_cast<uint32_t>(full * ((P / kStageTokens + SW - 1) / SW) + item_slots(len, full, P, SW));
@@ -224,7 +238,8 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
     uint64_t *xfree = xfull + 8;                       //           and have been read
     uint32_t *warp_tot = reinterpret_cast<uint32_t *>(xfree + 8);
     int *len_s = reinterpret_cast<int *>(warp_tot + 32);
-    int *aux_s = len_s + E;                            // suffix: first block; prefix: sequence | members << 27
+    int *aux_s = len_s + E;                            // suffix: first block; prefix: sequence | members << 27;
+                                                       // whole: the group's first sequence
     uint32_t *prefix = reinterpret_cast<uint32_t *>(aux_s + E);
     // Scales of 4 or 8 heads are 16 or 32 bytes per token: boxes.  Fewer are below
     // a box's least width: 4-byte copies by all lanes of the producer.
@@ -259,8 +274,7 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
         if (mode == kSplitPrefix) {
             const int g = (p.e0 + i) / p.chunks, ck = (p.e0 + i) % p.chunks;
             const int q0 = __ldg(p.cu_groups + g), q1 = __ldg(p.cu_groups + g + 1);
-            if (q0 < 0 || q1 < q0 || q1 > p.num_seqs || q1 - q0 > p.max_group_size || (g == 0 && q0 != 0) ||
-                (g == p.num_groups - 1 && q1 != p.num_seqs)) {
+            if (bad_group(p, g, q0, q1)) {
                 if (tell) report(p.err_flag, 0x4 /* PA_FLAG_BAD_CONTEXT_LEN */);
             } else {
                 const int s0 = q0 + ck * p.chunk_seqs, m = min(p.chunk_seqs, q1 - s0);
@@ -273,10 +287,23 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                 }
             }
         } else {
-            len = context_of(p, p.e0 + i, tell);
+            const int s = p.e0 + i;
+            len = context_of(p, s, tell);
             if (mode == kSplitSuffix) {
-                aux = shared_blocks(p, p.e0 + i, len, tell);
+                aux = shared_blocks(p, s, len, tell);
                 len -= aux * bs;
+            } else if (mode == kSplitWhole) {
+                int a = 0, b = p.num_groups;             // the last group that starts at or before s
+                while (b - a > 1) {
+                    const int m = (a + b) >> 1;
+                    if (__ldg(p.cu_groups + m) <= s) a = m; else b = m;
+                }
+                const int q0 = __ldg(p.cu_groups + a), q1 = __ldg(p.cu_groups + a + 1);
+                const bool bad = bad_group(p, a, q0, q1) || q0 > s || q1 <= s;
+                aux = bad ? s : q0;
+                if (tell && (bad || __ldg(p.shared_lens + s) != __ldg(p.shared_lens + aux)))
+                    report(p.err_flag, 0x4 /* PA_FLAG_BAD_CONTEXT_LEN */);
+                shared_blocks(p, s, len, tell);
             }
         }
         len_s[i] = len;
@@ -395,6 +422,7 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
             // the partition's block ids, one per lane
             const int fb = t0 / bs;
             int32_t bid = -1;
+            if (mode == kSplitWhole && fb + lane < shared_blocks(p, seq, ic.len, false)) row = aux_s[ic.e];
             if (ntok > 0 && lane <= (t0 + ntok - 1) / bs - fb)
                 bid = __ldg(p.block_tables + static_cast<int64_t>(row) * p.max_blocks_per_seq + blk0 + fb + lane);
             {
@@ -418,7 +446,7 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                 ++items;
                 __syncwarp();
             }
-            const int fin = mode == kSplitDecode && ic.nparts == 1 ? kFinal : 0;
+            const int fin = final_mode(mode) && ic.nparts == 1 ? kFinal : 0;
             for (int j = 0; j < ic.nslots; ++j) {
                 const int slot = take_slot();
                 if (!ok) break;
@@ -677,7 +705,7 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
             }
             // Weights under the present reference: 2^(x - m) for the sum, times the V
             // scale for the product.  The reference is raised only when a weight
-            // passes 2^8 (or there is none yet): one vote in the common case.
+            // passes 2^15 (or there is none yet): one vote in the common case.
             float pw[SUB][4], w4[SUB][4];
             auto weigh = [&]() {
 #pragma unroll
@@ -696,7 +724,7 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
             for (int e = 0; e < NE; ++e) {
                 nd = nd || m_run[e] == -INFINITY;
 #pragma unroll
-                for (int hs = 0; hs < SUB; ++hs) nd = nd || fmaxf(w4[hs][e], w4[hs][2 + e]) > 256.f;
+                for (int hs = 0; hs < SUB; ++hs) nd = nd || fmaxf(w4[hs][e], w4[hs][2 + e]) > kWeightMax;
             }
             if (__any_sync(kFull, nd)) {
 #pragma unroll
@@ -710,7 +738,7 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                             mx = fmaxf(mx, k8 ? x[hs][2 * k + e] + fast_log2(sv[hs][k]) : x[hs][2 * k + e]);
 #pragma unroll
                     for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
-                    const float mn = fmaxf(m_run[e], mx);
+                    const float mn = fmaxf(m_run[e], mx - kWeightExp);
                     const float al = mn == -INFINITY ? 1.f : fast_exp2(m_run[e] - mn);
                     m_run[e] = mn;
                     mu[e] = mn == -INFINITY ? 0.f : mn;

@@ -34,13 +34,13 @@ __global__ void __launch_bounds__(256)
     if (row_ok) {
         const int ctx = context_of(p, s, false);
         int shared = 0;
-        if (p.mode != kSplitDecode) {
+        if (!final_mode(p.mode)) {
             shared = shared_blocks(p, s, ctx, false) * p.block_size;
             npre = (shared + prefix_part - 1) / prefix_part * per_part;
         }
         np = npre + (ctx - shared + p.partition_size - 1) / p.partition_size;
     }
-    const bool active = row_ok && (np > 1 || p.mode != kSplitDecode);
+    const bool active = row_ok && (np > 1 || !final_mode(p.mode));
     float M = -INFINITY, l = 0.f, o[DPL];
 #pragma unroll
     for (int i = 0; i < DPL; ++i) o[i] = 0.f;

@@ -313,6 +313,31 @@ def test_decode_rising_keys_and_zero_rows():
     assert torch.all(run_decode(c, q, bt, lens) == 0)
 
 
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_decode_many_tokens_of_little_weight_count(fmt):
+    """One token of weight 1 and 20,000 of 2^-24.6 each: their share, 2^-10.3, must not be rounded away."""
+    L, hkv, d, bs = 20001, 8, 64, 32
+    bt, nb = Q.tables([L], bs, 1)
+    c = Q.quant_cache([1], bt, nb, bs, hkv, d, fmt, 1)
+    q = torch.zeros(1, hkv, d).half()
+    q[..., 0] = 1.0
+    scale = 1.0
+    k = torch.zeros(L, hkv, d)
+    k[0, :, 0] = 17.05 / 2          # the others: -17.05 / 2, so e^-17.05 = 2^-24.6 of the first's weight
+    k[1:, :, 0] = -17.05 / 2
+    v = torch.ones(L, hkv, d)
+    v[0] = 0.0
+    for n, x in (("k", k), ("v", v)):
+        codes, sc = Q.quantise(x.half(), fmt)
+        sl = Q.slots_of(bt, 0, 0, L, bs)
+        c[n].view(-1, hkv, d)[sl] = codes
+        c[n + "s"].view(-1, hkv)[sl] = sc
+    got = run_decode(c, q, bt, [L], scale=scale)[0].cpu().double()
+    sl = Q.slots_of(bt, 0, 0, L, bs)
+    ref = Q.attend(q[0], Q.quant_rows(c, "k", sl, fmt), Q.quant_rows(c, "v", sl, fmt), scale)
+    assert 5e-4 < ref.min() and ((got - ref).abs() / ref).max() < 1e-3
+
+
 def test_decode_poisoned_row_reaches_its_sequence_and_head_only():
     lens, hkv, d, bs = [100, 300, 100], 8, 64, 16
     bt, nb = Q.tables(lens, bs, 1)

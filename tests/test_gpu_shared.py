@@ -162,6 +162,25 @@ def test_a_scale_of_zero_averages(n):
     check(b)
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_many_tokens_of_little_weight_count(dtype):
+    """As for one token of weight 1 in a prefix of 20,000 others of 2^-24.6 each."""
+    n, hkv, d, L = 20, 1, 64, 20000
+    b = make([n], [L], [1] * n, 1, hkv, d, 16, dtype, seed=13)
+    used = torch.cat([Q.slots_of(b["bt"], s, 0, L + 1, 16) for s in range(n)])
+    kf, vf = b["k"].view(-1, hkv, d), b["v"].view(-1, hkv, d)
+    kf[used], vf[used] = 0.0, 1.0
+    kf[used, :, 0] = -8.5
+    first = Q.slots_of(b["bt"], 0, 0, 1, 16)
+    kf[first, :, 0], vf[first] = 8.5, 0.0
+    b["q"][:] = 0.0
+    b["q"][..., 0] = 1.0
+    b["scale"] = 1.0
+    got = run(b)[:, 0, 0].cpu().double()
+    share = (L * np.exp(-17.0)) / (1 + L * np.exp(-17.0))
+    assert (got - share).abs().max() < 1e-3 * share
+
+
 def test_loose_bounds_and_partition_sizes_agree():
     b = make([3, 20, 1], [300, 513, 40], [9] * 24, 8, 4, 64, 16, "f16", seed=6)
     a = check(b)
@@ -181,9 +200,10 @@ def test_matches_decode_on_the_same_tables():
     assert torch.equal(run(b), got)          # the same bits again
 
 
-def test_members_tables_may_name_other_blocks_for_the_prefix():
+@pytest.mark.parametrize("n,hq,hkv", [(5, 4, 4), (12, 32, 32), (60, 4, 4)])
+def test_members_tables_may_name_other_blocks_for_the_prefix(n, hq, hkv):
     """Only the first member's table is read for the whole prefix blocks."""
-    b = make([5], [256], [10] * 5, 4, 4, 64, 16, "f16", seed=8)
+    b = make([n], [256], [10] * n, hq, hkv, 64, 16, "f16", seed=8)
     a = run(b)
     b["bt"][1:, :16] = -9
     assert torch.equal(run(b), a)
@@ -281,11 +301,13 @@ def test_refusals():
     for name, bad in [("cu_groups", t["cu_groups"].long()), ("cu_groups", t["cu_groups"].cpu()),
                       ("shared_lens", t["shared_lens"][:1]), ("query", t["query"].bfloat16()),
                       ("k_cache", t["k_cache"][:, :, :, :32].contiguous()), ("context_lens", t["context_lens"].float()),
-                      ("max_shared_len", 4096), ("partition_size", 8),
-                      ("workspace", torch.empty(4, dtype=torch.uint8))]:
+                      ("max_shared_len", 4096), ("partition_size", 8), ("err_flag", torch.zeros(1, dtype=torch.int32))]:
         with pytest.raises((ValueError, TypeError)):
             pa.decode_shared(**{**t, name: bad})
     with pytest.raises(pa.PagedAttentionError):          # two sequences in one group of at most one
         pa.decode_shared(**t, max_group_size=1)
+    wide = {**t, "block_tables": b["bt"].repeat(1, 300).cuda()}      # bounds under which the call needs a workspace
+    with pytest.raises(ValueError):
+        pa.decode_shared(**wide, workspace=torch.empty(1 << 28, dtype=torch.uint8))
     with pytest.raises(pa.PagedAttentionError):
-        pa.decode_shared(**t, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+        pa.decode_shared(**wide, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))

@@ -84,7 +84,9 @@ def test_shared_refusals(lib):
 
 def test_planning(lib):
     ws = lib.pa_quant_decode_workspace_size
-    assert ws(4, 4, 4, 64, 16, 256, 0) == 0                  # nothing is cut up to 256 tokens
+    assert ws(4, 4, 4, 64, 16, 256, 0) == 0                  # a few ring slots are not cut
+    assert ws(256, 40, 40, 128, 16, 256, 0) == 0             # nor are lists that fill the GPU
+    assert ws(4, 8, 8, 128, 16, 256, 0) > 0
     assert ws(256, 40, 40, 128, 16, 2048, 0) >= 256 * 40 * 8 * 130 * 4
     # few sequences: finer partitions, more partials per row
     assert ws(1, 8, 8, 128, 16, 8192, 0) >= 8 * 64 * 130 * 4
@@ -92,6 +94,7 @@ def test_planning(lib):
     assert ws(1, 12, 8, 128, 16, 100, 0) == BAD
     sh = lib.pa_decode_shared_workspace_size
     assert sh(8, 2, 4, 8, 8, 128, 16, 2000, 1000, 0) > 0
+    assert sh(4, 1, 4, 4, 4, 64, 16, 100, 64, 0) == 0        # small: one pass, nothing to join
     assert sh(8, 2, 4, 8, 8, 128, 16, 2000, 2001, 0) == BAD
     assert sh(8, 2, 4, 8, 8, 128, 12, 2000, 1000, 0) == BAD
 
