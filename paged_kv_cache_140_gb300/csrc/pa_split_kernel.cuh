@@ -133,19 +133,32 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 // which bounds 2^(s_p - m) to 2^85.
 constexpr float kScaleFloor = 8.470329472543003e-22f;   // 2^-70
 
-// Four codes (bytes 0-3) as two f16 pairs.  Natural order: (0, 1), (2, 3);
-// interleaved: (0, 2), (1, 3).  An int8 code b is u - 128 for the byte
-// u = b ^ 0x80, and 0x6400 | u is binary16 1024 + u: all steps exact.
-template <int CT, bool Interleaved>
-__device__ __forceinline__ void widen(uint32_t w, uint32_t &lo, uint32_t &hi) {
+// Four K codes (bytes 0-3) as f16 pairs (0, 1) and (2, 3).  An int8 code b is
+// u - 128 for the byte u = b ^ 0x80, and 0x6400 | u is binary16 1024 + u: exact.
+template <int CT>
+__device__ __forceinline__ void widen_k(uint32_t w, uint32_t &lo, uint32_t &hi) {
     if constexpr (CT == kCacheE4M3) {
-        e4m3x4_to_f16x2x2(Interleaved ? prmt(w, 0x3120u) : w, lo, hi);
+        e4m3x4_to_f16x2x2(w, lo, hi);
     } else {
         const uint32_t u = w ^ 0x80808080u;
-        lo = __byte_perm(u, 0x64646464u, Interleaved ? 0x4240u : 0x4140u);
-        hi = __byte_perm(u, 0x64646464u, Interleaved ? 0x4341u : 0x4342u);
+        lo = __byte_perm(u, 0x64646464u, 0x4140u);
+        hi = __byte_perm(u, 0x64646464u, 0x4342u);
         asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(lo) : "r"(0x64806480u));
         asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(hi) : "r"(0x64806480u));
+    }
+}
+
+// Four V codes as f16 pairs (0, 2) and (1, 3).  int8: the byte u = b + 128 taken
+// as the binary16 subnormal u 2^-24, two steps less per pair than its value; the
+// product is put right once per item, sum w b = 2^24 (sum w u 2^-24) - 128 sum w,
+// which costs one bit of the 24 that it is summed in.
+template <int CT>
+__device__ __forceinline__ void widen_v(uint32_t w, uint32_t &ev, uint32_t &od) {
+    if constexpr (CT == kCacheE4M3) {
+        e4m3x4_to_f16x2x2(prmt(w, 0x3120u), ev, od);
+    } else {
+        ev = (w & 0x00ff00ffu) ^ 0x00800080u;
+        od = ((w >> 8) & 0x00ff00ffu) ^ 0x00800080u;
     }
 }
 
@@ -552,14 +565,20 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
     const uint32_t stage_off = half_off * L::kHalves;
     const uint32_t head_off = head * RB * L::kRowB;
     const uint32_t hi_off = per_stage == 1 ? 8 * L::kRowB : box;     // rows 8-15 of a stage
+    // A lane's 16-byte chunk 2 i + (0 or 1) of its row sits, swizzled, at the row's
+    // start + 16 ((2 i + b) ^ swz): the address for i = 0, with 32 i flipped in.
     const uint32_t swz = L::kRowB == 128 ? r8 : (r8 >> 1) & 3;
-    const uint32_t off_k = head_off + (j8 & 1) * hi_off + r8 * L::kRowB;
-    const uint32_t off_v = head_off + (j8 >> 1) * hi_off + r8 * L::kRowB;
+    const uint32_t off_k = head_off + (j8 & 1) * hi_off + r8 * L::kRowB + (((j8 >> 1) ^ swz) << 4);
+    const uint32_t off_v = L::kKVBytes + head_off + (j8 >> 1) * hi_off + r8 * L::kRowB + (((j8 & 1) ^ swz) << 4);
+    // 8-bit caches: my tokens' scales in a slot (K; V scales kScaleBytes further)
+    const uint32_t scl_off = 2 * L::kKVBytes + ((((sub * SUB * kStageTokens + g) << p.log2_heads) + head) << 2);
+    const uint32_t scl_8 = 32u << p.log2_heads;                      // 8 tokens further
     const uint64_t keep = l2_policy_evict_last();
 
     uint32_t qf[KS][2];
     float qs[2];                  // logit scale of columns 2t, 2t + 1
     float acc[MT][4], m_run[2], l_run[2];
+    float lw[2];                  // int8: sum of the weights that enter the V product
     float mu[2];                  // the reference that weights are taken under: m_run, or 0 while there is none
     int cslot = 0;
     uint32_t cphase = 0, citems = 0;
@@ -630,7 +649,7 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 m_run[e] = -INFINITY;
-                l_run[e] = mu[e] = 0.f;
+                l_run[e] = lw[e] = mu[e] = 0.f;
             }
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) acc[mt][0] = acc[mt][1] = acc[mt][2] = acc[mt][3] = 0.f;
@@ -667,19 +686,17 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                 if constexpr (!k8) {
 #pragma unroll
                     for (int ks = 0; ks < KS; ++ks) {
-                        const int ch = 2 * ks + (j8 >> 1);
                         uint32_t a[4];
-                        ldsm_x4(a, ka + (ch >> 3) * half_off + (((ch & 7) ^ swz) << 4));
+                        ldsm_x4(a, (ka + (ks >> 2) * half_off) ^ ((ks & 3) << 5));
                         mma_16816<BF16>(c[ks & 1], a, qf[ks][0], qf[ks][1]);
                     }
                 } else {
 #pragma unroll
                     for (int kc = 0; kc < D / 32; ++kc) {
-                        const int ch = 2 * kc + (j8 >> 1);
                         uint32_t a[4], lo4[4], hi4[4];
-                        ldsm_x4(a, ka + ((ch ^ swz) << 4));
+                        ldsm_x4(a, ka ^ (kc << 5));
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) widen<CT, false>(a[i], lo4[i], hi4[i]);
+                        for (int i = 0; i < 4; ++i) widen_k<CT>(a[i], lo4[i], hi4[i]);
                         mma_16816<false>(c[0], lo4, qf[2 * kc][0], qf[2 * kc][1]);
                         mma_16816<false>(c[1], hi4, qf[2 * kc + 1][0], qf[2 * kc + 1][1]);
                     }
@@ -688,12 +705,13 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                 float k_lo = 1.f, k_hi = 1.f;
                 if constexpr (k8) {
                     // a masked token's scales may be anything: its V scale counts as 0
-                    const float *scl = reinterpret_cast<const float *>(sp + 2 * L::kKVBytes) +
-                                       (((st0 + hs) * kStageTokens + g) << p.log2_heads) + head;
-                    k_lo = scl[0];
-                    k_hi = scl[8 << p.log2_heads];
-                    sv[hs][0] = v_lo ? max_nan(scl[L::kScaleBytes / 4], kScaleFloor) : 0.f;
-                    sv[hs][1] = v_hi ? max_nan(scl[L::kScaleBytes / 4 + (8 << p.log2_heads)], kScaleFloor) : 0.f;
+                    const uint8_t *lo = sp + scl_off + 2 * hs * scl_8, *hi = lo + scl_8;
+                    k_lo = *reinterpret_cast<const float *>(lo);
+                    k_hi = *reinterpret_cast<const float *>(hi);
+                    const float a = *reinterpret_cast<const float *>(lo + L::kScaleBytes);
+                    const float b = *reinterpret_cast<const float *>(hi + L::kScaleBytes);
+                    sv[hs][0] = v_lo ? max_nan(a, kScaleFloor) : 0.f;
+                    sv[hs][1] = v_hi ? max_nan(b, kScaleFloor) : 0.f;
                 }
 #pragma unroll
                 for (int e = 0; e < NE; ++e) {
@@ -743,6 +761,7 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                     m_run[e] = mn;
                     mu[e] = mn == -INFINITY ? 0.f : mn;
                     l_run[e] *= al;
+                    lw[e] *= al;
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt) {
                         acc[mt][e] *= al;
@@ -756,7 +775,10 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                 if constexpr (!kWhole)
                     if (hs > 0 && !second) continue;
 #pragma unroll
-                for (int e = 0; e < NE; ++e) l_run[e] += pw[hs][e] + pw[hs][2 + e];
+                for (int e = 0; e < NE; ++e) {
+                    l_run[e] += pw[hs][e] + pw[hs][2 + e];
+                    if constexpr (CT == kCacheInt8) lw[e] += w4[hs][e] + w4[hs][2 + e];
+                }
                 // weights as the PV B fragment: tokens 2t, 2t+1, 2t+8, 2t+9 of column g
                 uint32_t bhi[2], blo[2];
                 {
@@ -802,13 +824,12 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                         __syncwarp();
                     }
                 }
-                const uint32_t va = sa + vbase + off_v;
+                const uint32_t va = sa + (st0 + hs) * stage_off + off_v;
                 if constexpr (!k8) {
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt) {
-                        const int ch = 2 * mt + (j8 & 1);
                         uint32_t a[4];
-                        ldsm_x4_trans(a, va + (ch >> 3) * half_off + (((ch & 7) ^ swz) << 4));
+                        ldsm_x4_trans(a, (va + (mt >> 2) * half_off) ^ ((mt & 3) << 5));
                         mma_16816<BF16>(acc[mt], a, bhi[0], bhi[1]);
                         if constexpr (!L::kPaired) mma_16816<BF16>(acc[mt], a, blo[0], blo[1]);
                     }
@@ -817,11 +838,10 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                     // acc[2vc], odd dims acc[2vc+1].
 #pragma unroll
                     for (int vc = 0; vc < D / 32; ++vc) {
-                        const int ch = 2 * vc + (j8 & 1);
                         uint32_t a[4], ev[4], od[4];
-                        ldsm_x4_trans(a, va + ((ch ^ swz) << 4));
+                        ldsm_x4_trans(a, va ^ (vc << 5));
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) widen<CT, true>(a[i], ev[i], od[i]);
+                        for (int i = 0; i < 4; ++i) widen_v<CT>(a[i], ev[i], od[i]);
                         mma_16816<false>(acc[2 * vc], ev, bhi[0], bhi[1]);
                         if constexpr (!L::kPaired) mma_16816<false>(acc[2 * vc], ev, blo[0], blo[1]);
                         mma_16816<false>(acc[2 * vc + 1], od, bhi[0], bhi[1]);
@@ -853,7 +873,19 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1)
 #pragma unroll
-            for (int e = 0; e < NE; ++e) l_run[e] += __shfl_xor_sync(kFull, l_run[e], o);
+            for (int e = 0; e < NE; ++e) {
+                l_run[e] += __shfl_xor_sync(kFull, l_run[e], o);
+                if constexpr (CT == kCacheInt8) lw[e] += __shfl_xor_sync(kFull, lw[e], o);
+            }
+        if constexpr (CT == kCacheInt8) {   // sum w u 2^-24 -> sum w (u - 128)
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int e = 0; e < NE; ++e) {
+                    acc[mt][e] = fmaf(acc[mt][e], 16777216.f, -128.f * lw[e]);
+                    acc[mt][2 + e] = fmaf(acc[mt][2 + e], 16777216.f, -128.f * lw[e]);
+                }
+        }
         if (nsubs > 1) {
             // join the states of the head's warps: the others hand theirs to the first
             const uint32_t par = (citems - 1) & 1u;      // of this item

@@ -69,11 +69,13 @@ def tolerance(ref, vmax, length, d, xmax, out_dtype):
     A logit sums d products in fp32 (d / 2^24 of sum |q k|, which xmax bounds) and
     its exponential is off by that, by the rounding of x log2(e) - m and by 2 ulp
     of the exponential: xmax (d + 4) + 4 half steps.  Weights enter the product
-    as two 16-bit parts (2^-17 at the least), and up to 2 length + 16 fp32
-    additions form the sums (each off by half a step of at most the final sum of
-    magnitudes); all of it is relative to the largest |v|.  The output is rounded
-    once more."""
-    rel = 2.0 ** -24 * (xmax * (d + 4) + 4 + 2 * length + 16) + 2.0 ** -16
+    as two 16-bit parts (2^-17 at the least).  Up to length + 8 fp32 additions
+    form the sum of the weights and as many the product (each off by half a step
+    of at most the final sum of magnitudes); for int8 codes the product is summed
+    with 128 added to each code, which doubles its magnitudes, and the sum of its
+    weights taken off again: 4 (length + 8) in all, relative to the largest |v|.
+    The output is rounded once more."""
+    rel = 2.0 ** -24 * (xmax * (d + 4) + 4 + 4 * (length + 8)) + 2.0 ** -16
     tol = rel * vmax + 1e-30
     if out_dtype != "f32":
         fi = torch.finfo(DT[out_dtype])
