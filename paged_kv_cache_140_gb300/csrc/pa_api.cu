@@ -658,9 +658,7 @@ int split_cache(pa_dtype d) {
     return d == PA_F16 ? pa::kCacheF16 : d == PA_BF16 ? pa::kCacheBF16 : d == PA_FP8_E4M3 ? pa::kCacheE4M3 : pa::kCacheInt8;
 }
 
-// Entries (sequences, or chunks of groups) of one launch: the kernel keeps 12
-// bytes for each in shared memory; longer lists take several launches.
-constexpr int kSplitEntries = 2048;
+using pa::kSplitEntries;
 // SMs the cuts are planned for (a constant: the workspace's size does not depend
 // on the device), and the work items a launch should have, six for each (an SM's
 // share is uneven by up to one item).
@@ -734,7 +732,8 @@ struct SplitPlan {
     int prefix_part = 0;         // tokens per prefix_per partials
     int prefix_per = 1, prefix_parts = 0;
     int max_parts = 1;
-    size_t acc_off = 0, bytes = 0;
+    int64_t cut_row = 0;
+    size_t acc_off = 0, prefix_off = 0, bytes = 0;
 };
 
 bool split_shape_ok(int num_heads, int num_kv_heads, int head_dim, int block_size) {
@@ -787,9 +786,14 @@ bool plan_split(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int
         w.max_parts += w.prefix_parts;
     }
     if ((!shared || w.whole) && w.max_parts <= 1) return true;
-    const int64_t rows = static_cast<int64_t>(num_seqs) * num_heads * w.max_parts;
+    // Rows of (reference, sum, weighted sum): one per partial, and for cut items
+    // one per launch, CTA and head of its box; then the slots before each entry.
+    const int64_t launches = (num_seqs + kSplitEntries - 1) / kSplitEntries;
+    w.cut_row = static_cast<int64_t>(num_seqs) * num_heads * w.max_parts;
+    const int64_t rows = w.cut_row + (launches * pa::kSplitMaxCtas * w.G << w.log2_heads);
     w.acc_off = static_cast<size_t>(round_up(rows * 2 * 4, 256));
-    w.bytes = w.acc_off + static_cast<size_t>(rows) * head_dim * 4;
+    w.prefix_off = w.acc_off + static_cast<size_t>(rows) * head_dim * 4;
+    w.bytes = w.prefix_off + static_cast<size_t>(launches) * pa::kSplitPrefixWords * 4;
     return true;
 }
 
@@ -842,7 +846,7 @@ pa_status run_split(pa::SplitParams p, int cache, int head_dim, int cols, int en
         if (need.fixed + 2 * need.slot > room) return PA_ERR_UNSUPPORTED;
         p.stages = static_cast<int>(std::min<size_t>(8, (room - need.fixed) / need.slot));
         const size_t smem = need.fixed + p.stages * need.slot;
-        const int grid = static_cast<int>(std::min<int64_t>(dev.sms, p.entries * per_entry));
+        const int grid = static_cast<int>(std::min<int64_t>(std::min(dev.sms, pa::kSplitMaxCtas), p.entries * per_entry));
         auto launch = cache == pa::kCacheF16    ? pa::launch_split_f16
                       : cache == pa::kCacheBF16 ? pa::launch_split_bf16
                       : cache == pa::kCacheE4M3 ? pa::launch_split_e4m3
@@ -899,6 +903,9 @@ pa::SplitParams split_params(void *out, pa_dtype out_dtype, const void *query, p
     if (w.bytes) {
         p.ws_ml = static_cast<float *>(workspace);
         p.ws_acc = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + w.acc_off);
+        p.ws_prefix = reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(workspace) + w.prefix_off);
+        p.cut_row = w.cut_row;
+        p.cut = 1;
     }
     p.err_flag = err_flag;
     p.log2_heads = w.log2_heads;
@@ -1010,7 +1017,7 @@ PA_EXPORT pa_status pa_quant_decode(void *out, pa_dtype out_dtype, const void *q
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const pa_status r = run_split(p, cache, head_dim, w.G, num_seqs, max_context_len, maps, dev, s);
     if (r != PA_OK || w.max_parts <= 1) return r;
-    return pa::launch_split_merge(p, head_dim, 1, 1, dev.sms, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+    return pa::launch_split_merge(p, head_dim, cache, 1, 1, dev.sms, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 PA_EXPORT size_t pa_decode_shared_workspace_size(int num_seqs, int num_groups, int max_group_size, int num_heads,
@@ -1069,7 +1076,7 @@ PA_EXPORT pa_status pa_decode_shared(void *out, pa_dtype out_dtype, const void *
         p.mode = pa::kSplitWhole;
         const pa_status r = run_split(p, cache, head_dim, w.G, num_seqs, max_context_len, maps, dev, s);
         if (r != PA_OK || w.max_parts <= 1) return r;
-        return pa::launch_split_merge(p, head_dim, 1, 1, dev.sms, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+        return pa::launch_split_merge(p, head_dim, cache, 1, 1, dev.sms, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
     }
     if (w.prefix_parts > 0 && w.prefix_tc) {
         if (pa::shared_prefix_smem(head_dim) + 1024 > static_cast<size_t>(dev.smem_optin)) return PA_ERR_UNSUPPORTED;
@@ -1087,6 +1094,7 @@ PA_EXPORT pa_status pa_decode_shared(void *out, pa_dtype out_dtype, const void *
     } else if (w.prefix_parts > 0) {
         pa::SplitParams pre = p;
         pre.mode = pa::kSplitPrefix;
+        pre.cut = 0;
         pre.partition_size = w.prefix_part;
         pre.chunk_seqs = w.prefix_cols / w.G;
         pre.chunks = (max_group_size + pre.chunk_seqs - 1) / pre.chunk_seqs;
@@ -1100,7 +1108,7 @@ PA_EXPORT pa_status pa_decode_shared(void *out, pa_dtype out_dtype, const void *
     p.late_wait = w.prefix_parts > 0;
     const pa_status r = run_split(p, cache, head_dim, w.G, num_seqs, max_context_len, maps, dev, s);
     if (r != PA_OK) return r;
-    return pa::launch_split_merge(p, head_dim, std::max(1, w.prefix_part), w.prefix_per, dev.sms, s) == cudaSuccess
+    return pa::launch_split_merge(p, head_dim, cache, std::max(1, w.prefix_part), w.prefix_per, dev.sms, s) == cudaSuccess
                ? PA_OK
                : PA_ERR_CUDA;
 }

@@ -14,6 +14,13 @@ namespace pa {
 // scale per token and KV head.
 constexpr int kCacheF16 = 0, kCacheBF16 = 1, kCacheE4M3 = 2, kCacheInt8 = 3;
 
+// Entries (sequences, or chunks of groups) of one launch: the kernel keeps 12
+// bytes for each in shared memory; longer lists take several launches.
+constexpr int kSplitEntries = 2048;
+constexpr int kSplitPrefixWords = kSplitEntries + 2;
+// CTAs of a launch at most (a row of the workspace for each).
+constexpr int kSplitMaxCtas = 256;
+
 // What a launch's entries are.
 constexpr int kSplitDecode = 0;   // sequences, whole contexts; results final where one partition holds them
 constexpr int kSplitSuffix = 1;   // sequences past their shared blocks; partial results only
@@ -39,8 +46,12 @@ struct SplitParams {
     int partition_size;          // tokens per partition, a multiple of 16, at most 32 blocks
     int max_parts;               // partial results per (sequence, KV head) in the workspace
     int part_off;                // where this launch's start among them
-    float *ws_ml;                // [num_seqs * Hkv * max_parts, G, 2]  (reference, sum)
-    float *ws_acc;               // [num_seqs * Hkv * max_parts, G, D]
+    float *ws_ml;                // [rows, 2]  (reference, sum); a row per (sequence, KV head, part, head of the
+                                 // group), then per (launch, CTA, head of its box, head of the group)
+    float *ws_acc;               // [rows, D]
+    int cut;                     // decode, suffix, whole: CTAs take equal shares of the slots, items may be cut
+    int64_t cut_row;             // where the CTAs' rows start
+    uint32_t *ws_prefix;         // per launch: CTAs (0: nothing was cut), slots before each entry
     const float *k_scales;       // 8-bit caches: [num_blocks, bs, Hkv]
     const float *v_scales;
     int *err_flag;
@@ -95,7 +106,7 @@ cudaError_t launch_split_int8(const SplitParams &p, int head_dim, int cols, cons
 // each prefix_part tokens of its shared blocks at index 0.. and one for each
 // partition_size of the rest at p.part_off.. (p.mode kSplitDecode: no shared
 // blocks, and sequences of one partition are final already).
-cudaError_t launch_split_merge(const SplitParams &p, int head_dim, int prefix_part, int per_part, int sms,
+cudaError_t launch_split_merge(const SplitParams &p, int head_dim, int cache, int prefix_part, int per_part, int sms,
                                cudaStream_t stream);
 
 // Quantising write and read-back (cache: kCacheE4M3 or kCacheInt8).

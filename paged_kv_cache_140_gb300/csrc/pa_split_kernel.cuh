@@ -76,14 +76,15 @@ struct SlotMeta {
     int seq;         // the entry's first query sequence; < 0: no more work
     int kvh0;        // first KV head of the box
     int part;
-    int flags;       // kFirst | kLast | kFinal, members << 8
+    int flags;       // kFirst | kLast | kFinal | kContinued, members << 8
     int ntok;        // valid tokens from the slot's first
     uint32_t bad;    // bit 2 i (+ 1): rows 0-7 (8-15) of the slot's stage i were not loaded
     int pad[2];
 };
-constexpr int kFirst = 1;    // the item's first slot: load the queries, reset the state
-constexpr int kLast = 2;     // the item's last slot: write the results
+constexpr int kFirst = 1;    // the first slot of an item (of this CTA's part of it): load the queries, reset the state
+constexpr int kLast = 2;     // its last slot: write the results
 constexpr int kFinal = 4;    // the item is the whole of the sequence's context
+constexpr int kContinued = 8;   // the item was begun by the CTA before: the result goes to this CTA's own row
 
 __device__ __forceinline__ void arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
@@ -187,6 +188,12 @@ __device__ __forceinline__ int context_of(const SplitParams &p, int s, bool tell
 __device__ __forceinline__ bool bad_group(const SplitParams &p, int g, int q0, int q1) {
     return q0 < 0 || q1 < q0 || q1 > p.num_seqs || q1 - q0 > p.max_group_size || (g == 0 && q0 != 0) ||
            (g == p.num_groups - 1 && q1 != p.num_seqs);
+}
+
+// First workspace row of what CTA `cta` of launch `launch` continued, head `head`
+// of its box.
+__device__ __forceinline__ int64_t cut_row_of(const SplitParams &p, int launch, uint32_t cta, int head) {
+    return p.cut_row + ((((static_cast<int64_t>(launch) * kSplitMaxCtas + cta) << p.log2_heads) + head) << p.log2_group);
 }
 
 // Items (entry, partition, box of heads) in that order, weighed in slots.  An
@@ -351,8 +358,17 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
         }
         __syncthreads();
     }
-    // This CTA takes the items whose first slot lies in its equal share.
+    // This CTA takes the items whose first slot lies in its equal share of the
+    // slots, or (p.cut, with shares at least as long as an item) exactly its share:
+    // an item across the end is continued by the next CTA, which leaves a partial
+    // result of its own.  The join learns from CTA 0 where the shares end.
     const uint32_t total = prefix[E];
+    const bool cut = p.cut && total >= gridDim.x * static_cast<uint32_t>((P / kStageTokens + SW - 1) / SW);
+    if (p.cut && blockIdx.x == 0) {
+        uint32_t *w = p.ws_prefix + static_cast<int64_t>(p.e0 / kSplitEntries) * kSplitPrefixWords;
+        for (int i = threadIdx.x; i <= E; i += blockDim.x) w[1 + i] = prefix[i];
+        if (threadIdx.x == 0) w[0] = cut ? gridDim.x : 0u;
+    }
     const uint32_t lo = static_cast<uint32_t>(static_cast<uint64_t>(total) * blockIdx.x / gridDim.x);
     const uint32_t hi = static_cast<uint32_t>(static_cast<uint64_t>(total) * (blockIdx.x + 1) / gridDim.x);
 
@@ -398,11 +414,35 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
             const uint32_t off = lo - prefix[a];
             set_part(min(ic.nparts - 1, static_cast<int>(off / pw)));
             const uint32_t pstart = prefix[a] + static_cast<uint32_t>(ic.part) * pw;
-            const int grp = static_cast<int>((lo - pstart + ic.nslots - 1) / ic.nslots);
+            const int grp = static_cast<int>((lo - pstart + (cut ? 0 : ic.nslots - 1)) / ic.nslots);
             ic.grp = min(grp, ngroups - 1);
             ic.start = pstart + static_cast<uint32_t>(ic.grp) * ic.nslots;
             if (grp >= ngroups) advance();
         }
+        // An item's sequence, members, table row and first block; its tokens and
+        // the block ids of its partition, one per lane.
+        int seq, members, blk0, t0, ntok, fb;
+        int32_t bid;
+        auto open_item = [&]() {
+            int row;
+            seq = row = p.e0 + ic.e;
+            members = 1;
+            blk0 = 0;
+            if (mode == kSplitPrefix) {
+                seq = aux_s[ic.e] & 0x7ffffff;
+                members = aux_s[ic.e] >> 27;
+                row = seq - ((p.e0 + ic.e) % p.chunks) * p.chunk_seqs;   // the group's first sequence
+            } else if (mode == kSplitSuffix) {
+                blk0 = aux_s[ic.e];
+            }
+            t0 = ic.part * P;
+            ntok = max(0, min(P, ic.len - t0));
+            fb = t0 / bs;
+            if (mode == kSplitWhole && fb + lane < shared_blocks(p, seq, ic.len, false)) row = aux_s[ic.e];
+            bid = -1;
+            if (ntok > 0 && lane <= (t0 + ntok - 1) / bs - fb)
+                bid = __ldg(p.block_tables + static_cast<int64_t>(row) * p.max_blocks_per_seq + blk0 + fb + lane);
+        };
         int islot = 0;
         uint32_t uses = 0, items = 0;
         bool ok = true;
@@ -422,22 +462,7 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
         };
         while (ok && work && ic.start < hi) {
             const int kvh0 = ic.grp << p.log2_heads;
-            int seq = p.e0 + ic.e, members = 1, row = seq, blk0 = 0;
-            if (mode == kSplitPrefix) {
-                seq = aux_s[ic.e] & 0x7ffffff;
-                members = aux_s[ic.e] >> 27;
-                row = seq - ((p.e0 + ic.e) % p.chunks) * p.chunk_seqs;   // the group's first sequence
-            } else if (mode == kSplitSuffix) {
-                blk0 = aux_s[ic.e];
-            }
-            const int t0 = ic.part * P;
-            const int ntok = max(0, min(P, ic.len - t0));
-            // the partition's block ids, one per lane
-            const int fb = t0 / bs;
-            int32_t bid = -1;
-            if (mode == kSplitWhole && fb + lane < shared_blocks(p, seq, ic.len, false)) row = aux_s[ic.e];
-            if (ntok > 0 && lane <= (t0 + ntok - 1) / bs - fb)
-                bid = __ldg(p.block_tables + static_cast<int64_t>(row) * p.max_blocks_per_seq + blk0 + fb + lane);
+            open_item();
             {
                 const int qi = static_cast<int>(items % kQueryRing);
                 if (items >= static_cast<uint32_t>(kQueryRing)) {
@@ -459,8 +484,11 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                 ++items;
                 __syncwarp();
             }
-            const int fin = final_mode(mode) && ic.nparts == 1 ? kFinal : 0;
-            for (int j = 0; j < ic.nslots; ++j) {
+            // this CTA's slots of the item
+            const int jb = cut && ic.start < lo ? static_cast<int>(lo - ic.start) : 0;
+            const int je = cut ? min(ic.nslots, static_cast<int>(hi - ic.start)) : ic.nslots;
+            const int kind = jb > 0 ? kContinued : je == ic.nslots && final_mode(mode) && ic.nparts == 1 ? kFinal : 0;
+            for (int j = jb; j < je; ++j) {
                 const int slot = take_slot();
                 if (!ok) break;
                 uint8_t *sp = slots + static_cast<size_t>(slot) * L::kSlotBytes;
@@ -486,7 +514,7 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                     mt.seq = seq;
                     mt.kvh0 = kvh0;
                     mt.part = ic.part;
-                    mt.flags = (j == 0 ? kFirst : 0) | (j + 1 == ic.nslots ? kLast : 0) | fin | (members << 8);
+                    mt.flags = (j == jb ? kFirst : 0) | (j + 1 == je ? kLast : 0) | kind | (members << 8);
                     mt.ntok = nt;
                     mt.bad = bad;
                     mt.pad[0] = mt.pad[1] = 0;
@@ -953,7 +981,10 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
             const int64_t sq = m.seq + (c >> lg);
             const int hq = c & ((1 << lg) - 1);
             const float sc = fin ? (l_run[e] == 0.f ? 0.f : 1.f / l_run[e]) : 1.f;
-            const int64_t r = ((sq * Hkv + kvh) * p.max_parts + p.part_off + m.part << lg) + hq;
+            const int64_t r =
+                (m.flags & kContinued)
+                    ? cut_row_of(p, p.e0 / kSplitEntries, blockIdx.x, head) + hq
+                    : (((sq * Hkv + kvh) * p.max_parts + p.part_off + m.part) << lg) + hq;
             if (!fin && g == 0) st_global_hint(p.ws_ml + 2 * r, make_float2(m_run[e], l_run[e]), keep);
             const int64_t orow = fin ? (sq * Hq + (kvh << lg) + hq) * D : r * D;
             auto put2 = [&](int d, float a, float b) {   // two consecutive elements

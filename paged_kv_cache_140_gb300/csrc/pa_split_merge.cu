@@ -18,7 +18,7 @@ constexpr int kBatch = 8;     // partials a warp loads at a time
 
 template <int D>
 __global__ void __launch_bounds__(256)
-    split_merge_kernel(const __grid_constant__ SplitParams p, int prefix_part, int per_part, int wt) {
+    split_merge_kernel(const __grid_constant__ SplitParams p, int prefix_part, int per_part, int slot_stages, int wt) {
     constexpr int DPL = D / 32;
     __shared__ float red_o[8][D];
     __shared__ float2 red_ml[8];
@@ -30,17 +30,39 @@ __global__ void __launch_bounds__(256)
     const int hq = row_ok ? static_cast<int>(task % p.num_heads) : 0;
     const int G = 1 << p.log2_group, d0 = lane * DPL;
     pdl_wait();
-    int npre = 0, np = 0;
+    int npre = 0, np = 0, len = 0;
+    uint32_t ctas = 0, before = 0, total = 1;
     if (row_ok) {
+        if (p.cut) {
+            const uint32_t *w = p.ws_prefix + static_cast<int64_t>(s / kSplitEntries) * kSplitPrefixWords;
+            ctas = __ldcg(w);
+            before = __ldcg(w + 1 + s % kSplitEntries);
+            total = __ldcg(w + 1 + min(kSplitEntries, p.num_seqs - s / kSplitEntries * kSplitEntries));
+        }
         const int ctx = context_of(p, s, false);
         int shared = 0;
         if (!final_mode(p.mode)) {
             shared = shared_blocks(p, s, ctx, false) * p.block_size;
             npre = (shared + prefix_part - 1) / prefix_part * per_part;
         }
-        np = npre + (ctx - shared + p.partition_size - 1) / p.partition_size;
+        len = ctx - shared;
+        np = npre + (len + p.partition_size - 1) / p.partition_size;
     }
-    const bool active = row_ok && (np > 1 || !final_mode(p.mode));
+    // Of the private parts 32 i .. 32 i + 31 (one per lane): the CTA that
+    // continued mine, or 0.  Slot x lies in CTA ceil((x + 1) ctas / total) - 1.
+    const int grp = (hq >> p.log2_group) >> p.log2_heads, ngroups = p.num_kv_heads >> p.log2_heads;
+    auto continued = [&](int part) -> uint32_t {
+        if (ctas == 0 || part >= np - npre) return 0u;
+        const uint32_t n = item_slots(len, part, p.partition_size, slot_stages);
+        const uint32_t full = (p.partition_size / kStageTokens + slot_stages - 1) / slot_stages;
+        const uint32_t x = before + static_cast<uint32_t>(part) * ngroups * full + grp * n;
+        const uint64_t a = (static_cast<uint64_t>(x + 1) * ctas + total - 1) / total;
+        const uint64_t b = (static_cast<uint64_t>(x + n) * ctas + total - 1) / total;
+        return a != b ? static_cast<uint32_t>(b - 1) : 0u;
+    };
+    const uint32_t cont0 = continued(lane);
+    const bool split0 = __any_sync(kFull, cont0 != 0);
+    const bool active = row_ok && (np > 1 || !final_mode(p.mode) || split0);
     float M = -INFINITY, l = 0.f, o[DPL];
 #pragma unroll
     for (int i = 0; i < DPL; ++i) o[i] = 0.f;
@@ -88,6 +110,24 @@ __global__ void __launch_bounds__(256)
                 l = fmaf(ml[u].y, w, l);
 #pragma unroll
                 for (int i = 0; i < DPL; ++i) o[i] = fmaf(v[u][i], w, o[i]);
+            }
+        }
+        // parts that a second CTA continued: few
+        for (int c0 = 0; sub == 0 && ctas != 0 && c0 < np - npre; c0 += 32) {
+            const uint32_t mine = c0 == 0 ? cont0 : continued(c0 + lane);
+            for (uint32_t left = __ballot_sync(kFull, mine != 0); left != 0; left &= left - 1) {
+                const uint32_t cta = __shfl_sync(kFull, mine, __ffs(left) - 1);
+                const int64_t r = cut_row_of(p, s / kSplitEntries, cta, (hq >> p.log2_group) & ((1 << p.log2_heads) - 1)) +
+                                  (hq & (G - 1));
+                const float2 ml = __ldcg(reinterpret_cast<const float2 *>(p.ws_ml) + r);
+                const float *a = p.ws_acc + r * D + d0;
+                const float mb = fmaxf(M, ml.x);
+                const float al = mb == -INFINITY ? 1.f : fast_exp2(M - mb);
+                const float w = ml.x == -INFINITY ? 1.f : fast_exp2(ml.x - mb);
+                M = mb;
+                l = fmaf(ml.y, w, l * al);
+#pragma unroll
+                for (int i = 0; i < DPL; ++i) o[i] = fmaf(__ldcg(a + i), w, o[i] * al);
             }
         }
     }
@@ -145,7 +185,7 @@ int split_slot_stages(int cache, int log2_heads) {
            log2_heads;
 }
 
-cudaError_t launch_split_merge(const SplitParams &p, int head_dim, int prefix_part, int per_part, int sms,
+cudaError_t launch_split_merge(const SplitParams &p, int head_dim, int cache, int prefix_part, int per_part, int sms,
                                cudaStream_t stream) {
     const int64_t rows = static_cast<int64_t>(p.num_seqs) * p.num_heads;
     // one warp per row, more while the rows leave warps idle and there is something to share out
@@ -153,7 +193,8 @@ cudaError_t launch_split_merge(const SplitParams &p, int head_dim, int prefix_pa
     while (wt < 8 && rows * wt * 2 <= static_cast<int64_t>(sms) * 16 && p.max_parts > kBatch * wt) wt *= 2;
     const int64_t blocks = (rows + 8 / wt - 1) / (8 / wt);
     auto kern = head_dim == 128 ? split_merge_kernel<128> : split_merge_kernel<64>;
-    return launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream, p, prefix_part, per_part, wt);
+    return launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream, p, prefix_part, per_part,
+                      split_slot_stages(cache, p.log2_heads), wt);
 }
 
 }  // namespace pa

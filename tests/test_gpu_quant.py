@@ -272,6 +272,22 @@ def test_decode_partitions(P, hkv):
     check_decode([0, 1, 48, 49, 511, 513, 2050], hkv * 2, hkv, 128, 16, "e4m3", "bf16", partition_size=P)
 
 
+@pytest.mark.parametrize("hq,hkv,n,hi,P", [(8, 8, 60, 900, 128), (16, 16, 50, 700, 0), (32, 8, 70, 1000, 256),
+                                           (4, 1, 60, 3000, 512), (4, 4, 90, 1200, 0), (6, 3, 80, 2000, 512)])
+def test_decode_enough_work_for_items_to_be_cut_between_sms(hq, hkv, n, hi, P):
+    rng = np.random.default_rng(n)
+    lens = rng.integers(1, hi, n).tolist()
+    lens[3], lens[7], lens[n - 1] = 0, hi, 0
+    check_decode(lens, hq, hkv, 64, 32, "e4m3" if hkv % 3 else "int8", "bf16", seed=n, partition_size=P)
+
+
+def test_decode_launches_of_many_sequences_cut_items_apart():
+    """Two launches of a long batch, both with items cut between SMs."""
+    rng = np.random.default_rng(3)
+    lens = rng.integers(1, 120, 4000).tolist()
+    check_decode(lens, 8, 8, 64, 16, "int8", "f16", seed=3, partition_size=64)
+
+
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
 @pytest.mark.parametrize("hkv", [2, 8])
 def test_decode_long_context(hkv, fmt):

@@ -135,6 +135,13 @@ def test_groups_of_mixed_sizes(dtype):
     check(make(members, shared, rng.integers(0, 40, sum(members)).tolist(), 16, 4, 128, 16, dtype, seed=5))
 
 
+@pytest.mark.parametrize("members,hq,hkv", [([9, 30, 4], 16, 8), ([2] * 30, 8, 8), ([60], 16, 2)])
+def test_enough_private_tokens_for_items_to_be_cut_between_sms(members, hq, hkv):
+    rng = np.random.default_rng(4)
+    n = sum(members)
+    check(make(members, [300] * len(members), rng.integers(0, 1800, n).tolist(), hq, hkv, 64, 16, "bf16", seed=14))
+
+
 @pytest.mark.parametrize("n,hq,hkv", [(3, 8, 8), (50, 8, 2)])
 def test_long_prefix(n, hq, hkv):
     rng = np.random.default_rng(2)
