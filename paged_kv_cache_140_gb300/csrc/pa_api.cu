@@ -660,29 +660,30 @@ int split_cache(pa_dtype d) {
 
 using pa::kSplitEntries;
 // SMs the cuts are planned for (a constant: the workspace's size does not depend
-// on the device), and the work items a launch should have, six for each (an SM's
-// share is uneven by up to one item).
-constexpr int64_t kSmsTarget = 152, kSplitItems = 6 * kSmsTarget;
+// on the device).
+constexpr int64_t kSmsTarget = 152;
 
-// Partition length, in tokens, for `lists` lists (entries x boxes of heads) of
-// about `len` tokens at most; 0 when the request is invalid.  Lists that fill the
-// GPU by themselves are cut at 256 tokens (512 beyond 8 K), which bounds the
-// imbalance between SMs; fewer lists are cut finer, down to 4 ring slots, so that
-// kSplitItems items exist.  Lists of up to 6 slots are not cut: reading a slot
-// takes an SM about a microsecond, joining partials a launch of its own.
-int split_partition(int64_t lists, int64_t len, int block_size, int slot_tokens, int requested) {
-    const int cap = 32 * block_size;
+// Partition length, in tokens, for `lists` lists (entries x boxes of heads, `boxes`
+// of them per entry) of about `len` tokens at most; 0 when the request is invalid.
+// Partitions are as long as they may be while an SM's equal share of the slots is
+// no shorter (shares are cut exactly then, and fewer partials joined; lists are
+// taken to be 2/5 of `len` on average), and at least 4 slots.  Entries of several
+// boxes are cut at 512 tokens: their boxes' rows and scales lie next to one another
+// in memory and are best read at about the same time.  Lists of up to 6 slots are
+// not cut: reading a slot takes an SM about a microsecond, joining partials a
+// launch of its own.
+int split_partition(int64_t lists, int64_t boxes, int64_t len, int block_size, int slot_tokens, int requested) {
+    const int64_t cap = 32 * block_size;
     if (requested != 0) {
         // a partition's block ids sit in the 32 lanes of a warp; one that does not
         // start on a block boundary may reach into one block more
         if (requested < 16 || requested % 16 != 0 || requested > cap) return 0;
         return requested % block_size != 0 && requested > cap - block_size + 16 ? 0 : requested;
     }
-    int64_t P = len <= 8192 ? 256 : 512;
-    if (lists * ((len + P - 1) / P) < kSplitItems) {
-        P = std::min<int64_t>(P, round_up(lists * len / kSplitItems + 1, slot_tokens));
-        P = std::max<int64_t>(P, 4 * slot_tokens);
-    }
+    const double share = static_cast<double>(lists) * len * 0.4 / (static_cast<double>(slot_tokens) * kSmsTarget);
+    int64_t P = static_cast<int64_t>(std::min(share, 1e6)) * slot_tokens;
+    if (boxes > 1) P = std::min<int64_t>(P, 512);
+    P = std::max<int64_t>(P, 4 * slot_tokens);
     if (len <= std::min<int64_t>(cap, std::max<int64_t>(P, 6 * slot_tokens)))
         return static_cast<int>(std::max<int64_t>(16, round_up(len, 16)));   // one partition
     P = std::min<int64_t>(P, cap);
@@ -732,8 +733,8 @@ struct SplitPlan {
     int prefix_part = 0;         // tokens per prefix_per partials
     int prefix_per = 1, prefix_parts = 0;
     int max_parts = 1;
-    int64_t cut_row = 0;
-    size_t acc_off = 0, prefix_off = 0, bytes = 0;
+    int64_t cut_row = 0, prefix_cut_row = 0;
+    size_t acc_off = 0, bytes = 0;
 };
 
 bool split_shape_ok(int num_heads, int num_kv_heads, int head_dim, int block_size) {
@@ -762,10 +763,11 @@ bool plan_split(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int
     // Private parts are about as long as the bounds differ (only the cut goes by
     // that; a part may be longer).
     const int64_t part_len = shared && !w.whole ? std::max(256, max_context_len - max_shared_len) : max_context_len;
-    w.partition = split_partition(num_seqs * ngroups, part_len, block_size, slot_tokens, partition_size);
+    w.partition = split_partition(num_seqs * ngroups, ngroups, part_len, block_size, slot_tokens, partition_size);
     if (w.partition == 0) return false;
     w.parts = std::max(1, static_cast<int>((static_cast<int64_t>(max_context_len) + w.partition - 1) / w.partition));
     w.max_parts = w.parts;
+    int64_t prefix_entries = 0;
     if (shared && !w.whole) {
         const int shared_tokens = max_shared_len / block_size * block_size;
         const int64_t rows = static_cast<int64_t>(max_group_size) * w.G;
@@ -780,20 +782,24 @@ bool plan_split(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int
         while (w.prefix_cols < 8 && w.prefix_cols < static_cast<int64_t>(max_group_size) * w.G) w.prefix_cols *= 2;
         const int chunk_seqs = w.prefix_cols / w.G;
         const int64_t chunks = (static_cast<int64_t>(max_group_size) + chunk_seqs - 1) / chunk_seqs;
-        if (!w.prefix_tc)
-            w.prefix_part = split_partition(num_groups * chunks * ngroups, max_shared_len, block_size, slot_tokens, 0);
+        if (!w.prefix_tc) {
+            prefix_entries = num_groups * chunks;
+            w.prefix_part = split_partition(num_groups * chunks * ngroups, ngroups, max_shared_len, block_size,
+                                            slot_tokens, 0);
+        }
         w.prefix_parts = (shared_tokens + w.prefix_part - 1) / w.prefix_part * w.prefix_per;
         w.max_parts += w.prefix_parts;
     }
     if ((!shared || w.whole) && w.max_parts <= 1) return true;
     // Rows of (reference, sum, weighted sum): one per partial, and for cut items
-    // one per launch, CTA and head of its box; then the slots before each entry.
-    const int64_t launches = (num_seqs + kSplitEntries - 1) / kSplitEntries;
+    // one per launch, CTA and head of its box.
+    const int64_t per_launch = static_cast<int64_t>(pa::kSplitMaxCtas) << w.log2_heads;
     w.cut_row = static_cast<int64_t>(num_seqs) * num_heads * w.max_parts;
-    const int64_t rows = w.cut_row + (launches * pa::kSplitMaxCtas * w.G << w.log2_heads);
-    w.acc_off = static_cast<size_t>(round_up(rows * 2 * 4, 256));
-    w.prefix_off = w.acc_off + static_cast<size_t>(rows) * head_dim * 4;
-    w.bytes = w.prefix_off + static_cast<size_t>(launches) * pa::kSplitPrefixWords * 4;
+    w.prefix_cut_row = w.cut_row + (num_seqs + kSplitEntries - 1) / kSplitEntries * per_launch * w.G;
+    const int64_t rows = w.prefix_cut_row +
+                         (prefix_entries + kSplitEntries - 1) / kSplitEntries * per_launch * w.prefix_cols;
+    w.acc_off = static_cast<size_t>(round_up(rows * 4 * 4, 256));
+    w.bytes = w.acc_off + static_cast<size_t>(rows) * head_dim * 4;
     return true;
 }
 
@@ -903,8 +909,9 @@ pa::SplitParams split_params(void *out, pa_dtype out_dtype, const void *query, p
     if (w.bytes) {
         p.ws_ml = static_cast<float *>(workspace);
         p.ws_acc = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + w.acc_off);
-        p.ws_prefix = reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(workspace) + w.prefix_off);
         p.cut_row = w.cut_row;
+        p.prefix_cut_row = w.prefix_cut_row;
+        p.cut_cols = w.G;
         p.cut = 1;
     }
     p.err_flag = err_flag;
@@ -1017,7 +1024,7 @@ PA_EXPORT pa_status pa_quant_decode(void *out, pa_dtype out_dtype, const void *q
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const pa_status r = run_split(p, cache, head_dim, w.G, num_seqs, max_context_len, maps, dev, s);
     if (r != PA_OK || w.max_parts <= 1) return r;
-    return pa::launch_split_merge(p, head_dim, cache, 1, 1, dev.sms, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+    return pa::launch_split_merge(p, head_dim, 1, 1, dev.sms, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 PA_EXPORT size_t pa_decode_shared_workspace_size(int num_seqs, int num_groups, int max_group_size, int num_heads,
@@ -1076,7 +1083,7 @@ PA_EXPORT pa_status pa_decode_shared(void *out, pa_dtype out_dtype, const void *
         p.mode = pa::kSplitWhole;
         const pa_status r = run_split(p, cache, head_dim, w.G, num_seqs, max_context_len, maps, dev, s);
         if (r != PA_OK || w.max_parts <= 1) return r;
-        return pa::launch_split_merge(p, head_dim, cache, 1, 1, dev.sms, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+        return pa::launch_split_merge(p, head_dim, 1, 1, dev.sms, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
     }
     if (w.prefix_parts > 0 && w.prefix_tc) {
         if (pa::shared_prefix_smem(head_dim) + 1024 > static_cast<size_t>(dev.smem_optin)) return PA_ERR_UNSUPPORTED;
@@ -1094,7 +1101,8 @@ PA_EXPORT pa_status pa_decode_shared(void *out, pa_dtype out_dtype, const void *
     } else if (w.prefix_parts > 0) {
         pa::SplitParams pre = p;
         pre.mode = pa::kSplitPrefix;
-        pre.cut = 0;
+        pre.cut_row = w.prefix_cut_row;
+        pre.cut_cols = w.prefix_cols;
         pre.partition_size = w.prefix_part;
         pre.chunk_seqs = w.prefix_cols / w.G;
         pre.chunks = (max_group_size + pre.chunk_seqs - 1) / pre.chunk_seqs;
@@ -1108,7 +1116,7 @@ PA_EXPORT pa_status pa_decode_shared(void *out, pa_dtype out_dtype, const void *
     p.late_wait = w.prefix_parts > 0;
     const pa_status r = run_split(p, cache, head_dim, w.G, num_seqs, max_context_len, maps, dev, s);
     if (r != PA_OK) return r;
-    return pa::launch_split_merge(p, head_dim, cache, std::max(1, w.prefix_part), w.prefix_per, dev.sms, s) == cudaSuccess
+    return pa::launch_split_merge(p, head_dim, std::max(1, w.prefix_part), w.prefix_per, dev.sms, s) == cudaSuccess
                ? PA_OK
                : PA_ERR_CUDA;
 }

@@ -531,10 +531,11 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
             const int hq = row & (G - 1);
             if (row < rows) {
                 const int64_t mine = ((at + (duo ? 0 : x)) << lg) + hq;
-                *reinterpret_cast<float2 *>(p.ws_ml + 2 * mine) =
-                    none ? make_float2(-CUDART_INF_F, 0.f) : make_float2(m_run, l_run);
+                *reinterpret_cast<float4 *>(p.ws_ml + 4 * mine) =
+                    none ? make_float4(-CUDART_INF_F, 0.f, 0.f, 0.f) : make_float4(m_run, l_run, 0.f, 0.f);
                 if (duo)   // two query tiles write one partial per range
-                    *reinterpret_cast<float2 *>(p.ws_ml + 2 * (((at + 1) << lg) + hq)) = make_float2(-CUDART_INF_F, 0.f);
+                    *reinterpret_cast<float4 *>(p.ws_ml + 4 * (((at + 1) << lg) + hq)) =
+                        make_float4(-CUDART_INF_F, 0.f, 0.f, 0.f);
             }
             if (!none) {
                 float *dst = p.ws_acc + (((at + (duo ? 0 : x)) << lg) + hq) * D;

@@ -17,9 +17,9 @@ constexpr int kCacheF16 = 0, kCacheBF16 = 1, kCacheE4M3 = 2, kCacheInt8 = 3;
 // Entries (sequences, or chunks of groups) of one launch: the kernel keeps 12
 // bytes for each in shared memory; longer lists take several launches.
 constexpr int kSplitEntries = 2048;
-constexpr int kSplitPrefixWords = kSplitEntries + 2;
 // CTAs of a launch at most (a row of the workspace for each).
 constexpr int kSplitMaxCtas = 256;
+constexpr int kRowFinal = -1, kRowCut = 1;
 
 // What a launch's entries are.
 constexpr int kSplitDecode = 0;   // sequences, whole contexts; results final where one partition holds them
@@ -46,12 +46,15 @@ struct SplitParams {
     int partition_size;          // tokens per partition, a multiple of 16, at most 32 blocks
     int max_parts;               // partial results per (sequence, KV head) in the workspace
     int part_off;                // where this launch's start among them
-    float *ws_ml;                // [rows, 2]  (reference, sum); a row per (sequence, KV head, part, head of the
-                                 // group), then per (launch, CTA, head of its box, head of the group)
-    float *ws_acc;               // [rows, D]
-    int cut;                     // decode, suffix, whole: CTAs take equal shares of the slots, items may be cut
-    int64_t cut_row;             // where the CTAs' rows start
-    uint32_t *ws_prefix;         // per launch: CTAs (0: nothing was cut), slots before each entry
+    // Workspace rows: one per (sequence, KV head, part, head of the group), then
+    // those of cut items, per (launch, CTA, head of its box, query row).
+    float *ws_ml;                // [rows, 4]: reference, sum, and as ints 0, kRowFinal (the output is written) or
+                                 // kRowCut with the row, after cut_row, of what the next CTA did of the item
+    float *ws_acc;               // [rows, D]: weighted sum
+    int cut;                     // CTAs take equal shares of the slots, items may be cut
+    int cut_cols;                // query rows per head in a cut item's rows
+    int64_t cut_row;             // where the cut items' rows of this launch start
+    int64_t prefix_cut_row;      // join: where those of the prefix launches start
     const float *k_scales;       // 8-bit caches: [num_blocks, bs, Hkv]
     const float *v_scales;
     int *err_flag;
@@ -106,7 +109,7 @@ cudaError_t launch_split_int8(const SplitParams &p, int head_dim, int cols, cons
 // each prefix_part tokens of its shared blocks at index 0.. and one for each
 // partition_size of the rest at p.part_off.. (p.mode kSplitDecode: no shared
 // blocks, and sequences of one partition are final already).
-cudaError_t launch_split_merge(const SplitParams &p, int head_dim, int cache, int prefix_part, int per_part, int sms,
+cudaError_t launch_split_merge(const SplitParams &p, int head_dim, int prefix_part, int per_part, int sms,
                                cudaStream_t stream);
 
 // Quantising write and read-back (cache: kCacheE4M3 or kCacheInt8).

@@ -76,7 +76,7 @@ struct SlotMeta {
     int seq;         // the entry's first query sequence; < 0: no more work
     int kvh0;        // first KV head of the box
     int part;
-    int flags;       // kFirst | kLast | kFinal | kContinued, members << 8
+    int flags;       // kFirst | kLast and one of kFinal, kContinued, kCut, members << 8
     int ntok;        // valid tokens from the slot's first
     uint32_t bad;    // bit 2 i (+ 1): rows 0-7 (8-15) of the slot's stage i were not loaded
     int pad[2];
@@ -85,6 +85,7 @@ constexpr int kFirst = 1;    // the first slot of an item (of this CTA's part of
 constexpr int kLast = 2;     // its last slot: write the results
 constexpr int kFinal = 4;    // the item is the whole of the sequence's context
 constexpr int kContinued = 8;   // the item was begun by the CTA before: the result goes to this CTA's own row
+constexpr int kCut = 16;        // the CTA behind goes on with the item
 
 __device__ __forceinline__ void arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
@@ -190,10 +191,10 @@ __device__ __forceinline__ bool bad_group(const SplitParams &p, int g, int q0, i
            (g == p.num_groups - 1 && q1 != p.num_seqs);
 }
 
-// First workspace row of what CTA `cta` of launch `launch` continued, head `head`
-// of its box.
-__device__ __forceinline__ int64_t cut_row_of(const SplitParams &p, int launch, uint32_t cta, int head) {
-    return p.cut_row + ((((static_cast<int64_t>(launch) * kSplitMaxCtas + cta) << p.log2_heads) + head) << p.log2_group);
+// Row, after p.cut_row, of query row `col` of head `head` of a box in what CTA
+// `cta` of this launch continued.
+__device__ __forceinline__ int cut_row_of(const SplitParams &p, uint32_t cta, int head, int col) {
+    return static_cast<int>(((((p.e0 / kSplitEntries) * kSplitMaxCtas + cta) << p.log2_heads) + head) * p.cut_cols + col);
 }
 
 // Items (entry, partition, box of heads) in that order, weighed in slots.  An
@@ -361,14 +362,9 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
     // This CTA takes the items whose first slot lies in its equal share of the
     // slots, or (p.cut, with shares at least as long as an item) exactly its share:
     // an item across the end is continued by the next CTA, which leaves a partial
-    // result of its own.  The join learns from CTA 0 where the shares end.
+    // result of its own, named in the item's.
     const uint32_t total = prefix[E];
     const bool cut = p.cut && total >= gridDim.x * static_cast<uint32_t>((P / kStageTokens + SW - 1) / SW);
-    if (p.cut && blockIdx.x == 0) {
-        uint32_t *w = p.ws_prefix + static_cast<int64_t>(p.e0 / kSplitEntries) * kSplitPrefixWords;
-        for (int i = threadIdx.x; i <= E; i += blockDim.x) w[1 + i] = prefix[i];
-        if (threadIdx.x == 0) w[0] = cut ? gridDim.x : 0u;
-    }
     const uint32_t lo = static_cast<uint32_t>(static_cast<uint64_t>(total) * blockIdx.x / gridDim.x);
     const uint32_t hi = static_cast<uint32_t>(static_cast<uint64_t>(total) * (blockIdx.x + 1) / gridDim.x);
 
@@ -487,7 +483,10 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
             // this CTA's slots of the item
             const int jb = cut && ic.start < lo ? static_cast<int>(lo - ic.start) : 0;
             const int je = cut ? min(ic.nslots, static_cast<int>(hi - ic.start)) : ic.nslots;
-            const int kind = jb > 0 ? kContinued : je == ic.nslots && final_mode(mode) && ic.nparts == 1 ? kFinal : 0;
+            const int kind = jb > 0               ? kContinued
+                             : je < ic.nslots     ? kCut
+                             : final_mode(mode) && ic.nparts == 1 ? kFinal
+                                                                  : 0;
             for (int j = jb; j < je; ++j) {
                 const int slot = take_slot();
                 if (!ok) break;
@@ -983,9 +982,15 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
             const float sc = fin ? (l_run[e] == 0.f ? 0.f : 1.f / l_run[e]) : 1.f;
             const int64_t r =
                 (m.flags & kContinued)
-                    ? cut_row_of(p, p.e0 / kSplitEntries, blockIdx.x, head) + hq
+                    ? p.cut_row + cut_row_of(p, blockIdx.x, head, c)
                     : (((sq * Hkv + kvh) * p.max_parts + p.part_off + m.part) << lg) + hq;
-            if (!fin && g == 0) st_global_hint(p.ws_ml + 2 * r, make_float2(m_run[e], l_run[e]), keep);
+            if (g == 0 && !(fin && p.ws_ml == nullptr)) {
+                const bool more = (m.flags & kCut) != 0;
+                st_global_hint(p.ws_ml + 4 * r,
+                               make_float4(m_run[e], l_run[e], __int_as_float(fin ? kRowFinal : more ? kRowCut : 0),
+                                           __int_as_float(more ? cut_row_of(p, blockIdx.x + 1, head, c) : 0)),
+                               keep);
+            }
             const int64_t orow = fin ? (sq * Hq + (kvh << lg) + hq) * D : r * D;
             auto put2 = [&](int d, float a, float b) {   // two consecutive elements
                 if (!fin)

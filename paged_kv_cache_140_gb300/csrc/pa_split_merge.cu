@@ -5,8 +5,8 @@
 //
 // Bound by latency and by reading the partials, most of which the previous kernel
 // left in L2.  A row (sequence, query head) is joined by 1 to 8 warps, as many as
-// fill the GPU; a warp requests the states and rows of 8 partials at once, so that
-// up to 8 partials cost one trip to memory after the lengths, and carries a
+// fill the GPU; a warp requests the states and rows of 4 partials at once, so that
+// up to 4 partials cost one trip to memory after the lengths, and carries a
 // running (M, l, acc) over further ones.
 #include "pa_split_kernel.cuh"
 
@@ -14,11 +14,11 @@ namespace pa {
 
 namespace {
 
-constexpr int kBatch = 8;     // partials a warp loads at a time
+constexpr int kBatch = 4;     // partials a warp loads at a time
 
 template <int D>
 __global__ void __launch_bounds__(256)
-    split_merge_kernel(const __grid_constant__ SplitParams p, int prefix_part, int per_part, int slot_stages, int wt) {
+    split_merge_kernel(const __grid_constant__ SplitParams p, int prefix_part, int per_part, int wt) {
     constexpr int DPL = D / 32;
     __shared__ float red_o[8][D];
     __shared__ float2 red_ml[8];
@@ -30,106 +30,78 @@ __global__ void __launch_bounds__(256)
     const int hq = row_ok ? static_cast<int>(task % p.num_heads) : 0;
     const int G = 1 << p.log2_group, d0 = lane * DPL;
     pdl_wait();
-    int npre = 0, np = 0, len = 0;
-    uint32_t ctas = 0, before = 0, total = 1;
+    int npre = 0, np = 0;
     if (row_ok) {
-        if (p.cut) {
-            const uint32_t *w = p.ws_prefix + static_cast<int64_t>(s / kSplitEntries) * kSplitPrefixWords;
-            ctas = __ldcg(w);
-            before = __ldcg(w + 1 + s % kSplitEntries);
-            total = __ldcg(w + 1 + min(kSplitEntries, p.num_seqs - s / kSplitEntries * kSplitEntries));
-        }
         const int ctx = context_of(p, s, false);
         int shared = 0;
         if (!final_mode(p.mode)) {
             shared = shared_blocks(p, s, ctx, false) * p.block_size;
             npre = (shared + prefix_part - 1) / prefix_part * per_part;
         }
-        len = ctx - shared;
-        np = npre + (len + p.partition_size - 1) / p.partition_size;
+        np = npre + (ctx - shared + p.partition_size - 1) / p.partition_size;
     }
-    // Of the private parts 32 i .. 32 i + 31 (one per lane): the CTA that
-    // continued mine, or 0.  Slot x lies in CTA ceil((x + 1) ctas / total) - 1.
-    const int grp = (hq >> p.log2_group) >> p.log2_heads, ngroups = p.num_kv_heads >> p.log2_heads;
-    auto continued = [&](int part) -> uint32_t {
-        if (ctas == 0 || part >= np - npre) return 0u;
-        const uint32_t n = item_slots(len, part, p.partition_size, slot_stages);
-        const uint32_t full = (p.partition_size / kStageTokens + slot_stages - 1) / slot_stages;
-        const uint32_t x = before + static_cast<uint32_t>(part) * ngroups * full + grp * n;
-        const uint64_t a = (static_cast<uint64_t>(x + 1) * ctas + total - 1) / total;
-        const uint64_t b = (static_cast<uint64_t>(x + n) * ctas + total - 1) / total;
-        return a != b ? static_cast<uint32_t>(b - 1) : 0u;
-    };
-    const uint32_t cont0 = continued(lane);
-    const bool split0 = __any_sync(kFull, cont0 != 0);
-    const bool active = row_ok && (np > 1 || !final_mode(p.mode) || split0);
+    // A list of one partition has written its output unless it was cut; no other
+    // row is final.  (No private part and no prefix: a zero row.)
+    bool active = row_ok && (np > 0 || !final_mode(p.mode));
     float M = -INFINITY, l = 0.f, o[DPL];
 #pragma unroll
     for (int i = 0; i < DPL; ++i) o[i] = 0.f;
+    auto add = [&](float2 ml, const float (&v)[DPL]) {
+        if (ml.x == -INFINITY && ml.y == 0.f) return;      // empty: its row may be anything
+        const float mb = fmaxf(M, ml.x);
+        const float al = M == -INFINITY ? 1.f : fast_exp2(M - mb);
+        // (a state without a finite reference whose sum is no number counts fully)
+        const float w = ml.x == -INFINITY ? 1.f : fast_exp2(ml.x - mb);
+        M = mb;
+        l = fmaf(ml.y, w, l * al);
+#pragma unroll
+        for (int i = 0; i < DPL; ++i) o[i] = fmaf(v[i], w, o[i] * al);
+    };
+    auto load_row = [&](int64_t r, float (&v)[DPL]) {
+        const float *a = p.ws_acc + r * D + d0;
+        if constexpr (DPL == 4) {
+            const float4 x = __ldcg(reinterpret_cast<const float4 *>(a));
+            v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+        } else {
+            const float2 x = __ldcg(reinterpret_cast<const float2 *>(a));
+            v[0] = x.x; v[1] = x.y;
+        }
+    };
     if (active) {
+        const float4 *states = reinterpret_cast<const float4 *>(p.ws_ml);
         // partial j: workspace row slot(j) * G + head of the group
         const int64_t base = (static_cast<int64_t>(s) * p.num_kv_heads + (hq >> p.log2_group)) * p.max_parts;
-        for (int j0 = sub * kBatch; j0 < np; j0 += wt * kBatch) {
-            // states and rows are requested together; the row of an empty state
-            // (nothing was added) may be anything and is not used
-            float2 ml[kBatch];
+        for (int j0 = sub * kBatch; active && j0 < np; j0 += wt * kBatch) {
+            // states and rows are requested together
+            float4 st[kBatch];
             float v[kBatch][DPL];
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) {
-                ml[u] = make_float2(-INFINITY, 0.f);
+                st[u] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int i = 0; i < DPL; ++i) v[u][i] = 0.f;
                 const int j = j0 + u;
                 if (j < np) {
                     const int64_t r = ((base + (j < npre ? j : p.part_off + j - npre)) << p.log2_group) + (hq & (G - 1));
-                    ml[u] = __ldcg(reinterpret_cast<const float2 *>(p.ws_ml) + r);
-                    const float *a = p.ws_acc + r * D + d0;
-                    if constexpr (DPL == 4) {
-                        const float4 x = __ldcg(reinterpret_cast<const float4 *>(a));
-                        v[u][0] = x.x; v[u][1] = x.y; v[u][2] = x.z; v[u][3] = x.w;
-                    } else {
-                        const float2 x = __ldcg(reinterpret_cast<const float2 *>(a));
-                        v[u][0] = x.x; v[u][1] = x.y;
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < DPL; ++i) v[u][i] = 0.f;
+                    st[u] = __ldcg(states + r);
+                    load_row(r, v[u]);
                 }
             }
-            float mb = M;
-#pragma unroll
-            for (int u = 0; u < kBatch; ++u) mb = fmaxf(mb, ml[u].x);
-            const float al = mb == -INFINITY ? 1.f : fast_exp2(M - mb);
-            M = mb;
-            l *= al;
-#pragma unroll
-            for (int i = 0; i < DPL; ++i) o[i] *= al;
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) {
-                if (ml[u].x == -INFINITY && ml[u].y == 0.f) continue;
-                // (a state without a finite reference whose sum is no number counts fully)
-                const float w = ml[u].x == -INFINITY ? 1.f : fast_exp2(ml[u].x - M);
-                l = fmaf(ml[u].y, w, l);
-#pragma unroll
-                for (int i = 0; i < DPL; ++i) o[i] = fmaf(v[u][i], w, o[i]);
+                const int kind = __float_as_int(st[u].z);
+                if (kind == kRowFinal) active = false;
+                add(make_float2(st[u].x, st[u].y), v[u]);
+                if (kind == kRowCut) {   // few: what a second CTA did of the item
+                    const int64_t r = (j0 + u < npre ? p.prefix_cut_row : p.cut_row) + __float_as_int(st[u].w);
+                    const float4 x = __ldcg(states + r);
+                    float w[DPL];
+                    load_row(r, w);
+                    add(make_float2(x.x, x.y), w);
+                }
             }
         }
-        // parts that a second CTA continued: few
-        for (int c0 = 0; sub == 0 && ctas != 0 && c0 < np - npre; c0 += 32) {
-            const uint32_t mine = c0 == 0 ? cont0 : continued(c0 + lane);
-            for (uint32_t left = __ballot_sync(kFull, mine != 0); left != 0; left &= left - 1) {
-                const uint32_t cta = __shfl_sync(kFull, mine, __ffs(left) - 1);
-                const int64_t r = cut_row_of(p, s / kSplitEntries, cta, (hq >> p.log2_group) & ((1 << p.log2_heads) - 1)) +
-                                  (hq & (G - 1));
-                const float2 ml = __ldcg(reinterpret_cast<const float2 *>(p.ws_ml) + r);
-                const float *a = p.ws_acc + r * D + d0;
-                const float mb = fmaxf(M, ml.x);
-                const float al = mb == -INFINITY ? 1.f : fast_exp2(M - mb);
-                const float w = ml.x == -INFINITY ? 1.f : fast_exp2(ml.x - mb);
-                M = mb;
-                l = fmaf(ml.y, w, l * al);
-#pragma unroll
-                for (int i = 0; i < DPL; ++i) o[i] = fmaf(__ldcg(a + i), w, o[i] * al);
-            }
-        }
+        if (final_mode(p.mode) && np == 0) active = false;
     }
     if (wt > 1) {
 #pragma unroll
@@ -185,16 +157,15 @@ int split_slot_stages(int cache, int log2_heads) {
            log2_heads;
 }
 
-cudaError_t launch_split_merge(const SplitParams &p, int head_dim, int cache, int prefix_part, int per_part, int sms,
+cudaError_t launch_split_merge(const SplitParams &p, int head_dim, int prefix_part, int per_part, int sms,
                                cudaStream_t stream) {
     const int64_t rows = static_cast<int64_t>(p.num_seqs) * p.num_heads;
     // one warp per row, more while the rows leave warps idle and there is something to share out
     int wt = 1;
-    while (wt < 8 && rows * wt * 2 <= static_cast<int64_t>(sms) * 16 && p.max_parts > kBatch * wt) wt *= 2;
+    while (wt < 8 && rows * wt * 2 <= static_cast<int64_t>(sms) * 32 && p.max_parts > kBatch * wt) wt *= 2;
     const int64_t blocks = (rows + 8 / wt - 1) / (8 / wt);
     auto kern = head_dim == 128 ? split_merge_kernel<128> : split_merge_kernel<64>;
-    return launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream, p, prefix_part, per_part,
-                      split_slot_stages(cache, p.log2_heads), wt);
+    return launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream, p, prefix_part, per_part, wt);
 }
 
 }  // namespace pa

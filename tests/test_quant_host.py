@@ -87,9 +87,9 @@ def test_planning(lib):
     assert ws(4, 4, 4, 64, 16, 256, 0) == 0                  # a few ring slots are not cut
     assert ws(256, 40, 40, 128, 16, 256, 0) == 0             # nor are lists that fill the GPU
     assert ws(4, 8, 8, 128, 16, 256, 0) > 0
-    assert ws(256, 40, 40, 128, 16, 2048, 0) >= 256 * 40 * 8 * 130 * 4
+    assert ws(256, 40, 40, 128, 16, 2048, 0) >= 256 * 40 * 4 * 132 * 4
     # few sequences: finer partitions, more partials per row
-    assert ws(1, 8, 8, 128, 16, 8192, 0) >= 8 * 64 * 130 * 4
+    assert ws(1, 8, 8, 128, 16, 8192, 0) >= 8 * 64 * 132 * 4
     assert ws(1, 8, 8, 128, 16, 8192, 8192) == BAD           # more than 32 blocks
     assert ws(1, 12, 8, 128, 16, 100, 0) == BAD
     sh = lib.pa_decode_shared_workspace_size
