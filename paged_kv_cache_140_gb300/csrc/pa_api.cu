@@ -1024,7 +1024,7 @@ PA_EXPORT pa_status pa_quant_decode(void *out, pa_dtype out_dtype, const void *q
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const pa_status r = run_split(p, cache, head_dim, w.G, num_seqs, max_context_len, maps, dev, s);
     if (r != PA_OK || w.max_parts <= 1) return r;
-    return pa::launch_split_merge(p, head_dim, 1, 1, dev.sms, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+    return pa::launch_split_merge(p, head_dim, 1, 1, false, dev.sms, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 PA_EXPORT size_t pa_decode_shared_workspace_size(int num_seqs, int num_groups, int max_group_size, int num_heads,
@@ -1083,7 +1083,7 @@ PA_EXPORT pa_status pa_decode_shared(void *out, pa_dtype out_dtype, const void *
         p.mode = pa::kSplitWhole;
         const pa_status r = run_split(p, cache, head_dim, w.G, num_seqs, max_context_len, maps, dev, s);
         if (r != PA_OK || w.max_parts <= 1) return r;
-        return pa::launch_split_merge(p, head_dim, 1, 1, dev.sms, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+        return pa::launch_split_merge(p, head_dim, 1, 1, false, dev.sms, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
     }
     if (w.prefix_parts > 0 && w.prefix_tc) {
         if (pa::shared_prefix_smem(head_dim) + 1024 > static_cast<size_t>(dev.smem_optin)) return PA_ERR_UNSUPPORTED;
@@ -1116,7 +1116,8 @@ PA_EXPORT pa_status pa_decode_shared(void *out, pa_dtype out_dtype, const void *
     p.late_wait = w.prefix_parts > 0;
     const pa_status r = run_split(p, cache, head_dim, w.G, num_seqs, max_context_len, maps, dev, s);
     if (r != PA_OK) return r;
-    return pa::launch_split_merge(p, head_dim, std::max(1, w.prefix_part), w.prefix_per, dev.sms, s) == cudaSuccess
+    return pa::launch_split_merge(p, head_dim, std::max(1, w.prefix_part), w.prefix_per,
+                                  static_cast<int64_t>(max_group_size) * w.G > pa::kSharedTile, dev.sms, s) == cudaSuccess
                ? PA_OK
                : PA_ERR_CUDA;
 }

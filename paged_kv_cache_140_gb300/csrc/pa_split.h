@@ -108,8 +108,9 @@ cudaError_t launch_split_int8(const SplitParams &p, int head_dim, int cols, cons
 // Joins partial results into output rows.  Sequence s has per_part partials for
 // each prefix_part tokens of its shared blocks at index 0.. and one for each
 // partition_size of the rest at p.part_off.. (p.mode kSplitDecode: no shared
-// blocks, and sequences of one partition are final already).
-cudaError_t launch_split_merge(const SplitParams &p, int head_dim, int prefix_part, int per_part, int sms,
+// blocks, and sequences of one partition are final already).  holes: every second
+// partial of a prefix may be empty.
+cudaError_t launch_split_merge(const SplitParams &p, int head_dim, int prefix_part, int per_part, bool holes, int sms,
                                cudaStream_t stream);
 
 // Quantising write and read-back (cache: kCacheE4M3 or kCacheInt8).
