@@ -697,18 +697,20 @@ int split_partition(int64_t lists, int64_t boxes, int64_t len, int block_size, i
 constexpr int kSharedSplitRows = 16;
 
 // Tokens per unit of the tensor-core prefix kernel, for `lists` lists (groups x
-// pairs x KV heads) of up to `tokens`: the cut with the least estimated time,
-// whole waves of CTAs over the GPU's SMs times the tiles of one unit (a tile
-// costs about half as much where one query tile's products, not two, wait on it)
-// plus a CTA's own start and end, worth about 5 tiles.
-int shared_unit(int64_t lists, int tokens, bool two_tiles) {
+// tiles x KV heads) of up to `tokens`: the cut with the least estimated time, whole
+// waves of CTAs times the tiles of one unit plus a CTA's own start and end.  Pairs
+// of query tiles take one CTA per SM, about 2 us per K/V tile and five times that to
+// start and end; single ones two, each a little slower, which hide one another's
+// ends.
+int shared_unit(int64_t lists, int tokens, bool paired) {
     const int tiles = std::max(1, (tokens + pa::kSharedTile - 1) / pa::kSharedTile);
-    const double tile = two_tiles ? 1.0 : 0.6;
+    const int64_t ctas = paired ? kSmsTarget : 2 * kSmsTarget;
+    const double tile = paired ? 1.0 : 1.1, ends = paired ? 5.0 : 3.0;
     int best = tiles;
     double best_cost = 1e30;
     for (int per = tiles; per >= 1; per = std::min(per - 1, per * 15 / 16)) {
         const int64_t units = lists * ((tiles + per - 1) / per);
-        const double cost = static_cast<double>((units + kSmsTarget - 1) / kSmsTarget) * (per * tile + 5.0);
+        const double cost = static_cast<double>((units + ctas - 1) / ctas) * (per * tile + ends);
         if (cost < best_cost) {
             best_cost = cost;
             best = per;
@@ -729,7 +731,8 @@ struct SplitPlan {
     bool whole = false;          // shared prefixes are not worth a pass of their own
     bool prefix_tc = false;      // shared prefixes: on the tensor-core kernel (else the split kernel)
     int prefix_cols = 0;         // split kernel: query rows per entry
-    int prefix_pairs = 0;        // tensor-core kernel: pairs of query tiles per group
+    bool prefix_paired = false;  // tensor-core kernel: query tiles in pairs (more than one per group)
+    int prefix_tiles = 0;        // query tiles (pairs) per group
     int prefix_part = 0;         // tokens per prefix_per partials
     int prefix_per = 1, prefix_parts = 0;
     int max_parts = 1;
@@ -773,10 +776,12 @@ bool plan_split(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int
         const int64_t rows = static_cast<int64_t>(max_group_size) * w.G;
         w.prefix_tc = rows > kSharedSplitRows && block_size <= pa::kSharedTile && (block_size & (block_size - 1)) == 0;
         if (w.prefix_tc) {
-            w.prefix_pairs = static_cast<int>((rows + 2 * pa::kSharedTile - 1) / (2 * pa::kSharedTile));
-            w.prefix_part = shared_unit(static_cast<int64_t>(num_groups) * w.prefix_pairs * num_kv_heads, shared_tokens,
-                                        rows > pa::kSharedTile);
-            w.prefix_per = 2;
+            w.prefix_paired = rows > pa::kSharedTile;
+            w.prefix_per = w.prefix_paired ? 2 : 1;
+            const int per = w.prefix_per * pa::kSharedTile;
+            w.prefix_tiles = static_cast<int>((rows + per - 1) / per);
+            w.prefix_part = shared_unit(static_cast<int64_t>(num_groups) * w.prefix_tiles * num_kv_heads, shared_tokens,
+                                        w.prefix_paired);
         }
         w.prefix_cols = w.G;
         while (w.prefix_cols < 8 && w.prefix_cols < static_cast<int64_t>(max_group_size) * w.G) w.prefix_cols *= 2;
@@ -1088,15 +1093,15 @@ PA_EXPORT pa_status pa_decode_shared(void *out, pa_dtype out_dtype, const void *
     if (w.prefix_parts > 0 && w.prefix_tc) {
         if (pa::shared_prefix_smem(head_dim) + 1024 > static_cast<size_t>(dev.smem_optin)) return PA_ERR_UNSUPPORTED;
         const int ranges = w.prefix_parts / w.prefix_per, tile_seqs = pa::kSharedTile / w.G;
-        if (static_cast<int64_t>(num_groups) * ranges * num_kv_heads * w.prefix_pairs >= (int64_t{1} << 31))
+        if (static_cast<int64_t>(num_groups) * ranges * num_kv_heads * w.prefix_tiles >= (int64_t{1} << 31))
             return PA_ERR_UNSUPPORTED;
         CUtensorMap tq, sk, sv;
         if (!encode_map_128b(&tq, query, 2, head_dim, num_heads, num_seqs, w.G, tile_seqs) ||
             !encode_map_128b(&sk, k_cache, 2, head_dim, num_kv_heads, num_blocks * block_size, 1, block_size) ||
             !encode_map_128b(&sv, v_cache, 2, head_dim, num_kv_heads, num_blocks * block_size, 1, block_size))
             return PA_ERR_CUDA;
-        if (pa::launch_shared_prefix(p, head_dim, kv_dtype == PA_BF16, w.prefix_pairs, w.prefix_part, ranges, tq, sk, sv,
-                                     s) != cudaSuccess)
+        if (pa::launch_shared_prefix(p, head_dim, kv_dtype == PA_BF16, w.prefix_paired, w.prefix_tiles, w.prefix_part,
+                                     ranges, tq, sk, sv, s) != cudaSuccess)
             return PA_ERR_CUDA;
     } else if (w.prefix_parts > 0) {
         pa::SplitParams pre = p;
@@ -1117,7 +1122,7 @@ PA_EXPORT pa_status pa_decode_shared(void *out, pa_dtype out_dtype, const void *
     const pa_status r = run_split(p, cache, head_dim, w.G, num_seqs, max_context_len, maps, dev, s);
     if (r != PA_OK) return r;
     return pa::launch_split_merge(p, head_dim, std::max(1, w.prefix_part), w.prefix_per,
-                                  static_cast<int64_t>(max_group_size) * w.G > pa::kSharedTile, dev.sms, s) == cudaSuccess
+                                  w.prefix_tc && w.prefix_paired, dev.sms, s) == cudaSuccess
                ? PA_OK
                : PA_ERR_CUDA;
 }

@@ -43,17 +43,21 @@ namespace {
 
 constexpr int kTile = kSharedTile;
 constexpr int kRegion = kTile * 128;     // 128 rows x 128 bytes: one swizzled operand region
-constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColS = 0, kColO = 256;   // S/P of stream X at 128 X, O of X at 256 + 128 X
-constexpr int kWarpK = 8, kWarpMma = 9, kWarpV = 10;
-constexpr int kSharedThreads = 11 * 32;
+// NS streams: S/P of stream X in tensor-memory columns 128 X, O of X behind them.
+template <int NS> struct Streams {
+    static constexpr uint32_t kCols = 256 * NS, kColO = 128 * NS;
+    static constexpr int kWarpK = 4 * NS, kWarpMma = kWarpK + 1, kWarpV = kWarpK + 2;
+    static constexpr int kThreads = (4 * NS + 3) * 32;
+    static constexpr int kCtas = 3 - NS;     // per SM
+};
 constexpr int kChunks = 4;
 constexpr int kMaxRing = 4;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
-template <int D> struct SharedRings;
-template <> struct SharedRings<128> { static constexpr int N = 2; };
-template <> struct SharedRings<64> { static constexpr int N = 4; };
+// K and V tiles in flight, each: what fits next to the query tiles (two streams:
+// two of them and one CTA per SM; one stream: one and two CTAs).
+template <int D, int NS> constexpr int kSharedRing = (D == 128 ? 1 : 2) * NS;
+template <int D, int NS> constexpr size_t kSharedSmem = 1024 + static_cast<size_t>(D / 64) * kRegion * (NS + 2 * kSharedRing<D, NS>);
 
 struct PrefixShared {
     uint64_t q_full;
@@ -187,14 +191,16 @@ __device__ __forceinline__ void load_tile(TableWindow &win, int tile, int bs, in
     }
 }
 
-template <int D, bool BF16>
-__global__ void __launch_bounds__(kSharedThreads, 1)
-    shared_prefix_kernel(const __grid_constant__ SplitParams p, int pairs, int unit_tokens, int units_per_list,
+template <int D, bool BF16, int NS>
+__global__ void __launch_bounds__(Streams<NS>::kThreads, Streams<NS>::kCtas)
+    shared_prefix_kernel(const __grid_constant__ SplitParams p, int tiles, int unit_tokens, int units_per_list,
                          const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                          const __grid_constant__ CUtensorMap tv) {
     constexpr int R = D / 64;               // 128-byte regions per row
     constexpr int kOp = R * kRegion;        // one 128-row operand tile
-    constexpr int NR = SharedRings<D>::N;   // K and V tiles in flight
+    constexpr int NR = kSharedRing<D, NS>;
+    using W = Streams<NS>;
+    constexpr uint32_t kColS = 0, kColO = W::kColO;
     constexpr int kKSteps = D / 16;
     constexpr int kPVSteps = kTile / 16;
     constexpr uint32_t kIdescQK = umma::idesc_f16(BF16, kTile, kTile, false);
@@ -204,13 +210,13 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~static_cast<uintptr_t>(1023));
-    uint8_t *sQ = base, *sK = sQ + 2 * kOp, *sV = sK + NR * kOp;
+    uint8_t *sQ = base, *sK = sQ + NS * kOp, *sV = sK + NR * kOp;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    // ---- work unit: pairs of one K/V range run next to each other (L2) ----
+    // ---- work unit: the query tiles (pairs of them) of one K/V range run next to each other (L2) ----
     int u = blockIdx.x;
-    const int pi = u % pairs;
-    u /= pairs;
+    const int pi = u % tiles;
+    u /= tiles;
     const int kvh = u % p.num_kv_heads;
     u /= p.num_kv_heads;
     const int range = u % units_per_list, g = u / units_per_list;
@@ -232,19 +238,18 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
             if (__ldg(p.shared_lens + s) != n0) report(p.err_flag, PA_FLAG_BAD_CONTEXT_LEN);
     }
     const int len = shared_blocks(p, q0, context_of(p, q0, false), false) * p.block_size;
-    const int t0 = range * unit_tokens, tA = pi * 2 * TT;   // first token, first sequence of the group
+    const int t0 = range * unit_tokens, tA = pi * NS * TT;  // first token, first sequence of the group
     if (t0 >= len || tA >= q1 - q0) return;
-    const int n_seq = q1 - q0 - tA;                         // sequences from this pair's first on
-    const bool duo = n_seq > TT;                            // two query tiles
+    const int n_seq = NS == 1 ? min(TT, q1 - q0 - tA) : q1 - q0 - tA;   // sequences from this unit's first on
+    const bool duo = NS == 2 && n_seq > TT;                 // two query tiles
     const int end = min(len, t0 + unit_tokens);
     const int tile0 = t0 / kTile;
     const int nt = (end - t0 + kTile - 1) / kTile;          // K/V tiles of the range
-    const int nA = duo ? nt : (nt + 1) / 2, nB = nt - (duo ? 0 : nA);
-    const int total = duo ? nt : nA + nB;                   // K/V tiles loaded (= nt)
+    const int nA = duo || NS == 1 ? nt : (nt + 1) / 2, nB = duo ? nt : nt - nA;
     // The last tile reaches past the prefix: its V rows there, not loaded, are
     // zeroed before a product reads them (0 x NaN).
     const bool zero_tail = (end - t0) % kTile != 0;
-    const int zx = duo || nB > 0 ? 1 : 0;                   // the stream that zeroes them
+    const int zx = nB > 0 ? 1 : 0;                          // the stream that zeroes them
 
     if (threadIdx.x == 0) {
         mbar_init(&sh.q_full, 1);
@@ -254,7 +259,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
             mbar_init(&sh.v_full[i], 1);
             mbar_init(&sh.v_empty[i], 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < NS; ++i) {
             mbar_init(&sh.s_full[i], 1);
             for (int c = 0; c < kChunks; ++c) mbar_init(&sh.p_full[i][c], 128);
         }
@@ -264,8 +269,8 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
         sh.bad = 0;
         fence_barrier_init();
     }
-    if (warp == kWarpMma) {
-        umma::tmem_alloc(smem_addr(&sh.tmem_base), kTmemCols);
+    if (warp == W::kWarpMma) {
+        umma::tmem_alloc(smem_addr(&sh.tmem_base), W::kCols);
         umma::tmem_relinquish();
     }
     umma::fence_before_sync();
@@ -274,11 +279,11 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
     const uint32_t tmem = sh.tmem_base;
 
     // K/V tile number (in load order) of stream x's i-th tile, and back
-    auto seqno = [&](int x, int i) { return duo ? i : i < nB ? 2 * i + x : nB + i; };
+    auto seqno = [&](int x, int i) { return duo || NS == 1 ? i : i < nB ? 2 * i + x : nB + i; };
 
-    if (warp == kWarpK || warp == kWarpV) {
+    if (warp == W::kWarpK || warp == W::kWarpV) {
         // ---------------------------------------------------- TMA loaders
-        const bool is_k = warp == kWarpK;
+        const bool is_k = warp == W::kWarpK;
         const CUtensorMap *map = is_k ? &tk : &tv;
         uint64_t *full = is_k ? sh.k_full : sh.v_full;
         uint64_t *empty = is_k ? sh.k_empty : sh.v_empty;
@@ -298,11 +303,11 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
         const int32_t *table = p.block_tables + static_cast<int64_t>(q0) * p.max_blocks_per_seq;
         TableWindow winA{table, len / p.block_size}, winB{table, len / p.block_size};
         int issued = 0;
-        for (int s = 0; s < total; ++s) {
+        for (int s = 0; s < nt; ++s) {
             const int st = s % NR;
             if (s >= NR && !warp_wait(&empty[st], ((s / NR) - 1) & 1, sh, p.err_flag)) break;
-            const bool inB = !duo && s < 2 * nB && (s & 1);
-            const int tile = tile0 + (duo ? s : inB ? nA + (s >> 1) : s < 2 * nB ? s >> 1 : s - nB);
+            const bool inB = NS == 2 && !duo && s < 2 * nB && (s & 1);
+            const int tile = tile0 + (duo || NS == 1 ? s : inB ? nA + (s >> 1) : s < 2 * nB ? s >> 1 : s - nB);
             load_tile<R>(inB ? winB : winA, tile, p.block_size, end, kvh, p.num_blocks, ring + st * kOp, map, &full[st],
                          lane, sh, p.err_flag);
             ++issued;
@@ -313,14 +318,14 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
                 mbar_wait_bounded(&full[s % NR], (s / NR) & 1, kWaitLimitNs);
             if (is_k) mbar_wait_bounded(&sh.q_full, 0, kWaitLimitNs);
         }
-    } else if (warp == kWarpMma) {
+    } else if (warp == W::kWarpMma) {
         // ------------------------------------------------------- MMA issuer
         const bool leader = elect_one();
         const uint64_t qd0 = umma::desc_sw128(smem_addr(sQ), 16, 1024);
         const uint64_t kd0 = umma::desc_sw128(smem_addr(sK), 16, 1024);
         const uint64_t vd0 = umma::desc_sw128(smem_addr(sV), kRegion, 1024);
         constexpr uint32_t kOpDesc = kOp >> 4;
-        const int nx[2] = {nA, duo ? nt : nB};
+        const int nx[2] = {nA, nB};
         bool ok = warp_wait(&sh.q_full, 0, sh, p.err_flag);
         auto qk = [&](int x, int i) -> bool {   // S_x = Q_x K^T
             const int s = seqno(x, i), st = s % NR;
@@ -345,7 +350,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
         if (ok) ok = qk(0, 0);
         if (ok && nx[1] > 0) ok = qk(1, 0);
         for (int i = 0; ok && i < nA; ++i) {
-            for (int x = 0; ok && x < 2; ++x) {
+            for (int x = 0; ok && x < NS; ++x) {
                 if (i >= nx[x]) continue;
                 const int s = seqno(x, i), st = s % NR;
                 if (zero_tail && i == nx[x] - 1 && (duo || x == zx) && !warp_wait(&sh.zeroed, 0, sh, p.err_flag)) {
@@ -392,11 +397,11 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
         __syncwarp();
     } else {
         // -------------------------------------------- softmax and output
-        const int x = (warp >> 2) & 1, q4 = warp & 3;
+        const int x = NS == 2 ? (warp >> 2) & 1 : 0, q4 = warp & 3;
         const int row = 32 * q4 + lane;                     // of the query tile
         const int rows = (duo ? min(TT, n_seq - x * TT) : n_seq) << lg;
         const bool live = 32 * q4 < rows;                   // some row of this warp is a query
-        const int n = x == 0 ? nA : duo ? nt : nB;
+        const int n = x == 0 ? nA : nB;
         const uint32_t lane_off = static_cast<uint32_t>(32 * q4) << 16;
         const uint32_t tS = tmem + kColS + 128u * x + lane_off;
         const uint32_t tO = tmem + kColO + 128u * x + lane_off;
@@ -436,25 +441,49 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
                 for (int c = 0; c < kChunks; ++c) arrive(&sh.p_full[x][c]);
                 continue;
             }
-            uint32_t v[kTile];
+            // Two streams: the row's 128 scores stay in registers.  One stream, two
+            // CTAs per SM and so 128 registers: they are read twice, 32 at a time,
+            // for the maximum and for the weights.
+            constexpr int kHeld = NS == 2 ? kTile : 32;
+            uint32_t v[kHeld];
+            auto mask = [&](uint32_t *w, int c) {        // columns 32 c .. of the last tile
+                if (lim < kTile) {
 #pragma unroll
-            for (int c = 0; c < kChunks; ++c)
-                umma::ld_32x32b_x32(tS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(v + 32 * c));
-            umma::wait_ld();
-            if (lim < kTile) {
+                    for (int i = 0; i < 32; ++i)
+                        if (32 * c + i >= lim) w[i] = 0xff800000u;     // -inf
+                }
+            };
+            float mx;
+            if constexpr (NS == 2) {
 #pragma unroll
-                for (int i = 0; i < kTile; ++i)
-                    if (i >= lim) v[i] = 0xff800000u;     // -inf
+                for (int c = 0; c < kChunks; ++c)
+                    umma::ld_32x32b_x32(tS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(v + 32 * c));
+                umma::wait_ld();
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c) mask(v + 32 * c, c);
+                float a[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) a[k] = fmaxf(__uint_as_float(v[k]), __uint_as_float(v[k + 8]));
+#pragma unroll
+                for (int i = 1; i < kTile / 16; ++i)
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        a[k] = max3(a[k], __uint_as_float(v[16 * i + k]), __uint_as_float(v[16 * i + 8 + k]));
+                mx = max3(max3(a[0], a[1], a[2]), max3(a[3], a[4], a[5]), fmaxf(a[6], a[7]));
+            } else {
+                mx = -CUDART_INF_F;
+                uint32_t w[32];
+#pragma unroll
+                for (int c = 0; c < kChunks; c += 2) {   // two loads in flight
+                    umma::ld_32x32b_x32(tS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(v));
+                    umma::ld_32x32b_x32(tS + 32 * c + 32, w);
+                    umma::wait_ld();
+                    mask(v, c);
+                    mask(w, c + 1);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) mx = max3(mx, __uint_as_float(v[i]), __uint_as_float(w[i]));
+                }
             }
-            float a[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) a[k] = fmaxf(__uint_as_float(v[k]), __uint_as_float(v[k + 8]));
-#pragma unroll
-            for (int i = 1; i < kTile / 16; ++i)
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    a[k] = max3(a[k], __uint_as_float(v[16 * i + k]), __uint_as_float(v[16 * i + 8 + k]));
-            const float mx = max3(max3(a[0], a[1], a[2]), max3(a[3], a[4], a[5]), fmaxf(a[6], a[7]));
             const float x_tile = mx * sl;
             // The reference is 2^7 below the maximum it was set by and moves when that
             // grows by more than 2^8: binary16 weights reach 2^15 and end at 2^-24,
@@ -492,12 +521,19 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
             uint64_t acc0 = f2(0.f, 0.f), acc1 = f2(0.f, 0.f);
 #pragma unroll
             for (int c = 0; c < kChunks; ++c) {
+                constexpr bool kReload = NS == 1;
+                if constexpr (kReload) {
+                    umma::ld_32x32b_x32(tS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(v));
+                    umma::wait_ld();
+                    mask(v, c);
+                }
+                const uint32_t *vc = v + (kReload ? 0 : 32 * c);
                 uint32_t hi[16];
                 [[maybe_unused]] uint32_t lo[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const float2 xv = unf2(
-                        fma2(f2(__uint_as_float(v[32 * c + 2 * i]), __uint_as_float(v[32 * c + 2 * i + 1])), sl2, nm2));
+                    const float2 xv =
+                        unf2(fma2(f2(__uint_as_float(vc[2 * i]), __uint_as_float(vc[2 * i + 1])), sl2, nm2));
                     const float p0 = fast_exp2(xv.x), p1 = fast_exp2(xv.y);
                     hi[i] = pack2<BF16>(p0, p1);
                     const float2 hv = Half2x<BF16>::to_float2(hi[i]);
@@ -527,7 +563,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
             const bool bad = *reinterpret_cast<volatile int *>(&sh.bad) != 0;
             const bool none = n == 0 || bad;                // nothing to add: an empty partial
             const int64_t sq = q0 + tA + (duo ? x * TT : 0) + (row >> lg);
-            const int64_t at = (sq * p.num_kv_heads + kvh) * p.max_parts + 2 * range;
+            const int64_t at = (sq * p.num_kv_heads + kvh) * p.max_parts + NS * range;
             const int hq = row & (G - 1);
             if (row < rows) {
                 const int64_t mine = ((at + (duo ? 0 : x)) << lg) + hq;
@@ -557,40 +593,43 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
 
     umma::fence_before_sync();
     __syncthreads();
-    if (warp == kWarpMma) {
+    if (warp == W::kWarpMma) {
         umma::fence_after_sync();
-        umma::tmem_dealloc(tmem, kTmemCols);
+        umma::tmem_dealloc(tmem, W::kCols);
     }
 }
 
-template <int D, bool BF16>
-cudaError_t launch_t(const SplitParams &p, int pairs, int unit_tokens, int units_per_list, const CUtensorMap &tq,
+template <int D, bool BF16, int NS>
+cudaError_t launch_t(const SplitParams &p, int tiles, int unit_tokens, int units_per_list, const CUtensorMap &tq,
                      const CUtensorMap &tk, const CUtensorMap &tv, cudaStream_t stream) {
-    auto kern = shared_prefix_kernel<D, BF16>;
-    const size_t smem = shared_prefix_smem(D);
-    const cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    auto kern = shared_prefix_kernel<D, BF16, NS>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(kSharedSmem<D, NS>));
     if (e != cudaSuccess) return e;
-    const int64_t grid = static_cast<int64_t>(p.num_groups) * units_per_list * p.num_kv_heads * pairs;
-    return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(kSharedThreads), smem, stream, p, pairs, unit_tokens,
-                      units_per_list, tq, tk, tv);
+    const int64_t grid = static_cast<int64_t>(p.num_groups) * units_per_list * p.num_kv_heads * tiles;
+    return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(Streams<NS>::kThreads), kSharedSmem<D, NS>, stream, p,
+                      tiles, unit_tokens, units_per_list, tq, tk, tv);
+}
+
+template <int D>
+cudaError_t launch_d(const SplitParams &p, bool bf16, bool pairs, int tiles, int unit_tokens, int units_per_list,
+                     const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, cudaStream_t stream) {
+    if (pairs)
+        return bf16 ? launch_t<D, true, 2>(p, tiles, unit_tokens, units_per_list, tq, tk, tv, stream)
+                    : launch_t<D, false, 2>(p, tiles, unit_tokens, units_per_list, tq, tk, tv, stream);
+    return bf16 ? launch_t<D, true, 1>(p, tiles, unit_tokens, units_per_list, tq, tk, tv, stream)
+                : launch_t<D, false, 1>(p, tiles, unit_tokens, units_per_list, tq, tk, tv, stream);
 }
 
 }  // namespace
 
-size_t shared_prefix_smem(int head_dim) {
-    const size_t op = static_cast<size_t>(head_dim / 64) * kRegion;
-    return 1024 + op * (2 + 2 * (head_dim == 128 ? SharedRings<128>::N : SharedRings<64>::N));
-}
+size_t shared_prefix_smem(int head_dim) { return head_dim == 128 ? kSharedSmem<128, 2> : kSharedSmem<64, 2>; }
 
-cudaError_t launch_shared_prefix(const SplitParams &p, int head_dim, bool bf16, int pairs, int unit_tokens,
+cudaError_t launch_shared_prefix(const SplitParams &p, int head_dim, bool bf16, bool pairs, int tiles, int unit_tokens,
                                  int units_per_list, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                                  cudaStream_t stream) {
-    if (head_dim == 128)
-        return bf16 ? launch_t<128, true>(p, pairs, unit_tokens, units_per_list, tq, tk, tv, stream)
-                    : launch_t<128, false>(p, pairs, unit_tokens, units_per_list, tq, tk, tv, stream);
-    return bf16 ? launch_t<64, true>(p, pairs, unit_tokens, units_per_list, tq, tk, tv, stream)
-                : launch_t<64, false>(p, pairs, unit_tokens, units_per_list, tq, tk, tv, stream);
+    return head_dim == 128 ? launch_d<128>(p, bf16, pairs, tiles, unit_tokens, units_per_list, tq, tk, tv, stream)
+                           : launch_d<64>(p, bf16, pairs, tiles, unit_tokens, units_per_list, tq, tk, tv, stream);
 }
 
 }  // namespace pa
