@@ -693,23 +693,30 @@ int split_partition(int64_t lists, int64_t boxes, int64_t len, int block_size, i
 
 // A group with more query rows per KV head than this has its prefix computed on
 // the tensor-core kernel, whose 128-row tiles read each K/V row once for up to
-// 256 query rows; up to it the split kernel reads them once for every 8.
-constexpr int kSharedSplitRows = 16;
+// 256 query rows; up to it the split kernel does, which reads them once for every
+// 8 rows.  Whole calls, 16 prompts of 2,000 tokens: 8 rows 51 us split against 57,
+// 12 rows 72 against 61, 24 rows 93 against 69 (one prompt of 4,000 to 8,000 tokens:
+// 33 against 27, 30 against 24, 34 against 24; 64 of 1,000 with 4 rows 256 against 282).
+constexpr int kSharedSplitRows = 8;
 
 // Tokens per unit of the tensor-core prefix kernel, for `lists` lists (groups x
 // tiles x KV heads) of up to `tokens`: the cut with the least estimated time, whole
 // waves of CTAs times the tiles of one unit plus a CTA's own start and end.  Pairs
 // of query tiles take one CTA per SM, about 2 us per K/V tile and five times that to
 // start and end; single ones two, each a little slower, which hide one another's
-// ends.
-int shared_unit(int64_t lists, int tokens, bool paired) {
+// ends.  The prefixes of several groups are taken to be of any length up to the
+// longest alike, with a tenth more units than that gives: a second wave costs more
+// than longer units (24 groups of 0 to 4,096 tokens: 130 us, with shorter units 135
+// to 148).
+int shared_unit(int64_t lists, int tokens, bool paired, bool several) {
     const int tiles = std::max(1, (tokens + pa::kSharedTile - 1) / pa::kSharedTile);
     const int64_t ctas = paired ? kSmsTarget : 2 * kSmsTarget;
     const double tile = paired ? 1.0 : 1.1, ends = paired ? 5.0 : 3.0;
     int best = tiles;
     double best_cost = 1e30;
     for (int per = tiles; per >= 1; per = std::min(per - 1, per * 15 / 16)) {
-        const int64_t units = lists * ((tiles + per - 1) / per);
+        const int64_t units =
+            several ? static_cast<int64_t>(1.1 * lists * (0.5 * tiles / per + 0.5)) : lists * ((tiles + per - 1) / per);
         const double cost = static_cast<double>((units + ctas - 1) / ctas) * (per * tile + ends);
         if (cost < best_cost) {
             best_cost = cost;
@@ -781,7 +788,7 @@ bool plan_split(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int
             const int per = w.prefix_per * pa::kSharedTile;
             w.prefix_tiles = static_cast<int>((rows + per - 1) / per);
             w.prefix_part = shared_unit(static_cast<int64_t>(num_groups) * w.prefix_tiles * num_kv_heads, shared_tokens,
-                                        w.prefix_paired);
+                                        w.prefix_paired, num_groups > 1);
         }
         w.prefix_cols = w.G;
         while (w.prefix_cols < 8 && w.prefix_cols < static_cast<int64_t>(max_group_size) * w.G) w.prefix_cols *= 2;
