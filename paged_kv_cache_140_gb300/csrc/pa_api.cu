@@ -743,7 +743,7 @@ struct SplitPlan {
     int prefix_part = 0;         // tokens per prefix_per partials
     int prefix_per = 1, prefix_parts = 0;
     int max_parts = 1;
-    int64_t cut_row = 0, prefix_cut_row = 0;
+    int64_t cut_row = 0, prefix_cut_row = 0, rows = 0;
     size_t acc_off = 0, bytes = 0;
 };
 
@@ -808,10 +808,10 @@ bool plan_split(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int
     const int64_t per_launch = static_cast<int64_t>(pa::kSplitMaxCtas) << w.log2_heads;
     w.cut_row = static_cast<int64_t>(num_seqs) * num_heads * w.max_parts;
     w.prefix_cut_row = w.cut_row + (num_seqs + kSplitEntries - 1) / kSplitEntries * per_launch * w.G;
-    const int64_t rows = w.prefix_cut_row +
-                         (prefix_entries + kSplitEntries - 1) / kSplitEntries * per_launch * w.prefix_cols;
-    w.acc_off = static_cast<size_t>(round_up(rows * 4 * 4, 256));
-    w.bytes = w.acc_off + static_cast<size_t>(rows) * head_dim * 4;
+    w.rows = w.prefix_cut_row +
+             (prefix_entries + kSplitEntries - 1) / kSplitEntries * per_launch * w.prefix_cols;
+    w.acc_off = static_cast<size_t>(round_up(w.rows * 4 * 4, 256));
+    w.bytes = w.acc_off + static_cast<size_t>(w.rows) * head_dim * 4;
     return true;
 }
 
@@ -855,10 +855,10 @@ bool encode_scale_map(CUtensorMap *map, const float *scales, int64_t num_blocks,
 pa_status run_split(pa::SplitParams p, int cache, int head_dim, int cols, int entries, int max_len,
                     const pa::SplitMaps &maps, const DeviceInfo &dev, cudaStream_t stream) {
     const int64_t per_entry = static_cast<int64_t>(p.num_kv_heads >> p.log2_heads) *
-                              std::max(1, (max_len + p.partition_size - 1) / p.partition_size);
-    for (int e = 0; e < entries; e += kSplitEntries) {
-        p.e0 = e;
-        p.entries = std::min(kSplitEntries, entries - e);
+                              std::max<int64_t>(1, (static_cast<int64_t>(max_len) + p.partition_size - 1) / p.partition_size);
+    for (int64_t e = 0; e < entries; e += kSplitEntries) {
+        p.e0 = static_cast<int>(e);
+        p.entries = static_cast<int>(std::min<int64_t>(kSplitEntries, entries - e));
         const pa::SplitSmem need = pa::split_smem(head_dim, cols, cache, p.log2_heads, p.entries);
         const size_t room = static_cast<size_t>(dev.smem_optin);
         if (need.fixed + 2 * need.slot > room) return PA_ERR_UNSUPPORTED;
@@ -885,7 +885,8 @@ pa_status check_split(pa_dtype out_dtype, pa_dtype q_dtype, int max_blocks_per_s
     if (!split_shape_ok(num_heads, num_kv_heads, head_dim, block_size)) return PA_ERR_UNSUPPORTED;
     if (static_cast<int64_t>(max_context_len) > static_cast<int64_t>(max_blocks_per_seq) * block_size)
         return PA_ERR_INVALID_ARG;
-    if (num_blocks > INT32_MAX / block_size || num_seqs >= (1 << 27)) return PA_ERR_UNSUPPORTED;
+    if (num_blocks > INT32_MAX / block_size || num_seqs >= (1 << 27) || max_context_len > (1 << 30))
+        return PA_ERR_UNSUPPORTED;
     if (!(scale == scale) || scale > 3.0e38f || scale < -3.0e38f) return PA_ERR_INVALID_ARG;
     // Work is counted in 16-token stages in 32-bit arithmetic on the device,
     // and one join warp per output row.
@@ -923,6 +924,8 @@ pa::SplitParams split_params(void *out, pa_dtype out_dtype, const void *query, p
         p.ws_acc = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + w.acc_off);
         p.cut_row = w.cut_row;
         p.prefix_cut_row = w.prefix_cut_row;
+        p.cut_rows = static_cast<uint32_t>(w.prefix_cut_row - w.cut_row);
+        p.prefix_cut_rows = static_cast<uint32_t>(w.rows - w.prefix_cut_row);
         p.cut_cols = w.G;
         p.cut = 1;
     }

@@ -55,6 +55,7 @@ struct SplitParams {
     int cut_cols;                // query rows per head in a cut item's rows
     int64_t cut_row;             // where the cut items' rows of this launch start
     int64_t prefix_cut_row;      // join: where those of the prefix launches start
+    uint32_t cut_rows, prefix_cut_rows;   // join: how many there are of each
     const float *k_scales;       // 8-bit caches: [num_blocks, bs, Hkv]
     const float *v_scales;
     int *err_flag;

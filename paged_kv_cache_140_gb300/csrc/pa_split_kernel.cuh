@@ -26,12 +26,21 @@
 //
 // What bounds it: reading the cache.  One producer warp brings ring slots in by
 // TMA (boxes of up to 8 KV heads: 16 rows of one physical block of each land as
-// one swizzled tile) and, for 8-bit caches, the scales by 4- or 16-byte
-// asynchronous copies that complete on the same barrier.  A slot holds one tile
-// of 16 tokens (two for 8-bit caches with 8 warps) for each consumer warp: the
-// box's heads times as many 16-token stages as make up the warps, so KV-head
-// counts that are not a multiple of 8 keep every warp busy; warps that share a
-// head keep states of their own and join them at the item's end.
+// one swizzled tile) and, for 8-bit caches, the scales, as boxes too where 4 or 8
+// heads make them wide enough, else by 4-byte asynchronous copies that complete on
+// the same barrier.  A slot holds one tile of 16 tokens (two for 8-bit caches) for
+// each of 8 consumer warps: the box's heads times as many 16-token stages as make
+// up the warps, so KV-head counts that are not a multiple of 8 keep every warp busy;
+// warps that share a head keep states of their own and join them at the item's end.
+// The SMs take equal shares of all slots; an item across a share's end is cut there.
+//
+// Measured (GB300, whole calls, join included; of the measured copy rate): 256
+// 13B-shaped sequences over e4m3 codes 217 us, 0.91; 64 7B-shaped over int8 97 us,
+// 0.87; 16 of 16 K to 32 K tokens, 32 heads on 8, e4m3, 127 us, 0.95.  With the math
+// left out the first took 216, without the scales' loads too 202: the 3 % of bytes
+// that scales are cost 7 %, as 32-byte pieces.  Tried and slower: 16 consumer warps
+// (240 us against 221 at that time), one stage per slot (277), two ring slots instead
+// of three (241), a warp that prefetches slots into L2 (2 ahead 220, 8 ahead 296).
 // Waits are bounded (2 s) and report PA_FLAG_TIMEOUT.
 #pragma once
 
@@ -197,8 +206,9 @@ __device__ __forceinline__ int cut_row_of(const SplitParams &p, uint32_t cta, in
     return static_cast<int>(((((p.e0 / kSplitEntries) * kSplitMaxCtas + cta) << p.log2_heads) + head) * p.cut_cols + col);
 }
 
-// Items (entry, partition, box of heads) in that order, weighed in slots.  An
-// entry without tokens weighs nothing, except where it costs the slot that writes
+// Items (entry, partition, box of heads) in that order, weighed in slots: the
+// boxes of one partition, whose rows lie next to one another, are read one after
+// the other.  An entry without tokens weighs nothing, except where it costs the slot that writes
 // its zero row.
 struct ItemCursor {
     int e, len, nparts, part, grp, nslots;

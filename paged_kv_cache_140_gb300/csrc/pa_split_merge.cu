@@ -79,8 +79,10 @@ __global__ void __launch_bounds__(256)
         };
         // what a second CTA did of a cut item: few
         auto add_cut = [&](float4 st, int j) {
-            if (__float_as_int(st.z) != kRowCut) return;
-            const int64_t r = (j < npre ? p.prefix_cut_row : p.cut_row) + __float_as_int(st.w);
+            // (a row that no kernel wrote, after a reported error, may hold any index)
+            const uint32_t at = __float_as_uint(st.w);
+            if (__float_as_int(st.z) != kRowCut || at >= (j < npre ? p.prefix_cut_rows : p.cut_rows)) return;
+            const int64_t r = (j < npre ? p.prefix_cut_row : p.cut_row) + at;
             const float4 x = __ldcg(states + r);
             float w[DPL];
             load_row(r, w);
