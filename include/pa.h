@@ -482,13 +482,14 @@ pa_status pa_quant_gather(void *out_k, void *out_v, pa_dtype out_dtype, const vo
  * or F32; shapes as there, FP8 and INT8 codes alike for head_dim 64 and 128).
  * partition_size is 0 (auto), or a multiple of 16 of at most 32 * block_size, and
  * above 31 * block_size + 16 a multiple of block_size.
- * partition_size 0 (auto) also splits moderate contexts when there are few
- * sequences.  The workspace is pa_quant_decode_workspace_size(...) bytes (0
- * when nothing is split) and needs no initial contents.  Codes and scales at
- * positions >= context_lens[s] are never used.  Products run in binary16 (codes
- * are exact there; each query row is first scaled by a power of two), sums and
- * softmax in fp32.  Results do not depend on the physical block ids and are
- * bitwise reproducible for a given partition size.
+ * Contexts are also split where the SMs' equal shares of the work end.  The
+ * workspace is pa_quant_decode_workspace_size(...) bytes (0 when nothing is split)
+ * and needs no initial contents.  Codes and scales at positions >= context_lens[s]
+ * are never used.  Products run in binary16 (codes are exact there; each query row
+ * is first scaled by a power of two), sums and softmax in fp32.  Results do not
+ * depend on the physical block ids or on timing and are bitwise reproducible run to
+ * run on one GPU; where contexts are split, and so the last bits, depends on the
+ * batch's lengths, the bounds and the number of SMs.
  */
 size_t pa_quant_decode_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size,
                                       int max_context_len, int partition_size);
@@ -514,11 +515,13 @@ pa_status pa_quant_decode(void *out, pa_dtype out_dtype, const void *query, pa_d
  * arguments and rules hold otherwise; 16-bit caches, the query's type kv_dtype).
  *
  *   cu_groups    : [num_groups + 1] int32 (device), cu_groups[0] = 0,
- *                  non-decreasing, cu_groups[num_groups] = num_seqs
+ *                  non-decreasing (groups may be empty),
+ *                  cu_groups[num_groups] = num_seqs
  *   shared_lens  : [num_seqs] int32 (device), 0 <= shared_lens[s] <=
  *                  context_lens[s], equal within a group; 0: nothing is shared
  *   max_group_size, max_shared_len : host-known upper bounds of the group sizes
- *                  and of shared_lens (<= max_context_len)
+ *                  (num_groups * max_group_size >= num_seqs) and of shared_lens
+ *                  (<= max_context_len); tight ones make the call faster
  *   scale        : >= 0
  *   workspace    : pa_decode_shared_workspace_size(...) bytes (may be 0); no
  *                  initial contents
@@ -528,7 +531,7 @@ pa_status pa_quant_decode(void *out, pa_dtype out_dtype, const void *query, pa_d
  * cu_groups or shared_lens that break these rules set PA_FLAG_BAD_CONTEXT_LEN;
  * the groups concerned are then undefined (no memory out of bounds is touched).
  * partition_size is that of the private parts; the prefixes are cut by a rule of
- * the library's own.
+ * the library's own.  Reproducibility as for pa_quant_decode.
  */
 size_t pa_decode_shared_workspace_size(int num_seqs, int num_groups, int max_group_size, int num_heads,
                                        int num_kv_heads, int head_dim, int block_size, int max_context_len,

@@ -19,7 +19,9 @@ for K and for V ("LLMæ¨ç†ä¼˜åŒ–ï¼švLLM PagedAttentionæ·±åº¦è§£æä¸å·¥ç¨‹å®è
 Caches are float16 / bfloat16, or FP8 e4m3 codes (``torch.float8_e4m3fn`` or
 ``torch.uint8``) with per-tensor ``k_scale`` / ``v_scale``; the ``quant_*`` calls
 keep int8 or e4m3 codes with a float32 scale per token and KV head,
-``[num_blocks, block_size, num_kv_heads]``.
+``[num_blocks, block_size, num_kv_heads]``.  :func:`copy_blocks` and
+:func:`swap_blocks` move such a cache as bytes: ``codes.view(torch.uint8)``, and
+``scales.view(torch.uint8).view(NB, bs, Hkv, 4)``.
 """
 from __future__ import annotations
 

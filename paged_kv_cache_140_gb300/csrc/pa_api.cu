@@ -766,6 +766,7 @@ bool plan_split(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int
     const int slot_tokens = 16 * pa::split_slot_stages(cache, w.log2_heads);
     if (shared) {
         if (num_groups < 0 || max_group_size < 0 || max_shared_len < 0 || max_shared_len > max_context_len) return false;
+        max_group_size = std::min(max_group_size, num_seqs);
         const int shared_tokens = max_shared_len / block_size * block_size;
         w.whole = static_cast<double>(std::max(0, num_seqs - num_groups)) * shared_tokens * num_kv_heads * head_dim * 4 <=
                   kSharedWholeBytes;
@@ -1065,9 +1066,7 @@ PA_EXPORT pa_status pa_decode_shared(void *out, pa_dtype out_dtype, const void *
     const pa_status st = check_split(out_dtype, kv_dtype, max_blocks_per_seq, max_context_len, num_seqs, num_heads,
                                      num_kv_heads, head_dim, block_size, num_blocks, scale);
     if (st != PA_OK) return st;
-    if (num_seqs > 0 && (static_cast<int64_t>(num_groups) * max_group_size < num_seqs || num_groups > num_seqs ||
-                         max_group_size > num_seqs))
-        return PA_ERR_INVALID_ARG;
+    if (static_cast<int64_t>(num_groups) * max_group_size < num_seqs) return PA_ERR_INVALID_ARG;
     const int cache = split_cache(kv_dtype);
     SplitPlan w;
     if (!plan_split(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context_len, partition_size, cache,
@@ -1120,7 +1119,7 @@ PA_EXPORT pa_status pa_decode_shared(void *out, pa_dtype out_dtype, const void *
         pre.cut_cols = w.prefix_cols;
         pre.partition_size = w.prefix_part;
         pre.chunk_seqs = w.prefix_cols / w.G;
-        pre.chunks = (max_group_size + pre.chunk_seqs - 1) / pre.chunk_seqs;
+        pre.chunks = (std::min(max_group_size, num_seqs) + pre.chunk_seqs - 1) / pre.chunk_seqs;
         if (static_cast<int64_t>(num_groups) * pre.chunks >= (int64_t{1} << 31)) return PA_ERR_UNSUPPORTED;
         const pa_status r = run_split(pre, cache, head_dim, w.prefix_cols, num_groups * pre.chunks, max_shared_len,
                                       maps, dev, s);

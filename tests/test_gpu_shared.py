@@ -196,6 +196,51 @@ def test_loose_bounds_and_partition_sizes_agree():
         check(b, **kw)
 
 
+@pytest.mark.parametrize("n,hq,hkv", [(4, 4, 2), (9, 32, 32), (60, 8, 4)])
+def test_empty_groups_and_padded_sequences(n, hq, hkv):
+    """Empty groups before, between and behind, more groups than sequences, a bound
+    above the batch, and padding sequences of no tokens in a group of their own."""
+    b = make([n, 2, 3], [300, 0, 16], [7] * n + [5, 9] + [1] * 3, hq, hkv, 128, 16, "bf16", seed=15)
+    want = check(b)
+    pad = 3
+    z = {k: b[k] for k in ("k", "v", "bs", "scale", "ms")}
+    z["q"] = torch.cat([b["q"], torch.randn(pad, hq, 128).bfloat16()])
+    z["bt"] = torch.cat([b["bt"], torch.full((pad, b["bt"].shape[1]), -1, dtype=torch.int32)])
+    z["ctx"] = b["ctx"] + [0] * pad
+    z["sh"] = np.concatenate([b["sh"], np.zeros(pad, np.int32)])
+    c = b["cu"].tolist()
+    z["cu"] = np.asarray([0, 0, c[1], c[1], c[2], c[3], c[3] + pad] + [c[3] + pad] * 80, np.int32)
+    z["mg"] = 1000
+    got = run(z)
+    assert torch.all(got[-pad:] == 0)
+    assert (got[:-pad] - want).abs().max() < 1e-3
+    check(z)
+
+
+def test_context_lengths_may_change_between_replays():
+    """A captured step whose contexts grow by a token before each replay, as in a serving loop."""
+    n, hkv, d, bs = 40, 4, 64, 16
+    b = make([n], [200], [50] * n, 8, hkv, d, bs, "f16", seed=16)
+    dev = {k: b[k].cuda() for k in ("q", "k", "v", "bt")}
+    ctx = torch.tensor([230] * n, dtype=torch.int32).cuda()
+    cu, sh = torch.from_numpy(b["cu"]).cuda(), torch.from_numpy(b["sh"]).cuda()
+    out = torch.empty(n, 8, d, device="cuda")
+
+    def step():
+        ctx.add_(1)
+        pa.decode_shared(out, dev["q"], dev["k"], dev["v"], dev["bt"], ctx, cu, sh, b["scale"], max_group_size=n,
+                         max_shared_len=200, max_context_len=250)
+    graph = pa.StepGraph(step)
+    ctx.fill_(230)
+    for i in range(1, 20):
+        graph.replay()
+        torch.cuda.synchronize()
+        got = out.clone()
+        assert ctx[0].item() == 230 + i
+        eager = run({**b, "ctx": [230 + i] * n})
+        assert (got - eager).abs().max() < 1e-3
+
+
 def test_matches_decode_on_the_same_tables():
     b = make([4, 4, 30], [1000, 64, 256], [int(x) for x in np.random.default_rng(0).integers(1, 99, 38)], 8, 8, 128, 16,
              "bf16", seed=7)
