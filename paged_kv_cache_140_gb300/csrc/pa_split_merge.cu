@@ -116,7 +116,8 @@ __global__ void __launch_bounds__(256)
             for (int c0 = sub * per; c0 < end; c0 += 32) {
                 float4 st = make_float4(-INFINITY, 0.f, 0.f, 0.f);
                 if (c0 + lane < end) st = __ldcg(states + row_of(c0 + lane));
-                uint32_t left = __ballot_sync(kFull, !(st.x == -INFINITY && st.y == 0.f));
+                // (an empty state that was cut still names the row of what follows it)
+                uint32_t left = __ballot_sync(kFull, !(st.x == -INFINITY && st.y == 0.f) || __float_as_int(st.z) == kRowCut);
                 while (left != 0) {
                     int at[kRows];
                     float v[kRows][DPL];

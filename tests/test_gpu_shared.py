@@ -142,6 +142,29 @@ def test_enough_private_tokens_for_items_to_be_cut_between_sms(members, hq, hkv)
     check(make(members, [300] * len(members), rng.integers(0, 1800, n).tolist(), hq, hkv, 64, 16, "bf16", seed=14))
 
 
+@pytest.mark.parametrize("n", [20, 60, 140])
+def test_private_parts_whose_first_tokens_weigh_nothing(n):
+    """Keys of -infinity (all queries positive) before the last private token: where
+    an item is cut among them, the part before the cut holds nothing and the part
+    behind it the token that outweighs the rest."""
+    hkv, d, L, own = 8, 64, 320, 504
+    b = make([n], [L], [own] * n, hkv, hkv, d, 16, "bf16", seed=17)
+    b["q"] = b["q"].abs() + 0.125
+    kf = b["k"].view(-1, hkv, d)
+    for s in range(n):
+        kf[Q.slots_of(b["bt"], s, L, L + own - 1, 16)] = float("-inf")
+        kf[Q.slots_of(b["bt"], s, L + own - 1, L + own, 16)] = 1.0
+    out = run(b).cpu().double()
+    for s in range(n):
+        sl = torch.cat([Q.slots_of(b["bt"], s, 0, L, 16), Q.slots_of(b["bt"], s, L + own - 1, L + own, 16)])
+        k, v = kf[sl].double(), b["v"].view(-1, hkv, d)[sl].double()
+        ref = Q.attend(b["q"][s], k, v, b["scale"])
+        xs = torch.einsum("hgd,lhd->hgl", b["q"][s].double().view(hkv, 1, d), k.abs()) * b["scale"]
+        tol = Q.tolerance(ref.numpy(), v.abs().amax((0, 2))[:, None].numpy(), L + own, d,
+                          xs.reshape(hkv, -1).amax(-1)[:, None].numpy(), "f32")
+        assert np.all((out[s] - ref).abs().numpy() <= tol), f"sequence {s}"
+
+
 @pytest.mark.parametrize("n,hq,hkv", [(3, 8, 8), (50, 8, 2)])
 def test_long_prefix(n, hq, hkv):
     rng = np.random.default_rng(2)
