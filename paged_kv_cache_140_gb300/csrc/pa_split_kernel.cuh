@@ -300,6 +300,10 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
     pdl_launch_dependents();
     // ---- the entries' lengths ----
     const bool tell = blockIdx.x == 0;
+    if (mode == kSplitWhole && tell)   // every group's bounds, the warps with the fewest entries first
+        for (int g = blockDim.x - 1 - threadIdx.x; g < p.num_groups; g += blockDim.x)
+            if (bad_group(p, g, __ldg(p.cu_groups + g), __ldg(p.cu_groups + g + 1)))
+                report(p.err_flag, 0x4 /* PA_FLAG_BAD_CONTEXT_LEN */);
     for (int i = threadIdx.x; i < E; i += blockDim.x) {
         int len = 0, aux = 0;
         if (mode == kSplitPrefix) {

@@ -310,6 +310,17 @@ def test_bad_block_ids_and_lengths_are_reported(n):
     assert torch.all(o[n + 1] == 0) and torch.equal(o[:n + 1], clean[:n + 1])
 
 
+@pytest.mark.parametrize("n,hq,hkv", [(4, 4, 2), (60, 8, 8), (9, 32, 32)])
+def test_group_bounds_that_no_sequence_meets_are_reported(n, hq, hkv):
+    """Bounds that break the rules where every sequence still finds a group that holds it."""
+    b = make([n - 2, 2], [320, 320], [20] * n, hq, hkv, 128, 16, "bf16", seed=18)
+    b["mg"] = n
+    for cu in ([0, n, n + 1], [0, n - 1, n - 2, n], [1, n], [0, n - 1, n - 1, n + 5], [0, n, -1, n]):
+        err = pa.new_err_flag()
+        run({**b, "cu": np.asarray(cu, np.int32)}, err=err)
+        assert pa.read_err_flag(err) & pa.FLAG_BAD_CONTEXT_LEN, cu
+
+
 def test_nan_in_one_member_stays_with_it():
     b = make([40], [200], [20] * 40, 4, 4, 128, 16, "bf16", seed=10)
     clean = run(b)
