@@ -484,7 +484,8 @@ pa_status pa_quant_gather(void *out_k, void *out_v, pa_dtype out_dtype, const vo
  * above 31 * block_size + 16 a multiple of block_size.
  * Contexts are also split where the SMs' equal shares of the work end.  The
  * workspace is pa_quant_decode_workspace_size(...) bytes (0 when nothing is split)
- * and needs no initial contents.  Codes and scales at positions >= context_lens[s]
+ * and needs no initial contents; calls made by several host threads at once, on one
+ * stream too, need one each.  Codes and scales at positions >= context_lens[s]
  * are never used.  Products run in binary16 (codes are exact there; each query row
  * is first scaled by a power of two), sums and softmax in fp32.  Results do not
  * depend on the physical block ids or on timing and are bitwise reproducible run to

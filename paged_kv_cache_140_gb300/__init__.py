@@ -27,6 +27,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import threading
 
 from . import _lib
 from ._lib import (FLAG_BAD_BLOCK_ID, FLAG_BAD_CONTEXT_LEN, FLAG_BAD_COPY_PAIR, FLAG_BAD_SLOT,
@@ -381,17 +382,19 @@ def _flag(err_flag, dev: int):
 
 
 def _scratch(rt, workspace, nbytes: int, dev: int, stream: int):
-    """The workspace of one call: the caller's, the default one of the current
-    stream, or, while a graph is captured, one of the graph's own (so that graphs
-    never share one and none is replaced by a larger one later)."""
+    """The workspace of one call: the caller's, the calling thread's default one for
+    the current stream (a call is several launches, between which another thread's
+    may come), or, while a graph is captured, one of the graph's own (so that
+    graphs never share one and none is replaced by a larger one later)."""
     if nbytes == 0:
         return None
     if workspace is None:
         if rt.capturing():
             return rt.empty(nbytes, dtype=rt.u8, device=dev)
-        workspace = _default_ws.get((dev, stream))
+        key = (dev, stream, threading.get_ident())
+        workspace = _default_ws.get(key)
         if workspace is None:
-            workspace = _default_ws.setdefault((dev, stream), DecodeWorkspace(_torch().device("cuda", dev)))
+            workspace = _default_ws.setdefault(key, DecodeWorkspace(_torch().device("cuda", dev)))
     if isinstance(workspace, DecodeWorkspace):
         workspace = workspace.get(nbytes)
     if workspace.get_device() != dev or not workspace.is_contiguous():

@@ -1,5 +1,7 @@
 """GPU tests of the quantised cache: write, read-back and decode against their
 64-bit plain forms (codes and scales bit for bit), and runs of them together."""
+import threading
+
 import numpy as np
 import pytest
 
@@ -526,6 +528,37 @@ def test_calls_on_two_streams_at_once():
     torch.cuda.synchronize()
     for o, w in zip(outs, want):
         assert torch.equal(o, w)
+
+
+def test_threads_on_one_stream():
+    """Calls of several launches, made by threads on the same stream with the default workspaces."""
+    hkv, d, bs = 8, 128, 16
+    work = []
+    for i, lens in enumerate(([5000, 2500, 17], [700] * 40, [9000])):
+        bt, nb = Q.tables(lens, bs, i)
+        c = {n: t.cuda() for n, t in Q.quant_cache(lens, bt, nb, bs, hkv, d, "e4m3", i).items()}
+        q = torch.randn(len(lens), hkv, d, device="cuda").half()
+        work.append((q, c, bt.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(), max(lens)))
+
+    def call(w):
+        q, c, bt, ctx, most = w
+        o = torch.empty(q.shape, device="cuda")
+        pa.quant_decode(o, q, c["k"], c["v"], c["ks"], c["vs"], bt, ctx, 0.1, max_context_len=most)
+        return o
+    want = [call(w) for w in work]
+    torch.cuda.synchronize()
+    wrong = torch.zeros(len(work), dtype=torch.int32, device="cuda")
+
+    def loop(i):
+        for _ in range(200):
+            wrong[i] += (call(work[i]) != want[i]).any()
+    threads = [threading.Thread(target=loop, args=(i,)) for i in range(len(work))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert wrong.tolist() == [0] * len(work)
 
 
 def test_cache_slots_past_two_to_the_thirty_one_bytes():
