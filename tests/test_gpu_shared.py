@@ -211,6 +211,13 @@ def test_many_tokens_of_little_weight_count(dtype):
     assert (got - share).abs().max() < 1e-3 * share
 
 
+@pytest.mark.parametrize("size,groups", [(2, 2100), (9, 250)])
+def test_more_sequences_and_groups_than_one_launch_takes(size, groups):
+    rng = np.random.default_rng(19)
+    check(make([size] * groups, rng.integers(16, 40, groups).tolist(), rng.integers(0, 40, size * groups).tolist(), 4, 4, 64,
+               16, "bf16", seed=19))
+
+
 def test_loose_bounds_and_partition_sizes_agree():
     b = make([3, 20, 1], [300, 513, 40], [9] * 24, 8, 4, 64, 16, "f16", seed=6)
     a = check(b)
