@@ -18,6 +18,7 @@
 #include "pa_prefill.h"
 #include "pa_shared_prefix.h"
 #include "pa_split.h"
+#include "pa_split_plan.h"
 
 #define PA_EXPORT extern "C" __attribute__((visibility("default")))
 
@@ -658,38 +659,9 @@ int split_cache(pa_dtype d) {
     return d == PA_F16 ? pa::kCacheF16 : d == PA_BF16 ? pa::kCacheBF16 : d == PA_FP8_E4M3 ? pa::kCacheE4M3 : pa::kCacheInt8;
 }
 
+using pa::kSmsTarget;
 using pa::kSplitEntries;
-// SMs the cuts are planned for (a constant: the workspace's size does not depend
-// on the device).
-constexpr int64_t kSmsTarget = 152;
-
-// Partition length, in tokens, for `lists` lists (entries x boxes of heads, `boxes`
-// of them per entry) of about `len` tokens at most; 0 when the request is invalid.
-// Partitions are as long as they may be while an SM's equal share of the slots is
-// no shorter (shares are cut exactly then, and fewer partials joined; lists are
-// taken to be 2/5 of `len` on average), and at least 4 slots.  Entries of several
-// boxes are cut at 512 tokens: their boxes' rows and scales lie next to one another
-// in memory and are best read at about the same time.  Lists of up to 6 slots are
-// not cut: reading a slot takes an SM about a microsecond, joining partials a
-// launch of its own.
-int split_partition(int64_t lists, int64_t boxes, int64_t len, int block_size, int slot_tokens, int requested) {
-    const int64_t cap = 32 * block_size;
-    if (requested != 0) {
-        // a partition's block ids sit in the 32 lanes of a warp; one that does not
-        // start on a block boundary may reach into one block more
-        if (requested < 16 || requested % 16 != 0 || requested > cap) return 0;
-        return requested % block_size != 0 && requested > cap - block_size + 16 ? 0 : requested;
-    }
-    const double share = static_cast<double>(lists) * len * 0.4 / (static_cast<double>(slot_tokens) * kSmsTarget);
-    int64_t P = static_cast<int64_t>(std::min(share, 1e6)) * slot_tokens;
-    if (boxes > 1) P = std::min<int64_t>(P, 512);
-    P = std::max<int64_t>(P, 4 * slot_tokens);
-    if (len <= std::min<int64_t>(cap, std::max<int64_t>(P, 6 * slot_tokens)))
-        return static_cast<int>(std::max<int64_t>(16, round_up(len, 16)));   // one partition
-    P = std::min<int64_t>(P, cap);
-    if (P > slot_tokens) P -= P % slot_tokens;   // whole ring slots
-    return static_cast<int>(P);
-}
+using pa::split_partition;
 
 // A group with more query rows per KV head than this has its prefix computed on
 // the tensor-core kernel, whose 128-row tiles read each K/V row once for up to
