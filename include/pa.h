@@ -522,7 +522,10 @@ pa_status pa_quant_decode(void *out, pa_dtype out_dtype, const void *query, pa_d
  *                  context_lens[s], equal within a group; 0: nothing is shared
  *   max_group_size, max_shared_len : host-known upper bounds of the group sizes
  *                  (num_groups * max_group_size >= num_seqs) and of shared_lens
- *                  (<= max_context_len); tight ones make the call faster
+ *                  (<= max_context_len); tight ones make the call faster.  A list of
+ *                  num_groups >= num_seqs counts as padded with empty groups (as the
+ *                  fixed list of a captured step is): they cost little, and the call is
+ *                  planned for ceil(num_seqs / max_group_size) groups
  *   scale        : >= 0
  *   workspace    : pa_decode_shared_workspace_size(...) bytes (may be 0); no
  *                  initial contents

@@ -705,6 +705,8 @@ constexpr int64_t kSharedWholeBytes = 8 << 20;
 
 struct SplitPlan {
     int log2_heads = 0, G = 1;
+    bool padded = false;         // the list of groups is taken to be padded with empty ones
+    int64_t groups = 0;          // groups that the prefixes are planned for
     int partition = 0;           // decode and suffix entries
     int parts = 1;               // their partials per row
     bool whole = false;          // shared prefixes are not worth a pass of their own
@@ -740,8 +742,13 @@ bool plan_split(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int
         if (num_groups < 0 || max_group_size < 0 || max_shared_len < 0 || max_shared_len > max_context_len) return false;
         max_group_size = std::min(max_group_size, num_seqs);
         const int shared_tokens = max_shared_len / block_size * block_size;
-        w.whole = static_cast<double>(std::max(0, num_seqs - num_groups)) * shared_tokens * num_kv_heads * head_dim * 4 <=
-                  kSharedWholeBytes;
+        // A list of at least as many groups as sequences shares nothing or is padded with
+        // empty ones (as the fixed list of a captured step is): it is planned for the
+        // fewest groups that hold all sequences.  A shorter one is taken at its word.
+        w.padded = num_groups >= num_seqs && max_group_size > 1;
+        w.groups = w.padded ? (static_cast<int64_t>(num_seqs) + max_group_size - 1) / max_group_size : num_groups;
+        w.whole = static_cast<double>(std::max<int64_t>(0, num_seqs - w.groups)) * shared_tokens * num_kv_heads * head_dim *
+                      4 <= kSharedWholeBytes;
     }
     // Private parts are about as long as the bounds differ (only the cut goes by
     // that; a part may be longer).
@@ -760,8 +767,7 @@ bool plan_split(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int
             w.prefix_per = w.prefix_paired ? 2 : 1;
             const int per = w.prefix_per * pa::kSharedTile;
             w.prefix_tiles = static_cast<int>((rows + per - 1) / per);
-            w.prefix_part = shared_unit(static_cast<int64_t>(num_groups) * w.prefix_tiles * num_kv_heads, shared_tokens,
-                                        w.prefix_paired, num_groups > 1);
+            w.prefix_part = shared_unit(w.groups * w.prefix_tiles * num_kv_heads, shared_tokens, w.prefix_paired, w.groups > 1);
         }
         w.prefix_cols = w.G;
         while (w.prefix_cols < 8 && w.prefix_cols < static_cast<int64_t>(max_group_size) * w.G) w.prefix_cols *= 2;
@@ -769,8 +775,7 @@ bool plan_split(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int
         const int64_t chunks = (static_cast<int64_t>(max_group_size) + chunk_seqs - 1) / chunk_seqs;
         if (!w.prefix_tc) {
             prefix_entries = num_groups * chunks;
-            w.prefix_part = split_partition(num_groups * chunks * ngroups, ngroups, max_shared_len, block_size,
-                                            slot_tokens, 0);
+            w.prefix_part = split_partition(w.groups * chunks * ngroups, ngroups, max_shared_len, block_size, slot_tokens, 0);
         }
         w.prefix_parts = (shared_tokens + w.prefix_part - 1) / w.prefix_part * w.prefix_per;
         w.max_parts += w.prefix_parts;
@@ -1074,15 +1079,17 @@ PA_EXPORT pa_status pa_decode_shared(void *out, pa_dtype out_dtype, const void *
     if (w.prefix_parts > 0 && w.prefix_tc) {
         if (pa::shared_prefix_smem(head_dim) + 1024 > static_cast<size_t>(dev.smem_optin)) return PA_ERR_UNSUPPORTED;
         const int ranges = w.prefix_parts / w.prefix_per, tile_seqs = pa::kSharedTile / w.G;
-        if (static_cast<int64_t>(num_groups) * ranges * num_kv_heads * w.prefix_tiles >= (int64_t{1} << 31))
-            return PA_ERR_UNSUPPORTED;
+        int64_t grid = w.groups * ranges * num_kv_heads * w.prefix_tiles;
+        // at least a whole wave where there may be more units than planned for
+        if (w.padded) grid = std::max(grid, kSmsTarget * (w.prefix_paired ? 1 : 2));
+        if (grid >= (int64_t{1} << 31)) return PA_ERR_UNSUPPORTED;
         CUtensorMap tq, sk, sv;
         if (!encode_map_128b(&tq, query, 2, head_dim, num_heads, num_seqs, w.G, tile_seqs) ||
             !encode_map_128b(&sk, k_cache, 2, head_dim, num_kv_heads, num_blocks * block_size, 1, block_size) ||
             !encode_map_128b(&sv, v_cache, 2, head_dim, num_kv_heads, num_blocks * block_size, 1, block_size))
             return PA_ERR_CUDA;
-        if (pa::launch_shared_prefix(p, head_dim, kv_dtype == PA_BF16, w.prefix_paired, w.prefix_tiles, w.prefix_part,
-                                     ranges, tq, sk, sv, s) != cudaSuccess)
+        if (pa::launch_shared_prefix(p, head_dim, kv_dtype == PA_BF16, w.prefix_paired, static_cast<int>(grid), w.padded,
+                                     w.prefix_tiles, w.prefix_part, ranges, tq, sk, sv, s) != cudaSuccess)
             return PA_ERR_CUDA;
     } else if (w.prefix_parts > 0) {
         pa::SplitParams pre = p;

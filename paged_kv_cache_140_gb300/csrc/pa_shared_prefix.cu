@@ -67,6 +67,9 @@ struct PrefixShared {
     uint64_t done;
     uint32_t tmem_base;
     int abort, bad;
+    int group, local, sums[Streams<2>::kThreads / 32];   // find_unit
+    int held;                            // padded lists: tensor memory is held, the barriers have been used
+    int64_t listed, next;                //               units that there are, the CTA's next
 };
 
 // Bounded wait that also gives up once another thread has aborted the CTA.
@@ -89,6 +92,10 @@ __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, PrefixS
 // The warp goes on only if all its lanes saw the phase complete.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, PrefixShared &sh, int *err_flag) {
     return __all_sync(kFull, wait_bar(bar, parity, sh, err_flag));
+}
+
+__device__ __forceinline__ void mbar_inval(uint64_t *bar) {
+    asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
 __device__ __forceinline__ bool elect_one() {
@@ -191,11 +198,60 @@ __device__ __forceinline__ void load_tile(TableWindow &win, int tile, int bs, in
     }
 }
 
-template <int D, bool BF16, int NS>
-__global__ void __launch_bounds__(Streams<NS>::kThreads, Streams<NS>::kCtas)
-    shared_prefix_kernel(const __grid_constant__ SplitParams p, int tiles, int unit_tokens, int units_per_list,
-                         const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
-                         const __grid_constant__ CUtensorMap tv) {
+__device__ __forceinline__ int group_shared_blocks(const SplitParams &p, int q0) {
+    return shared_blocks(p, q0, context_of(p, q0, false), false);
+}
+
+// Unit n of those that the groups really have, in order: its group and its number
+// among the group's units; sh.listed: how many units there are.  (A group that breaks the rules
+// counts as one unit, which reports it.)  All threads of the CTA.
+__device__ __forceinline__ void find_unit(const SplitParams &p, int64_t n, int tile_seqs, int unit_tokens, PrefixShared &sh,
+                                          int &group, int &local) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int64_t total = 0;
+    for (int g0 = 0; g0 < p.num_groups; g0 += blockDim.x) {
+        const int g = g0 + threadIdx.x;
+        int units = 0;
+        if (g < p.num_groups) {
+            const int q0 = __ldg(p.cu_groups + g), q1 = __ldg(p.cu_groups + g + 1);
+            if (bad_group(p, g, q0, q1)) {
+                units = 1;
+            } else if (q0 < q1) {
+                const int len = group_shared_blocks(p, q0) * p.block_size;
+                units = (q1 - q0 + tile_seqs - 1) / tile_seqs * ((len + unit_tokens - 1) / unit_tokens) * p.num_kv_heads;
+            }
+        }
+        int incl = units;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(kFull, incl, o);
+            if (lane >= o) incl += v;
+        }
+        if (lane == 31) sh.sums[warp] = incl;
+        __syncthreads();
+        int64_t before = total + incl - units;
+        for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) {
+            if (w < warp) before += sh.sums[w];
+            total += sh.sums[w];
+        }
+        if (n >= before && n < before + units) {
+            sh.group = g;
+            sh.local = static_cast<int>(n - before);
+        }
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) sh.listed = total;
+    __syncthreads();
+    group = sh.group;
+    local = sh.local;
+}
+
+// One unit: the CTA's only one (kOnly), or one of several.  `begun`: an earlier one used
+// the barriers and left the tensor memory held; `more`: another follows.
+template <int D, bool BF16, int NS, bool kOnly>
+__device__ __forceinline__ void prefix_unit(const SplitParams &p, PrefixShared &sh, uint8_t *base, int g, int pi, int kvh,
+                                            int range, int unit_tokens, bool &begun, bool more, const CUtensorMap &tq,
+                                            const CUtensorMap &tk, const CUtensorMap &tv) {
     constexpr int R = D / 64;               // 128-byte regions per row
     constexpr int kOp = R * kRegion;        // one 128-row operand tile
     constexpr int NR = kSharedRing<D, NS>;
@@ -206,25 +262,11 @@ __global__ void __launch_bounds__(Streams<NS>::kThreads, Streams<NS>::kCtas)
     constexpr uint32_t kIdescQK = umma::idesc_f16(BF16, kTile, kTile, false);
     constexpr uint32_t kIdescPV = umma::idesc_f16(BF16, kTile, D, true);
 
-    __shared__ PrefixShared sh;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                                ~static_cast<uintptr_t>(1023));
     uint8_t *sQ = base, *sK = sQ + NS * kOp, *sV = sK + NR * kOp;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    // ---- work unit: the query tiles (pairs of them) of one K/V range run next to each other (L2) ----
-    int u = blockIdx.x;
-    const int pi = u % tiles;
-    u /= tiles;
-    const int kvh = u % p.num_kv_heads;
-    u /= p.num_kv_heads;
-    const int range = u % units_per_list, g = u / units_per_list;
     const int lg = p.log2_group, G = 1 << lg;
     const int TT = kTile >> lg;             // sequences per query tile
-
-    pdl_wait();
-    pdl_launch_dependents();
     const int q0 = __ldg(p.cu_groups + g), q1 = __ldg(p.cu_groups + g + 1);
     const bool first = pi == 0 && kvh == 0 && range == 0;
     if (bad_group(p, g, q0, q1)) {
@@ -237,7 +279,7 @@ __global__ void __launch_bounds__(Streams<NS>::kThreads, Streams<NS>::kCtas)
         for (int s = q0 + threadIdx.x; s < q1; s += blockDim.x)
             if (__ldg(p.shared_lens + s) != n0) report(p.err_flag, PA_FLAG_BAD_CONTEXT_LEN);
     }
-    const int len = shared_blocks(p, q0, context_of(p, q0, false), false) * p.block_size;
+    const int len = group_shared_blocks(p, q0) * p.block_size;
     const int t0 = range * unit_tokens, tA = pi * NS * TT;  // first token, first sequence of the group
     if (t0 >= len || tA >= q1 - q0) return;
     const int n_seq = NS == 1 ? min(TT, q1 - q0 - tA) : q1 - q0 - tA;   // sequences from this unit's first on
@@ -252,6 +294,9 @@ __global__ void __launch_bounds__(Streams<NS>::kThreads, Streams<NS>::kCtas)
     const int zx = nB > 0 ? 1 : 0;                          // the stream that zeroes them
 
     if (threadIdx.x == 0) {
+        if (begun) {
+            for (uint64_t *bar = &sh.q_full; bar <= &sh.done; ++bar) mbar_inval(bar);
+        }
         mbar_init(&sh.q_full, 1);
         for (int i = 0; i < NR; ++i) {
             mbar_init(&sh.k_full[i], 1);
@@ -269,10 +314,11 @@ __global__ void __launch_bounds__(Streams<NS>::kThreads, Streams<NS>::kCtas)
         sh.bad = 0;
         fence_barrier_init();
     }
-    if (warp == W::kWarpMma) {
+    if (!begun && warp == W::kWarpMma) {
         umma::tmem_alloc(smem_addr(&sh.tmem_base), W::kCols);
         umma::tmem_relinquish();
     }
+    begun = true;
     umma::fence_before_sync();
     __syncthreads();
     umma::fence_after_sync();
@@ -393,6 +439,13 @@ __global__ void __launch_bounds__(Streams<NS>::kThreads, Streams<NS>::kCtas)
         if (leader) {
             umma::commit(smem_addr(&sh.done));
             mbar_wait_bounded(&sh.done, 0, kWaitLimitNs);
+            // the last arrivals on these, which nobody else waits for, before the barriers are set up again
+            for (int st = 0; more && ok && st < min(NR, nt); ++st) {
+                const uint32_t par = ((nt - 1 - st) / NR) & 1;
+                ok = mbar_wait_bounded(&sh.k_empty[st], par, kWaitLimitNs) &&
+                     mbar_wait_bounded(&sh.v_empty[st], par, kWaitLimitNs);
+            }
+            if (!ok) *reinterpret_cast<volatile int *>(&sh.abort) = 1;
         }
         __syncwarp();
     } else {
@@ -593,43 +646,109 @@ __global__ void __launch_bounds__(Streams<NS>::kThreads, Streams<NS>::kCtas)
 
     umma::fence_before_sync();
     __syncthreads();
-    if (warp == W::kWarpMma) {
+    if (kOnly && warp == W::kWarpMma) {
         umma::fence_after_sync();
         umma::tmem_dealloc(tmem, W::kCols);
     }
 }
 
+// kPadded: the list of groups is padded with empty ones; the grid's CTAs take the
+// units that there really are in turn.
+template <int D, bool BF16, int NS, bool kPadded>
+__global__ void __launch_bounds__(Streams<NS>::kThreads, Streams<NS>::kCtas)
+    shared_prefix_kernel(const __grid_constant__ SplitParams p, int tiles, int unit_tokens, int units_per_list,
+                         const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                         const __grid_constant__ CUtensorMap tv) {
+    using W = Streams<NS>;
+    __shared__ PrefixShared sh;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                ~static_cast<uintptr_t>(1023));
+    // Units in this order: the query tiles (pairs of them) of one K/V range run next to each other (L2).
+    if constexpr (!kPadded) {
+        int u = blockIdx.x;
+        const int pi = u % tiles;
+        u /= tiles;
+        const int kvh = u % p.num_kv_heads;
+        u /= p.num_kv_heads;
+        const int range = u % units_per_list, g = u / units_per_list;
+        pdl_wait();
+        pdl_launch_dependents();
+        bool begun = false;
+        prefix_unit<D, BF16, NS, true>(p, sh, base, g, pi, kvh, range, unit_tokens, begun, false, tq, tk, tv);
+    } else {
+        const int tile_seqs = NS * (kTile >> p.log2_group);
+        pdl_wait();
+        pdl_launch_dependents();
+        if (blockIdx.x == 0)   // groups without whole shared blocks: one length for all of each, as the units check
+            for (int g = threadIdx.x; g < p.num_groups; g += blockDim.x) {
+                const int q0 = __ldg(p.cu_groups + g), q1 = __ldg(p.cu_groups + g + 1);
+                if (bad_group(p, g, q0, q1) || q0 == q1 || group_shared_blocks(p, q0) > 0) continue;
+                for (int s = q0 + 1; s < q1; ++s)
+                    if (__ldg(p.shared_lens + s) != __ldg(p.shared_lens + q0)) report(p.err_flag, PA_FLAG_BAD_CONTEXT_LEN);
+            }
+        if (threadIdx.x == 0) sh.held = 0;
+        // What an iteration needs comes out of shared memory again: kept in registers across
+        // the unit it makes the softmax spill (8,192 tokens before 256 sequences, 255 of 256
+        // groups empty: 101 us, with it 111; without the empty groups 99).
+        volatile PrefixShared &now = sh;
+#pragma unroll 1
+        for (int64_t n = blockIdx.x;; n = now.next) {
+            int g, local;
+            find_unit(p, n, tile_seqs, unit_tokens, sh, g, local);
+            const int64_t listed = now.listed;
+            if (n >= listed) break;
+            if (threadIdx.x == 0) sh.next = n + gridDim.x;
+            // (a group that breaks the rules: any query tile)
+            const int have = max(1, (__ldg(p.cu_groups + g + 1) - __ldg(p.cu_groups + g) + tile_seqs - 1) / tile_seqs);
+            bool held = now.held != 0;
+            uint8_t *b = base;
+            asm volatile("" : "+l"(b));
+            prefix_unit<D, BF16, NS, false>(p, sh, b, g, local % have, local / have % p.num_kv_heads,
+                                     local / have / p.num_kv_heads, unit_tokens, held, n + gridDim.x < listed, tq, tk, tv);
+            if (threadIdx.x == 0) sh.held = held;
+            __syncthreads();
+            if ((now.held && now.abort) || now.next >= now.listed) break;
+        }
+        __syncthreads();
+        if (now.held && (threadIdx.x >> 5) == W::kWarpMma) {
+            umma::fence_after_sync();
+            umma::tmem_dealloc(sh.tmem_base, W::kCols);
+        }
+    }
+}
+
 template <int D, bool BF16, int NS>
-cudaError_t launch_t(const SplitParams &p, int tiles, int unit_tokens, int units_per_list, const CUtensorMap &tq,
-                     const CUtensorMap &tk, const CUtensorMap &tv, cudaStream_t stream) {
-    auto kern = shared_prefix_kernel<D, BF16, NS>;
+cudaError_t launch_t(const SplitParams &p, int grid, bool padded, int tiles, int unit_tokens, int units_per_list,
+                     const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, cudaStream_t stream) {
+    auto kern = padded ? shared_prefix_kernel<D, BF16, NS, true> : shared_prefix_kernel<D, BF16, NS, false>;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(kSharedSmem<D, NS>));
     if (e != cudaSuccess) return e;
-    const int64_t grid = static_cast<int64_t>(p.num_groups) * units_per_list * p.num_kv_heads * tiles;
     return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(Streams<NS>::kThreads), kSharedSmem<D, NS>, stream, p,
                       tiles, unit_tokens, units_per_list, tq, tk, tv);
 }
 
 template <int D>
-cudaError_t launch_d(const SplitParams &p, bool bf16, bool pairs, int tiles, int unit_tokens, int units_per_list,
-                     const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, cudaStream_t stream) {
+cudaError_t launch_d(const SplitParams &p, bool bf16, bool pairs, int grid, bool padded, int tiles, int unit_tokens,
+                     int units_per_list, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
+                     cudaStream_t stream) {
     if (pairs)
-        return bf16 ? launch_t<D, true, 2>(p, tiles, unit_tokens, units_per_list, tq, tk, tv, stream)
-                    : launch_t<D, false, 2>(p, tiles, unit_tokens, units_per_list, tq, tk, tv, stream);
-    return bf16 ? launch_t<D, true, 1>(p, tiles, unit_tokens, units_per_list, tq, tk, tv, stream)
-                : launch_t<D, false, 1>(p, tiles, unit_tokens, units_per_list, tq, tk, tv, stream);
+        return bf16 ? launch_t<D, true, 2>(p, grid, padded, tiles, unit_tokens, units_per_list, tq, tk, tv, stream)
+                    : launch_t<D, false, 2>(p, grid, padded, tiles, unit_tokens, units_per_list, tq, tk, tv, stream);
+    return bf16 ? launch_t<D, true, 1>(p, grid, padded, tiles, unit_tokens, units_per_list, tq, tk, tv, stream)
+                : launch_t<D, false, 1>(p, grid, padded, tiles, unit_tokens, units_per_list, tq, tk, tv, stream);
 }
 
 }  // namespace
 
 size_t shared_prefix_smem(int head_dim) { return head_dim == 128 ? kSharedSmem<128, 2> : kSharedSmem<64, 2>; }
 
-cudaError_t launch_shared_prefix(const SplitParams &p, int head_dim, bool bf16, bool pairs, int tiles, int unit_tokens,
-                                 int units_per_list, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
-                                 cudaStream_t stream) {
-    return head_dim == 128 ? launch_d<128>(p, bf16, pairs, tiles, unit_tokens, units_per_list, tq, tk, tv, stream)
-                           : launch_d<64>(p, bf16, pairs, tiles, unit_tokens, units_per_list, tq, tk, tv, stream);
+cudaError_t launch_shared_prefix(const SplitParams &p, int head_dim, bool bf16, bool pairs, int grid, bool padded, int tiles,
+                                 int unit_tokens, int units_per_list, const CUtensorMap &tq, const CUtensorMap &tk,
+                                 const CUtensorMap &tv, cudaStream_t stream) {
+    auto launch = head_dim == 128 ? launch_d<128> : launch_d<64>;
+    return launch(p, bf16, pairs, grid, padded, tiles, unit_tokens, units_per_list, tq, tk, tv, stream);
 }
 
 }  // namespace pa

@@ -68,3 +68,18 @@ def test_requested_partitions_are_taken_exactly_where_32_blocks_hold_them(rule, 
             assert ok, P
         elif ok:                                          # what the rule refuses beyond need: none but long unaligned ones
             assert P % bs != 0 and P > 31 * bs + 16, P
+
+
+def test_empty_groups_do_not_change_the_plan():
+    """256 sequences over one prompt: the workspace (the partial results planned for) of a
+    list of groups that is padded is that of the tight one."""
+    from paged_kv_cache_140_gb300 import _build, _lib
+    _build.build()
+    size = _lib.load().pa_decode_shared_workspace_size
+    for hkv, d, bs, shared in ((8, 128, 16, 8192), (32, 64, 32, 2000), (4, 64, 128, 4000)):
+        tight = size(256, 1, 256, 32, hkv, d, bs, shared + 512, shared, 0)
+        for groups in (256, 300):
+            assert size(256, groups, 256, 32, hkv, d, bs, shared + 512, shared, 0) == tight, (hkv, groups)
+    # nothing shared, and the bounds say so: one pass, as for as many groups as sequences
+    assert size(256, 256, 1, 32, 8, 128, 16, 512, 500, 0) == size(256, 300, 1, 32, 8, 128, 16, 512, 500, 0)
+    assert size(256, 256, 1, 32, 8, 128, 16, 512, 500, 0) <= size(256, 256, 256, 32, 8, 128, 16, 512, 500, 0)
