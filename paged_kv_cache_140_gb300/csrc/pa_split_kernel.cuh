@@ -159,17 +159,19 @@ __device__ __forceinline__ void widen_k(uint32_t w, uint32_t &lo, uint32_t &hi) 
     }
 }
 
-// Four V codes as f16 pairs (0, 2) and (1, 3).  int8: the byte u = b + 128 taken
-// as the binary16 subnormal u 2^-24, two steps less per pair than its value; the
-// product is put right once per item, sum w b = 2^24 (sum w u 2^-24) - 128 sum w,
-// which costs one bit of the 24 that it is summed in.
+// Four V codes as f16 pairs (0, 2) and (1, 3), exactly, as K's.  (With u in their place
+// and 128 sum w taken off an item's sum, 64 7B-shaped sequences took 98.2 us against 99.2,
+// but a sum over values of both signs kept the roundings of 128 sum w: 2e-5 of the result
+// there and 2e-4 at 16 K to 32 K tokens, against 6e-7 and 1e-6.)
 template <int CT>
 __device__ __forceinline__ void widen_v(uint32_t w, uint32_t &ev, uint32_t &od) {
     if constexpr (CT == kCacheE4M3) {
         e4m3x4_to_f16x2x2(prmt(w, 0x3120u), ev, od);
     } else {
-        ev = (w & 0x00ff00ffu) ^ 0x00800080u;
-        od = ((w >> 8) & 0x00ff00ffu) ^ 0x00800080u;
+        ev = (w & 0x00ff00ffu) ^ 0x64806480u;
+        od = ((w >> 8) & 0x00ff00ffu) ^ 0x64806480u;
+        asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(ev) : "r"(0x64806480u));
+        asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(od) : "r"(0x64806480u));
     }
 }
 
@@ -619,7 +621,6 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
     uint32_t qf[KS][2];
     float qs[2];                  // logit scale of columns 2t, 2t + 1
     float acc[MT][4], m_run[2], l_run[2];
-    float lw[2];                  // int8: sum of the weights that enter the V product
     float mu[2];                  // the reference that weights are taken under: m_run, or 0 while there is none
     int cslot = 0;
     uint32_t cphase = 0, citems = 0;
@@ -690,7 +691,7 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 m_run[e] = -INFINITY;
-                l_run[e] = lw[e] = mu[e] = 0.f;
+                l_run[e] = mu[e] = 0.f;
             }
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) acc[mt][0] = acc[mt][1] = acc[mt][2] = acc[mt][3] = 0.f;
@@ -802,7 +803,6 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                     m_run[e] = mn;
                     mu[e] = mn == -INFINITY ? 0.f : mn;
                     l_run[e] *= al;
-                    lw[e] *= al;
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt) {
                         acc[mt][e] *= al;
@@ -816,10 +816,7 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                 if constexpr (!kWhole)
                     if (hs > 0 && !second) continue;
 #pragma unroll
-                for (int e = 0; e < NE; ++e) {
-                    l_run[e] += pw[hs][e] + pw[hs][2 + e];
-                    if constexpr (CT == kCacheInt8) lw[e] += w4[hs][e] + w4[hs][2 + e];
-                }
+                for (int e = 0; e < NE; ++e) l_run[e] += pw[hs][e] + pw[hs][2 + e];
                 // weights as the PV B fragment: tokens 2t, 2t+1, 2t+8, 2t+9 of column g
                 uint32_t bhi[2], blo[2];
                 {
@@ -914,19 +911,7 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1)
 #pragma unroll
-            for (int e = 0; e < NE; ++e) {
-                l_run[e] += __shfl_xor_sync(kFull, l_run[e], o);
-                if constexpr (CT == kCacheInt8) lw[e] += __shfl_xor_sync(kFull, lw[e], o);
-            }
-        if constexpr (CT == kCacheInt8) {   // sum w u 2^-24 -> sum w (u - 128)
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int e = 0; e < NE; ++e) {
-                    acc[mt][e] = fmaf(acc[mt][e], 16777216.f, -128.f * lw[e]);
-                    acc[mt][2 + e] = fmaf(acc[mt][2 + e], 16777216.f, -128.f * lw[e]);
-                }
-        }
+            for (int e = 0; e < NE; ++e) l_run[e] += __shfl_xor_sync(kFull, l_run[e], o);
         if (nsubs > 1) {
             // join the states of the head's warps: the others hand theirs to the first
             const uint32_t par = (citems - 1) & 1u;      // of this item
