@@ -527,7 +527,9 @@ pa_status pa_quant_decode(void *out, pa_dtype out_dtype, const void *query, pa_d
  *                  fixed list of a captured step is): they cost little, and the call is
  *                  planned for ceil(num_seqs / max_group_size) groups
  *   scale        : >= 0
- *   workspace    : pa_decode_shared_workspace_size(...) bytes (may be 0); no
+ *   workspace    : pa_decode_shared_workspace_size(...) bytes (may be 0; it holds
+ *                  partial results for prefixes and private parts as long as the
+ *                  bounds let them be, so loose bounds cost hundreds of MB); no
  *                  initial contents
  * Large groups run on the tensor cores as pa_prefill does (softmax weights
  * rounded to binary16, or split into two bfloat16 parts); there a block id out

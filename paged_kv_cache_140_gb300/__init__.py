@@ -381,20 +381,25 @@ def _flag(err_flag, dev: int):
     return err_flag.data_ptr()
 
 
+_thread_ws = threading.local()       # .by_stream: {(device, stream): DecodeWorkspace} of one thread
+
+
 def _scratch(rt, workspace, nbytes: int, dev: int, stream: int):
     """The workspace of one call: the caller's, the calling thread's default one for
     the current stream (a call is several launches, between which another thread's
-    may come), or, while a graph is captured, one of the graph's own (so that
+    may come), kept until the thread ends, or, while a graph is captured, one of the graph's own (so that
     graphs never share one and none is replaced by a larger one later)."""
     if nbytes == 0:
         return None
     if workspace is None:
         if rt.capturing():
             return rt.empty(nbytes, dtype=rt.u8, device=dev)
-        key = (dev, stream, threading.get_ident())
-        workspace = _default_ws.get(key)
+        try:
+            workspace = _thread_ws.by_stream.get((dev, stream))
+        except AttributeError:
+            _thread_ws.by_stream = {}
         if workspace is None:
-            workspace = _default_ws.setdefault(key, DecodeWorkspace(_torch().device("cuda", dev)))
+            workspace = _thread_ws.by_stream[dev, stream] = DecodeWorkspace(_torch().device("cuda", dev))
     if isinstance(workspace, DecodeWorkspace):
         workspace = workspace.get(nbytes)
     if workspace.get_device() != dev or not workspace.is_contiguous():
@@ -565,7 +570,8 @@ def decode_shared(out, query, k_cache, v_cache, block_tables, context_lens, cu_g
     the first ``shared_lens[s]`` tokens (int32 [B], one value per group) hold the
     same K/V rows in every member.  ``max_group_size`` and ``max_shared_len`` are
     host-side bounds (defaults: the batch size and ``max_context_len``; tight
-    bounds make the call faster)."""
+    bounds make the call faster and its workspace smaller:
+    :func:`decode_shared_workspace_size`)."""
     rt = _rt or _runtime()
     dev, cache = query.get_device(), k_cache.shape
     if (dev != rt.current_device() or out.get_device() != dev or k_cache.get_device() != dev or
