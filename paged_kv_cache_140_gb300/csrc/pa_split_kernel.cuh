@@ -468,8 +468,10 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                 }
             }
             ok = __all_sync(kFull, ok);
-            islot = (islot + 1 == S) ? 0 : islot + 1;
-            ++uses;
+            if (ok) {
+                islot = (islot + 1 == S) ? 0 : islot + 1;
+                ++uses;
+            }
             return slot;
         };
         while (ok && work && ic.start < hi) {
@@ -590,6 +592,13 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                     arrive(&full[slot]);
                 }
             }
+        }
+        // After a wait that gave up, let the copies still in flight land before the CTA ends.
+        if (!ok) {
+            for (uint32_t u = uses > static_cast<uint32_t>(S) ? uses - S : 0u; u < uses; ++u)
+                mbar_wait_bounded(&full[u % S], (u / S) & 1u);
+            for (uint32_t i = items > static_cast<uint32_t>(kQueryRing) ? items - kQueryRing : 0u; i < items; ++i)
+                mbar_wait_bounded(&qfull[i % kQueryRing], (i / kQueryRing) & 1u);
         }
         if (p.late_wait) pdl_wait();   // the grid does not finish before the prefix kernel
         return;
