@@ -112,3 +112,42 @@ def test_inputs_written_right_before_the_call(members):
     torch.cuda.synchronize()
     for i, o in enumerate(outs):
         assert torch.equal(o, outs[i % 2]) and (o - sets[i % 2][1]).abs().max() < 1e-3, i
+
+
+def test_calls_on_several_streams_at_once():
+    """Prefixes of one query tile, of pairs, of a padded list and a prefill, all of which hold
+    tensor memory, on four streams."""
+    work = []
+    for members, pad in (([12] * 10, 0), ([150], 0), ([30, 20], 60)):
+        hq, hkv, d, bs = 8, 4, 128, 16
+        assert own_pass(members, [900], hkv, d)
+        b = S.make(members, [900] * len(members), [30] * sum(members), hq, hkv, d, bs, "bf16", seed=70)
+        cu = np.concatenate([b["cu"], np.full(pad, b["cu"][-1], np.int32)])
+        t = [x.cuda() for x in (b["q"], b["k"], b["v"], b["bt"], torch.tensor(b["ctx"], dtype=torch.int32), torch.from_numpy(cu),
+                                torch.from_numpy(b["sh"]))]
+
+        def call(out, t=t, b=b):
+            pa.decode_shared(out, *t, b["scale"], max_group_size=b["mg"], max_shared_len=900, max_context_len=930)
+        work.append((call, torch.empty(b["q"].shape, device="cuda")))
+    q = torch.randn(600, 8, 128, device="cuda").bfloat16()
+    cache = torch.randn(2, 80, 16, 4, 128, device="cuda").bfloat16()
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")       # noqa: E731
+    table, ctx, cu_q = torch.arange(75, device="cuda").int()[None].contiguous(), i32([1200]), i32([0, 600])
+
+    def prefill(out):
+        pa.prefill(out, q, cache[0], cache[1], table, ctx, cu_q, 128 ** -0.5, max_q_len=600)
+    work.append((prefill, torch.empty(q.shape, device="cuda")))
+    want = []
+    for call, out in work:
+        call(out)
+        want.append(out.clone())
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in work]
+    wrong = torch.zeros(len(work), dtype=torch.int32, device="cuda")
+    for _ in range(40):
+        for i, ((call, out), s) in enumerate(zip(work, streams)):
+            with torch.cuda.stream(s):
+                call(out)
+                wrong[i] += (out != want[i]).any()
+    torch.cuda.synchronize()
+    assert wrong.tolist() == [0] * len(work)
