@@ -129,6 +129,10 @@ int resolve_partition(int max_context_len, int block_size, int requested) {
     const int cap = 32 * block_size;
     if (requested != 0) {
         if (requested < 16 || requested % 16 != 0 || requested > cap) return 0;
+        // A partition's block ids sit in the 32 lanes of a warp.  A long one that starts
+        // inside a block would reach into a 33rd: it is cut to whole blocks.
+        if (requested % block_size != 0 && requested > cap - block_size + 16 && max_context_len > requested)
+            return requested - requested % block_size;
         return requested;
     }
     int P;

@@ -133,3 +133,21 @@ def test_the_longest_requests_that_start_inside_blocks(bs):
     lens = [3 * P + 5, 2 * P, P + 1, 40, 0, 5 * P - 1]
     quant_case(lens, -(-5 * P // bs), 8, 4, 64, bs, "e4m3", 7, partition_size=P)
     shared_case([1] * 6, [0] * 6, lens, -(-5 * P // bs), 8, 4, 64, bs, "bf16", 8, partition_size=P, max_shared_len=0)
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(8, 8, 128), (4, 2, 64)])
+@pytest.mark.parametrize("bs,P", [(64, 2032), (128, 4064), (48, 1520), (64, 2000)])
+def test_decode_with_long_requests_that_start_inside_blocks(bs, P, hq, hkv, d):
+    """pa.decode on the cooperative (d = 128) and the per-warp kernel."""
+    lens = [3 * P + 5, 2 * P, P + 1, P, 40, 1]
+    nb, width = 70, -(-(3 * P + 5) // bs)
+    bt = pool_tables(len(lens), width, nb, 9)
+    g = torch.Generator().manual_seed(9)
+    c = {n: torch.randn(nb, bs, hkv, d, generator=g).bfloat16() for n in "kv"}
+    q = (2 * torch.randn(len(lens), hq, d, generator=g)).bfloat16()
+    out = torch.empty(q.shape, device="cuda")
+    err = pa.new_err_flag()
+    args = (bt.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(), d ** -0.5)
+    pa.decode(out, q.cuda(), c["k"].cuda(), c["v"].cuda(), *args, partition_size=P, err_flag=err)
+    assert pa.read_err_flag(err) == 0
+    compare(out, q, lambda n, sl: c[n].view(-1, hkv, d)[sl].double(), bt, lens, bs, d ** -0.5)

@@ -83,3 +83,16 @@ def test_empty_groups_do_not_change_the_plan():
     # nothing shared, and the bounds say so: one pass, as for as many groups as sequences
     assert size(256, 256, 1, 32, 8, 128, 16, 512, 500, 0) == size(256, 300, 1, 32, 8, 128, 16, 512, 500, 0)
     assert size(256, 256, 1, 32, 8, 128, 16, 512, 500, 0) <= size(256, 256, 256, 32, 8, 128, 16, 512, 500, 0)
+
+
+def test_decode_takes_long_requests_that_start_inside_blocks_as_whole_blocks():
+    from paged_kv_cache_140_gb300 import _build, _lib
+    _build.build()
+    used = _lib.load().pa_decode_partition_size
+    for bs in BLOCK_SIZES:
+        for P in range(16, 32 * bs + 1, 16):
+            got = used(4, 8, 8, 128, bs, 100000, P)
+            assert most_blocks(got, bs) <= 32
+            assert got == (P if most_blocks(P, bs) <= 32 else P - P % bs), (bs, P)
+            assert used(4, 8, 8, 128, bs, P, P) == P         # one partition starts at 0
+        assert used(4, 8, 8, 128, bs, 100000, 32 * bs + 16) == 0
