@@ -190,9 +190,9 @@ int pa_decode_partition_size(int num_seqs, int num_heads, int num_kv_heads,
  *                  workspace); must be <= max_blocks_per_seq * block_size
  *   scale        : softmax scale, usually 1/sqrt(head_dim)
  *   partition_size : 0 (auto) or a multiple of 16 tokens, at most
- *                  32 * block_size; one above 31 * block_size + 16 that is no
- *                  multiple of block_size is taken as the next lower multiple
- *                  where max_context_len exceeds it
+ *                  32 * block_size; one whose repetitions would reach into a 33rd
+ *                  block (2032 tokens of blocks of 64) is taken as the next lower
+ *                  multiple of block_size where max_context_len exceeds it
  *                  (pa_decode_partition_size tells the length used)
  *   workspace    : device buffer of pa_decode_workspace_size(...) bytes
  *                  (may be NULL if that size is 0)

@@ -11,6 +11,7 @@
 #include <algorithm>
 #include <atomic>
 #include <mutex>
+#include <numeric>
 
 #include "pa.h"
 #include "pa_cache_ops.h"
@@ -129,9 +130,10 @@ int resolve_partition(int max_context_len, int block_size, int requested) {
     const int cap = 32 * block_size;
     if (requested != 0) {
         if (requested < 16 || requested % 16 != 0 || requested > cap) return 0;
-        // A partition's block ids sit in the 32 lanes of a warp.  A long one that starts
-        // inside a block would reach into a 33rd: it is cut to whole blocks.
-        if (requested % block_size != 0 && requested > cap - block_size + 16 && max_context_len > requested)
+        // A partition's block ids sit in the 32 lanes of a warp.  Partitions start at most
+        // block_size - gcd inside a block; a long one that reaches into a 33rd from there
+        // is cut to whole blocks.
+        if (requested > cap - block_size + std::gcd(requested, block_size) && max_context_len > requested)
             return requested - requested % block_size;
         return requested;
     }
