@@ -209,6 +209,10 @@ class DecodeWorkspace:
         if nbytes == 0:
             return None
         if self.buf is None or self.buf.numel() < nbytes:
+            if self.buf is not None:
+                # allocated on another stream perhaps, which may have its memory back once
+                # this one is past the calls that used it
+                self.buf.record_stream(torch.cuda.current_stream(self.buf.device))
             self.buf = torch.empty(nbytes, dtype=torch.uint8, device=self.device or "cuda")
         return self.buf
 

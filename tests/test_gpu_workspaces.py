@@ -71,3 +71,22 @@ def test_a_thread_keeps_its_workspace_between_calls():
     for _ in range(5):
         call(out)
     assert torch.cuda.memory_allocated() == before
+
+
+def test_a_replaced_buffer_is_not_handed_out_while_its_last_stream_runs():
+    """A workspace made on one stream, used on another and grown there."""
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    ws, size = pa.DecodeWorkspace("cuda"), 40 << 20
+    first, second = torch.cuda.Stream(), torch.cuda.Stream()
+    with torch.cuda.stream(first):
+        old = ws.get(size).data_ptr()
+    second.wait_stream(first)
+    with torch.cuda.stream(second):
+        ws.get(size).zero_()
+        torch.cuda._sleep(200_000_000)          # what still uses the buffer
+        assert ws.get(2 * size).data_ptr() != old
+    with torch.cuda.stream(first):
+        fresh = torch.empty(size, dtype=torch.uint8, device="cuda")
+    assert not second.query() and fresh.data_ptr() != old
+    torch.cuda.synchronize()
