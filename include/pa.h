@@ -534,9 +534,13 @@ pa_status pa_quant_decode(void *out, pa_dtype out_dtype, const void *query, pa_d
  *                  partial results for prefixes and private parts as long as the
  *                  bounds let them be, so loose bounds cost hundreds of MB); no
  *                  initial contents
- * Large groups run on the tensor cores as pa_prefill does (softmax weights
- * rounded to binary16, or split into two bfloat16 parts); there a block id out
- * of range may leave out more of the prefix than its own tokens.
+ * Where max_group_size allows more than 8 query rows per KV head (sequences x
+ * num_heads / num_kv_heads) and block_size is a power of two up to 128, prefixes run
+ * on the tensor cores as pa_prefill does: each K/V row is read once for up to 256
+ * query rows, softmax weights are rounded to binary16 (f16 caches: 2^-11 of the
+ * weight) or split into two bfloat16 parts, and a block id out of range may leave out
+ * more of the prefix than its own tokens.  Otherwise a prefix is read once for every 8
+ * query rows, with the weights of pa_decode: two 16-bit parts of the cache's type.
  * cu_groups or shared_lens that break these rules set PA_FLAG_BAD_CONTEXT_LEN;
  * the groups concerned are then undefined (no memory out of bounds is touched).
  * partition_size is that of the private parts; the prefixes are cut by a rule of

@@ -12,24 +12,32 @@
 //
 // What bounds it: with 128 rows per K/V tile the tensor cores (2 x 128 x 128 x D
 // products per tile, half as many again for bfloat16, whose weights go in as a
-// high and a low part), with few rows the K/V loads.  A unit is a pair of query
-// tiles of 128 rows, a KV head and a range of tokens; the range is chosen by the
-// host so that the units fill the SMs in whole waves.  A CTA runs two streams,
-// X = A and B, each with its own scores and output in tensor memory, so that
-// one stream's softmax runs under the other's products:
+// high and a low part; binary16 weights are rounded once, 11 bits, and summed as
+// rounded), with few rows the K/V loads.  A unit is a query tile of 128 rows or a pair
+// of them, a KV head and a range of tokens; the range is chosen by the host so that
+// the units fill the SMs in whole waves.
+//
+// Groups of up to 128 rows (NS = 1): one stream per CTA, a query tile over every K/V
+// tile of the range, and two CTAs per SM, so that one's start, end and softmax run
+// under the other's loads and products.  Its 128 registers a thread hold 32 scores of a
+// row at a time.
+// Larger groups (NS = 2): pairs of tiles, one CTA per SM with two streams, X = A and B,
+// each with its own scores and output in tensor memory, so that one stream's softmax
+// runs under the other's products:
 //   two query tiles: stream X is query tile X, both over every K/V tile loaded
 //                    (each byte brought in feeds 256 rows);
-//   one query tile:  the streams take the range's first and second half of the
-//                    K/V tiles, with the same queries, and write two partials.
+//   one query tile (the odd last, or a smaller group): the streams take the range's
+//                    first and second half of the K/V tiles, with the same queries,
+//                    and write two partials.
 // Per stream and K/V tile: S = Q K^T (tcgen05.mma from shared memory), softmax by
-// one thread per row (its 128 scores in registers; the output rescaled only when
-// the maximum grows by more than 2^8), weights back over S in four chunks of 32
+// one thread per row (NS = 2: its 128 scores in registers; the output rescaled only
+// when the maximum grows by more than 2^8), weights back over S in four chunks of 32
 // keys released one by one, O += P V (P from tensor memory).
 //
-// Warps: 0-7 softmax and output (four per stream), 8 and 10 load K and V tiles
-// by TMA (one box per block and 64 columns), 9 issues the products.  Warps whose
-// rows are all past the group's end skip the softmax.  Every wait is bounded
-// (2 s) and reports PA_FLAG_TIMEOUT.
+// Warps: four per stream for softmax and output, then one that loads K tiles, one that
+// issues the products and one that loads V tiles (TMA, one box per block and 64
+// columns): 7 or 11.  Warps whose rows are all past the group's end skip the softmax.
+// Every wait is bounded (2 s) and reports PA_FLAG_TIMEOUT.
 #include <math_constants.h>
 
 #include "pa.h"

@@ -15,9 +15,10 @@
 // m follows the maximum of s_p + log2 v_p, the exponent of the weights that
 // enter the V product, less 7: the largest weight 2^(s_p - m) v_p lies between
 // 2^7 and 2^15 (m is raised only when one passes 2^15) whatever the scales are.
-// They go into the product as binary16 high and low parts, ~22 bits down to
-// 2^-24, that is 2^-31 of the largest, so that even 2^15 tokens of the least
-// weight lose no more than 2^-16.  2^(s_p - m) itself is then off by up to 1 / v_p,
+// They go into the product as a high and a low part of the products' type: binary16
+// (f16 and 8-bit caches), ~22 bits down to 2^-24, that is 2^-31 of the largest, so
+// that even 2^15 tokens of the least weight lose no more than 2^-16; or, for bf16
+// caches, bfloat16, 16 bits (2^-17 off at most) of any size.  2^(s_p - m) itself is then off by up to 1 / v_p,
 // which 32 bits hold for every scale the cache write makes from rows below 2^60.
 //
 // 8-bit codes are exact in binary16 and the products run there; the query is
@@ -35,8 +36,8 @@
 // The SMs take equal shares of all slots; an item across a share's end is cut there.
 //
 // Measured (GB300, whole calls, join included; of the measured copy rate): 256
-// 13B-shaped sequences over e4m3 codes 217 us, 0.91; 64 7B-shaped over int8 97 us,
-// 0.87; 16 of 16 K to 32 K tokens, 32 heads on 8, e4m3, 127 us, 0.95.  With the math
+// 13B-shaped sequences over e4m3 codes 217 us, 0.91; 64 7B-shaped over int8 99 us,
+// 0.85; 16 of 16 K to 32 K tokens, 32 heads on 8, e4m3, 127 us, 0.95.  With the math
 // left out the first took 216, without the scales' loads too 202: the 3 % of bytes
 // that scales are cost 7 %, as 32-byte pieces.  Tried and slower: 16 consumer warps
 // (240 us against 221 at that time), one stage per slot (277), two ring slots instead
@@ -295,9 +296,17 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
         prefetch_tensormap(&tmap_k);
         prefetch_tensormap(&tmap_v);
     }
-    // Launched with programmatic dependent launch.  late_wait: the previous
-    // kernel is this call's prefix kernel, which let this one start only after
-    // everything before the call had completed.
+    // Launched with programmatic dependent launch.  late_wait: the previous kernel is
+    // this call's prefix kernel (or an earlier launch of this one behind it), whose
+    // results are not read here, and this one waits for it only at its end.  Lengths,
+    // tables, queries and K/V are read before that wait although a kernel ahead of the
+    // call may have written them.  The programming model promises what earlier kernels
+    // wrote to a grid that has waited itself; here every CTA of the prefix kernel waited
+    // before it let dependents start, so all of that was complete and in memory before
+    // this grid's first CTA began, as before any launch, and no cache of a new grid holds
+    // older lines.  The workspace rows written here were last read by the join before the
+    // prefix kernel.  (Waiting at the start: one long prompt 108 us against 99, 24 mixed
+    // groups 141 against 129, 64 x 4 samples 266 against 254.)
     if (!p.late_wait) pdl_wait();
     pdl_launch_dependents();
     // ---- the entries' lengths ----
