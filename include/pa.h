@@ -528,7 +528,8 @@ pa_status pa_quant_decode(void *out, pa_dtype out_dtype, const void *query, pa_d
  *                  (<= max_context_len); tight ones make the call faster.  A list of
  *                  num_groups >= num_seqs counts as padded with empty groups (as the
  *                  fixed list of a captured step is): they cost little, and the call is
- *                  planned for ceil(num_seqs / max_group_size) groups
+ *                  planned for ceil(num_seqs / max_group_size) groups; where nothing is
+ *                  shared, say so (max_group_size 1 or max_shared_len 0)
  *   scale        : >= 0
  *   workspace    : pa_decode_shared_workspace_size(...) bytes (may be 0; it holds
  *                  partial results for prefixes and private parts as long as the

@@ -575,7 +575,8 @@ def decode_shared(out, query, k_cache, v_cache, block_tables, context_lens, cu_g
     same K/V rows in every member.  ``max_group_size`` and ``max_shared_len`` are
     host-side bounds (defaults: the batch size and ``max_context_len``; tight
     bounds make the call faster and its workspace smaller:
-    :func:`decode_shared_workspace_size`)."""
+    :func:`decode_shared_workspace_size`).  A list of groups may be padded with
+    empty ones up to any length, as a captured step's is."""
     rt = _rt or _runtime()
     dev, cache = query.get_device(), k_cache.shape
     if (dev != rt.current_device() or out.get_device() != dev or k_cache.get_device() != dev or
