@@ -505,6 +505,65 @@ pa_status pa_quant_decode(void *out, pa_dtype out_dtype, const void *query, pa_d
                           size_t workspace_bytes, int *err_flag, void *stream);
 
 /*
+ * ------------------------------------------------------------------------
+ * Cache of 4-bit codes
+ * ------------------------------------------------------------------------
+ * Codes of 0 to 15, two to a byte: k_cache and v_cache are bytes [num_blocks,
+ * block_size, num_kv_heads, head_dim / 2], element 2 i of a row in the low half of
+ * byte i, element 2 i + 1 in the high half.  Every 64 neighbouring elements of a row
+ * are a group with a scale s and a zero z, two bfloat16 numbers of k_scales, v_scales
+ * [num_blocks, num_kv_heads, block_size, head_dim / 64, 2] (heads before tokens; s
+ * first); a code u stands for s * (u + z).  Scales are block-major like the codes, so
+ * pa_copy_blocks and pa_swap_blocks move both (as PA_FP8_E4M3 caches of as many bytes
+ * a block).
+ *
+ * head_dim 64 or 128, num_blocks * block_size and num_blocks * num_kv_heads below
+ * 2^31; arithmetic in fp32.  Attention is accurate for queries below 2^100 and V rows
+ * below 2^60 in magnitude.
+ *
+ * pa_int4_reshape_and_cache -- write new K/V rows as 4-bit codes.
+ *
+ * For a group x, in fp32, bf16() rounding to nearest even:
+ *     s = bf16(max((max x / 2 - min x / 2) / 7.5, max |x| / 2^8, 2^-60)),
+ *     z = bf16(min x / s),   u_i = round(x_i * (1 / s) - z), at least 0, at most 15
+ * so an element is off by about half of s, a fifteenth of the group's range (or,
+ * where a group's values lie far from zero, 2^-8 of the largest).  A group that holds
+ * an infinity or NaN gets the scale NaN and codes 0: its elements read back as NaN,
+ * and attention over it gives NaN (a V group: in the elements of that group alone).
+ *   Arguments and rules of pa_quant_reshape_and_cache.
+ */
+pa_status pa_int4_reshape_and_cache(const void *key, const void *value, int64_t key_stride, int64_t value_stride,
+                                    void *k_cache, void *v_cache, void *k_scales, void *v_scales,
+                                    const int64_t *slot_mapping, int64_t num_tokens, int64_t num_blocks, int block_size,
+                                    int num_kv_heads, int head_dim, pa_dtype dtype, int *err_flag, void *stream);
+
+/*
+ * pa_int4_gather -- read a 4-bit cache back into dense rows: s * (u + z), the sum and
+ * the product in fp32, rounded once to out_dtype.  Arguments and rules of
+ * pa_quant_gather.
+ */
+pa_status pa_int4_gather(void *out_k, void *out_v, pa_dtype out_dtype, const void *k_cache, const void *v_cache,
+                         const void *k_scales, const void *v_scales, const int32_t *block_tables, int max_blocks_per_seq,
+                         const int32_t *cu_seqlens, const int32_t *seq_starts, int num_seqs, int64_t num_tokens,
+                         int num_kv_heads, int head_dim, int block_size, int64_t num_blocks, int *err_flag, void *stream);
+
+/*
+ * pa_int4_decode -- pa_decode over a 4-bit cache, without the rows being widened in
+ * memory.  Arguments, rules, workspace and reproducibility of pa_quant_decode
+ * (head_dim 64 or 128, any number of KV heads, block_size 8 or a multiple of 16 up to
+ * 256, 1, 2, 4 or 8 query heads per KV head).  Codes are exact in the products, each
+ * query row is first scaled by a power of two and taken in binary16, softmax weights
+ * enter as two binary16 parts; sums and softmax are fp32.
+ */
+size_t pa_int4_decode_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size,
+                                     int max_context_len, int partition_size);
+pa_status pa_int4_decode(void *out, pa_dtype out_dtype, const void *query, pa_dtype q_dtype, const void *k_cache,
+                         const void *v_cache, const void *k_scales, const void *v_scales, const int32_t *block_tables,
+                         int max_blocks_per_seq, const int32_t *context_lens, int max_context_len, int num_seqs,
+                         int num_heads, int num_kv_heads, int head_dim, int block_size, int64_t num_blocks, float scale,
+                         int partition_size, void *workspace, size_t workspace_bytes, int *err_flag, void *stream);
+
+/*
  * pa_decode_shared -- pa_decode for a batch whose sequences share long
  * prefixes, each prefix computed once for all sequences of its group.
  *

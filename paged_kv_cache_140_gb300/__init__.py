@@ -13,6 +13,7 @@ PyTorch fallback - a missing library raises.
     quant_reshape_and_cache(key, value, k_cache, v_cache, k_scales, v_scales, slot_mapping)
     quant_gather(out_k, out_v, k_cache, v_cache, k_scales, v_scales, block_tables, cu_seqlens, ...)
     quant_decode(out, query, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, scale, ...)
+    int4_reshape_and_cache, int4_gather, int4_decode: the same over caches of 4-bit codes
 
 Cache layout: ``[num_blocks, block_size, num_kv_heads, head_dim]`` per layer
 for K and for V ("LLM推理优化：vLLM PagedAttention深度解析与工程实践", §4.1).
@@ -21,7 +22,9 @@ Caches are float16 / bfloat16, or FP8 e4m3 codes (``torch.float8_e4m3fn`` or
 keep int8 or e4m3 codes with a float32 scale per token and KV head,
 ``[num_blocks, block_size, num_kv_heads]``.  :func:`copy_blocks` and
 :func:`swap_blocks` move such a cache as bytes: ``codes.view(torch.uint8)``, and
-``scales.view(torch.uint8).view(NB, bs, Hkv, 4)``.
+``scales.view(torch.uint8).view(NB, bs, Hkv, 4)``.  The ``int4_*`` calls keep two
+codes to a byte, ``torch.uint8`` ``[NB, bs, Hkv, D/2]``, with a bfloat16 scale and zero
+per 64 elements, ``[NB, Hkv, bs, D/64, 2]`` (heads before tokens).
 """
 from __future__ import annotations
 
@@ -36,6 +39,7 @@ from ._lib import (FLAG_BAD_BLOCK_ID, FLAG_BAD_CONTEXT_LEN, FLAG_BAD_COPY_PAIR, 
 __all__ = ["reshape_and_cache", "decode", "decode_append", "prefill", "copy_blocks", "copy_blocks_layers", "swap_blocks", "decode_workspace_size",
            "decode_partition_size", "DecodeWorkspace", "new_err_flag", "read_err_flag",
            "quant_reshape_and_cache", "quant_gather", "quant_decode", "quant_decode_workspace_size", "decode_shared",
+           "int4_reshape_and_cache", "int4_gather", "int4_decode", "int4_decode_workspace_size",
            "decode_shared_workspace_size", "PagedAttentionError", "FLAG_BAD_SLOT", "FLAG_BAD_BLOCK_ID", "FLAG_BAD_CONTEXT_LEN",
            "FLAG_BAD_COPY_PAIR", "FLAG_TIMEOUT", "library_path", "StepGraph"]
 
@@ -353,6 +357,7 @@ class _Runtime:
         self.half = _Codes({torch.float16: PA_F16, torch.bfloat16: PA_BF16})
         self.out = _Codes({**self.half, torch.float32: PA_F32})
         self.codes = _Codes({torch.int8: PA_INT8, torch.uint8: PA_FP8_E4M3, torch.float8_e4m3fn: PA_FP8_E4M3})
+        self.b16 = torch.bfloat16
         self.f32, self.i32, self.i64, self.u8 = torch.float32, torch.int32, torch.int64, torch.uint8
         self.current_device = torch.cuda.current_device
         self.capturing = torch.cuda.is_current_stream_capturing
@@ -551,6 +556,137 @@ def quant_decode(out, query, k_cache, v_cache, k_scales, v_scales, block_tables,
         None if err_flag is None else _flag(err_flag, dev), stream)
     if st:
         _lib.check(st, "pa_quant_decode")
+
+
+def _int4_cache(rt, k_cache, v_cache, k_scales, v_scales, d: int):
+    """(num_blocks, block_size, num_kv_heads) of a 4-bit cache for rows of d elements."""
+    shape = k_cache.shape
+    if (len(shape) != 4 or v_cache.shape != shape or 2 * shape[3] != d or k_cache.dtype != rt.u8 or
+            v_cache.dtype != rt.u8):
+        raise ValueError("caches must be uint8 [NB, bs, Hkv, D/2]")
+    nb, bs, hkv, _ = shape
+    words = (nb, hkv, bs, d // 64, 2)
+    if k_scales.shape != words or v_scales.shape != words or k_scales.dtype != rt.b16 or v_scales.dtype != rt.b16:
+        raise ValueError("scales must be bfloat16 [NB, Hkv, bs, D/64, 2]")
+    return nb, bs, hkv
+
+
+def int4_reshape_and_cache(key, value, k_cache, v_cache, k_scales, v_scales, slot_mapping, err_flag=None) -> None:
+    """Write key/value rows [T, Hkv, D] (f16 or bf16) into cache slots (slot < 0:
+    skip) as 4-bit codes, a scale and a zero per 64 elements.
+
+    key and value may be slices of a wider tensor, as for :func:`quant_reshape_and_cache`."""
+    rt = _rt or _runtime()
+    dev, shape = key.get_device(), key.shape
+    if (dev != rt.current_device() or value.get_device() != dev or k_cache.get_device() != dev or
+            v_cache.get_device() != dev or k_scales.get_device() != dev or v_scales.get_device() != dev or
+            slot_mapping.get_device() != dev or not k_cache.is_contiguous() or not v_cache.is_contiguous() or
+            not k_scales.is_contiguous() or not v_scales.is_contiguous() or not slot_mapping.is_contiguous()):
+        _refuse((("k_cache", k_cache), ("v_cache", v_cache), ("k_scales", k_scales), ("v_scales", v_scales),
+                 ("slot_mapping", slot_mapping)), "key and value must be on the device of the caches")
+    if len(shape) != 3 or value.shape != shape or value.dtype != key.dtype:
+        raise ValueError("key/value must be [T, Hkv, D] of one dtype")
+    T, hkv, d = shape
+    nb, bs, heads = _int4_cache(rt, k_cache, v_cache, k_scales, v_scales, d)
+    if heads != hkv:
+        raise ValueError("cache and key heads differ")
+    if slot_mapping.dtype != rt.i64 or slot_mapping.numel() != T:
+        raise ValueError("slot_mapping must be int64 [T]")
+    ks, vs = key.stride(), value.stride()
+    if ks[2] != 1 or vs[2] != 1 or (hkv != 1 and (ks[1] != d or vs[1] != d)):
+        raise ValueError("key/value: the rows of one token must be dense")
+    one = T <= 1
+    st = rt.lib.pa_int4_reshape_and_cache(
+        key.data_ptr(), value.data_ptr(), hkv * d if one else ks[0], hkv * d if one else vs[0], k_cache.data_ptr(),
+        v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), slot_mapping.data_ptr(), T, nb, bs, hkv,
+        d, rt.half[key.dtype], None if err_flag is None else _flag(err_flag, dev), rt.stream(dev))
+    if st:
+        _lib.check(st, "pa_int4_reshape_and_cache")
+
+
+def int4_gather(out_k, out_v, k_cache, v_cache, k_scales, v_scales, block_tables, cu_seqlens, seq_starts=None,
+                err_flag=None) -> None:
+    """:func:`quant_gather` from a 4-bit cache written by :func:`int4_reshape_and_cache`."""
+    rt = _rt or _runtime()
+    dev, shape, table = out_k.get_device(), out_k.shape, block_tables.shape
+    if (dev != rt.current_device() or out_v.get_device() != dev or k_cache.get_device() != dev or
+            v_cache.get_device() != dev or k_scales.get_device() != dev or v_scales.get_device() != dev or
+            block_tables.get_device() != dev or cu_seqlens.get_device() != dev or not out_k.is_contiguous() or
+            not out_v.is_contiguous() or not k_cache.is_contiguous() or not v_cache.is_contiguous() or
+            not k_scales.is_contiguous() or not v_scales.is_contiguous() or not block_tables.is_contiguous() or
+            not cu_seqlens.is_contiguous()):
+        _refuse((("out_k", out_k), ("out_v", out_v), ("k_cache", k_cache), ("v_cache", v_cache), ("k_scales", k_scales),
+                 ("v_scales", v_scales), ("block_tables", block_tables), ("cu_seqlens", cu_seqlens)))
+    if len(shape) != 3 or out_v.shape != shape or out_v.dtype != out_k.dtype:
+        raise ValueError("out_k/out_v must be [T, Hkv, D] of one dtype")
+    d = shape[2]
+    nb, bs, hkv = _int4_cache(rt, k_cache, v_cache, k_scales, v_scales, d)
+    if shape[1] != hkv:
+        raise ValueError("cache and out_k heads differ")
+    if len(table) != 2 or block_tables.dtype != rt.i32:
+        raise ValueError("block_tables must be int32 [B, maxNB]")
+    B = table[0]
+    if cu_seqlens.dtype != rt.i32 or cu_seqlens.numel() != B + 1:
+        raise ValueError("cu_seqlens must be int32 [B+1]")
+    if seq_starts is not None:
+        if seq_starts.get_device() != dev or not seq_starts.is_contiguous():
+            _refuse((("seq_starts", seq_starts),))
+        if seq_starts.dtype != rt.i32 or seq_starts.numel() != B:
+            raise ValueError("seq_starts must be int32 [B]")
+    st = rt.lib.pa_int4_gather(
+        out_k.data_ptr(), out_v.data_ptr(), rt.out[out_k.dtype], k_cache.data_ptr(), v_cache.data_ptr(),
+        k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(), table[1], cu_seqlens.data_ptr(),
+        None if seq_starts is None else seq_starts.data_ptr(), B, shape[0], hkv, d, bs, nb,
+        None if err_flag is None else _flag(err_flag, dev), rt.stream(dev))
+    if st:
+        _lib.check(st, "pa_int4_gather")
+
+
+@functools.lru_cache(maxsize=1024)
+def int4_decode_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context_len,
+                               partition_size=0) -> int:
+    n = _lib.load().pa_int4_decode_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim, block_size,
+                                                  max_context_len, partition_size)
+    if n == ctypes.c_size_t(-1).value:
+        raise ValueError("arguments rejected by pa_int4_decode_workspace_size")
+    return n
+
+
+def int4_decode(out, query, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, scale: float,
+                max_context_len: int | None = None, partition_size: int = 0, workspace=None, err_flag=None) -> None:
+    """:func:`decode` over a 4-bit cache written by :func:`int4_reshape_and_cache`."""
+    rt = _rt or _runtime()
+    dev, shape, table = query.get_device(), query.shape, block_tables.shape
+    if (dev != rt.current_device() or out.get_device() != dev or k_cache.get_device() != dev or
+            v_cache.get_device() != dev or k_scales.get_device() != dev or v_scales.get_device() != dev or
+            block_tables.get_device() != dev or context_lens.get_device() != dev or not query.is_contiguous() or
+            not out.is_contiguous() or not k_cache.is_contiguous() or not v_cache.is_contiguous() or
+            not k_scales.is_contiguous() or not v_scales.is_contiguous() or not block_tables.is_contiguous() or
+            not context_lens.is_contiguous()):
+        _refuse((("query", query), ("out", out), ("k_cache", k_cache), ("v_cache", v_cache), ("k_scales", k_scales),
+                 ("v_scales", v_scales), ("block_tables", block_tables), ("context_lens", context_lens)))
+    if len(shape) != 3 or out.shape != shape:
+        raise ValueError("query/out must be [B, Hq, D]")
+    B, Hq, D = shape
+    nb, bs, hkv = _int4_cache(rt, k_cache, v_cache, k_scales, v_scales, D)
+    if len(table) != 2 or table[0] != B or block_tables.dtype != rt.i32:
+        raise ValueError("block_tables must be int32 [B, maxNB]")
+    if context_lens.dtype != rt.i32 or context_lens.numel() != B:
+        raise ValueError("context_lens must be int32 [B]")
+    maxnb = table[1]
+    if max_context_len is None:
+        max_context_len = maxnb * bs
+    stream = rt.stream(dev)
+    buf = _scratch(rt, workspace, int4_decode_workspace_size(B, Hq, hkv, D, bs, max_context_len, partition_size), dev,
+                   stream)
+    st = rt.lib.pa_int4_decode(
+        out.data_ptr(), rt.out[out.dtype], query.data_ptr(), rt.half[query.dtype], k_cache.data_ptr(),
+        v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(), maxnb,
+        context_lens.data_ptr(), max_context_len, B, Hq, hkv, D, bs, nb, scale, partition_size,
+        None if buf is None else buf.data_ptr(), 0 if buf is None else buf.nbytes,
+        None if err_flag is None else _flag(err_flag, dev), stream)
+    if st:
+        _lib.check(st, "pa_int4_decode")
 
 
 @functools.lru_cache(maxsize=1024)

@@ -40,6 +40,11 @@ SIGNATURES = {
     "pa_quant_decode_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I, _I]),
     "pa_quant_decode": (_I, [_P, _I, _P, _I, _P, _P, _I, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _I64, _F, _I, _P,
                              _SZ, _P, _P]),
+    "pa_int4_reshape_and_cache": (_I, [_P, _P, _I64, _I64, _P, _P, _P, _P, _P, _I64, _I64, _I, _I, _I, _I, _P, _P]),
+    "pa_int4_gather": (_I, [_P, _P, _I, _P, _P, _P, _P, _P, _I, _P, _P, _I, _I64, _I, _I, _I, _I64, _P, _P]),
+    "pa_int4_decode_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I, _I]),
+    "pa_int4_decode": (_I, [_P, _I, _P, _I, _P, _P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _I64, _F, _I, _P, _SZ,
+                            _P, _P]),
     "pa_decode_shared_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I, _I, _I, _I, _I]),
     "pa_decode_shared": (_I, [_P, _I, _P, _P, _P, _I, _P, _I, _P, _I, _P, _I, _I, _P, _I, _I, _I, _I, _I, _I, _I64, _F,
                               _I, _P, _SZ, _P, _P]),

@@ -816,7 +816,10 @@ bool encode_split_map(CUtensorMap *map, const void *cache, int64_t num_blocks, i
     const cuuint32_t estr[3] = {1u, 1u, 1u};
     return fn(map, es == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 3,
               const_cast<void *>(cache), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              row == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              row == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+              : row == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                          : CU_TENSOR_MAP_SWIZZLE_32B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -831,6 +834,22 @@ bool encode_scale_map(CUtensorMap *map, const float *scales, int64_t num_blocks,
     const cuuint32_t box[2] = {static_cast<cuuint32_t>(heads), static_cast<cuuint32_t>(std::min(block_size, 16))};
     const cuuint32_t estr[2] = {1u, 1u};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<float *>(scales), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Tensor map over the scale words [NB, Hkv, bs, groups] of a 4-bit cache taken as
+// (token and group, block and head), boxes of min(16, bs) tokens x `heads` heads.
+bool encode_word_map(CUtensorMap *map, const void *words, int64_t num_blocks, int block_size, int num_kv_heads,
+                     int groups, int heads) {
+    EncodeTiledFn fn = encode_tiled();
+    if (fn == nullptr) return false;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(block_size) * groups,
+                                static_cast<cuuint64_t>(num_blocks) * num_kv_heads};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(block_size) * groups * 4};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(std::min(block_size, 16) * groups), static_cast<cuuint32_t>(heads)};
+    const cuuint32_t estr[2] = {1u, 1u};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void *>(words), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -852,7 +871,8 @@ pa_status run_split(pa::SplitParams p, int cache, int head_dim, int cols, int en
         auto launch = cache == pa::kCacheF16    ? pa::launch_split_f16
                       : cache == pa::kCacheBF16 ? pa::launch_split_bf16
                       : cache == pa::kCacheE4M3 ? pa::launch_split_e4m3
-                                                : pa::launch_split_int8;
+                      : cache == pa::kCacheInt8 ? pa::launch_split_int8
+                                                : pa::launch_split_int4;
         if (launch(p, head_dim, cols, maps, grid, smem, stream) != cudaSuccess) return PA_ERR_CUDA;
     }
     return PA_OK;
@@ -920,15 +940,24 @@ pa::SplitParams split_params(void *out, pa_dtype out_dtype, const void *query, p
 
 }  // namespace
 
-PA_EXPORT pa_status pa_quant_reshape_and_cache(const void *key, const void *value, int64_t key_stride,
-                                               int64_t value_stride, void *k_cache, void *v_cache, float *k_scales,
-                                               float *v_scales, const int64_t *slot_mapping, int64_t num_tokens,
-                                               int64_t num_blocks, int block_size, int num_kv_heads, int head_dim,
-                                               pa_dtype dtype, pa_dtype cache_dtype, int *err_flag, void *stream) {
-    if (num_tokens < 0 || num_blocks <= 0 || block_size <= 0 || num_kv_heads <= 0 || head_dim <= 0 ||
-        !half_dtype(dtype) || !quant_dtype(cache_dtype))
+namespace {
+
+// The quantised calls for any codes; `cache` is the codes' kCache value, scales float
+// per row or, for 4-bit codes, words per group.
+bool quant_slots_ok(int cache, int64_t num_blocks, int block_size, int num_kv_heads) {
+    if (cache != pa::kCacheInt4) return true;
+    return num_blocks <= INT32_MAX / block_size && num_blocks <= INT32_MAX / num_kv_heads;
+}
+
+pa_status quant_write(const void *key, const void *value, int64_t key_stride, int64_t value_stride, void *k_cache,
+                      void *v_cache, void *k_scales, void *v_scales, const int64_t *slot_mapping, int64_t num_tokens,
+                      int64_t num_blocks, int block_size, int num_kv_heads, int head_dim, pa_dtype dtype, int cache,
+                      int *err_flag, void *stream) {
+    if (num_tokens < 0 || num_blocks <= 0 || block_size <= 0 || num_kv_heads <= 0 || head_dim <= 0 || !half_dtype(dtype))
         return PA_ERR_INVALID_ARG;
-    if (!supported_head_dim(head_dim) || num_kv_heads > (1 << 20)) return PA_ERR_UNSUPPORTED;
+    if (!supported_head_dim(head_dim) || num_kv_heads > (1 << 20) ||
+        !quant_slots_ok(cache, num_blocks, block_size, num_kv_heads))
+        return PA_ERR_UNSUPPORTED;
     const int64_t row = static_cast<int64_t>(num_kv_heads) * head_dim;
     if (key_stride < row || value_stride < row || key_stride % 8 != 0 || value_stride % 8 != 0)
         return PA_ERR_INVALID_ARG;
@@ -940,57 +969,54 @@ PA_EXPORT pa_status pa_quant_reshape_and_cache(const void *key, const void *valu
     DeviceInfo dev;
     if (!device_info(dev)) return PA_ERR_CUDA;
     const cudaError_t e = pa::launch_quant_write(
-        key, value, key_stride, value_stride, k_cache, v_cache, k_scales, v_scales, slot_mapping, num_tokens,
-        num_blocks * block_size, num_kv_heads, head_dim, dtype == PA_BF16, split_cache(cache_dtype), dev.sms, err_flag,
-        static_cast<cudaStream_t>(stream));
+        key, value, key_stride, value_stride, k_cache, v_cache, static_cast<float *>(k_scales),
+        static_cast<float *>(v_scales), slot_mapping, num_tokens, num_blocks * block_size, block_size, num_kv_heads,
+        head_dim, dtype == PA_BF16, cache, dev.sms, err_flag, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
-PA_EXPORT pa_status pa_quant_gather(void *out_k, void *out_v, pa_dtype out_dtype, const void *k_cache,
-                                    const void *v_cache, pa_dtype cache_dtype, const float *k_scales,
-                                    const float *v_scales, const int32_t *block_tables, int max_blocks_per_seq,
-                                    const int32_t *cu_seqlens, const int32_t *seq_starts, int num_seqs,
-                                    int64_t num_tokens, int num_kv_heads, int head_dim, int block_size,
-                                    int64_t num_blocks, int *err_flag, void *stream) {
+pa_status quant_gather(void *out_k, void *out_v, pa_dtype out_dtype, const void *k_cache, const void *v_cache, int cache,
+                       const void *k_scales, const void *v_scales, const int32_t *block_tables, int max_blocks_per_seq,
+                       const int32_t *cu_seqlens, const int32_t *seq_starts, int num_seqs, int64_t num_tokens,
+                       int num_kv_heads, int head_dim, int block_size, int64_t num_blocks, int *err_flag, void *stream) {
     if (num_seqs < 0 || num_tokens < 0 || num_blocks <= 0 || block_size <= 0 || num_kv_heads <= 0 || head_dim <= 0 ||
-        max_blocks_per_seq <= 0 || !out_dtype_ok(out_dtype) || !quant_dtype(cache_dtype))
+        max_blocks_per_seq <= 0 || !out_dtype_ok(out_dtype))
         return PA_ERR_INVALID_ARG;
-    if (!supported_head_dim(head_dim) || num_kv_heads > (1 << 20) || num_tokens > INT32_MAX) return PA_ERR_UNSUPPORTED;
+    if (!supported_head_dim(head_dim) || num_kv_heads > (1 << 20) || num_tokens > INT32_MAX ||
+        !quant_slots_ok(cache, num_blocks, block_size, num_kv_heads))
+        return PA_ERR_UNSUPPORTED;
     if (num_seqs == 0 || num_tokens == 0) return PA_OK;
     if (!out_k || !out_v || !k_cache || !v_cache || !k_scales || !v_scales || !block_tables || !cu_seqlens)
         return PA_ERR_INVALID_ARG;
     if (!aligned16(out_k) || !aligned16(out_v) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_scales) ||
         !aligned16(v_scales))
         return PA_ERR_INVALID_ARG;
-    const cudaError_t e = pa::launch_quant_gather(out_k, out_v, static_cast<int>(out_dtype), k_cache, v_cache,
-                                                  split_cache(cache_dtype), k_scales, v_scales, block_tables,
-                                                  max_blocks_per_seq, cu_seqlens, seq_starts, num_seqs, num_tokens,
-                                                  num_kv_heads, head_dim, block_size, num_blocks, err_flag,
-                                                  static_cast<cudaStream_t>(stream));
+    const cudaError_t e = pa::launch_quant_gather(
+        out_k, out_v, static_cast<int>(out_dtype), k_cache, v_cache, cache, static_cast<const float *>(k_scales),
+        static_cast<const float *>(v_scales), block_tables, max_blocks_per_seq, cu_seqlens, seq_starts, num_seqs,
+        num_tokens, num_kv_heads, head_dim, block_size, num_blocks, err_flag, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
-PA_EXPORT size_t pa_quant_decode_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
-                                                int block_size, int max_context_len, int partition_size) {
+size_t quant_workspace(int cache, int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size,
+                       int max_context_len, int partition_size) {
     SplitPlan w;
-    if (!plan_split(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context_len, partition_size,
-                    pa::kCacheInt8, false, 0, 0, 0, w))
+    if (!plan_split(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context_len, partition_size, cache,
+                    false, 0, 0, 0, w))
         return static_cast<size_t>(-1);
     return w.bytes;
 }
 
-PA_EXPORT pa_status pa_quant_decode(void *out, pa_dtype out_dtype, const void *query, pa_dtype q_dtype,
-                                    const void *k_cache, const void *v_cache, pa_dtype cache_dtype,
-                                    const float *k_scales, const float *v_scales, const int32_t *block_tables,
-                                    int max_blocks_per_seq, const int32_t *context_lens, int max_context_len,
-                                    int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size,
-                                    int64_t num_blocks, float scale, int partition_size, void *workspace,
-                                    size_t workspace_bytes, int *err_flag, void *stream) {
-    if (!quant_dtype(cache_dtype)) return PA_ERR_INVALID_ARG;
+pa_status quant_decode(void *out, pa_dtype out_dtype, const void *query, pa_dtype q_dtype, const void *k_cache,
+                       const void *v_cache, int cache, const float *k_scales, const float *v_scales,
+                       const int32_t *block_tables, int max_blocks_per_seq, const int32_t *context_lens,
+                       int max_context_len, int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size,
+                       int64_t num_blocks, float scale, int partition_size, void *workspace, size_t workspace_bytes,
+                       int *err_flag, void *stream) {
     const pa_status st = check_split(out_dtype, q_dtype, max_blocks_per_seq, max_context_len, num_seqs, num_heads,
                                      num_kv_heads, head_dim, block_size, num_blocks, scale);
     if (st != PA_OK) return st;
-    const int cache = split_cache(cache_dtype);
+    if (!quant_slots_ok(cache, num_blocks, block_size, num_kv_heads)) return PA_ERR_UNSUPPORTED;
     SplitPlan w;
     if (!plan_split(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context_len, partition_size, cache,
                     false, 0, 0, 0, w))
@@ -1006,11 +1032,18 @@ PA_EXPORT pa_status pa_quant_decode(void *out, pa_dtype out_dtype, const void *q
     DeviceInfo dev;
     if (!device_info(dev)) return PA_ERR_CUDA;
     const int box_heads = 1 << w.log2_heads;
+    const bool four = cache == pa::kCacheInt4;
+    const int row = four ? head_dim / 2 : head_dim, groups = head_dim / 64;
     pa::SplitMaps maps{};
-    if (!encode_split_map(&maps.k, k_cache, num_blocks, block_size, num_kv_heads, head_dim, 1, box_heads) ||
-        !encode_split_map(&maps.v, v_cache, num_blocks, block_size, num_kv_heads, head_dim, 1, box_heads))
+    if (!encode_split_map(&maps.k, k_cache, num_blocks, block_size, num_kv_heads, row, 1, box_heads) ||
+        !encode_split_map(&maps.v, v_cache, num_blocks, block_size, num_kv_heads, row, 1, box_heads))
         return PA_ERR_CUDA;
-    if (box_heads >= 4 &&
+    // where the kernel takes scales as boxes (pa_split_kernel.cuh)
+    if (four && std::min(block_size, 16) * groups * 4 * box_heads >= 128 &&
+        (!encode_word_map(&maps.ks, k_scales, num_blocks, block_size, num_kv_heads, groups, box_heads) ||
+         !encode_word_map(&maps.vs, v_scales, num_blocks, block_size, num_kv_heads, groups, box_heads)))
+        return PA_ERR_CUDA;
+    if (!four && box_heads >= 4 &&
         (!encode_scale_map(&maps.ks, k_scales, num_blocks, block_size, num_kv_heads, box_heads) ||
          !encode_scale_map(&maps.vs, v_scales, num_blocks, block_size, num_kv_heads, box_heads)))
         return PA_ERR_CUDA;
@@ -1024,6 +1057,89 @@ PA_EXPORT pa_status pa_quant_decode(void *out, pa_dtype out_dtype, const void *q
     const pa_status r = run_split(p, cache, head_dim, w.G, num_seqs, max_context_len, maps, dev, s);
     if (r != PA_OK || w.max_parts <= 1) return r;
     return pa::launch_split_merge(p, head_dim, 1, 1, false, dev.sms, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+}  // namespace
+
+PA_EXPORT pa_status pa_quant_reshape_and_cache(const void *key, const void *value, int64_t key_stride,
+                                               int64_t value_stride, void *k_cache, void *v_cache, float *k_scales,
+                                               float *v_scales, const int64_t *slot_mapping, int64_t num_tokens,
+                                               int64_t num_blocks, int block_size, int num_kv_heads, int head_dim,
+                                               pa_dtype dtype, pa_dtype cache_dtype, int *err_flag, void *stream) {
+    if (!quant_dtype(cache_dtype)) return PA_ERR_INVALID_ARG;
+    return quant_write(key, value, key_stride, value_stride, k_cache, v_cache, k_scales, v_scales, slot_mapping,
+                       num_tokens, num_blocks, block_size, num_kv_heads, head_dim, dtype, split_cache(cache_dtype),
+                       err_flag, stream);
+}
+
+PA_EXPORT pa_status pa_quant_gather(void *out_k, void *out_v, pa_dtype out_dtype, const void *k_cache,
+                                    const void *v_cache, pa_dtype cache_dtype, const float *k_scales,
+                                    const float *v_scales, const int32_t *block_tables, int max_blocks_per_seq,
+                                    const int32_t *cu_seqlens, const int32_t *seq_starts, int num_seqs,
+                                    int64_t num_tokens, int num_kv_heads, int head_dim, int block_size,
+                                    int64_t num_blocks, int *err_flag, void *stream) {
+    if (!quant_dtype(cache_dtype)) return PA_ERR_INVALID_ARG;
+    return quant_gather(out_k, out_v, out_dtype, k_cache, v_cache, split_cache(cache_dtype), k_scales, v_scales,
+                        block_tables, max_blocks_per_seq, cu_seqlens, seq_starts, num_seqs, num_tokens, num_kv_heads,
+                        head_dim, block_size, num_blocks, err_flag, stream);
+}
+
+PA_EXPORT size_t pa_quant_decode_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                                                int block_size, int max_context_len, int partition_size) {
+    return quant_workspace(pa::kCacheInt8, num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context_len,
+                           partition_size);
+}
+
+PA_EXPORT pa_status pa_quant_decode(void *out, pa_dtype out_dtype, const void *query, pa_dtype q_dtype,
+                                    const void *k_cache, const void *v_cache, pa_dtype cache_dtype,
+                                    const float *k_scales, const float *v_scales, const int32_t *block_tables,
+                                    int max_blocks_per_seq, const int32_t *context_lens, int max_context_len,
+                                    int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size,
+                                    int64_t num_blocks, float scale, int partition_size, void *workspace,
+                                    size_t workspace_bytes, int *err_flag, void *stream) {
+    if (!quant_dtype(cache_dtype)) return PA_ERR_INVALID_ARG;
+    return quant_decode(out, out_dtype, query, q_dtype, k_cache, v_cache, split_cache(cache_dtype), k_scales, v_scales,
+                        block_tables, max_blocks_per_seq, context_lens, max_context_len, num_seqs, num_heads,
+                        num_kv_heads, head_dim, block_size, num_blocks, scale, partition_size, workspace,
+                        workspace_bytes, err_flag, stream);
+}
+
+PA_EXPORT pa_status pa_int4_reshape_and_cache(const void *key, const void *value, int64_t key_stride,
+                                              int64_t value_stride, void *k_cache, void *v_cache, void *k_scales,
+                                              void *v_scales, const int64_t *slot_mapping, int64_t num_tokens,
+                                              int64_t num_blocks, int block_size, int num_kv_heads, int head_dim,
+                                              pa_dtype dtype, int *err_flag, void *stream) {
+    return quant_write(key, value, key_stride, value_stride, k_cache, v_cache, k_scales, v_scales, slot_mapping,
+                       num_tokens, num_blocks, block_size, num_kv_heads, head_dim, dtype, pa::kCacheInt4, err_flag,
+                       stream);
+}
+
+PA_EXPORT pa_status pa_int4_gather(void *out_k, void *out_v, pa_dtype out_dtype, const void *k_cache,
+                                   const void *v_cache, const void *k_scales, const void *v_scales,
+                                   const int32_t *block_tables, int max_blocks_per_seq, const int32_t *cu_seqlens,
+                                   const int32_t *seq_starts, int num_seqs, int64_t num_tokens, int num_kv_heads,
+                                   int head_dim, int block_size, int64_t num_blocks, int *err_flag, void *stream) {
+    return quant_gather(out_k, out_v, out_dtype, k_cache, v_cache, pa::kCacheInt4, k_scales, v_scales, block_tables,
+                        max_blocks_per_seq, cu_seqlens, seq_starts, num_seqs, num_tokens, num_kv_heads, head_dim,
+                        block_size, num_blocks, err_flag, stream);
+}
+
+PA_EXPORT size_t pa_int4_decode_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                                               int block_size, int max_context_len, int partition_size) {
+    return quant_workspace(pa::kCacheInt4, num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context_len,
+                           partition_size);
+}
+
+PA_EXPORT pa_status pa_int4_decode(void *out, pa_dtype out_dtype, const void *query, pa_dtype q_dtype,
+                                   const void *k_cache, const void *v_cache, const void *k_scales, const void *v_scales,
+                                   const int32_t *block_tables, int max_blocks_per_seq, const int32_t *context_lens,
+                                   int max_context_len, int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                                   int block_size, int64_t num_blocks, float scale, int partition_size, void *workspace,
+                                   size_t workspace_bytes, int *err_flag, void *stream) {
+    return quant_decode(out, out_dtype, query, q_dtype, k_cache, v_cache, pa::kCacheInt4,
+                        static_cast<const float *>(k_scales), static_cast<const float *>(v_scales), block_tables,
+                        max_blocks_per_seq, context_lens, max_context_len, num_seqs, num_heads, num_kv_heads, head_dim,
+                        block_size, num_blocks, scale, partition_size, workspace, workspace_bytes, err_flag, stream);
 }
 
 PA_EXPORT size_t pa_decode_shared_workspace_size(int num_seqs, int num_groups, int max_group_size, int num_heads,

@@ -1,12 +1,23 @@
-// The quantised cache's write and read-back: 8-bit codes (e4m3 or int8) with
-// one 32-bit scale per token and KV head.
+// The quantised caches' write and read-back: 8-bit codes (e4m3 or int8) with
+// one 32-bit scale per token and KV head, and 4-bit codes with a scale and a zero
+// per 64 values.
 //
-// For a row x of D elements (one token, one KV head), in 32-bit arithmetic,
+// 8 bits: for a row x of D elements (one token, one KV head), in 32-bit arithmetic,
 //     a = max(max |x_i|, 2^-60),  scale = a / qmax,  code_i = rn(x_i (qmax / a)),
 // qmax = 448 (e4m3) or 127 (int8), rn to nearest with ties to even; the row
 // stands for code_i * scale.  The floor on a keeps qmax / a finite and gives a
 // row of zeros the codes 0.  A row that holds an infinity or NaN gets the
 // scale NaN and codes 0, so that it reads back, and attends, as NaN.
+//
+// 4 bits: for a group x of 64 neighbouring elements of a row, in 32-bit arithmetic,
+//     s = bf16(max((max x / 2 - min x / 2) / 7.5, max |x| / 2^8, 2^-60)),  z = bf16(min x / s),
+//     code_i = rn(x_i (1 / s) - z), kept within 0 .. 15;
+// the group stands for s (code_i + z).  The term in max |x| keeps z within 2^8, where
+// bf16 holds it to half a code: values far from zero are then off by 2^-8 of
+// themselves at most.  A group that holds an infinity or NaN gets the scale NaN.
+// Codes lie two to a byte, the even element in the low half.  The scales of a block
+// are ordered [head][token][group], so that a block's 16 tokens of one head are 128
+// neighbouring bytes for the decode.
 //
 // Both are data movement: per row, write reads 2 D bytes and writes D + 4,
 // read-back reads D + 4 and writes 2 D (16-bit output).  A thread takes 16
@@ -15,6 +26,7 @@
 // shared memory; each thread has several rows in flight.
 #include "pa_decode_common.cuh"
 #include "pa_device.cuh"
+#include "pa_quant_codes.cuh"
 #include "pa_split.h"
 
 namespace pa {
@@ -24,25 +36,20 @@ namespace {
 using decode_common::kFull;
 using decode_common::launch_pdl;
 
-constexpr float kAmaxFloor = 8.673617379884035e-19f;   // 2^-60
 constexpr int kThreads = 256;
 
 __device__ __forceinline__ uint32_t vmax_u16x2(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
-
-// Four values -> four int8 codes.  v + 1.5 * 2^23 holds round(v) (nearest,
-// ties to even) in its low bits for |v| < 2^22.
-__device__ __forceinline__ uint32_t int8x4(float a, float b, float c, float d) {
-    constexpr float k = 12582912.f;
-    const uint32_t ia = __float_as_uint(__fadd_rn(a, k)), ib = __float_as_uint(__fadd_rn(b, k));
-    const uint32_t ic = __float_as_uint(__fadd_rn(c, k)), id = __float_as_uint(__fadd_rn(d, k));
-    return __byte_perm(__byte_perm(ia, ib, 0x0040u), __byte_perm(ic, id, 0x0040u), 0x5410u);
-}
 
 // One 32-byte store (dst on a 32-byte boundary).
 __device__ __forceinline__ void store32(void *dst, const uint32_t (&h)[8]) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(h[0]), "r"(h[1]), "r"(h[2]),
                  "r"(h[3]), "r"(h[4]), "r"(h[5]), "r"(h[6]), "r"(h[7])
                  : "memory");
+}
+
+// Where the (scale, zero) words of a 4-bit row start: [block][head][token][group].
+__device__ __forceinline__ int64_t word_row(int64_t block, int offset, int head, int hkv, int bs) {
+    return (block * hkv + head) * bs + offset;
 }
 
 struct QuantWrite {
@@ -54,6 +61,7 @@ struct QuantWrite {
     uint32_t rows;               // tokens * Hkv, per tensor
     uint32_t hkv;
     int64_t num_slots;
+    int bs;                      // 4-bit codes
     int *err_flag;
 };
 
@@ -121,6 +129,80 @@ __global__ void __launch_bounds__(kThreads) quant_write_kernel(const __grid_cons
     }
 }
 
+// As quant_write_kernel, 4-bit codes: a group is four neighbouring lanes, which
+// take the extremes as packed 16-bit values.
+template <int D, bool BF16, int U>
+__global__ void __launch_bounds__(kThreads) quant4_write_kernel(const __grid_constant__ QuantWrite p) {
+    constexpr int LPR = D / 16, LPG = kGroup4 / 16;
+    constexpr int RPB = kThreads / LPR;
+    pdl_wait();
+    pdl_launch_dependents();
+    const int part = threadIdx.x % LPR;
+    const uint32_t r0 = blockIdx.x * (RPB * U) + threadIdx.x / LPR;
+    const int kv = blockIdx.y;
+    uint4 a[U], b[U];
+    int64_t slot[U];
+    uint32_t head[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const uint32_t r = r0 + u * RPB;
+        slot[u] = -1;
+        a[u] = b[u] = make_uint4(0u, 0u, 0u, 0u);
+        if (r >= p.rows) continue;
+        const uint32_t tok = r / p.hkv;
+        head[u] = r - tok * p.hkv;
+        slot[u] = __ldg(p.slots + tok);
+        const uint4 *src = reinterpret_cast<const uint4 *>(p.src[kv] + static_cast<int64_t>(tok) * p.stride[kv] +
+                                                           static_cast<int64_t>(head[u]) * D + part * 16);
+        a[u] = __ldg(src);
+        b[u] = __ldg(src + 1);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const uint32_t w[8] = {a[u].x, a[u].y, a[u].z, a[u].w, b[u].x, b[u].y, b[u].z, b[u].w};
+        uint32_t hi2 = w[0], lo2 = w[0];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) {
+            hi2 = max2_nan<BF16>(hi2, w[i]);
+            lo2 = min2_nan<BF16>(lo2, w[i]);
+        }
+#pragma unroll
+        for (int o = 1; o < LPG; o <<= 1) {
+            hi2 = max2_nan<BF16>(hi2, __shfl_xor_sync(kFull, hi2, o));
+            lo2 = min2_nan<BF16>(lo2, __shfl_xor_sync(kFull, lo2, o));
+        }
+        const float2 hh = Half2x<BF16>::to_float2(hi2), ll = Half2x<BF16>::to_float2(lo2);
+        const float hi = fmaxf(hh.x, hh.y), lo = fminf(ll.x, ll.y);
+        // a NaN anywhere is in one of the four; an infinity is an extreme
+        const bool finite = !isnan(hh.x + hh.y) && fmaxf(hi, -lo) < INFINITY;
+        const Group4 g = group4(lo, hi, finite);
+        uint32_t code[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            float v[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float2 x = Half2x<BF16>::to_float2(w[4 * i + k]);
+                v[2 * k] = x.x;
+                v[2 * k + 1] = x.y;
+            }
+            code[i] = finite ? code4x8(v, g) : 0u;
+        }
+        if (slot[u] < 0) continue;
+        if (slot[u] >= p.num_slots) {
+            report(p.err_flag, 0x1 /* PA_FLAG_BAD_SLOT */);
+            continue;
+        }
+        *reinterpret_cast<uint2 *>(p.codes[kv] + (slot[u] * p.hkv + head[u]) * (D / 2) + part * 8) =
+            make_uint2(code[0], code[1]);
+        if (part % LPG == 0) {
+            const uint32_t s = static_cast<uint32_t>(slot[u]), blk = s / p.bs;
+            reinterpret_cast<uint32_t *>(p.scales[kv])[word_row(blk, s - blk * p.bs, head[u], p.hkv, p.bs) * (D / kGroup4) +
+                                                       part / LPG] = g.word;
+        }
+    }
+}
+
 // ------------------------------------------------------------- read-back
 
 constexpr int kGatherTokens = 8;      // dense rows per block
@@ -147,7 +229,9 @@ struct QuantGather {
 template <int D, int CT, int OUT>
 __global__ void __launch_bounds__(kThreads) quant_gather_kernel(const __grid_constant__ QuantGather p) {
     constexpr int LPR = D / 16;
+    constexpr bool k4 = CT == kCacheInt4;
     __shared__ int64_t src_slot[kGatherTokens];   // >= 0: cache slot; -1: no such slot (zeros); -2: not a row
+    __shared__ int64_t src_word[kGatherTokens];   // 4-bit codes: the row of its first head's scales
     __shared__ int32_t cu_s[kSmemSeqs + 1];
     pdl_wait();
     pdl_launch_dependents();
@@ -180,10 +264,12 @@ __global__ void __launch_bounds__(kThreads) quant_gather_kernel(const __grid_con
                 slot = -1;
                 if (pos >= 0 && pos < static_cast<int64_t>(p.max_blocks) * p.bs) {
                     const int32_t id = __ldg(p.tables + static_cast<int64_t>(a) * p.max_blocks + pos / p.bs);
-                    if (id >= 0 && static_cast<int64_t>(id) < p.num_blocks)
+                    if (id >= 0 && static_cast<int64_t>(id) < p.num_blocks) {
                         slot = static_cast<int64_t>(id) * p.bs + pos % p.bs;
-                    else
+                        if constexpr (k4) src_word[threadIdx.x] = word_row(id, static_cast<int>(pos % p.bs), 0, p.hkv, p.bs);
+                    } else {
                         report(p.err_flag, 0x2 /* PA_FLAG_BAD_BLOCK_ID */);
+                    }
                 } else {
                     report(p.err_flag, 0x4 /* PA_FLAG_BAD_CONTEXT_LEN */);
                 }
@@ -197,8 +283,8 @@ __global__ void __launch_bounds__(kThreads) quant_gather_kernel(const __grid_con
     const int n = kGatherTokens * per_tok;
     constexpr int U = 4;
     for (int i0 = threadIdx.x; i0 < n; i0 += U * kThreads) {
-        uint4 w[U];
-        float sc[U];
+        uint4 w[U];                    // (4-bit codes: half of it)
+        float sc[U];                   // (4-bit codes: a scale and a zero, bfloat16)
         int64_t dst[U];
         int kv[U];
 #pragma unroll
@@ -216,18 +302,35 @@ __global__ void __launch_bounds__(kThreads) quant_gather_kernel(const __grid_con
             w[u] = make_uint4(0u, 0u, 0u, 0u);
             sc[u] = 0.f;
             if (slot >= 0) {
-                w[u] = __ldcs(reinterpret_cast<const uint4 *>(p.codes[kv[u]]) + slot * per_tensor + off);
-                sc[u] = __ldg(p.scales[kv[u]] + slot * p.hkv + off / LPR);
+                if constexpr (k4) {
+                    const uint2 c = __ldcs(reinterpret_cast<const uint2 *>(p.codes[kv[u]]) + slot * per_tensor + off);
+                    w[u].x = c.x;
+                    w[u].y = c.y;
+                    const int64_t row = src_word[tok] + static_cast<int64_t>(off / LPR) * p.bs;
+                    sc[u] = __ldg(p.scales[kv[u]] + row * (D / kGroup4) + off % LPR / (kGroup4 / 16));
+                } else {
+                    w[u] = __ldcs(reinterpret_cast<const uint4 *>(p.codes[kv[u]]) + slot * per_tensor + off);
+                    sc[u] = __ldg(p.scales[kv[u]] + slot * p.hkv + off / LPR);
+                }
             }
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (dst[u] < 0) continue;
             const uint32_t c4[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
-            float v[16];
+            float v[16], scale = sc[u];
+            if constexpr (k4) {
+                const uint32_t sz = __float_as_uint(sc[u]);
+                const float zero = __uint_as_float(sz & 0xffff0000u);
+                scale = __uint_as_float(sz << 16);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] = static_cast<float>((c4[i / 8] >> (4 * (i % 8))) & 15u) + zero;
+            }
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                if constexpr (CT == kCacheE4M3) {
+                if constexpr (k4) {
+                    continue;
+                } else if constexpr (CT == kCacheE4M3) {
                     uint32_t lo, hi;
                     e4m3x4_to_f16x2x2(c4[k], lo, hi);
                     const float2 a = Half2x<false>::to_float2(lo), b = Half2x<false>::to_float2(hi);
@@ -242,12 +345,12 @@ __global__ void __launch_bounds__(kThreads) quant_gather_kernel(const __grid_con
                 float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(p.out[kv[u]]) + dst[u] * 16);
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    __stcs(o + k, make_float4(v[4 * k] * sc[u], v[4 * k + 1] * sc[u], v[4 * k + 2] * sc[u],
-                                              v[4 * k + 3] * sc[u]));
+                    __stcs(o + k, make_float4(v[4 * k] * scale, v[4 * k + 1] * scale, v[4 * k + 2] * scale,
+                                              v[4 * k + 3] * scale));
             } else {
                 uint32_t h[8];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) h[k] = pack2<OUT == 1>(v[2 * k] * sc[u], v[2 * k + 1] * sc[u]);
+                for (int k = 0; k < 8; ++k) h[k] = pack2<OUT == 1>(v[2 * k] * scale, v[2 * k + 1] * scale);
                 uint16_t *o = static_cast<uint16_t *>(p.out[kv[u]]) + dst[u] * 16;
                 if (p.wide_out) {
                     store32(o, h);
@@ -271,8 +374,18 @@ cudaError_t write_t(const QuantWrite &p, int sms, cudaStream_t stream) {
                       p);
 }
 
+template <int D, bool BF16>
+cudaError_t write4_t(const QuantWrite &p, int sms, cudaStream_t stream) {
+    constexpr int RPB = kThreads / (D / 16);
+    const uint32_t blocks4 = (p.rows + RPB * 4 - 1) / (RPB * 4);
+    if (blocks4 * 2 >= static_cast<uint32_t>(8 * sms))
+        return launch_pdl(quant4_write_kernel<D, BF16, 4>, dim3(blocks4, 2), dim3(kThreads), 0, stream, p);
+    return launch_pdl(quant4_write_kernel<D, BF16, 1>, dim3((p.rows + RPB - 1) / RPB, 2), dim3(kThreads), 0, stream, p);
+}
+
 template <int D>
 cudaError_t write_d(const QuantWrite &p, bool bf16, int cache, int sms, cudaStream_t stream) {
+    if (cache == kCacheInt4) return bf16 ? write4_t<D, true>(p, sms, stream) : write4_t<D, false>(p, sms, stream);
     if (cache == kCacheE4M3)
         return bf16 ? write_t<D, true, kCacheE4M3>(p, sms, stream) : write_t<D, false, kCacheE4M3>(p, sms, stream);
     return bf16 ? write_t<D, true, kCacheInt8>(p, sms, stream) : write_t<D, false, kCacheInt8>(p, sms, stream);
@@ -290,8 +403,8 @@ cudaError_t gather_t(const QuantGather &p, int out_dtype, cudaStream_t stream) {
 
 cudaError_t launch_quant_write(const void *key, const void *value, int64_t key_stride, int64_t value_stride,
                                void *k_cache, void *v_cache, float *k_scales, float *v_scales,
-                               const int64_t *slot_mapping, int64_t num_tokens, int64_t num_slots, int num_kv_heads,
-                               int head_dim, bool bf16, int cache, int sms, int *err_flag, cudaStream_t stream) {
+                               const int64_t *slot_mapping, int64_t num_tokens, int64_t num_slots, int block_size,
+                               int num_kv_heads, int head_dim, bool bf16, int cache, int sms, int *err_flag, cudaStream_t stream) {
     // tokens per launch such that row indices stay below 2^30
     const int64_t most = (int64_t{1} << 30) / num_kv_heads;
     for (int64_t t = 0; t < num_tokens; t += most) {
@@ -309,6 +422,7 @@ cudaError_t launch_quant_write(const void *key, const void *value, int64_t key_s
         p.rows = static_cast<uint32_t>(n * num_kv_heads);
         p.hkv = static_cast<uint32_t>(num_kv_heads);
         p.num_slots = num_slots;
+        p.bs = block_size;
         p.err_flag = err_flag;
         const cudaError_t e =
             head_dim == 128 ? write_d<128>(p, bf16, cache, sms, stream) : write_d<64>(p, bf16, cache, sms, stream);
@@ -340,6 +454,8 @@ cudaError_t launch_quant_gather(void *out_k, void *out_v, int out_dtype, const v
     p.num_blocks = num_blocks;
     p.wide_out = ((reinterpret_cast<uintptr_t>(out_k) | reinterpret_cast<uintptr_t>(out_v)) & 31u) == 0;
     p.err_flag = err_flag;
+    if (cache == kCacheInt4)
+        return head_dim == 128 ? gather_t<128, kCacheInt4>(p, out_dtype, stream) : gather_t<64, kCacheInt4>(p, out_dtype, stream);
     if (head_dim == 128)
         return cache == kCacheE4M3 ? gather_t<128, kCacheE4M3>(p, out_dtype, stream)
                                    : gather_t<128, kCacheInt8>(p, out_dtype, stream);

@@ -11,8 +11,9 @@
 namespace pa {
 
 // Cache element types of the split kernels.  The 8-bit ones carry one float
-// scale per token and KV head.
-constexpr int kCacheF16 = 0, kCacheBF16 = 1, kCacheE4M3 = 2, kCacheInt8 = 3;
+// scale per token and KV head, the 4-bit one a bfloat16 scale and zero per 64
+// elements of them ([block][head][token][group], the scale in the low half of a word).
+constexpr int kCacheF16 = 0, kCacheBF16 = 1, kCacheE4M3 = 2, kCacheInt8 = 3, kCacheInt4 = 4;
 
 // Entries (sequences, or chunks of groups) of one launch: the kernel keeps 12
 // bytes for each in shared memory; longer lists take several launches.
@@ -56,7 +57,7 @@ struct SplitParams {
     int64_t cut_row;             // where the cut items' rows of this launch start
     int64_t prefix_cut_row;      // join: where those of the prefix launches start
     uint32_t cut_rows, prefix_cut_rows;   // join: how many there are of each
-    const float *k_scales;       // 8-bit caches: [num_blocks, bs, Hkv]
+    const float *k_scales;       // 8-bit caches: [num_blocks, bs, Hkv]; 4-bit: words [num_blocks, Hkv, bs, D / 64]
     const float *v_scales;
     int *err_flag;
     int mode;
@@ -91,7 +92,8 @@ int split_slot_stages(int cache, int log2_heads);
 
 // The caches viewed as (dim, token, head), boxes {min(128 bytes, row), min(16,
 // bs), heads}; 8-bit caches with 4 or 8 heads per box: the scales as (head,
-// token), boxes {heads, min(16, bs)}.
+// token), boxes {heads, min(16, bs)}.  4-bit caches: codes as bytes, and where a box has
+// 128 bytes the scale words as (token and group, block and head), boxes {min(16, bs) x D / 64, heads}.
 struct SplitMaps {
     CUtensorMap k, v, ks, vs;
 };
@@ -106,6 +108,9 @@ cudaError_t launch_split_e4m3(const SplitParams &p, int head_dim, int cols, cons
 cudaError_t launch_split_int8(const SplitParams &p, int head_dim, int cols, const SplitMaps &m, int grid, size_t smem,
                               cudaStream_t stream);
 
+cudaError_t launch_split_int4(const SplitParams &p, int head_dim, int cols, const SplitMaps &m, int grid, size_t smem,
+                             cudaStream_t stream);
+
 // Joins partial results into output rows.  Sequence s has per_part partials for
 // each prefix_part tokens of its shared blocks at index 0.. and one for each
 // partition_size of the rest at p.part_off.. (p.mode kSplitDecode: no shared
@@ -114,11 +119,12 @@ cudaError_t launch_split_int8(const SplitParams &p, int head_dim, int cols, cons
 cudaError_t launch_split_merge(const SplitParams &p, int head_dim, int prefix_part, int per_part, bool holes, int sms,
                                cudaStream_t stream);
 
-// Quantising write and read-back (cache: kCacheE4M3 or kCacheInt8).
+// Quantising write and read-back (cache: kCacheE4M3, kCacheInt8 or kCacheInt4, whose
+// scales are words of two bfloat16).
 cudaError_t launch_quant_write(const void *key, const void *value, int64_t key_stride, int64_t value_stride,
                                void *k_cache, void *v_cache, float *k_scales, float *v_scales,
-                               const int64_t *slot_mapping, int64_t num_tokens, int64_t num_slots, int num_kv_heads,
-                               int head_dim, bool bf16, int cache, int sms, int *err_flag, cudaStream_t stream);
+                               const int64_t *slot_mapping, int64_t num_tokens, int64_t num_slots, int block_size,
+                               int num_kv_heads, int head_dim, bool bf16, int cache, int sms, int *err_flag, cudaStream_t stream);
 
 cudaError_t launch_quant_gather(void *out_k, void *out_v, int out_dtype, const void *k_cache, const void *v_cache,
                                 int cache, const float *k_scales, const float *v_scales, const int32_t *block_tables,

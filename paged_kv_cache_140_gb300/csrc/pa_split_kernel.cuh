@@ -61,8 +61,10 @@ constexpr int kQueryRing = 2;
 
 template <int D, int C, int CT>
 struct SplitLayout {
-    static constexpr bool k8 = CT >= kCacheE4M3;
-    static constexpr int kES = k8 ? 1 : 2;
+    static constexpr bool k8 = CT >= kCacheE4M3;         // codes with scales
+    static constexpr bool k4 = CT == kCacheInt4;
+    static constexpr int kRow = k4 ? D / 2 : k8 ? D : D * 2;     // bytes of one token and head
+    static constexpr int kGroups = k4 ? D / 64 : 1;      // scales of a token and head
     static constexpr int kWarps = 8;                     // consumer warps
     static constexpr int kSub = k8 ? 2 : 1;              // stages per consumer warp and slot
     // Up to 4 query rows leave half of the products' 8 columns free: the weights'
@@ -70,10 +72,10 @@ struct SplitLayout {
     // repeated there), one product in place of two.
     static constexpr bool kPaired = C <= 4;
     static constexpr int kTiles = kWarps * kSub;         // (stage, head) tiles of a slot
-    static constexpr int kRowB = D * kES < 128 ? D * kES : 128;   // bytes of one box row
-    static constexpr int kHalves = D * kES / kRowB;
-    static constexpr int kKVBytes = kTiles * kStageTokens * D * kES;   // a slot's K (or V) rows
-    static constexpr int kScaleBytes = k8 ? kTiles * kStageTokens * 4 : 0;
+    static constexpr int kRowB = kRow < 128 ? kRow : 128;         // bytes of one box row
+    static constexpr int kHalves = kRow / kRowB;
+    static constexpr int kKVBytes = kTiles * kStageTokens * kRow;      // a slot's K (or V) rows
+    static constexpr int kScaleBytes = k8 ? kTiles * kStageTokens * 4 * kGroups : 0;
     static constexpr int kSlotBytes = (2 * kKVBytes + 2 * kScaleBytes + 1023) / 1024 * 1024;
     static constexpr int kThreads = (kWarps + 1) * 32;
     static constexpr int kMT = D / 16;
@@ -176,6 +178,36 @@ __device__ __forceinline__ void widen_v(uint32_t w, uint32_t &ev, uint32_t &od) 
     }
 }
 
+// 4-bit codes enter the products as they lie in a byte: four bits at the bottom of a
+// binary16 are u 2^-24, the next four u 2^-20 (subnormal numbers, exact), so that a
+// register of eight codes takes four ANDs and a shift and no conversion.  The query
+// elements of the former are scaled up by 16, and an accumulator of the V product holds
+// either kind only.
+// d_i += A_i B_i for the four steps i of a register's codes.
+__device__ __forceinline__ void mma_codes4(float (&d0)[4], float (&d1)[4], float (&d2)[4], float (&d3)[4],
+                                           const uint32_t (&a)[4], const uint32_t (&b0)[2], const uint32_t (&b1)[2],
+                                           const uint32_t (&b2)[2], const uint32_t (&b3)[2]) {
+    uint32_t lo[4], hi[4], s[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        s[i] = a[i] >> 8;
+        lo[i] = a[i] & 0x000f000fu;
+        hi[i] = a[i] & 0x00f000f0u;
+    }
+    mma_16816<false>(d0, lo, b0[0], b0[1]);
+    mma_16816<false>(d1, hi, b1[0], b1[1]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        lo[i] = s[i] & 0x000f000fu;
+        hi[i] = s[i] & 0x00f000f0u;
+    }
+    mma_16816<false>(d2, lo, b2[0], b2[1]);
+    mma_16816<false>(d3, hi, b3[0], b3[1]);
+}
+// Query elements, in [1, 2) at the largest, are taken this much larger (16 times that
+// stays below binary16's 65504), so that those 2^-24 of it still are normal numbers.
+constexpr float kQ4 = 1024.f;
+
 // Sequence s's shared blocks; a length that is negative, above the bound or
 // beyond the sequence's context counts as none and is reported.
 __device__ __forceinline__ int shared_blocks(const SplitParams &p, int s, int ctx, bool tell) {
@@ -276,12 +308,18 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                                                        // whole: the group's first sequence
     uint32_t *prefix = reinterpret_cast<uint32_t *>(aux_s + E);
     // Scales of 4 or 8 heads are 16 or 32 bytes per token: boxes.  Fewer are below
-    // a box's least width: 4-byte copies by all lanes of the producer.
-    const bool scale_boxes = k8 && p.log2_heads >= 2;
+    // a box's least width: 4-byte copies by all lanes of the producer.  Those of 4-bit
+    // codes are 32 to 128 neighbouring bytes per head and piece: boxes too, from 128 bytes
+    // on (what a box's place in shared memory has to be a multiple of), else a bulk copy each.
+    constexpr int kScaleTok = 4 * L::kGroups;          // bytes of a token's scales
+    const uint32_t shead = static_cast<uint32_t>(L::k4 ? RB * kScaleTok : 4);   // next head's
+    const uint32_t sbox = k8 ? static_cast<uint32_t>(RB * kScaleTok) << p.log2_heads : 0u;
+    const bool scale_boxes = L::k4 ? sbox >= 128u : k8 && p.log2_heads >= 2;
+    const bool lane_copies = k8 && !L::k4 && !scale_boxes;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < S; ++i) {
-            mbar_init(&full[i], k8 && !scale_boxes ? 33 : 1);
+            mbar_init(&full[i], lane_copies ? 33 : 1);
             mbar_init(&empty[i], W);
         }
         for (int i = 0; i < kQueryRing; ++i) {
@@ -534,7 +572,6 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                     bad = w;
                 }
                 const uint32_t box = static_cast<uint32_t>(RB * L::kRowB) << p.log2_heads;
-                const uint32_t sbox = scale_boxes ? static_cast<uint32_t>(RB * 4) << p.log2_heads : 0u;
                 if (lane == 0) {
                     SlotMeta mt;
                     mt.seq = seq;
@@ -546,22 +583,39 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                     mt.pad[0] = mt.pad[1] = 0;
                     meta[slot] = mt;
                     mbar_arrive_expect_tx(&full[slot],
-                                          static_cast<uint32_t>(__popc(loaded)) * 2u * (box * L::kHalves + sbox));
+                                          static_cast<uint32_t>(__popc(loaded)) * 2u * (box * L::kHalves + (lane_copies ? 0u : sbox)));
                 }
                 __syncwarp();
                 const int z = load ? id * bs + ptok % bs : 0;               // the piece's first cache slot
                 if (load) {
                     const int st = lane / per_stage, b = lane % per_stage;
-                    uint8_t *dst = sp + ((static_cast<size_t>(st) * kStageTokens * D * L::kES) << p.log2_heads) + b * box;
+                    uint8_t *dst = sp + ((static_cast<size_t>(st) * kStageTokens * L::kRow) << p.log2_heads) + b * box;
 #pragma unroll
                     for (int h = 0; h < L::kHalves; ++h) {
                         const uint32_t ho = h * per_stage * box;
-                        tma_load_3d(dst + ho, &tmap_k, &full[slot], h * (L::kRowB / L::kES), z, kvh0, policy);
-                        tma_load_3d(dst + L::kKVBytes + ho, &tmap_v, &full[slot], h * (L::kRowB / L::kES), z, kvh0,
+                        tma_load_3d(dst + ho, &tmap_k, &full[slot], h * (D / L::kHalves), z, kvh0, policy);
+                        tma_load_3d(dst + L::kKVBytes + ho, &tmap_v, &full[slot], h * (D / L::kHalves), z, kvh0,
                                     policy);
                     }
                 }
-                if constexpr (k8) {
+                if constexpr (L::k4) {
+                    // scales, [piece][head of the box][token][group], K then V
+                    uint8_t *ss = sp + 2 * L::kKVBytes + lane * sbox;
+                    if (load) {
+                        const int y = id * Hkv + kvh0, x = ptok % bs * L::kGroups;
+                        if (scale_boxes) {
+                            tma_load_2d(ss, &tmap_ks, &full[slot], x, y);
+                            tma_load_2d(ss + L::kScaleBytes, &tmap_vs, &full[slot], x, y);
+                        } else {
+                            const int64_t src = static_cast<int64_t>(y) * bs * L::kGroups + x;
+                            for (int h = 0; h < H; ++h) {
+                                bulk_load(ss + h * shead, p.k_scales + src + h * bs * L::kGroups, shead, &full[slot]);
+                                bulk_load(ss + L::kScaleBytes + h * shead, p.v_scales + src + h * bs * L::kGroups, shead,
+                                          &full[slot]);
+                            }
+                        }
+                    }
+                } else if constexpr (k8) {
                     // scales, [token of the slot][head of the box], K then V
                     uint8_t *ss = sp + 2 * L::kKVBytes;
                     if (scale_boxes) {
@@ -596,7 +650,7 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                     meta[slot] = mt;
                     arrive(&full[slot]);
                 }
-                if (k8 && !scale_boxes) {
+                if (lane_copies) {
                     __syncwarp();
                     arrive(&full[slot]);
                 }
@@ -628,17 +682,22 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
     const uint32_t hi_off = per_stage == 1 ? 8 * L::kRowB : box;     // rows 8-15 of a stage
     // A lane's 16-byte chunk 2 i + (0 or 1) of its row sits, swizzled, at the row's
     // start + 16 ((2 i + b) ^ swz): the address for i = 0, with 32 i flipped in.
-    const uint32_t swz = L::kRowB == 128 ? r8 : (r8 >> 1) & 3;
+    const uint32_t swz = L::kRowB == 128 ? r8 : L::kRowB == 64 ? (r8 >> 1) & 3 : (r8 >> 2) & 1;
     const uint32_t off_k = head_off + (j8 & 1) * hi_off + r8 * L::kRowB + (((j8 >> 1) ^ swz) << 4);
     const uint32_t off_v = L::kKVBytes + head_off + (j8 >> 1) * hi_off + r8 * L::kRowB + (((j8 & 1) ^ swz) << 4);
     // 8-bit caches: my tokens' scales in a slot (K; V scales kScaleBytes further)
     const uint32_t scl_off = 2 * L::kKVBytes + ((((sub * SUB * kStageTokens + g) << p.log2_heads) + head) << 2);
     const uint32_t scl_8 = 32u << p.log2_heads;                      // 8 tokens further
+    // 4-bit: my head's tokens of my first stage; the next stage's; 8 tokens further
+    const uint32_t s4_off = 2 * L::kKVBytes + sub * SUB * per_stage * sbox + head * shead;
+    const uint32_t s4_8 = per_stage == 1 ? 8 * kScaleTok : sbox, s4_st = per_stage * sbox;
     const uint64_t keep = l2_policy_evict_last();
 
     uint32_t qf[KS][2];
     float qs[2];                  // logit scale of columns 2t, 2t + 1
     float acc[MT][4], m_run[2], l_run[2];
+    float qsum[L::kGroups][2];    // 4-bit: columns 2t, 2t + 1: the sum of a group's query elements, as kQ4 has it
+    float zs[L::kGroups];         // 4-bit: column g, my tokens: the sum of weight, scale and zero
     float mu[2];                  // the reference that weights are taken under: m_run, or 0 while there is none
     int cslot = 0;
     uint32_t cphase = 0, citems = 0;
@@ -677,6 +736,52 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                     qf[ks][1] = live ? qw[(ks * 16 + 2 * t + 8) >> 1] : 0u;
                 }
                 qs[0] = qs[1] = p.scale_log2;
+            } else if constexpr (L::k4) {
+                // Step 4 gr + i takes elements 8t + i and 8t + i + 4 of group gr's first
+                // half and of its second; even steps' codes arrive 16 times smaller.
+                uint4 w[2 * L::kGroups];
+#pragma unroll
+                for (int c = 0; c < 2 * L::kGroups; ++c)
+                    w[c] = live ? *reinterpret_cast<const uint4 *>(qw + (32 * c + 8 * t) / 2) : make_uint4(0u, 0u, 0u, 0u);
+                float f[2 * L::kGroups][8], amax = 0.f;
+#pragma unroll
+                for (int c = 0; c < 2 * L::kGroups; ++c) {
+                    const uint32_t v[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 x = p.q_bf16 ? Half2x<true>::to_float2(v[k]) : Half2x<false>::to_float2(v[k]);
+                        f[c][2 * k] = x.x;
+                        f[c][2 * k + 1] = x.y;
+                        amax = fmaxf(amax, fmaxf(fabsf(x.x), fabsf(x.y)));
+                    }
+                }
+                amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
+                amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
+                const uint32_t eb = min(max(__float_as_uint(amax) & 0x7f800000u, 0x00800000u), 0x7e800000u);
+                const float inv = __uint_as_float(0x7f000000u - eb);
+#pragma unroll
+                for (int gr = 0; gr < L::kGroups; ++gr) {
+                    float sum = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float m = i & 1 ? kQ4 : 16.f * kQ4;
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const uint32_t b = pack2<false>(f[2 * gr + k][i] * inv * m, f[2 * gr + k][i + 4] * inv * m);
+                            qf[4 * gr + i][k] = b;
+                            const float2 r = Half2x<false>::to_float2(b);
+                            sum += (r.x + r.y) * (i & 1 ? 0x1p-20f : 0x1p-24f);
+                        }
+                    }
+                    sum += __shfl_xor_sync(kFull, sum, 1);
+                    sum += __shfl_xor_sync(kFull, sum, 2);
+                    qsum[gr][0] = __shfl_sync(kFull, sum, 8 * t);
+                    qsum[gr][1] = __shfl_sync(kFull, sum, 8 * t + 4);
+                    zs[gr] = 0.f;
+                }
+                const float up = __uint_as_float(eb) * p.scale_log2 * (0x1p20f / kQ4);
+                qs[0] = __shfl_sync(kFull, up, 8 * t);
+                qs[1] = __shfl_sync(kFull, up, 8 * t + 4);
             } else {
                 // Dims in the order the widened K fragments arrive: step
                 // 2kc + hl takes dims 32kc + 4t + 2hl (+1) and the same + 16.
@@ -743,7 +848,14 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                 // ---- QK: 16 tokens x 8 columns ----
                 const uint32_t ka = sa + (st0 + hs) * stage_off + off_k;
                 float c[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-                if constexpr (!k8) {
+                if constexpr (L::k4) {
+#pragma unroll
+                    for (int gr = 0; gr < L::kGroups; ++gr) {
+                        uint32_t a[4];
+                        ldsm_x4(a, ka ^ (gr << 5));
+                        mma_codes4(c[gr], c[gr], c[gr], c[gr], a, qf[4 * gr], qf[4 * gr + 1], qf[4 * gr + 2], qf[4 * gr + 3]);
+                    }
+                } else if constexpr (!k8) {
 #pragma unroll
                     for (int ks = 0; ks < KS; ++ks) {
                         uint32_t a[4];
@@ -763,7 +875,27 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                 }
                 const bool v_lo = kWhole || ((smask[hs] >> g) & 1u), v_hi = kWhole || ((smask[hs] >> (g + 8)) & 1u);
                 float k_lo = 1.f, k_hi = 1.f;
-                if constexpr (k8) {
+                if constexpr (L::k4) {
+                    const uint8_t *ks = sp + s4_off + hs * s4_st + g * kScaleTok, *vs = ks + L::kScaleBytes;
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        float sum[2] = {0.f, 0.f}, big = kScaleFloor;
+#pragma unroll
+                        for (int gr = 0; gr < L::kGroups; ++gr) {
+                            const uint32_t w = *reinterpret_cast<const uint32_t *>(ks + k * s4_8 + 4 * gr);
+                            const float sc = __uint_as_float(w << 16), z = __uint_as_float(w & 0xffff0000u);
+#pragma unroll
+                            for (int e = 0; e < NE; ++e)
+                                sum[e] = fmaf(sc, fmaf(z, qsum[gr][e], c[gr][2 * k + e]), sum[e]);
+                            // (a scale that is no number makes its own group's sums such, not the reference)
+                            big = fmaxf(big, __uint_as_float(*reinterpret_cast<const uint32_t *>(vs + k * s4_8 + 4 * gr) << 16));
+                        }
+                        const bool ok = k ? v_hi : v_lo;
+                        sv[hs][k] = ok ? big : 0.f;
+#pragma unroll
+                        for (int e = 0; e < NE; ++e) x[hs][2 * k + e] = ok ? sum[e] * qs[e] : -INFINITY;
+                    }
+                } else if constexpr (k8) {
                     // a masked token's scales may be anything: its V scale counts as 0
                     const uint8_t *lo = sp + scl_off + 2 * hs * scl_8, *hi = lo + scl_8;
                     k_lo = *reinterpret_cast<const float *>(lo);
@@ -774,7 +906,7 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                     sv[hs][1] = v_hi ? max_nan(b, kScaleFloor) : 0.f;
                 }
 #pragma unroll
-                for (int e = 0; e < NE; ++e) {
+                for (int e = 0; e < (L::k4 ? 0 : NE); ++e) {
                     const float a = (c[0][e] + c[1][e]) * (k8 ? k_lo * qs[e] : qs[e]);
                     const float b = (c[0][2 + e] + c[1][2 + e]) * (k8 ? k_hi * qs[e] : qs[e]);
                     x[hs][e] = v_lo ? a : -INFINITY;
@@ -826,6 +958,12 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                         acc[mt][e] *= al;
                         acc[mt][2 + e] *= al;
                     }
+                    if constexpr (L::k4) {      // of column g: held by lane g / 2 as its element g % 2
+                        const float ag = __shfl_sync(kFull, al, g >> 1);
+                        if ((g & 1) == e)
+#pragma unroll
+                            for (int gr = 0; gr < L::kGroups; ++gr) zs[gr] *= ag;
+                    }
                 }
                 weigh();
             }
@@ -839,20 +977,51 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                 uint32_t bhi[2], blo[2];
                 {
                     const int srcA = 8 * t + (g >> 1), srcB = srcA + 4;
+                    const float(&src)[4] = L::k4 ? pw[hs] : w4[hs];   // (4-bit: the groups' scales come below)
                     float w[4];
-                    w[0] = __shfl_sync(kFull, w4[hs][0], srcA);
-                    w[1] = __shfl_sync(kFull, w4[hs][0], srcB);
-                    w[2] = __shfl_sync(kFull, w4[hs][2], srcA);
-                    w[3] = __shfl_sync(kFull, w4[hs][2], srcB);
+                    w[0] = __shfl_sync(kFull, src[0], srcA);
+                    w[1] = __shfl_sync(kFull, src[0], srcB);
+                    w[2] = __shfl_sync(kFull, src[2], srcA);
+                    w[3] = __shfl_sync(kFull, src[2], srcB);
                     if constexpr (NE == 2) {
-                        const float o0 = __shfl_sync(kFull, w4[hs][1], srcA), o1 = __shfl_sync(kFull, w4[hs][1], srcB);
-                        const float o2 = __shfl_sync(kFull, w4[hs][3], srcA), o3 = __shfl_sync(kFull, w4[hs][3], srcB);
+                        const float o0 = __shfl_sync(kFull, src[1], srcA), o1 = __shfl_sync(kFull, src[1], srcB);
+                        const float o2 = __shfl_sync(kFull, src[3], srcA), o3 = __shfl_sync(kFull, src[3], srcB);
                         if (g & 1) {
                             w[0] = o0;
                             w[1] = o1;
                             w[2] = o2;
                             w[3] = o3;
                         }
+                    }
+                    if constexpr (L::k4) {
+                        const uint8_t *vs = sp + s4_off + L::kScaleBytes + hs * s4_st + 2 * t * kScaleTok;
+                        const uint32_t va = sa + (st0 + hs) * stage_off + off_v;
+#pragma unroll
+                        for (int gr = 0; gr < L::kGroups; ++gr) {
+                            float ws[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {     // tokens 2t, 2t + 1, 2t + 8, 2t + 9
+                                const uint32_t word =
+                                    *reinterpret_cast<const uint32_t *>(vs + (k >> 1) * s4_8 + (k & 1) * kScaleTok + 4 * gr);
+                                // a masked token's scales may be anything
+                                const bool ok = kWhole || ((smask[hs] >> (2 * t + (k & 1) + 4 * (k & 2))) & 1u);
+                                ws[k] = w[k] * (ok ? __uint_as_float(word << 16) : 0.f);
+                                zs[gr] = fmaf(ws[k], ok ? __uint_as_float(word & 0xffff0000u) : 0.f, zs[gr]);
+                            }
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                bhi[k] = pack2<false>(ws[2 * k], ws[2 * k + 1]);
+                                const float2 h = Cvt::to_float2(bhi[k]);
+                                blo[k] = pack2<false>(ws[2 * k] - h.x, ws[2 * k + 1] - h.y);
+                                if (L::kPaired && g >= 4) bhi[k] = blo[k];
+                            }
+                            uint32_t a[4];
+                            ldsm_x4_trans(a, va ^ (gr << 5));
+                            mma_codes4(acc[4 * gr], acc[4 * gr + 1], acc[4 * gr + 2], acc[4 * gr + 3], a, bhi, bhi, bhi, bhi);
+                            if constexpr (!L::kPaired)
+                                mma_codes4(acc[4 * gr], acc[4 * gr + 1], acc[4 * gr + 2], acc[4 * gr + 3], a, blo, blo, blo, blo);
+                        }
+                        continue;
                     }
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
@@ -865,7 +1034,7 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                 const uint32_t vbase = (st0 + hs) * stage_off + L::kKVBytes;
                 // V rows that are masked are zeroed first: stale slots may hold NaN
                 // (not so int8 codes, which a zero weight always cancels)
-                if constexpr (!kWhole && CT != kCacheInt8) {
+                if constexpr (!kWhole && CT != kCacheInt8 && !L::k4) {
                     if (smask[hs] != 0xffffu) {
                         constexpr int kCh = L::kRowB / 16;                  // 16-byte chunks per box row
 #pragma unroll
@@ -917,6 +1086,12 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
 
         if (!(m.flags & kLast)) continue;
         // ---- item end ----
+        if constexpr (L::k4) {      // the codes' powers of two, taken off before the parts are added
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[mt][e] *= mt & 1 ? 0x1p20f : 0x1p24f;
+        }
         if constexpr (L::kPaired) {   // the low parts' columns (c + 4: lane t + 2) onto the high parts'
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
@@ -925,6 +1100,23 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                     acc[mt][e] += __shfl_xor_sync(kFull, acc[mt][e], 2);
                     acc[mt][2 + e] += __shfl_xor_sync(kFull, acc[mt][2 + e], 2);
                 }
+        }
+        if constexpr (L::k4) {      // the zeros' share of every element of a group
+#pragma unroll
+            for (int gr = 0; gr < L::kGroups; ++gr) {
+                float z = zs[gr];
+                z += __shfl_xor_sync(kFull, z, 1);
+                z += __shfl_xor_sync(kFull, z, 2);
+#pragma unroll
+                for (int e = 0; e < NE; ++e) {
+                    const float ze = __shfl_sync(kFull, z, 8 * t + 4 * e);
+#pragma unroll
+                    for (int mt = 4 * gr; mt < 4 * gr + 4; ++mt) {
+                        acc[mt][e] += ze;
+                        acc[mt][2 + e] += ze;
+                    }
+                }
+            }
         }
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1)
@@ -1026,7 +1218,16 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                 else
                     static_cast<uint16_t *>(p.out)[orow + d] = p.out_dtype == 1 ? float_to_bf16_bits(a) : float_to_f16_bits(a);
             };
-            if constexpr (k8) {
+            if constexpr (L::k4) {
+#pragma unroll
+                for (int gr = 0; gr < L::kGroups; ++gr)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const int d = 64 * gr + 32 * r + 4 * g, i = 2 * r + e;
+                        put2(d, acc[4 * gr][i] * sc, acc[4 * gr + 1][i] * sc);
+                        put2(d + 2, acc[4 * gr + 2][i] * sc, acc[4 * gr + 3][i] * sc);
+                    }
+            } else if constexpr (k8) {
 #pragma unroll
                 for (int vc = 0; vc < D / 32; ++vc) {
                     put2(32 * vc + 2 * g, acc[2 * vc][e] * sc, acc[2 * vc + 1][e] * sc);

@@ -182,6 +182,9 @@ SplitSmem smem_for(int cols, int log2_heads, int entries) {
 }  // namespace
 
 SplitSmem split_smem(int head_dim, int cols, int cache, int log2_heads, int entries) {
+    if (cache == kCacheInt4)
+        return head_dim == 128 ? smem_for<128, kCacheInt4>(cols, log2_heads, entries)
+                               : smem_for<64, kCacheInt4>(cols, log2_heads, entries);
     if (cache >= kCacheE4M3)
         return head_dim == 128 ? smem_for<128, kCacheInt8>(cols, log2_heads, entries)
                                : smem_for<64, kCacheInt8>(cols, log2_heads, entries);
@@ -190,7 +193,9 @@ SplitSmem split_smem(int head_dim, int cols, int cache, int log2_heads, int entr
 }
 
 int split_slot_stages(int cache, int log2_heads) {
-    return (cache >= kCacheE4M3 ? SplitLayout<128, 8, kCacheInt8>::kTiles : SplitLayout<128, 8, kCacheF16>::kTiles) >>
+    return (cache == kCacheInt4   ? SplitLayout<128, 8, kCacheInt4>::kTiles
+            : cache >= kCacheE4M3 ? SplitLayout<128, 8, kCacheInt8>::kTiles
+                                  : SplitLayout<128, 8, kCacheF16>::kTiles) >>
            log2_heads;
 }
 
