@@ -866,6 +866,10 @@ pa_status run_split(pa::SplitParams p, int cache, int head_dim, int cols, int en
         const size_t room = static_cast<size_t>(dev.smem_optin);
         if (need.fixed + 2 * need.slot > room) return PA_ERR_UNSUPPORTED;
         p.stages = static_cast<int>(std::min<size_t>(8, (room - need.fixed) / need.slot));
+        if (cache == pa::kCacheInt4) {
+            if (p.stages == 5 || p.stages == 7) --p.stages;
+            p.producers = p.stages % 4 == 0 ? 4 : p.stages % 3 == 0 ? 3 : 2;
+        }
         const size_t smem = need.fixed + p.stages * need.slot;
         const int grid = static_cast<int>(std::min<int64_t>(std::min(dev.sms, pa::kSplitMaxCtas), p.entries * per_entry));
         auto launch = cache == pa::kCacheF16    ? pa::launch_split_f16
@@ -1033,10 +1037,12 @@ pa_status quant_decode(void *out, pa_dtype out_dtype, const void *query, pa_dtyp
     if (!device_info(dev)) return PA_ERR_CUDA;
     const int box_heads = 1 << w.log2_heads;
     const bool four = cache == pa::kCacheInt4;
-    const int row = four ? head_dim / 2 : head_dim, groups = head_dim / 64;
+    // 4-bit rows: as many heads to a row of the boxes as make up 128 bytes
+    const int side = four ? std::min(box_heads, 256 / head_dim) : 1;
+    const int row = four ? side * head_dim / 2 : head_dim, groups = head_dim / 64;
     pa::SplitMaps maps{};
-    if (!encode_split_map(&maps.k, k_cache, num_blocks, block_size, num_kv_heads, row, 1, box_heads) ||
-        !encode_split_map(&maps.v, v_cache, num_blocks, block_size, num_kv_heads, row, 1, box_heads))
+    if (!encode_split_map(&maps.k, k_cache, num_blocks, block_size, num_kv_heads / side, row, 1, box_heads / side) ||
+        !encode_split_map(&maps.v, v_cache, num_blocks, block_size, num_kv_heads / side, row, 1, box_heads / side))
         return PA_ERR_CUDA;
     // where the kernel takes scales as boxes (pa_split_kernel.cuh)
     if (four && std::min(block_size, 16) * groups * 4 * box_heads >= 128 &&

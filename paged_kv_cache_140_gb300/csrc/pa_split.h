@@ -70,6 +70,7 @@ struct SplitParams {
     int e0, entries;             // this launch's entries
     int log2_heads;              // KV heads per box: 1, 2, 4 or 8
     int stages;                  // ring depth
+    int producers;               // 4-bit caches: producer warps, of which the ring's depth is a multiple
     int late_wait;               // the previous kernel is the call's own prefix kernel, whose results this
                                  // one does not read: wait for it only at the end
 };

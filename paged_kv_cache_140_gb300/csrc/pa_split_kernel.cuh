@@ -77,7 +77,10 @@ struct SplitLayout {
     static constexpr int kKVBytes = kTiles * kStageTokens * kRow;      // a slot's K (or V) rows
     static constexpr int kScaleBytes = k8 ? kTiles * kStageTokens * 4 * kGroups : 0;
     static constexpr int kSlotBytes = (2 * kKVBytes + 2 * kScaleBytes + 1023) / 1024 * 1024;
-    static constexpr int kThreads = (kWarps + 1) * 32;
+    // Producer warps, which take the slots in turn: a 4-bit slot is consumed in less time
+    // than one of them takes to bring in the next.  (p.producers of them work.)
+    static constexpr int kProducers = k4 ? 4 : 1;
+    static constexpr int kThreads = (kWarps + kProducers) * 32;
     static constexpr int kMT = D / 16;
     static constexpr int kStateRow = D + 4;              // floats per query row of a warp's state
     static constexpr int kStateBytes = C * kStateRow * 4;
@@ -183,26 +186,42 @@ __device__ __forceinline__ void widen_v(uint32_t w, uint32_t &ev, uint32_t &od) 
 // register of eight codes takes four ANDs and a shift and no conversion.  The query
 // elements of the former are scaled up by 16, and an accumulator of the V product holds
 // either kind only.
-// d_i += A_i B_i for the four steps i of a register's codes.
-__device__ __forceinline__ void mma_codes4(float (&d0)[4], float (&d1)[4], float (&d2)[4], float (&d3)[4],
-                                           const uint32_t (&a)[4], const uint32_t (&b0)[2], const uint32_t (&b1)[2],
-                                           const uint32_t (&b2)[2], const uint32_t (&b3)[2]) {
-    uint32_t lo[4], hi[4], s[4];
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+// Step i (0 to 3) of the registers' codes.
+__device__ __forceinline__ void codes4(uint32_t (&f)[4], const uint32_t (&a)[4], int i) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        s[i] = a[i] >> 8;
-        lo[i] = a[i] & 0x000f000fu;
-        hi[i] = a[i] & 0x00f000f0u;
+    for (int k = 0; k < 4; ++k) f[k] = (i < 2 ? a[k] : a[k] >> 8) & (i & 1 ? 0x00f000f0u : 0x000f000fu);
+}
+// N words of scale and zero, neighbours in shared memory.
+template <int N>
+struct Words {
+    uint32_t w[N];
+};
+template <int N>
+__device__ __forceinline__ Words<N> load_words(const uint8_t *p) {
+    Words<N> r;
+    if constexpr (N == 1) {
+        r.w[0] = *reinterpret_cast<const uint32_t *>(p);
+    } else {
+        const uint2 v = *reinterpret_cast<const uint2 *>(p);
+        r.w[0] = v.x;
+        r.w[1] = v.y;
     }
-    mma_16816<false>(d0, lo, b0[0], b0[1]);
-    mma_16816<false>(d1, hi, b1[0], b1[1]);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        lo[i] = s[i] & 0x000f000fu;
-        hi[i] = s[i] & 0x00f000f0u;
-    }
-    mma_16816<false>(d2, lo, b2[0], b2[1]);
-    mma_16816<false>(d3, hi, b3[0], b3[1]);
+    return r;
+}
+__device__ __forceinline__ float word_scale(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float word_zero(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// Weights' high parts, as many bits as binary16 has (cut off, not rounded).
+__device__ __forceinline__ float high_part(float w) { return __uint_as_float(__float_as_uint(w) & 0xffffe000u); }
+__device__ __forceinline__ uint32_t pack2_rz(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
 }
 // Query elements, in [1, 2) at the largest, are taken this much larger (16 times that
 // stays below binary16's 65504), so that those 2^-24 of it still are normal numbers.
@@ -316,6 +335,10 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
     const uint32_t sbox = k8 ? static_cast<uint32_t>(RB * kScaleTok) << p.log2_heads : 0u;
     const bool scale_boxes = L::k4 ? sbox >= 128u : k8 && p.log2_heads >= 2;
     const bool lane_copies = k8 && !L::k4 && !scale_boxes;
+    // Heads side by side in a row of a box: 4-bit rows of 32 or 64 bytes fill 128 together
+    // (a box's rows, not its bytes, are what the copies' rate goes by).
+    const int log2_row_heads = L::k4 ? min(p.log2_heads, D == 128 ? 1 : 2) : 0;
+    const uint32_t rowB = static_cast<uint32_t>(L::kRowB) << log2_row_heads;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < S; ++i) {
@@ -431,8 +454,15 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
     const uint32_t lo = static_cast<uint32_t>(static_cast<uint64_t>(total) * blockIdx.x / gridDim.x);
     const uint32_t hi = static_cast<uint32_t>(static_cast<uint64_t>(total) * (blockIdx.x + 1) / gridDim.x);
 
-    if (warp == W) {
-        // ------------------------------------------------------------ producer
+    if (warp >= W) {
+        // ------------------------------------------------------------ producers
+        // Producer pi brings in the CTA's slots pi, pi + NP, ...  The ring's depth is a multiple
+        // of NP: each of its slots belongs to one producer, which waits for every use of it in
+        // turn (a barrier's parity says nothing to one that may be two uses away).  For the
+        // same reason the first one loads all items' queries.
+        const int NP = L::kProducers == 1 ? 1 : p.producers;
+        const uint32_t pi = warp - W;
+        if (pi >= static_cast<uint32_t>(NP)) return;
         const uint64_t policy =
             mode == kSplitPrefix && p.chunks > 1 ? l2_policy_evict_normal() : l2_policy_evict_first();
         ItemCursor ic{};
@@ -502,13 +532,14 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
             if (ntok > 0 && lane <= (t0 + ntok - 1) / bs - fb)
                 bid = __ldg(p.block_tables + static_cast<int64_t>(row) * p.max_blocks_per_seq + blk0 + fb + lane);
         };
-        int islot = 0;
-        uint32_t uses = 0, items = 0;
+        uint32_t uses = 0, items = 0;                  // of the CTA, up to the present item
+        uint32_t mine = pi, rounds = 0;                // my next slot, and how often the ring was gone round before it
+        int islot = pi;
         bool ok = true;
         auto take_slot = [&]() -> int {
             const int slot = islot;
-            if (uses >= static_cast<uint32_t>(S)) {
-                const uint32_t par = ((uses / S) - 1) & 1u;
+            if (rounds > 0) {
+                const uint32_t par = (rounds - 1) & 1u;
                 if (!mbar_try_wait(&empty[slot], par) && !mbar_wait_bounded(&empty[slot], par)) {
                     if (lane == 0) report(p.err_flag, 0x10 /* PA_FLAG_TIMEOUT */);
                     ok = false;
@@ -516,15 +547,28 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
             }
             ok = __all_sync(kFull, ok);
             if (ok) {
-                islot = (islot + 1 == S) ? 0 : islot + 1;
-                ++uses;
+                mine += NP;
+                if ((islot += NP) >= S) {
+                    islot -= S;
+                    ++rounds;
+                }
             }
             return slot;
         };
         while (ok && work && ic.start < hi) {
             const int kvh0 = ic.grp << p.log2_heads;
+            // this CTA's slots of the item, and the first of mine
+            const int jb = cut && ic.start < lo ? static_cast<int>(lo - ic.start) : 0;
+            const int je = cut ? min(ic.nslots, static_cast<int>(hi - ic.start)) : ic.nslots;
+            const int j0 = jb + static_cast<int>(mine - uses);
+            if (pi > 0 && j0 >= je) {
+                uses += je - jb;
+                ++items;
+                advance();
+                continue;
+            }
             open_item();
-            {
+            if (pi == 0) {
                 const int qi = static_cast<int>(items % kQueryRing);
                 if (items >= static_cast<uint32_t>(kQueryRing)) {
                     const uint32_t par = ((items / kQueryRing) - 1) & 1u;
@@ -542,17 +586,14 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                                   p.q + (static_cast<int64_t>(seq + m) * Hq + (kvh0 << lg)) * D,
                                   static_cast<uint32_t>(qmember), &qfull[qi]);
                 }
-                ++items;
                 __syncwarp();
             }
-            // this CTA's slots of the item
-            const int jb = cut && ic.start < lo ? static_cast<int>(lo - ic.start) : 0;
-            const int je = cut ? min(ic.nslots, static_cast<int>(hi - ic.start)) : ic.nslots;
+            ++items;
             const int kind = jb > 0               ? kContinued
                              : je < ic.nslots     ? kCut
                              : final_mode(mode) && ic.nparts == 1 ? kFinal
                                                                   : 0;
-            for (int j = jb; j < je; ++j) {
+            for (int j = j0; j < je; j += NP) {
                 const int slot = take_slot();
                 if (!ok) break;
                 uint8_t *sp = slots + static_cast<size_t>(slot) * L::kSlotBytes;
@@ -593,9 +634,9 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
 #pragma unroll
                     for (int h = 0; h < L::kHalves; ++h) {
                         const uint32_t ho = h * per_stage * box;
-                        tma_load_3d(dst + ho, &tmap_k, &full[slot], h * (D / L::kHalves), z, kvh0, policy);
-                        tma_load_3d(dst + L::kKVBytes + ho, &tmap_v, &full[slot], h * (D / L::kHalves), z, kvh0,
-                                    policy);
+                        tma_load_3d(dst + ho, &tmap_k, &full[slot], h * (D / L::kHalves), z, kvh0 >> log2_row_heads, policy);
+                        tma_load_3d(dst + L::kKVBytes + ho, &tmap_v, &full[slot], h * (D / L::kHalves), z,
+                                    kvh0 >> log2_row_heads, policy);
                     }
                 }
                 if constexpr (L::k4) {
@@ -638,10 +679,11 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                 }
                 __syncwarp();
             }
+            uses += je - jb;
             advance();
         }
         // one more slot tells the consumers to stop
-        if (ok) {
+        if (ok && mine == uses) {
             const int slot = take_slot();
             if (ok) {
                 if (lane == 0) {
@@ -658,9 +700,11 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
         }
         // After a wait that gave up, let the copies still in flight land before the CTA ends.
         if (!ok) {
-            for (uint32_t u = uses > static_cast<uint32_t>(S) ? uses - S : 0u; u < uses; ++u)
+            for (uint32_t u = mine, n = 0; u >= static_cast<uint32_t>(NP) && n < static_cast<uint32_t>(S); n += NP) {
+                u -= NP;
                 mbar_wait_bounded(&full[u % S], (u / S) & 1u);
-            for (uint32_t i = items > static_cast<uint32_t>(kQueryRing) ? items - kQueryRing : 0u; i < items; ++i)
+            }
+            for (uint32_t i = items > static_cast<uint32_t>(kQueryRing) ? items - kQueryRing : 0u; pi == 0 && i < items; ++i)
                 mbar_wait_bounded(&qfull[i % kQueryRing], (i / kQueryRing) & 1u);
         }
         if (p.late_wait) pdl_wait();   // the grid does not finish before the prefix kernel
@@ -678,13 +722,15 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
     const uint32_t box = static_cast<uint32_t>(RB * L::kRowB) << p.log2_heads;
     const uint32_t half_off = box * per_stage;                       // next 128-byte column block
     const uint32_t stage_off = half_off * L::kHalves;
-    const uint32_t head_off = head * RB * L::kRowB;
-    const uint32_t hi_off = per_stage == 1 ? 8 * L::kRowB : box;     // rows 8-15 of a stage
+    const int row_head = head & ((1 << log2_row_heads) - 1);         // my head's place in a row
+    const uint32_t head_off = (head >> log2_row_heads) * RB * rowB;
+    const uint32_t hi_off = per_stage == 1 ? 8 * rowB : box;         // rows 8-15 of a stage
     // A lane's 16-byte chunk 2 i + (0 or 1) of its row sits, swizzled, at the row's
     // start + 16 ((2 i + b) ^ swz): the address for i = 0, with 32 i flipped in.
-    const uint32_t swz = L::kRowB == 128 ? r8 : L::kRowB == 64 ? (r8 >> 1) & 3 : (r8 >> 2) & 1;
-    const uint32_t off_k = head_off + (j8 & 1) * hi_off + r8 * L::kRowB + (((j8 >> 1) ^ swz) << 4);
-    const uint32_t off_v = L::kKVBytes + head_off + (j8 >> 1) * hi_off + r8 * L::kRowB + (((j8 & 1) ^ swz) << 4);
+    const uint32_t swz = rowB == 128 ? r8 : rowB == 64 ? (r8 >> 1) & 3 : (r8 >> 2) & 1;
+    const uint32_t chunk0 = row_head * (L::kRowB / 16);
+    const uint32_t off_k = head_off + (j8 & 1) * hi_off + r8 * rowB + (((chunk0 + (j8 >> 1)) ^ swz) << 4);
+    const uint32_t off_v = L::kKVBytes + head_off + (j8 >> 1) * hi_off + r8 * rowB + (((chunk0 + (j8 & 1)) ^ swz) << 4);
     // 8-bit caches: my tokens' scales in a slot (K; V scales kScaleBytes further)
     const uint32_t scl_off = 2 * L::kKVBytes + ((((sub * SUB * kStageTokens + g) << p.log2_heads) + head) << 2);
     const uint32_t scl_8 = 32u << p.log2_heads;                      // 8 tokens further
@@ -696,8 +742,16 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
     uint32_t qf[KS][2];
     float qs[2];                  // logit scale of columns 2t, 2t + 1
     float acc[MT][4], m_run[2], l_run[2];
-    float qsum[L::kGroups][2];    // 4-bit: columns 2t, 2t + 1: the sum of a group's query elements, as kQ4 has it
-    float zs[L::kGroups];         // 4-bit: column g, my tokens: the sum of weight, scale and zero
+    // 4-bit codes: what a lane weighs of the logits it holds (rows g and g + 8 of a stage's
+    // tokens, columns 2t and 2t + 1).  Up to 4 query rows are repeated in the even columns,
+    // so that every lane has logits to weigh, and each weighs one column:
+    //   1 query row:  the slot's stage t & 1; its V weights for group t >> 1
+    //   2 query rows: row t & 1, stage t >> 1
+    //   4: row t, both stages; 8: rows 2t and 2t + 1 (both columns), both stages.
+    constexpr int NX = C == 8 ? 2 : 1, NB = C <= 2 ? 1 : SUB, ZG = C == 1 ? 1 : L::kGroups;
+    const int my_stage = C == 1 ? t & 1 : t >> 1, my_group = t >> 1;
+    float qsum[L::kGroups][2];    // the sum of a group's query elements, as large as the products have them
+    float zs[ZG][NX];             // the sum of weight, scale and zero
     float mu[2];                  // the reference that weights are taken under: m_run, or 0 while there is none
     int cslot = 0;
     uint32_t cphase = 0, citems = 0;
@@ -725,7 +779,7 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                 if (lane == 0) report(p.err_flag, 0x10 /* PA_FLAG_TIMEOUT */);
                 return;
             }
-            const int gq = L::kPaired ? g & 3 : g;        // my column's query row
+            const int gq = !L::kPaired ? g : L::k4 ? (g >> 1) & (C - 1) : g & 3;   // my column's query row
             const bool live = gq < (members << lg);
             const uint32_t *qw = reinterpret_cast<const uint32_t *>(qbuf + qi * kQEntry * H + (live ? gq >> lg : 0) * qmember) +
                                  ((head << lg) + (gq & ((1 << lg) - 1))) * (D / 2);
@@ -777,8 +831,11 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                     sum += __shfl_xor_sync(kFull, sum, 2);
                     qsum[gr][0] = __shfl_sync(kFull, sum, 8 * t);
                     qsum[gr][1] = __shfl_sync(kFull, sum, 8 * t + 4);
-                    zs[gr] = 0.f;
                 }
+#pragma unroll
+                for (int gr = 0; gr < ZG; ++gr)
+#pragma unroll
+                    for (int e = 0; e < NX; ++e) zs[gr][e] = 0.f;
                 const float up = __uint_as_float(eb) * p.scale_log2 * (0x1p20f / kQ4);
                 qs[0] = __shfl_sync(kFull, up, 8 * t);
                 qs[1] = __shfl_sync(kFull, up, 8 * t + 4);
@@ -848,14 +905,7 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                 // ---- QK: 16 tokens x 8 columns ----
                 const uint32_t ka = sa + (st0 + hs) * stage_off + off_k;
                 float c[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-                if constexpr (L::k4) {
-#pragma unroll
-                    for (int gr = 0; gr < L::kGroups; ++gr) {
-                        uint32_t a[4];
-                        ldsm_x4(a, ka ^ (gr << 5));
-                        mma_codes4(c[gr], c[gr], c[gr], c[gr], a, qf[4 * gr], qf[4 * gr + 1], qf[4 * gr + 2], qf[4 * gr + 3]);
-                    }
-                } else if constexpr (!k8) {
+                if constexpr (!k8) {
 #pragma unroll
                     for (int ks = 0; ks < KS; ++ks) {
                         uint32_t a[4];
@@ -875,27 +925,7 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                 }
                 const bool v_lo = kWhole || ((smask[hs] >> g) & 1u), v_hi = kWhole || ((smask[hs] >> (g + 8)) & 1u);
                 float k_lo = 1.f, k_hi = 1.f;
-                if constexpr (L::k4) {
-                    const uint8_t *ks = sp + s4_off + hs * s4_st + g * kScaleTok, *vs = ks + L::kScaleBytes;
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        float sum[2] = {0.f, 0.f}, big = kScaleFloor;
-#pragma unroll
-                        for (int gr = 0; gr < L::kGroups; ++gr) {
-                            const uint32_t w = *reinterpret_cast<const uint32_t *>(ks + k * s4_8 + 4 * gr);
-                            const float sc = __uint_as_float(w << 16), z = __uint_as_float(w & 0xffff0000u);
-#pragma unroll
-                            for (int e = 0; e < NE; ++e)
-                                sum[e] = fmaf(sc, fmaf(z, qsum[gr][e], c[gr][2 * k + e]), sum[e]);
-                            // (a scale that is no number makes its own group's sums such, not the reference)
-                            big = fmaxf(big, __uint_as_float(*reinterpret_cast<const uint32_t *>(vs + k * s4_8 + 4 * gr) << 16));
-                        }
-                        const bool ok = k ? v_hi : v_lo;
-                        sv[hs][k] = ok ? big : 0.f;
-#pragma unroll
-                        for (int e = 0; e < NE; ++e) x[hs][2 * k + e] = ok ? sum[e] * qs[e] : -INFINITY;
-                    }
-                } else if constexpr (k8) {
+                if constexpr (k8) {
                     // a masked token's scales may be anything: its V scale counts as 0
                     const uint8_t *lo = sp + scl_off + 2 * hs * scl_8, *hi = lo + scl_8;
                     k_lo = *reinterpret_cast<const float *>(lo);
@@ -906,7 +936,7 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                     sv[hs][1] = v_hi ? max_nan(b, kScaleFloor) : 0.f;
                 }
 #pragma unroll
-                for (int e = 0; e < (L::k4 ? 0 : NE); ++e) {
+                for (int e = 0; e < NE; ++e) {
                     const float a = (c[0][e] + c[1][e]) * (k8 ? k_lo * qs[e] : qs[e]);
                     const float b = (c[0][2 + e] + c[1][2 + e]) * (k8 ? k_hi * qs[e] : qs[e]);
                     x[hs][e] = v_lo ? a : -INFINITY;
@@ -958,12 +988,6 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                         acc[mt][e] *= al;
                         acc[mt][2 + e] *= al;
                     }
-                    if constexpr (L::k4) {      // of column g: held by lane g / 2 as its element g % 2
-                        const float ag = __shfl_sync(kFull, al, g >> 1);
-                        if ((g & 1) == e)
-#pragma unroll
-                            for (int gr = 0; gr < L::kGroups; ++gr) zs[gr] *= ag;
-                    }
                 }
                 weigh();
             }
@@ -977,51 +1001,20 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                 uint32_t bhi[2], blo[2];
                 {
                     const int srcA = 8 * t + (g >> 1), srcB = srcA + 4;
-                    const float(&src)[4] = L::k4 ? pw[hs] : w4[hs];   // (4-bit: the groups' scales come below)
                     float w[4];
-                    w[0] = __shfl_sync(kFull, src[0], srcA);
-                    w[1] = __shfl_sync(kFull, src[0], srcB);
-                    w[2] = __shfl_sync(kFull, src[2], srcA);
-                    w[3] = __shfl_sync(kFull, src[2], srcB);
+                    w[0] = __shfl_sync(kFull, w4[hs][0], srcA);
+                    w[1] = __shfl_sync(kFull, w4[hs][0], srcB);
+                    w[2] = __shfl_sync(kFull, w4[hs][2], srcA);
+                    w[3] = __shfl_sync(kFull, w4[hs][2], srcB);
                     if constexpr (NE == 2) {
-                        const float o0 = __shfl_sync(kFull, src[1], srcA), o1 = __shfl_sync(kFull, src[1], srcB);
-                        const float o2 = __shfl_sync(kFull, src[3], srcA), o3 = __shfl_sync(kFull, src[3], srcB);
+                        const float o0 = __shfl_sync(kFull, w4[hs][1], srcA), o1 = __shfl_sync(kFull, w4[hs][1], srcB);
+                        const float o2 = __shfl_sync(kFull, w4[hs][3], srcA), o3 = __shfl_sync(kFull, w4[hs][3], srcB);
                         if (g & 1) {
                             w[0] = o0;
                             w[1] = o1;
                             w[2] = o2;
                             w[3] = o3;
                         }
-                    }
-                    if constexpr (L::k4) {
-                        const uint8_t *vs = sp + s4_off + L::kScaleBytes + hs * s4_st + 2 * t * kScaleTok;
-                        const uint32_t va = sa + (st0 + hs) * stage_off + off_v;
-#pragma unroll
-                        for (int gr = 0; gr < L::kGroups; ++gr) {
-                            float ws[4];
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {     // tokens 2t, 2t + 1, 2t + 8, 2t + 9
-                                const uint32_t word =
-                                    *reinterpret_cast<const uint32_t *>(vs + (k >> 1) * s4_8 + (k & 1) * kScaleTok + 4 * gr);
-                                // a masked token's scales may be anything
-                                const bool ok = kWhole || ((smask[hs] >> (2 * t + (k & 1) + 4 * (k & 2))) & 1u);
-                                ws[k] = w[k] * (ok ? __uint_as_float(word << 16) : 0.f);
-                                zs[gr] = fmaf(ws[k], ok ? __uint_as_float(word & 0xffff0000u) : 0.f, zs[gr]);
-                            }
-#pragma unroll
-                            for (int k = 0; k < 2; ++k) {
-                                bhi[k] = pack2<false>(ws[2 * k], ws[2 * k + 1]);
-                                const float2 h = Cvt::to_float2(bhi[k]);
-                                blo[k] = pack2<false>(ws[2 * k] - h.x, ws[2 * k + 1] - h.y);
-                                if (L::kPaired && g >= 4) bhi[k] = blo[k];
-                            }
-                            uint32_t a[4];
-                            ldsm_x4_trans(a, va ^ (gr << 5));
-                            mma_codes4(acc[4 * gr], acc[4 * gr + 1], acc[4 * gr + 2], acc[4 * gr + 3], a, bhi, bhi, bhi, bhi);
-                            if constexpr (!L::kPaired)
-                                mma_codes4(acc[4 * gr], acc[4 * gr + 1], acc[4 * gr + 2], acc[4 * gr + 3], a, blo, blo, blo, blo);
-                        }
-                        continue;
                     }
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
@@ -1034,7 +1027,7 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                 const uint32_t vbase = (st0 + hs) * stage_off + L::kKVBytes;
                 // V rows that are masked are zeroed first: stale slots may hold NaN
                 // (not so int8 codes, which a zero weight always cancels)
-                if constexpr (!kWhole && CT != kCacheInt8 && !L::k4) {
+                if constexpr (!kWhole && CT != kCacheInt8) {
                     if (smask[hs] != 0xffffu) {
                         constexpr int kCh = L::kRowB / 16;                  // 16-byte chunks per box row
 #pragma unroll
@@ -1075,10 +1068,178 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                 }
             }
         };
+        auto attend4 = [&](auto whole_tag) {
+            constexpr bool kWhole = decltype(whole_tag)::value;
+            const bool second = kWhole || mine > kStageTokens;
+            // ---- QK: 16 tokens x 8 columns, a group's codes apart; the chains side by side ----
+            float c[SUB][L::kGroups][4];
+            {
+                uint32_t a[SUB][L::kGroups][4], f[4];
+#pragma unroll
+                for (int hs = 0; hs < SUB; ++hs)
+#pragma unroll
+                    for (int gr = 0; gr < L::kGroups; ++gr) {
+                        ldsm_x4(a[hs][gr], (sa + (st0 + hs) * stage_off + off_k) ^ (gr << 5));
+                        c[hs][gr][0] = c[hs][gr][1] = c[hs][gr][2] = c[hs][gr][3] = 0.f;
+                    }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int hs = 0; hs < SUB; ++hs)
+#pragma unroll
+                        for (int gr = 0; gr < L::kGroups; ++gr) {
+                            codes4(f, a[hs][gr], i);
+                            mma_f16(c[hs][gr], f, qf[4 * gr + i]);
+                        }
+            }
+            // ---- logits, and the scales and zeros of the weights to come ----
+            float x[NB][2][NX], sv[NB][2], vsc[NB][2][ZG], vz[NB][2][ZG];
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                const int st = NB == 1 ? my_stage : b;
+                const uint8_t *ks = sp + s4_off + st * s4_st + g * kScaleTok, *vs = ks + L::kScaleBytes;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    // a masked token's scales may be anything: its V scales count as 0
+                    const bool ok = kWhole || (g + 8 * k < mine - st * kStageTokens && !((m.bad >> (2 * (st0 + st) + k)) & 1u));
+                    const Words<L::kGroups> kw = load_words<L::kGroups>(ks + k * s4_8), vw = load_words<L::kGroups>(vs + k * s4_8);
+                    float sum[NX] = {}, big = kScaleFloor;
+#pragma unroll
+                    for (int gr = 0; gr < L::kGroups; ++gr) {
+#pragma unroll
+                        for (int e = 0; e < NX; ++e) {
+                            const float cv = NB == SUB ? c[b][gr][2 * k + e] : my_stage ? c[SUB - 1][gr][2 * k + e] : c[0][gr][2 * k + e];
+                            sum[e] = fmaf(word_scale(kw.w[gr]), fmaf(word_zero(kw.w[gr]), qsum[gr][e], cv), sum[e]);
+                        }
+                        // (a scale that is no number makes its own group's sums such, not the reference)
+                        big = fmaxf(big, word_scale(vw.w[gr]));
+                    }
+                    sv[b][k] = ok ? big : 0.f;
+#pragma unroll
+                    for (int e = 0; e < NX; ++e) x[b][k][e] = ok ? sum[e] * qs[e] : -INFINITY;
+#pragma unroll
+                    for (int gr = 0; gr < ZG; ++gr) {
+                        const uint32_t w = ZG == 1 && my_group ? vw.w[L::kGroups - 1] : vw.w[gr];
+                        vsc[b][k][gr] = ok ? word_scale(w) : 0.f;
+                        vz[b][k][gr] = ok ? word_zero(w) : 0.f;
+                    }
+                }
+            }
+            // ---- weights under the present reference, as for 8 bits ----
+            float pw[NB][2][NX];
+            auto weigh = [&]() {
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+#pragma unroll
+                        for (int e = 0; e < NX; ++e) pw[b][k][e] = fast_exp2(x[b][k][e] - mu[e]);
+            };
+            weigh();
+            bool nd = false;
+#pragma unroll
+            for (int e = 0; e < NX; ++e) {
+                nd = nd || m_run[e] == -INFINITY;
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+                    nd = nd || fmaxf(pw[b][0][e] * sv[b][0], pw[b][1][e] * sv[b][1]) > kWeightMax;
+            }
+            if (__any_sync(kFull, nd)) {
+                float al[NX];
+#pragma unroll
+                for (int e = 0; e < NX; ++e) {
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int b = 0; b < NB; ++b)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) mx = fmaxf(mx, x[b][k][e] + fast_log2(sv[b][k]));
+#pragma unroll
+                    for (int o = C == 1 ? 1 : C == 2 ? 2 : 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
+                    const float mn = fmaxf(m_run[e], mx - kWeightExp);
+                    al[e] = mn == -INFINITY ? 1.f : fast_exp2(m_run[e] - mn);
+                    m_run[e] = mn;
+                    mu[e] = mn == -INFINITY ? 0.f : mn;
+                    l_run[e] *= al[e];
+#pragma unroll
+                    for (int gr = 0; gr < ZG; ++gr) zs[gr][e] *= al[e];
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {       // of column 2t + e of the V product
+                    const float a = C == 8 ? al[e % NX] : __shfl_sync(kFull, al[0], (2 * t + e) & (C - 1));
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        acc[mt][e] *= a;
+                        acc[mt][2 + e] *= a;
+                    }
+                }
+                weigh();
+            }
+            // ---- weights with their scales as binary16 parts: the high and low part of one
+            // column (8 rows: the two columns' high parts, and their low ones) ----
+            uint32_t ph[NB][2][ZG], pl[NB][2][ZG];
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+#pragma unroll
+                    for (int e = 0; e < NX; ++e) l_run[e] += pw[b][k][e];
+#pragma unroll
+                    for (int gr = 0; gr < ZG; ++gr) {
+                        float w[NX];
+#pragma unroll
+                        for (int e = 0; e < NX; ++e) {
+                            w[e] = pw[b][k][e] * vsc[b][k][gr];
+                            zs[gr][e] = fmaf(w[e], vz[b][k][gr], zs[gr][e]);
+                        }
+                        if constexpr (L::kPaired) {
+                            ph[b][k][gr] = pack2_rz(w[0], w[0] - high_part(w[0]));
+                        } else {
+                            ph[b][k][gr] = pack2_rz(w[0], w[NX - 1]);
+                            pl[b][k][gr] = pack2_rz(w[0] - high_part(w[0]), w[NX - 1] - high_part(w[NX - 1]));
+                        }
+                    }
+                }
+            // ---- PV: the weights of tokens 2t, 2t + 1, 2t + 8, 2t + 9 for column g, from where they were made ----
+            const uint32_t pick = (L::kPaired ? g < 4 : (g & 1) == 0) ? 0x5410u : 0x7632u;
+#pragma unroll
+            for (int hs = 0; hs < SUB; ++hs) {
+                if (!kWhole && hs > 0 && !second) continue;
+                const uint32_t va = sa + (st0 + hs) * stage_off + off_v;
+#pragma unroll
+                for (int gr = 0; gr < L::kGroups; ++gr) {
+                    const int src = 8 * t + (C == 1   ? hs + 2 * gr
+                                             : C == 2 ? (g & 1) + 2 * hs
+                                             : C == 4 ? g & 3
+                                                      : g >> 1);
+                    const int b = NB == 1 ? 0 : hs, gi = ZG == 1 ? 0 : gr;
+                    auto fragment = [&](const uint32_t(&p)[NB][2][ZG], uint32_t (&f)[2]) {
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            f[k] = __byte_perm(__shfl_sync(kFull, p[b][k][gi], src), __shfl_sync(kFull, p[b][k][gi], src + 4), pick);
+                    };
+                    uint32_t a[4], f[4], w[2], wl[2];
+                    ldsm_x4_trans(a, va ^ (gr << 5));
+                    fragment(ph, w);
+                    if constexpr (!L::kPaired) fragment(pl, wl);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        codes4(f, a, i);
+                        mma_f16(acc[4 * gr + i], f, w);
+                        if constexpr (!L::kPaired) mma_f16(acc[4 * gr + i], f, wl);
+                    }
+                }
+            }
+        };
+        auto consume = [&](auto whole_tag) {
+            if constexpr (L::k4)
+                attend4(whole_tag);
+            else
+                attend(whole_tag);
+        };
         if (mine >= SUB * kStageTokens && m.bad == 0)
-            attend(std::true_type{});
+            consume(std::true_type{});
         else if (mine > 0)
-            attend(std::false_type{});
+            consume(std::false_type{});
         // my reads (and zeroing) of the slot are done
         fence_proxy_async_smem();
         __syncwarp();
@@ -1101,15 +1262,33 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                     acc[mt][2 + e] += __shfl_xor_sync(kFull, acc[mt][2 + e], 2);
                 }
         }
-        if constexpr (L::k4) {      // the zeros' share of every element of a group
+        if constexpr (L::k4) {
+            // sums over the lanes that weighed for one query row, then everything by the
+            // columns 2t, 2t + 1 of the V product, the zeros' share of each group added
+            constexpr int kFirstLane = C == 1 ? 1 : C == 2 ? 2 : 4;
+            auto total = [&](float v) {
+                if constexpr (C == 1) v += __shfl_xor_sync(kFull, v, 1);
+#pragma unroll
+                for (int o = C == 1 ? 4 : kFirstLane; o < 32; o <<= 1) v += __shfl_xor_sync(kFull, v, o);
+                return v;
+            };
+            float mo[2], lo[2], lt[NX];
+#pragma unroll
+            for (int e = 0; e < NX; ++e) lt[e] = total(l_run[e]);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int row = (2 * t + e) & (C - 1);       // lane `row` of the first four holds it (C < 8)
+                mo[e] = C == 8 ? m_run[e] : __shfl_sync(kFull, m_run[0], row);
+                lo[e] = C == 8 ? lt[e % NX] : __shfl_sync(kFull, lt[0], row);
+            }
 #pragma unroll
             for (int gr = 0; gr < L::kGroups; ++gr) {
-                float z = zs[gr];
-                z += __shfl_xor_sync(kFull, z, 1);
-                z += __shfl_xor_sync(kFull, z, 2);
+                float z[NX];
 #pragma unroll
-                for (int e = 0; e < NE; ++e) {
-                    const float ze = __shfl_sync(kFull, z, 8 * t + 4 * e);
+                for (int e = 0; e < NX; ++e) z[e] = total(zs[ZG == 1 ? 0 : gr][e]);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float ze = C == 8 ? z[e % NX] : __shfl_sync(kFull, z[0], C == 1 ? 2 * gr : (2 * t + e) & (C - 1));
 #pragma unroll
                     for (int mt = 4 * gr; mt < 4 * gr + 4; ++mt) {
                         acc[mt][e] += ze;
@@ -1117,11 +1296,17 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                     }
                 }
             }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                m_run[e] = mo[e];
+                l_run[e] = lo[e];
+            }
+        } else {
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1)
+#pragma unroll
+                for (int e = 0; e < NE; ++e) l_run[e] += __shfl_xor_sync(kFull, l_run[e], o);
         }
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1)
-#pragma unroll
-            for (int e = 0; e < NE; ++e) l_run[e] += __shfl_xor_sync(kFull, l_run[e], o);
         if (nsubs > 1) {
             // join the states of the head's warps: the others hand theirs to the first
             const uint32_t par = (citems - 1) & 1u;      // of this item
