@@ -723,6 +723,7 @@ struct SplitPlan {
     int prefix_part = 0;         // tokens per prefix_per partials
     int prefix_per = 1, prefix_parts = 0;
     int max_parts = 1;
+    int max_shares = 0;
     int64_t cut_row = 0, prefix_cut_row = 0, rows = 0;
     size_t acc_off = 0, bytes = 0;
 };
@@ -789,7 +790,8 @@ bool plan_split(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int
     if ((!shared || w.whole) && w.max_parts <= 1) return true;
     // Rows of (reference, sum, weighted sum): one per partial, and for cut items
     // one per launch, CTA and head of its box.
-    const int64_t per_launch = static_cast<int64_t>(pa::kSplitMaxCtas) << w.log2_heads;
+    w.max_shares = cache == pa::kCacheInt4 ? 2 * pa::kSplitMaxCtas : pa::kSplitMaxCtas;
+    const int64_t per_launch = static_cast<int64_t>(w.max_shares) << w.log2_heads;
     w.cut_row = static_cast<int64_t>(num_seqs) * num_heads * w.max_parts;
     w.prefix_cut_row = w.cut_row + (num_seqs + kSplitEntries - 1) / kSplitEntries * per_launch * w.G;
     w.rows = w.prefix_cut_row +
@@ -866,10 +868,6 @@ pa_status run_split(pa::SplitParams p, int cache, int head_dim, int cols, int en
         const size_t room = static_cast<size_t>(dev.smem_optin);
         if (need.fixed + 2 * need.slot > room) return PA_ERR_UNSUPPORTED;
         p.stages = static_cast<int>(std::min<size_t>(8, (room - need.fixed) / need.slot));
-        if (cache == pa::kCacheInt4) {
-            if (p.stages == 5 || p.stages == 7) --p.stages;
-            p.producers = p.stages % 4 == 0 ? 4 : p.stages % 3 == 0 ? 3 : 2;
-        }
         const size_t smem = need.fixed + p.stages * need.slot;
         const int grid = static_cast<int>(std::min<int64_t>(std::min(dev.sms, pa::kSplitMaxCtas), p.entries * per_entry));
         auto launch = cache == pa::kCacheF16    ? pa::launch_split_f16
@@ -935,6 +933,7 @@ pa::SplitParams split_params(void *out, pa_dtype out_dtype, const void *query, p
         p.cut_rows = static_cast<uint32_t>(w.prefix_cut_row - w.cut_row);
         p.prefix_cut_rows = static_cast<uint32_t>(w.rows - w.prefix_cut_row);
         p.cut_cols = w.G;
+        p.max_shares = w.max_shares;
         p.cut = 1;
     }
     p.err_flag = err_flag;

@@ -18,7 +18,7 @@ constexpr int kCacheF16 = 0, kCacheBF16 = 1, kCacheE4M3 = 2, kCacheInt8 = 3, kCa
 // Entries (sequences, or chunks of groups) of one launch: the kernel keeps 12
 // bytes for each in shared memory; longer lists take several launches.
 constexpr int kSplitEntries = 2048;
-// CTAs of a launch at most (a row of the workspace for each).
+// CTAs of a launch at most (a row of the workspace for each, two for 4-bit caches).
 constexpr int kSplitMaxCtas = 256;
 constexpr int kRowFinal = -1, kRowCut = 1;
 
@@ -54,6 +54,7 @@ struct SplitParams {
     float *ws_acc;               // [rows, D]: weighted sum
     int cut;                     // CTAs take equal shares of the slots, items may be cut
     int cut_cols;                // query rows per head in a cut item's rows
+    int max_shares;              // CTAs (4-bit caches: halves of them) that may leave some in a launch
     int64_t cut_row;             // where the cut items' rows of this launch start
     int64_t prefix_cut_row;      // join: where those of the prefix launches start
     uint32_t cut_rows, prefix_cut_rows;   // join: how many there are of each
@@ -70,7 +71,6 @@ struct SplitParams {
     int e0, entries;             // this launch's entries
     int log2_heads;              // KV heads per box: 1, 2, 4 or 8
     int stages;                  // ring depth
-    int producers;               // 4-bit caches: producer warps, of which the ring's depth is a multiple
     int late_wait;               // the previous kernel is the call's own prefix kernel, whose results this
                                  // one does not read: wait for it only at the end
 };

@@ -77,17 +77,17 @@ struct SplitLayout {
     static constexpr int kKVBytes = kTiles * kStageTokens * kRow;      // a slot's K (or V) rows
     static constexpr int kScaleBytes = k8 ? kTiles * kStageTokens * 4 * kGroups : 0;
     static constexpr int kSlotBytes = (2 * kKVBytes + 2 * kScaleBytes + 1023) / 1024 * 1024;
-    // Producer warps, which take the slots in turn: a 4-bit slot is consumed in less time
-    // than one of them takes to bring in the next.  (p.producers of them work.)
-    static constexpr int kProducers = k4 ? 4 : 1;
-    static constexpr int kThreads = (kWarps + kProducers) * 32;
+    // Teams of a producer and its consumers, each with a ring and a share of the slots of its
+    // own.  4-bit codes: two, since one's warps are too few to hide their own latencies.
+    static constexpr int kTeams = k4 ? 2 : 1;
+    static constexpr int kThreads = kTeams * (kWarps + 1) * 32;
     static constexpr int kMT = D / 16;
     static constexpr int kStateRow = D + 4;              // floats per query row of a warp's state
     static constexpr int kStateBytes = C * kStateRow * 4;
 };
 
 // One ring slot's description.
-struct SlotMeta {
+struct alignas(16) SlotMeta {
     int seq;         // the entry's first query sequence; < 0: no more work
     int kvh0;        // first KV head of the box
     int part;
@@ -181,20 +181,28 @@ __device__ __forceinline__ void widen_v(uint32_t w, uint32_t &ev, uint32_t &od) 
     }
 }
 
-// 4-bit codes enter the products as they lie in a byte: four bits at the bottom of a
-// binary16 are u 2^-24, the next four u 2^-20 (subnormal numbers, exact), so that a
-// register of eight codes takes four ANDs and a shift and no conversion.  The query
-// elements of the former are scaled up by 16, and an accumulator of the V product holds
-// either kind only.
+// 4-bit codes enter the products as they lie in a byte: as binary16 numbers, the low four
+// bits alone are n0 2^-24 (subnormal, exact), and a whole byte is (16 n1 + n0) 2^-24.
+// A register of eight codes so takes three ANDs and a byte permutation and no
+// conversion; n1's share is the byte's less the low bits':
+//   V product: an accumulator for either, subtracted once at an item's end;
+//   K product, up to 4 query rows: even columns take q0 n0 and q1 n1 + q1 n0 / 16, odd
+//   ones the q1 n0 / 16 to take off (8 rows fill the columns: n1 is masked out instead).
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
-// Step i (0 to 3) of the registers' codes.
-__device__ __forceinline__ void codes4(uint32_t (&f)[4], const uint32_t (&a)[4], int i) {
+// The registers' codes 0 and 4 (low) and, with 1 and 5, their bytes (kBytes) or 1 and 5
+// alone 16 times larger; second: codes 2, 6 and 3, 7.
+template <bool kBytes>
+__device__ __forceinline__ void codes4(uint32_t (&low)[4], uint32_t (&high)[4], const uint32_t (&a)[4], bool second) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) f[k] = (i < 2 ? a[k] : a[k] >> 8) & (i & 1 ? 0x00f000f0u : 0x000f000fu);
+    for (int k = 0; k < 4; ++k) {
+        const uint32_t w = second ? __byte_perm(a[k], 0u, 0x4341u) : a[k];
+        low[k] = w & 0x000f000fu;
+        high[k] = kBytes && second ? w : w & (kBytes ? 0x00ff00ffu : 0x00f000f0u);
+    }
 }
 // N words of scale and zero, neighbours in shared memory.
 template <int N>
@@ -257,7 +265,7 @@ __device__ __forceinline__ bool bad_group(const SplitParams &p, int g, int q0, i
 // Row, after p.cut_row, of query row `col` of head `head` of a box in what CTA
 // `cta` of this launch continued.
 __device__ __forceinline__ int cut_row_of(const SplitParams &p, uint32_t cta, int head, int col) {
-    return static_cast<int>(((((p.e0 / kSplitEntries) * kSplitMaxCtas + cta) << p.log2_heads) + head) * p.cut_cols + col);
+    return static_cast<int>(((((p.e0 / kSplitEntries) * p.max_shares + cta) << p.log2_heads) + head) * p.cut_cols + col);
 }
 
 // Items (entry, partition, box of heads) in that order, weighed in slots: the
@@ -293,7 +301,7 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
     using L = SplitLayout<D, C, CT>;
     constexpr bool k8 = L::k8;
     constexpr bool BF16 = CT == kCacheBF16;   // MMA operand type
-    constexpr int SUB = L::kSub, W = L::kWarps, MT = L::kMT, KS = D / 16;
+    constexpr int SUB = L::kSub, W = L::kWarps, TEAMS = L::kTeams, MT = L::kMT, KS = D / 16;
     constexpr int NE = C == 1 ? 1 : 2;        // live columns per lane (columns 2t, 2t + 1)
     using Cvt = Half2x<BF16>;
     extern __shared__ uint8_t smem_raw[];
@@ -310,8 +318,13 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
     const int qmember = H * D * 2 << lg;               // one sequence's query rows of a box
     constexpr int kQEntry = C * D * 2;                 // x H: one query-ring entry
 
-    uint8_t *slots = smem;
-    uint8_t *qbuf = smem + static_cast<size_t>(S) * L::kSlotBytes;
+    // A team's part of shared memory: ring, queries, states, slots' descriptions, barriers.
+    const int team = TEAMS == 1 ? 0 : warp / (W + 1), tw = TEAMS == 1 ? warp : warp % (W + 1);
+    const size_t team_slots = static_cast<size_t>(S) * L::kSlotBytes;
+    const size_t team_rest = kQueryRing * kQEntry * H + (W - H) * L::kStateBytes + W * 8 * sizeof(float2) +
+                             S * (sizeof(SlotMeta) + 16) + (2 * kQueryRing + 16) * 8;
+    uint8_t *slots = smem + team * team_slots;
+    uint8_t *qbuf = smem + TEAMS * team_slots + team * team_rest;
     uint8_t *xbuf = qbuf + kQueryRing * kQEntry * H;   // (W - H) warp states
     float2 *xml = reinterpret_cast<float2 *>(xbuf + (W - H) * L::kStateBytes);   // [warp][8]
     SlotMeta *meta = reinterpret_cast<SlotMeta *>(xml + W * 8);
@@ -321,7 +334,7 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
     uint64_t *qempty = qfull + kQueryRing;
     uint64_t *xfull = qempty + kQueryRing;             // per head: the other warps' states are written
     uint64_t *xfree = xfull + 8;                       //           and have been read
-    uint32_t *warp_tot = reinterpret_cast<uint32_t *>(xfree + 8);
+    uint32_t *warp_tot = reinterpret_cast<uint32_t *>(smem + TEAMS * (team_slots + team_rest));
     int *len_s = reinterpret_cast<int *>(warp_tot + 32);
     int *aux_s = len_s + E;                            // suffix: first block; prefix: sequence | members << 27;
                                                        // whole: the group's first sequence
@@ -340,7 +353,7 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
     const int log2_row_heads = L::k4 ? min(p.log2_heads, D == 128 ? 1 : 2) : 0;
     const uint32_t rowB = static_cast<uint32_t>(L::kRowB) << log2_row_heads;
 
-    if (threadIdx.x == 0) {
+    if (lane == 0 && tw == 0) {
         for (int i = 0; i < S; ++i) {
             mbar_init(&full[i], lane_copies ? 33 : 1);
             mbar_init(&empty[i], W);
@@ -450,19 +463,13 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
     // an item across the end is continued by the next CTA, which leaves a partial
     // result of its own, named in the item's.
     const uint32_t total = prefix[E];
-    const bool cut = p.cut && total >= gridDim.x * static_cast<uint32_t>((P / kStageTokens + SW - 1) / SW);
-    const uint32_t lo = static_cast<uint32_t>(static_cast<uint64_t>(total) * blockIdx.x / gridDim.x);
-    const uint32_t hi = static_cast<uint32_t>(static_cast<uint64_t>(total) * (blockIdx.x + 1) / gridDim.x);
+    const uint32_t shares = gridDim.x * TEAMS, share = blockIdx.x * TEAMS + team;
+    const bool cut = p.cut && total >= shares * static_cast<uint32_t>((P / kStageTokens + SW - 1) / SW);
+    const uint32_t lo = static_cast<uint32_t>(static_cast<uint64_t>(total) * share / shares);
+    const uint32_t hi = static_cast<uint32_t>(static_cast<uint64_t>(total) * (share + 1) / shares);
 
-    if (warp >= W) {
-        // ------------------------------------------------------------ producers
-        // Producer pi brings in the CTA's slots pi, pi + NP, ...  The ring's depth is a multiple
-        // of NP: each of its slots belongs to one producer, which waits for every use of it in
-        // turn (a barrier's parity says nothing to one that may be two uses away).  For the
-        // same reason the first one loads all items' queries.
-        const int NP = L::kProducers == 1 ? 1 : p.producers;
-        const uint32_t pi = warp - W;
-        if (pi >= static_cast<uint32_t>(NP)) return;
+    if (tw == W) {
+        // ------------------------------------------------------------ producer
         const uint64_t policy =
             mode == kSplitPrefix && p.chunks > 1 ? l2_policy_evict_normal() : l2_policy_evict_first();
         ItemCursor ic{};
@@ -532,14 +539,13 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
             if (ntok > 0 && lane <= (t0 + ntok - 1) / bs - fb)
                 bid = __ldg(p.block_tables + static_cast<int64_t>(row) * p.max_blocks_per_seq + blk0 + fb + lane);
         };
-        uint32_t uses = 0, items = 0;                  // of the CTA, up to the present item
-        uint32_t mine = pi, rounds = 0;                // my next slot, and how often the ring was gone round before it
-        int islot = pi;
+        int islot = 0;
+        uint32_t uses = 0, items = 0;
         bool ok = true;
         auto take_slot = [&]() -> int {
             const int slot = islot;
-            if (rounds > 0) {
-                const uint32_t par = (rounds - 1) & 1u;
+            if (uses >= static_cast<uint32_t>(S)) {
+                const uint32_t par = ((uses / S) - 1) & 1u;
                 if (!mbar_try_wait(&empty[slot], par) && !mbar_wait_bounded(&empty[slot], par)) {
                     if (lane == 0) report(p.err_flag, 0x10 /* PA_FLAG_TIMEOUT */);
                     ok = false;
@@ -547,28 +553,15 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
             }
             ok = __all_sync(kFull, ok);
             if (ok) {
-                mine += NP;
-                if ((islot += NP) >= S) {
-                    islot -= S;
-                    ++rounds;
-                }
+                islot = (islot + 1 == S) ? 0 : islot + 1;
+                ++uses;
             }
             return slot;
         };
         while (ok && work && ic.start < hi) {
             const int kvh0 = ic.grp << p.log2_heads;
-            // this CTA's slots of the item, and the first of mine
-            const int jb = cut && ic.start < lo ? static_cast<int>(lo - ic.start) : 0;
-            const int je = cut ? min(ic.nslots, static_cast<int>(hi - ic.start)) : ic.nslots;
-            const int j0 = jb + static_cast<int>(mine - uses);
-            if (pi > 0 && j0 >= je) {
-                uses += je - jb;
-                ++items;
-                advance();
-                continue;
-            }
             open_item();
-            if (pi == 0) {
+            {
                 const int qi = static_cast<int>(items % kQueryRing);
                 if (items >= static_cast<uint32_t>(kQueryRing)) {
                     const uint32_t par = ((items / kQueryRing) - 1) & 1u;
@@ -586,14 +579,17 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                                   p.q + (static_cast<int64_t>(seq + m) * Hq + (kvh0 << lg)) * D,
                                   static_cast<uint32_t>(qmember), &qfull[qi]);
                 }
+                ++items;
                 __syncwarp();
             }
-            ++items;
+            // this CTA's slots of the item
+            const int jb = cut && ic.start < lo ? static_cast<int>(lo - ic.start) : 0;
+            const int je = cut ? min(ic.nslots, static_cast<int>(hi - ic.start)) : ic.nslots;
             const int kind = jb > 0               ? kContinued
                              : je < ic.nslots     ? kCut
                              : final_mode(mode) && ic.nparts == 1 ? kFinal
                                                                   : 0;
-            for (int j = j0; j < je; j += NP) {
+            for (int j = jb; j < je; ++j) {
                 const int slot = take_slot();
                 if (!ok) break;
                 uint8_t *sp = slots + static_cast<size_t>(slot) * L::kSlotBytes;
@@ -679,11 +675,10 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                 }
                 __syncwarp();
             }
-            uses += je - jb;
             advance();
         }
         // one more slot tells the consumers to stop
-        if (ok && mine == uses) {
+        if (ok) {
             const int slot = take_slot();
             if (ok) {
                 if (lane == 0) {
@@ -700,11 +695,9 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
         }
         // After a wait that gave up, let the copies still in flight land before the CTA ends.
         if (!ok) {
-            for (uint32_t u = mine, n = 0; u >= static_cast<uint32_t>(NP) && n < static_cast<uint32_t>(S); n += NP) {
-                u -= NP;
+            for (uint32_t u = uses > static_cast<uint32_t>(S) ? uses - S : 0u; u < uses; ++u)
                 mbar_wait_bounded(&full[u % S], (u / S) & 1u);
-            }
-            for (uint32_t i = items > static_cast<uint32_t>(kQueryRing) ? items - kQueryRing : 0u; pi == 0 && i < items; ++i)
+            for (uint32_t i = items > static_cast<uint32_t>(kQueryRing) ? items - kQueryRing : 0u; i < items; ++i)
                 mbar_wait_bounded(&qfull[i % kQueryRing], (i / kQueryRing) & 1u);
         }
         if (p.late_wait) pdl_wait();   // the grid does not finish before the prefix kernel
@@ -715,7 +708,7 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
     // Warp w takes head kvh0 + w % H and, of a slot's stages, the SUB at
     // (w / H) * SUB.  Column c of its MMAs (c < 8) is query row c % G of member
     // c / G; columns without a query hold zero queries and are never written.
-    const int head = warp & (H - 1), sub = warp >> p.log2_heads;
+    const int head = tw & (H - 1), sub = tw >> p.log2_heads;
     const int g = lane >> 2, t = lane & 3;
     const int r8 = lane & 7, j8 = lane >> 3;
     const uint32_t slots_sa = smem_addr(slots);
@@ -747,8 +740,8 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
     // so that every lane has logits to weigh, and each weighs one column:
     //   1 query row:  the slot's stage t & 1; its V weights for group t >> 1
     //   2 query rows: row t & 1, stage t >> 1
-    //   4: row t, both stages; 8: rows 2t and 2t + 1 (both columns), both stages.
-    constexpr int NX = C == 8 ? 2 : 1, NB = C <= 2 ? 1 : SUB, ZG = C == 1 ? 1 : L::kGroups;
+    //   4: row t; 8: rows 2t and 2t + 1 (both columns); one stage after the other.
+    constexpr int NX = C == 8 ? 2 : 1, ZG = C == 1 ? 1 : L::kGroups;
     const int my_stage = C == 1 ? t & 1 : t >> 1, my_group = t >> 1;
     float qsum[L::kGroups][2];    // the sum of a group's query elements, as large as the products have them
     float zs[ZG][NX];             // the sum of weight, scale and zero
@@ -792,7 +785,8 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                 qs[0] = qs[1] = p.scale_log2;
             } else if constexpr (L::k4) {
                 // Step 4 gr + i takes elements 8t + i and 8t + i + 4 of group gr's first
-                // half and of its second; even steps' codes arrive 16 times smaller.
+                // half and of its second; even steps meet low codes, 16 times smaller.  Up
+                // to 4 rows: odd columns as said at codes4.
                 uint4 w[2 * L::kGroups];
 #pragma unroll
                 for (int c = 0; c < 2 * L::kGroups; ++c)
@@ -811,26 +805,31 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                 }
                 amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
                 amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
-                const uint32_t eb = min(max(__float_as_uint(amax) & 0x7f800000u, 0x00800000u), 0x7e800000u);
-                const float inv = __uint_as_float(0x7f000000u - eb);
+                // 2^e <= amax < 2^(e+1), e kept where 2^e and kQ4 16 2^-e are normal
+                const uint32_t eb = min(max(__float_as_uint(amax) & 0x7f800000u, 0x08000000u), 0x7e800000u);
+                const bool odd = L::kPaired && (g & 1);
+                const float inv = __uint_as_float(0x7f000000u - eb) * kQ4;
+                const float m0 = odd ? 0.f : 16.f * inv, m1 = odd ? 0.f : inv, m1low = odd ? inv : 0.f;
 #pragma unroll
                 for (int gr = 0; gr < L::kGroups; ++gr) {
-                    float sum = 0.f;
+                    float sums[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float m = i & 1 ? kQ4 : 16.f * kQ4;
+                    for (int i = 0; i < 4; i += 2) {
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
-                            const uint32_t b = pack2<false>(f[2 * gr + k][i] * inv * m, f[2 * gr + k][i + 4] * inv * m);
-                            qf[4 * gr + i][k] = b;
-                            const float2 r = Half2x<false>::to_float2(b);
-                            sum += (r.x + r.y) * (i & 1 ? 0x1p-20f : 0x1p-24f);
+                            const float(&v)[8] = f[2 * gr + k];
+                            qf[4 * gr + i][k] = pack2<false>(fmaf(v[i], m0, v[i + 1] * m1low), fmaf(v[i + 4], m0, v[i + 5] * m1low));
+                            qf[4 * gr + i + 1][k] = pack2<false>(v[i + 1] * m1, v[i + 5] * m1);
                         }
+                        // the sum of the elements: what codes of 1 would give
+                        const uint32_t one[4] = {0x00010001u, 0x00010001u, 0x00010001u, 0x00010001u};
+                        constexpr uint32_t kHigh = L::kPaired ? 0x00110011u : 0x00100010u;
+                        const uint32_t high[4] = {kHigh, kHigh, kHigh, kHigh};
+                        mma_f16(sums, one, qf[4 * gr + i]);
+                        mma_f16(sums, high, qf[4 * gr + i + 1]);
                     }
-                    sum += __shfl_xor_sync(kFull, sum, 1);
-                    sum += __shfl_xor_sync(kFull, sum, 2);
-                    qsum[gr][0] = __shfl_sync(kFull, sum, 8 * t);
-                    qsum[gr][1] = __shfl_sync(kFull, sum, 8 * t + 4);
+                    qsum[gr][0] = L::kPaired ? sums[0] - sums[1] : sums[0];
+                    qsum[gr][1] = sums[1];
                 }
 #pragma unroll
                 for (int gr = 0; gr < ZG; ++gr)
@@ -1068,91 +1067,82 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                 }
             }
         };
-        auto attend4 = [&](auto whole_tag) {
+        // 4-bit codes: NS stages from st0 + first on (both where a lane weighs one of them).
+        auto attend4 = [&](auto whole_tag, int first) {
             constexpr bool kWhole = decltype(whole_tag)::value;
-            const bool second = kWhole || mine > kStageTokens;
-            // ---- QK: 16 tokens x 8 columns, a group's codes apart; the chains side by side ----
-            float c[SUB][L::kGroups][4];
-            {
-                uint32_t a[SUB][L::kGroups][4], f[4];
+            constexpr int NS = C <= 2 ? SUB : 1;
+            const uint32_t stage = sa + (st0 + first) * stage_off;
+            // ---- QK: 16 tokens x 8 columns, a group's codes apart ----
+            float c[NS][L::kGroups][4];
 #pragma unroll
-                for (int hs = 0; hs < SUB; ++hs)
+            for (int hs = 0; hs < NS; ++hs) {
+                uint32_t a[L::kGroups][4], low[4], high[4];
+#pragma unroll
+                for (int gr = 0; gr < L::kGroups; ++gr) {
+                    ldsm_x4(a[gr], (stage + hs * stage_off + off_k) ^ (gr << 5));
+                    c[hs][gr][0] = c[hs][gr][1] = c[hs][gr][2] = c[hs][gr][3] = 0.f;
+                }
+#pragma unroll
+                for (int i = 0; i < 4; i += 2)
 #pragma unroll
                     for (int gr = 0; gr < L::kGroups; ++gr) {
-                        ldsm_x4(a[hs][gr], (sa + (st0 + hs) * stage_off + off_k) ^ (gr << 5));
-                        c[hs][gr][0] = c[hs][gr][1] = c[hs][gr][2] = c[hs][gr][3] = 0.f;
+                        codes4<L::kPaired>(low, high, a[gr], i > 0);
+                        mma_f16(c[hs][gr], low, qf[4 * gr + i]);
+                        mma_f16(c[hs][gr], high, qf[4 * gr + i + 1]);
                     }
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int hs = 0; hs < SUB; ++hs)
-#pragma unroll
-                        for (int gr = 0; gr < L::kGroups; ++gr) {
-                            codes4(f, a[hs][gr], i);
-                            mma_f16(c[hs][gr], f, qf[4 * gr + i]);
-                        }
             }
             // ---- logits, and the scales and zeros of the weights to come ----
-            float x[NB][2][NX], sv[NB][2], vsc[NB][2][ZG], vz[NB][2][ZG];
+            float x[2][NX], sv[2], vsc[2][ZG], vz[2][ZG];
+            const int st = first + (NS > 1 ? my_stage : 0);          // the stage I weigh
+            const uint8_t *ks = sp + s4_off + st * s4_st + g * kScaleTok, *vs = ks + L::kScaleBytes;
 #pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                const int st = NB == 1 ? my_stage : b;
-                const uint8_t *ks = sp + s4_off + st * s4_st + g * kScaleTok, *vs = ks + L::kScaleBytes;
+            for (int k = 0; k < 2; ++k) {
+                // a masked token's scales may be anything: its V scales count as 0
+                const bool ok = kWhole || (g + 8 * k < mine - st * kStageTokens && !((m.bad >> (2 * (st0 + st) + k)) & 1u));
+                const Words<L::kGroups> kw = load_words<L::kGroups>(ks + k * s4_8), vw = load_words<L::kGroups>(vs + k * s4_8);
+                float sum[NX] = {}, big = kScaleFloor;
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    // a masked token's scales may be anything: its V scales count as 0
-                    const bool ok = kWhole || (g + 8 * k < mine - st * kStageTokens && !((m.bad >> (2 * (st0 + st) + k)) & 1u));
-                    const Words<L::kGroups> kw = load_words<L::kGroups>(ks + k * s4_8), vw = load_words<L::kGroups>(vs + k * s4_8);
-                    float sum[NX] = {}, big = kScaleFloor;
+                for (int gr = 0; gr < L::kGroups; ++gr) {
 #pragma unroll
-                    for (int gr = 0; gr < L::kGroups; ++gr) {
+                    for (int e = 0; e < NX; ++e) {
+                        float cv[NS];
 #pragma unroll
-                        for (int e = 0; e < NX; ++e) {
-                            const float cv = NB == SUB ? c[b][gr][2 * k + e] : my_stage ? c[SUB - 1][gr][2 * k + e] : c[0][gr][2 * k + e];
-                            sum[e] = fmaf(word_scale(kw.w[gr]), fmaf(word_zero(kw.w[gr]), qsum[gr][e], cv), sum[e]);
-                        }
-                        // (a scale that is no number makes its own group's sums such, not the reference)
-                        big = fmaxf(big, word_scale(vw.w[gr]));
+                        for (int hs = 0; hs < NS; ++hs)
+                            cv[hs] = L::kPaired ? c[hs][gr][2 * k] - c[hs][gr][2 * k + 1] : c[hs][gr][2 * k + e];
+                        const float one = NS > 1 && my_stage ? cv[NS - 1] : cv[0];
+                        sum[e] = fmaf(word_scale(kw.w[gr]), fmaf(word_zero(kw.w[gr]), qsum[gr][e], one), sum[e]);
                     }
-                    sv[b][k] = ok ? big : 0.f;
+                    // (a scale that is no number makes its own group's sums such, not the reference)
+                    big = fmaxf(big, word_scale(vw.w[gr]));
+                }
+                sv[k] = ok ? big : 0.f;
 #pragma unroll
-                    for (int e = 0; e < NX; ++e) x[b][k][e] = ok ? sum[e] * qs[e] : -INFINITY;
+                for (int e = 0; e < NX; ++e) x[k][e] = ok ? sum[e] * qs[e] : -INFINITY;
 #pragma unroll
-                    for (int gr = 0; gr < ZG; ++gr) {
-                        const uint32_t w = ZG == 1 && my_group ? vw.w[L::kGroups - 1] : vw.w[gr];
-                        vsc[b][k][gr] = ok ? word_scale(w) : 0.f;
-                        vz[b][k][gr] = ok ? word_zero(w) : 0.f;
-                    }
+                for (int gr = 0; gr < ZG; ++gr) {
+                    const uint32_t w = ZG == 1 && my_group ? vw.w[L::kGroups - 1] : vw.w[gr];
+                    vsc[k][gr] = ok ? word_scale(w) : 0.f;
+                    vz[k][gr] = ok ? word_zero(w) : 0.f;
                 }
             }
             // ---- weights under the present reference, as for 8 bits ----
-            float pw[NB][2][NX];
+            float pw[2][NX];
             auto weigh = [&]() {
 #pragma unroll
-                for (int b = 0; b < NB; ++b)
+                for (int k = 0; k < 2; ++k)
 #pragma unroll
-                    for (int k = 0; k < 2; ++k)
-#pragma unroll
-                        for (int e = 0; e < NX; ++e) pw[b][k][e] = fast_exp2(x[b][k][e] - mu[e]);
+                    for (int e = 0; e < NX; ++e) pw[k][e] = fast_exp2(x[k][e] - mu[e]);
             };
             weigh();
             bool nd = false;
 #pragma unroll
-            for (int e = 0; e < NX; ++e) {
-                nd = nd || m_run[e] == -INFINITY;
-#pragma unroll
-                for (int b = 0; b < NB; ++b)
-                    nd = nd || fmaxf(pw[b][0][e] * sv[b][0], pw[b][1][e] * sv[b][1]) > kWeightMax;
-            }
+            for (int e = 0; e < NX; ++e)
+                nd = nd || m_run[e] == -INFINITY || fmaxf(pw[0][e] * sv[0], pw[1][e] * sv[1]) > kWeightMax;
             if (__any_sync(kFull, nd)) {
                 float al[NX];
 #pragma unroll
                 for (int e = 0; e < NX; ++e) {
-                    float mx = -INFINITY;
-#pragma unroll
-                    for (int b = 0; b < NB; ++b)
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) mx = fmaxf(mx, x[b][k][e] + fast_log2(sv[b][k]));
+                    float mx = fmaxf(x[0][e] + fast_log2(sv[0]), x[1][e] + fast_log2(sv[1]));
 #pragma unroll
                     for (int o = C == 1 ? 1 : C == 2 ? 2 : 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
                     const float mn = fmaxf(m_run[e], mx - kWeightExp);
@@ -1176,65 +1166,69 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
             }
             // ---- weights with their scales as binary16 parts: the high and low part of one
             // column (8 rows: the two columns' high parts, and their low ones) ----
-            uint32_t ph[NB][2][ZG], pl[NB][2][ZG];
+            uint32_t ph[2][ZG], pl[2][ZG];
 #pragma unroll
-            for (int b = 0; b < NB; ++b)
+            for (int k = 0; k < 2; ++k) {
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
+                for (int e = 0; e < NX; ++e) l_run[e] += pw[k][e];
 #pragma unroll
-                    for (int e = 0; e < NX; ++e) l_run[e] += pw[b][k][e];
+                for (int gr = 0; gr < ZG; ++gr) {
+                    float w[NX];
 #pragma unroll
-                    for (int gr = 0; gr < ZG; ++gr) {
-                        float w[NX];
-#pragma unroll
-                        for (int e = 0; e < NX; ++e) {
-                            w[e] = pw[b][k][e] * vsc[b][k][gr];
-                            zs[gr][e] = fmaf(w[e], vz[b][k][gr], zs[gr][e]);
-                        }
-                        if constexpr (L::kPaired) {
-                            ph[b][k][gr] = pack2_rz(w[0], w[0] - high_part(w[0]));
-                        } else {
-                            ph[b][k][gr] = pack2_rz(w[0], w[NX - 1]);
-                            pl[b][k][gr] = pack2_rz(w[0] - high_part(w[0]), w[NX - 1] - high_part(w[NX - 1]));
-                        }
+                    for (int e = 0; e < NX; ++e) {
+                        w[e] = pw[k][e] * vsc[k][gr];
+                        zs[gr][e] = fmaf(w[e], vz[k][gr], zs[gr][e]);
+                    }
+                    if constexpr (L::kPaired) {
+                        ph[k][gr] = pack2_rz(w[0], w[0] - high_part(w[0]));
+                    } else {
+                        ph[k][gr] = pack2_rz(w[0], w[NX - 1]);
+                        pl[k][gr] = pack2_rz(w[0] - high_part(w[0]), w[NX - 1] - high_part(w[NX - 1]));
                     }
                 }
+            }
             // ---- PV: the weights of tokens 2t, 2t + 1, 2t + 8, 2t + 9 for column g, from where they were made ----
             const uint32_t pick = (L::kPaired ? g < 4 : (g & 1) == 0) ? 0x5410u : 0x7632u;
 #pragma unroll
-            for (int hs = 0; hs < SUB; ++hs) {
-                if (!kWhole && hs > 0 && !second) continue;
-                const uint32_t va = sa + (st0 + hs) * stage_off + off_v;
+            for (int hs = 0; hs < NS; ++hs) {
 #pragma unroll
                 for (int gr = 0; gr < L::kGroups; ++gr) {
                     const int src = 8 * t + (C == 1   ? hs + 2 * gr
                                              : C == 2 ? (g & 1) + 2 * hs
                                              : C == 4 ? g & 3
                                                       : g >> 1);
-                    const int b = NB == 1 ? 0 : hs, gi = ZG == 1 ? 0 : gr;
-                    auto fragment = [&](const uint32_t(&p)[NB][2][ZG], uint32_t (&f)[2]) {
+                    auto fragment = [&](const uint32_t(&p)[2][ZG], uint32_t (&f)[2]) {
 #pragma unroll
                         for (int k = 0; k < 2; ++k)
-                            f[k] = __byte_perm(__shfl_sync(kFull, p[b][k][gi], src), __shfl_sync(kFull, p[b][k][gi], src + 4), pick);
+                            f[k] = __byte_perm(__shfl_sync(kFull, p[k][ZG == 1 ? 0 : gr], src),
+                                               __shfl_sync(kFull, p[k][ZG == 1 ? 0 : gr], src + 4), pick);
                     };
-                    uint32_t a[4], f[4], w[2], wl[2];
-                    ldsm_x4_trans(a, va ^ (gr << 5));
+                    uint32_t a[4], low[4], high[4], w[2], wl[2];
+                    ldsm_x4_trans(a, (stage + hs * stage_off + off_v) ^ (gr << 5));
                     fragment(ph, w);
                     if constexpr (!L::kPaired) fragment(pl, wl);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        codes4(f, a, i);
-                        mma_f16(acc[4 * gr + i], f, w);
-                        if constexpr (!L::kPaired) mma_f16(acc[4 * gr + i], f, wl);
+                    for (int i = 0; i < 4; i += 2) {
+                        codes4<true>(low, high, a, i > 0);
+                        mma_f16(acc[4 * gr + i], low, w);
+                        mma_f16(acc[4 * gr + i + 1], high, w);
+                        if constexpr (!L::kPaired) {
+                            mma_f16(acc[4 * gr + i], low, wl);
+                            mma_f16(acc[4 * gr + i + 1], high, wl);
+                        }
                     }
                 }
             }
         };
         auto consume = [&](auto whole_tag) {
-            if constexpr (L::k4)
-                attend4(whole_tag);
-            else
+            if constexpr (!L::k4) {
                 attend(whole_tag);
+            } else if constexpr (C <= 2) {
+                attend4(whole_tag, 0);
+            } else {
+#pragma unroll 1
+                for (int i = 0; i < SUB; ++i) attend4(whole_tag, i);
+            }
         };
         if (mine >= SUB * kStageTokens && m.bad == 0)
             consume(std::true_type{});
@@ -1247,11 +1241,14 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
 
         if (!(m.flags & kLast)) continue;
         // ---- item end ----
-        if constexpr (L::k4) {      // the codes' powers of two, taken off before the parts are added
+        if constexpr (L::k4) {      // sums over low codes and over bytes: their powers of two off, the bytes' low codes too
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+            for (int mt = 0; mt < MT; mt += 2)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[mt][e] *= mt & 1 ? 0x1p20f : 0x1p24f;
+                for (int e = 0; e < 4; ++e) {
+                    acc[mt + 1][e] = (acc[mt + 1][e] - acc[mt][e]) * 0x1p20f;
+                    acc[mt][e] *= 0x1p24f;
+                }
         }
         if constexpr (L::kPaired) {   // the low parts' columns (c + 4: lane t + 2) onto the high parts'
 #pragma unroll
@@ -1315,7 +1312,7 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                     if (lane == 0) report(p.err_flag, 0x10 /* PA_FLAG_TIMEOUT */);
                     return;
                 }
-                float *xs = reinterpret_cast<float *>(xbuf + (warp - H) * L::kStateBytes);
+                float *xs = reinterpret_cast<float *>(xbuf + (tw - H) * L::kStateBytes);
 #pragma unroll
                 for (int e = 0; e < NE; ++e) {
                     const int c = 2 * t + e;
@@ -1325,7 +1322,7 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                         xs[c * L::kStateRow + 16 * mt + g] = acc[mt][e];
                         xs[c * L::kStateRow + 16 * mt + 8 + g] = acc[mt][2 + e];
                     }
-                    if (g == 0) xml[warp * 8 + c] = make_float2(m_run[e], l_run[e]);
+                    if (g == 0) xml[tw * 8 + c] = make_float2(m_run[e], l_run[e]);
                 }
                 __syncwarp();
                 if (lane == 0) arrive(&xfull[head]);
@@ -1340,7 +1337,7 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                 const int c = 2 * t + e;
                 if (c >= C) continue;
                 float mn = m_run[e];
-                for (int k = 1; k < nsubs; ++k) mn = fmaxf(mn, xml[(warp + k * H) * 8 + c].x);
+                for (int k = 1; k < nsubs; ++k) mn = fmaxf(mn, xml[(tw + k * H) * 8 + c].x);
                 const float al = m_run[e] == -INFINITY ? 1.f : fast_exp2(m_run[e] - mn);
                 m_run[e] = mn;
                 l_run[e] *= al;
@@ -1350,9 +1347,9 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                     acc[mt][2 + e] *= al;
                 }
                 for (int k = 1; k < nsubs; ++k) {
-                    const float *xs = reinterpret_cast<const float *>(xbuf + (warp + (k - 1) * H) * L::kStateBytes) +
+                    const float *xs = reinterpret_cast<const float *>(xbuf + (tw + (k - 1) * H) * L::kStateBytes) +
                                       c * L::kStateRow + g;
-                    const float2 ml = xml[(warp + k * H) * 8 + c];
+                    const float2 ml = xml[(tw + k * H) * 8 + c];
                     const float be = ml.x == -INFINITY ? 1.f : fast_exp2(ml.x - mn);
                     l_run[e] = fmaf(ml.y, be, l_run[e]);
 #pragma unroll
@@ -1376,13 +1373,13 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
             const float sc = fin ? (l_run[e] == 0.f ? 0.f : 1.f / l_run[e]) : 1.f;
             const int64_t r =
                 (m.flags & kContinued)
-                    ? p.cut_row + cut_row_of(p, blockIdx.x, head, c)
+                    ? p.cut_row + cut_row_of(p, share, head, c)
                     : (((sq * Hkv + kvh) * p.max_parts + p.part_off + m.part) << lg) + hq;
             if (g == 0 && !(fin && p.ws_ml == nullptr)) {
                 const bool more = (m.flags & kCut) != 0;
                 st_global_hint(p.ws_ml + 4 * r,
                                make_float4(m_run[e], l_run[e], __int_as_float(fin ? kRowFinal : more ? kRowCut : 0),
-                                           __int_as_float(more ? cut_row_of(p, blockIdx.x + 1, head, c) : 0)),
+                                           __int_as_float(more ? cut_row_of(p, share + 1, head, c) : 0)),
                                keep);
             }
             const int64_t orow = fin ? (sq * Hq + (kvh << lg) + hq) * D : r * D;

@@ -172,10 +172,12 @@ SplitSmem smem_for(int cols, int log2_heads, int entries) {
     using L = SplitLayout<D, 1, CT>;
     const int H = 1 << log2_heads;
     SplitSmem s;
-    s.fixed = 1024 + static_cast<size_t>(kQueryRing) * cols * D * 2 * H +
-              static_cast<size_t>(L::kWarps - H) * cols * L::kStateBytes + L::kWarps * 8 * sizeof(float2) +
-              (2 * kQueryRing + 16) * 8 + 32 * 4 + static_cast<size_t>(entries) * 12 + 16;
-    s.slot = L::kSlotBytes + sizeof(SlotMeta) + 16;
+    s.fixed = 1024 +
+              L::kTeams * (static_cast<size_t>(kQueryRing) * cols * D * 2 * H +
+                           static_cast<size_t>(L::kWarps - H) * cols * L::kStateBytes + L::kWarps * 8 * sizeof(float2) +
+                           (2 * kQueryRing + 16) * 8) +
+              32 * 4 + static_cast<size_t>(entries) * 12 + 16;
+    s.slot = L::kTeams * (L::kSlotBytes + sizeof(SlotMeta) + 16);
     return s;
 }
 
