@@ -539,13 +539,20 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
             if (ntok > 0 && lane <= (t0 + ntok - 1) / bs - fb)
                 bid = __ldg(p.block_tables + static_cast<int64_t>(row) * p.max_blocks_per_seq + blk0 + fb + lane);
         };
+        // The slot's pieces are RB rows of one block (SW * per_stage of them, at most 32), one
+        // per lane.  Where a piece lies in a slot, and how far its token moves from slot to slot:
+        const int pieces = SW * per_stage;
+        const uint32_t box = static_cast<uint32_t>(RB * L::kRowB) << p.log2_heads;
+        const uint32_t piece_off = per_stage == 1 ? lane * (box * L::kHalves)
+                                                  : (lane >> 1) * (2 * box * L::kHalves) + (lane & 1) * box;
+        const int step_blocks = SW * kStageTokens / bs, step_rows = SW * kStageTokens % bs;
         int islot = 0;
-        uint32_t uses = 0, items = 0;
+        uint32_t uses = 0, items = 0, phase = 1;       // phase: of the wait for a slot, once the ring has been gone round
         bool ok = true;
         auto take_slot = [&]() -> int {
             const int slot = islot;
             if (uses >= static_cast<uint32_t>(S)) {
-                const uint32_t par = ((uses / S) - 1) & 1u;
+                const uint32_t par = phase;
                 if (!mbar_try_wait(&empty[slot], par) && !mbar_wait_bounded(&empty[slot], par)) {
                     if (lane == 0) report(p.err_flag, 0x10 /* PA_FLAG_TIMEOUT */);
                     ok = false;
@@ -553,7 +560,10 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
             }
             ok = __all_sync(kFull, ok);
             if (ok) {
-                islot = (islot + 1 == S) ? 0 : islot + 1;
+                if (++islot == S) {
+                    islot = 0;
+                    phase ^= 1u;
+                }
                 ++uses;
             }
             return slot;
@@ -589,16 +599,22 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                              : je < ic.nslots     ? kCut
                              : final_mode(mode) && ic.nparts == 1 ? kFinal
                                                                   : 0;
+            // my piece's block (of the partition's) and its first row in it
+            const int first = jb * SW * kStageTokens + (t0 - fb * bs) + lane * RB;
+            int pblk = first / bs, prow = first - pblk * bs;
             for (int j = jb; j < je; ++j) {
                 const int slot = take_slot();
                 if (!ok) break;
                 uint8_t *sp = slots + static_cast<size_t>(slot) * L::kSlotBytes;
-                const int tok0 = t0 + j * SW * kStageTokens;                 // the slot's first position
-                const int nt = max(0, min(SW * kStageTokens, t0 + ntok - tok0));
-                // The slot's pieces are RB rows of one block (SW * per_stage of them, at most 32), one per lane.
-                const int ptok = tok0 + lane * RB;
-                const bool has = lane < SW * per_stage && lane * RB < nt;
-                const int id = __shfl_sync(kFull, bid, has ? ptok / bs - fb : 0);
+                const int nt = max(0, min(SW * kStageTokens, ntok - j * SW * kStageTokens));   // valid tokens
+                const bool has = lane < pieces && lane * RB < nt;
+                const int id = __shfl_sync(kFull, bid, has ? pblk : 0);
+                const int row = prow;
+                pblk += step_blocks;
+                if ((prow += step_rows) >= bs) {
+                    prow -= bs;
+                    ++pblk;
+                }
                 const bool load = has && id >= 0 && static_cast<int64_t>(id) < p.num_blocks;
                 const uint32_t loaded = __ballot_sync(kFull, load);
                 uint32_t bad = __ballot_sync(kFull, has && !load);
@@ -608,7 +624,6 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                     for (int i = 0; i < SW; ++i) w |= ((bad >> i) & 1u) * (3u << (2 * i));
                     bad = w;
                 }
-                const uint32_t box = static_cast<uint32_t>(RB * L::kRowB) << p.log2_heads;
                 if (lane == 0) {
                     SlotMeta mt;
                     mt.seq = seq;
@@ -623,10 +638,9 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                                           static_cast<uint32_t>(__popc(loaded)) * 2u * (box * L::kHalves + (lane_copies ? 0u : sbox)));
                 }
                 __syncwarp();
-                const int z = load ? id * bs + ptok % bs : 0;               // the piece's first cache slot
+                const int z = load ? id * bs + row : 0;                     // the piece's first cache slot
                 if (load) {
-                    const int st = lane / per_stage, b = lane % per_stage;
-                    uint8_t *dst = sp + ((static_cast<size_t>(st) * kStageTokens * L::kRow) << p.log2_heads) + b * box;
+                    uint8_t *dst = sp + piece_off;
 #pragma unroll
                     for (int h = 0; h < L::kHalves; ++h) {
                         const uint32_t ho = h * per_stage * box;
@@ -639,7 +653,7 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                     // scales, [piece][head of the box][token][group], K then V
                     uint8_t *ss = sp + 2 * L::kKVBytes + lane * sbox;
                     if (load) {
-                        const int y = id * Hkv + kvh0, x = ptok % bs * L::kGroups;
+                        const int y = id * Hkv + kvh0, x = row * L::kGroups;
                         if (scale_boxes) {
                             tma_load_2d(ss, &tmap_ks, &full[slot], x, y);
                             tma_load_2d(ss + L::kScaleBytes, &tmap_vs, &full[slot], x, y);
@@ -1401,14 +1415,32 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                     static_cast<uint16_t *>(p.out)[orow + d] = p.out_dtype == 1 ? float_to_bf16_bits(a) : float_to_f16_bits(a);
             };
             if constexpr (L::k4) {
+                // four neighbouring elements at a time: the two halves of each group
+                constexpr int kQuads = 2 * L::kGroups;
+                auto quad = [&](int i) {
+                    const int mt = 4 * (i >> 1), r = 2 * (i & 1) + e;
+                    return make_float4(acc[mt][r] * sc, acc[mt + 1][r] * sc, acc[mt + 2][r] * sc, acc[mt + 3][r] * sc);
+                };
+                const int64_t at = orow + 4 * g;
+                if (!fin || p.out_dtype == 2) {
+                    float *o = (fin ? static_cast<float *>(p.out) : p.ws_acc) + at;
 #pragma unroll
-                for (int gr = 0; gr < L::kGroups; ++gr)
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        const int d = 64 * gr + 32 * r + 4 * g, i = 2 * r + e;
-                        put2(d, acc[4 * gr][i] * sc, acc[4 * gr + 1][i] * sc);
-                        put2(d + 2, acc[4 * gr + 2][i] * sc, acc[4 * gr + 3][i] * sc);
+                    for (int i = 0; i < kQuads; ++i) {
+                        if (fin)
+                            *reinterpret_cast<float4 *>(o + 32 * i) = quad(i);
+                        else
+                            st_global_hint(o + 32 * i, quad(i), keep);
                     }
+                } else {
+                    uint16_t *o = static_cast<uint16_t *>(p.out) + at;
+#pragma unroll
+                    for (int i = 0; i < kQuads; ++i) {
+                        const float4 v = quad(i);
+                        *reinterpret_cast<uint2 *>(o + 32 * i) =
+                            p.out_dtype == 1 ? make_uint2(pack2<true>(v.x, v.y), pack2<true>(v.z, v.w))
+                                             : make_uint2(pack2<false>(v.x, v.y), pack2<false>(v.z, v.w));
+                    }
+                }
             } else if constexpr (k8) {
 #pragma unroll
                 for (int vc = 0; vc < D / 32; ++vc) {
