@@ -83,7 +83,7 @@ typedef enum {
     PA_ERR_DEVICE_BOUNDS = 5   /* returned by pa_check_err_flag for a non-zero flag */
 } pa_status;
 
-typedef enum { PA_F16 = 0, PA_BF16 = 1, PA_F32 = 2, PA_FP8_E4M3 = 3, PA_INT8 = 4 } pa_dtype;
+typedef enum { PA_F16 = 0, PA_BF16 = 1, PA_F32 = 2, PA_FP8_E4M3 = 3, PA_INT8 = 4, PA_INT4 = 5 } pa_dtype;
 
 /* Bits OR-ed into *err_flag by the kernels. */
 #define PA_FLAG_BAD_SLOT        0x1   /* slot_mapping entry >= num_blocks * block_size */
@@ -91,6 +91,7 @@ typedef enum { PA_F16 = 0, PA_BF16 = 1, PA_F32 = 2, PA_FP8_E4M3 = 3, PA_INT8 = 4
 #define PA_FLAG_BAD_CONTEXT_LEN 0x4   /* context length < 0 or beyond the table/bound */
 #define PA_FLAG_BAD_COPY_PAIR   0x8   /* copy pair id outside [0, num_blocks) */
 #define PA_FLAG_TIMEOUT         0x10  /* a bounded wait on an async copy gave up */
+#define PA_FLAG_NO_BLOCKS       0x20  /* too few free blocks, or a free list out of range */
 
 /*
  * pa_reshape_and_cache -- write this step's new K/V rows into their slots.
@@ -527,7 +528,7 @@ pa_status pa_quant_decode(void *out, pa_dtype out_dtype, const void *query, pa_d
  *     s = bf16(max((max x / 2 - min x / 2) / 7.5, max |x| / 2^8, 2^-60)),
  *     z = bf16(min x / s),   u_i = round(x_i * (1 / s) - z), at least 0, at most 15
  * so an element is off by about half of s, a fifteenth of the group's range (or,
- * where a group's values lie far from zero, 2^-8 of the largest).  A group that holds
+ * where a group's values lie far from zero, up to 1.5 * 2^-8 of the largest).  A group that holds
  * an infinity or NaN gets the scale NaN and codes 0: its elements read back as NaN,
  * and attention over it gives NaN (a V group: in the elements of that group alone).
  *   Arguments and rules of pa_quant_reshape_and_cache.
@@ -562,6 +563,83 @@ pa_status pa_int4_decode(void *out, pa_dtype out_dtype, const void *query, pa_dt
                          int max_blocks_per_seq, const int32_t *context_lens, int max_context_len, int num_seqs,
                          int num_heads, int num_kv_heads, int head_dim, int block_size, int64_t num_blocks, float scale,
                          int partition_size, void *workspace, size_t workspace_bytes, int *err_flag, void *stream);
+
+/*
+ * ------------------------------------------------------------------------
+ * A step's bookkeeping and its rotation
+ * ------------------------------------------------------------------------
+ * pa_update_tables -- block tables, lengths, slot map and positions of a step, from
+ * how many tokens each sequence gains or loses (on the GPU, so that a captured step
+ * needs nothing from the host but the changes).
+ *
+ * Sequence s (a row of block_tables) grows by changes[s] tokens, or for a negative
+ * change drops its newest ones (drafted tokens taken back; -context_lens[s] or less: it
+ * ends).  Blocks it no longer reaches go onto the stack of free blocks, blocks it newly
+ * reaches (Page A §3.1, §3.2: ceil(tokens / block_size) in all) come off it:
+ *   - numbering all blocks that are given back by sequence, then place, from 0 to R - 1,
+ *     number j is put in free_blocks[free_count + R - 1 - j];
+ *   - numbering all blocks that are taken the same way, number k is
+ *     free_blocks[free_count + R - 1 - k]; the new count is free_count + R - (taken).
+ * So a step and one that undoes it leave the stack as it was, and nothing depends on
+ * timing.  Blocks must belong to one sequence only (shared ones are not to be dropped).
+ *
+ *   block_tables  : [num_seqs, max_blocks_per_seq] int32; entries past a sequence's
+ *                   length are left as they were
+ *   context_lens, changes : [num_seqs] int32;  out_lens : [num_seqs] int32, the new
+ *                   lengths (may be context_lens)
+ *   free_blocks   : [free_capacity] int32;  free_count : int32 on the device, how many of
+ *                   them there are, the next to take last;  out_free_count : the new
+ *                   count (may be free_count)
+ *   cu_seqlens    : [num_seqs + 1] int32, sums of the tokens gained before each sequence
+ *   slot_mapping, positions : [num_tokens] int64: of the gained tokens in order of
+ *                   sequence and position, then -1 (a padding slot) and 0
+ * All or nothing: a length that is negative or does not fit max_blocks_per_seq, more
+ * gained tokens than num_tokens (PA_FLAG_BAD_CONTEXT_LEN), too few free blocks or a
+ * count out of range (PA_FLAG_NO_BLOCKS) leave tables, stack and lengths as they were,
+ * with out_lens and out_free_count copied, cu_seqlens 0 and no slots.  A block id outside
+ * [0, num_blocks) in a table or on the stack sets PA_FLAG_BAD_BLOCK_ID; its tokens get
+ * the slot -1.  num_seqs <= 8192, max_blocks_per_seq * block_size and num_tokens <= 2^30.
+ */
+pa_status pa_update_tables(int32_t *block_tables, int max_blocks_per_seq, const int32_t *context_lens,
+                           const int32_t *changes, int32_t *out_lens, int num_seqs, int32_t *free_blocks,
+                           int64_t free_capacity, const int32_t *free_count, int32_t *out_free_count, int64_t num_blocks,
+                           int block_size, int32_t *cu_seqlens, int64_t *slot_mapping, int64_t *positions,
+                           int64_t num_tokens, int *err_flag, void *stream);
+
+/*
+ * pa_rope_and_cache -- queries and keys normalised per head and turned to their
+ * positions, keys and values written into the cache, in one pass.
+ *
+ * For a query or key row x (one token, one head), in fp32 and rounded once at the end:
+ *     x <- x * w / sqrt(mean(x^2) + eps)             where q_weight (k_weight) is given
+ *     (a, b) <- factor * (a cos - b sin, b cos + a sin)   for pair i of the first rot_dim
+ * elements, with the angle positions[t] * inv_freq[i]; a pair is the elements
+ * (i, i + rot_dim / 2), or (2 i, 2 i + 1) if interleaved.  Angles are exact to a few
+ * 2^-24 at any position.  Query rows go to out_q; key rows and (unchanged) value rows to
+ * cache slots as by the write of the cache's own kind:
+ *     cache_dtype = dtype          pa_reshape_and_cache
+ *     PA_FP8_E4M3, scales NULL     pa_reshape_and_cache with k_scale, v_scale (> 0)
+ *     PA_FP8_E4M3 or PA_INT8       pa_quant_reshape_and_cache
+ *     PA_INT4                      pa_int4_reshape_and_cache
+ * (codes are made of the fp32 values, without a rounding to dtype before).
+ *
+ *   out_q        : [num_tokens, num_heads, head_dim], dtype; may be query where that is dense
+ *   query, key, value : dtype (F16 or BF16), rows of one token dense, tokens q_stride,
+ *                  key_stride, value_stride elements apart (multiples of 8)
+ *   slot_mapping : [num_tokens] int64, as for pa_reshape_and_cache (a padding token's
+ *                  query row is turned all the same)
+ *   positions    : [num_tokens] int64, any
+ *   inv_freq     : [rot_dim / 2] double, the angles per position in radians, finite, below
+ *                  2^20 in magnitude;  rot_dim : a multiple of 8, up to head_dim
+ *   q_weight, k_weight : [head_dim] of dtype, or NULL for no norm;  eps >= 0
+ */
+pa_status pa_rope_and_cache(void *out_q, const void *query, const void *key, const void *value, int64_t q_stride,
+                            int64_t key_stride, int64_t value_stride, void *k_cache, void *v_cache,
+                            pa_dtype cache_dtype, void *k_scales, void *v_scales, float k_scale, float v_scale,
+                            const int64_t *slot_mapping, const int64_t *positions, const double *inv_freq, int rot_dim,
+                            int interleaved, float factor, const void *q_weight, const void *k_weight, float eps,
+                            int64_t num_tokens, int num_heads, int num_kv_heads, int head_dim, pa_dtype dtype,
+                            int64_t num_blocks, int block_size, int *err_flag, void *stream);
 
 /*
  * pa_decode_shared -- pa_decode for a batch whose sequences share long

@@ -14,6 +14,8 @@ PyTorch fallback - a missing library raises.
     quant_gather(out_k, out_v, k_cache, v_cache, k_scales, v_scales, block_tables, cu_seqlens, ...)
     quant_decode(out, query, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, scale, ...)
     int4_reshape_and_cache, int4_gather, int4_decode: the same over caches of 4-bit codes
+    update_tables(block_tables, context_lens, changes, free_blocks, free_count, slot_mapping, positions, cu_seqlens, ...)
+    rope_and_cache(out_q, query, key, value, k_cache, v_cache, slot_mapping, positions, inv_freq, ...)
 
 Cache layout: ``[num_blocks, block_size, num_kv_heads, head_dim]`` per layer
 for K and for V ("LLM推理优化：vLLM PagedAttention深度解析与工程实践", §4.1).
@@ -30,15 +32,18 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 import threading
 
 from . import _lib
 from ._lib import (FLAG_BAD_BLOCK_ID, FLAG_BAD_CONTEXT_LEN, FLAG_BAD_COPY_PAIR, FLAG_BAD_SLOT,
-                   FLAG_TIMEOUT, PA_BF16, PA_F16, PA_F32, PA_FP8_E4M3, PA_INT8, PagedAttentionError)
+                   FLAG_NO_BLOCKS, FLAG_TIMEOUT, PA_BF16, PA_F16, PA_F32, PA_FP8_E4M3, PA_INT4, PA_INT8,
+                   PagedAttentionError)
 
 __all__ = ["reshape_and_cache", "decode", "decode_append", "prefill", "copy_blocks", "copy_blocks_layers", "swap_blocks", "decode_workspace_size",
            "decode_partition_size", "DecodeWorkspace", "new_err_flag", "read_err_flag",
            "quant_reshape_and_cache", "quant_gather", "quant_decode", "quant_decode_workspace_size", "decode_shared",
+           "update_tables", "rope_and_cache", "rope_frequencies", "FLAG_NO_BLOCKS",
            "int4_reshape_and_cache", "int4_gather", "int4_decode", "int4_decode_workspace_size",
            "decode_shared_workspace_size", "PagedAttentionError", "FLAG_BAD_SLOT", "FLAG_BAD_BLOCK_ID", "FLAG_BAD_CONTEXT_LEN",
            "FLAG_BAD_COPY_PAIR", "FLAG_TIMEOUT", "library_path", "StepGraph"]
@@ -357,7 +362,7 @@ class _Runtime:
         self.half = _Codes({torch.float16: PA_F16, torch.bfloat16: PA_BF16})
         self.out = _Codes({**self.half, torch.float32: PA_F32})
         self.codes = _Codes({torch.int8: PA_INT8, torch.uint8: PA_FP8_E4M3, torch.float8_e4m3fn: PA_FP8_E4M3})
-        self.b16 = torch.bfloat16
+        self.b16, self.f64 = torch.bfloat16, torch.float64
         self.f32, self.i32, self.i64, self.u8 = torch.float32, torch.int32, torch.int64, torch.uint8
         self.current_device = torch.cuda.current_device
         self.capturing = torch.cuda.is_current_stream_capturing
@@ -687,6 +692,174 @@ def int4_decode(out, query, k_cache, v_cache, k_scales, v_scales, block_tables, 
         None if err_flag is None else _flag(err_flag, dev), stream)
     if st:
         _lib.check(st, "pa_int4_decode")
+
+
+# ------------------------------------- a step's bookkeeping and its rotation
+
+def update_tables(block_tables, context_lens, changes, free_blocks, free_count, slot_mapping, positions, cu_seqlens,
+                  block_size: int, num_blocks: int | None = None, out_lens=None, out_free_count=None, err_flag=None) -> None:
+    """Bring a batch's block tables and lengths up to date on the GPU.
+
+    Sequence s grows by ``changes[s]`` tokens (int32 [B]) or, for a negative change,
+    drops its newest ones (all of them: it ends); its blocks come from and go back to
+    the stack ``free_blocks`` (int32 [capacity], the first ``free_count`` (int32 [1]) of
+    them free, the last of those taken next).  ``block_tables`` (int32 [B, maxNB]),
+    ``context_lens`` (int32 [B]) and ``free_count`` are updated in place, or the latter
+    two into ``out_lens`` and ``out_free_count``; entries past a sequence's length are
+    left as they were.  Written too: ``slot_mapping`` and ``positions`` (int64 [T], T at
+    least the tokens gained) of the gained tokens, then -1 and 0, and ``cu_seqlens``
+    (int32 [B+1]), where each sequence's begin.  Where something does not fit, nothing
+    changes and the error flag says what (``include/pa.h`` has the order of blocks).
+    ``num_blocks`` (default: the capacity) bounds the block ids."""
+    rt = _rt or _runtime()
+    dev, table = block_tables.get_device(), block_tables.shape
+    if out_lens is None:
+        out_lens = context_lens
+    if out_free_count is None:
+        out_free_count = free_count
+    for t in (block_tables, context_lens, changes, free_blocks, free_count, slot_mapping, positions, cu_seqlens, out_lens,
+              out_free_count):
+        if t.get_device() != dev or not t.is_contiguous() or dev != rt.current_device():
+            _refuse((("block_tables", block_tables), ("context_lens", context_lens), ("changes", changes),
+                     ("free_blocks", free_blocks), ("free_count", free_count), ("slot_mapping", slot_mapping),
+                     ("positions", positions), ("cu_seqlens", cu_seqlens), ("out_lens", out_lens),
+                     ("out_free_count", out_free_count)))
+    if len(table) != 2 or block_tables.dtype != rt.i32:
+        raise ValueError("block_tables must be int32 [B, maxNB]")
+    B = table[0]
+    if (context_lens.dtype != rt.i32 or context_lens.numel() != B or changes.dtype != rt.i32 or changes.numel() != B or
+            out_lens.dtype != rt.i32 or out_lens.numel() != B):
+        raise ValueError("context_lens, changes and out_lens must be int32 [B]")
+    if cu_seqlens.dtype != rt.i32 or cu_seqlens.numel() != B + 1:
+        raise ValueError("cu_seqlens must be int32 [B+1]")
+    if (free_blocks.dtype != rt.i32 or free_count.dtype != rt.i32 or free_count.numel() != 1 or
+            out_free_count.dtype != rt.i32 or out_free_count.numel() != 1):
+        raise ValueError("free_blocks must be int32 [capacity], free_count and out_free_count int32 [1]")
+    if slot_mapping.dtype != rt.i64 or positions.dtype != rt.i64 or positions.numel() != slot_mapping.numel():
+        raise ValueError("slot_mapping and positions must be int64 [T]")
+    capacity = free_blocks.numel()
+    st = rt.lib.pa_update_tables(
+        block_tables.data_ptr(), table[1], context_lens.data_ptr(), changes.data_ptr(), out_lens.data_ptr(), B,
+        free_blocks.data_ptr(), capacity, free_count.data_ptr(), out_free_count.data_ptr(),
+        max(1, capacity) if num_blocks is None else num_blocks, block_size, cu_seqlens.data_ptr(), slot_mapping.data_ptr(),
+        positions.data_ptr(), slot_mapping.numel(), None if err_flag is None else _flag(err_flag, dev), rt.stream(dev))
+    if st:
+        _lib.check(st, "pa_update_tables")
+
+
+def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str | None = None, scale: float = 1.0,
+                     original_len: int = 4096, fast_turns: float = 32.0, slow_turns: float = 1.0, device=None):
+    """(``inv_freq``, ``factor``) for :func:`rope_and_cache`: the angles per position,
+    f_i = base^(-2i / rot_dim) (float64 [rot_dim / 2] on the GPU), and the factor on
+    turned pairs, for a context ``scale`` times longer than the ``original_len`` positions
+    a model was trained on:
+
+    None      f_i as they are
+    "linear"  f_i / scale: positions pressed together
+    "base"    f_i of the base grown by scale^(rot_dim / (rot_dim - 2)): the slowest pair
+              is slowed by scale, the fastest not at all
+    "parts"   pairs that turn at least ``fast_turns`` times in original_len positions as
+              they are, those that turn at most ``slow_turns`` times slowed by scale, the
+              others in between; factor 0.1 ln(scale) + 1"""
+    torch = _torch()
+    _need(rot_dim >= 8 and rot_dim % 8 == 0, "rot_dim must be a multiple of 8")
+    _need(base > 1.0 and scale >= 1.0 and math.isfinite(base) and math.isfinite(scale),
+          "base must be above 1 and scale at least 1")
+    n, factor = rot_dim // 2, 1.0
+    if scaling == "base":
+        base = base * scale ** (rot_dim / (rot_dim - 2))
+    freq = [base ** (-i / n) for i in range(n)]
+    if scaling == "linear":
+        freq = [f / scale for f in freq]
+    elif scaling == "parts":
+        _need(fast_turns > slow_turns, "fast_turns must be above slow_turns")
+        for i, f in enumerate(freq):
+            turns = original_len * f / (2 * math.pi)
+            keep = min(1.0, max(0.0, (turns - slow_turns) / (fast_turns - slow_turns)))
+            freq[i] = f * keep + f / scale * (1.0 - keep)
+        factor = 0.1 * math.log(scale) + 1.0
+    elif scaling not in (None, "base"):
+        raise ValueError('scaling must be None, "linear", "base" or "parts"')
+    return torch.tensor(freq, dtype=torch.float64, device=device or "cuda"), factor
+
+
+def rope_and_cache(out_q, query, key, value, k_cache, v_cache, slot_mapping, positions, inv_freq, *, interleaved: bool = False,
+                   factor: float = 1.0, q_weight=None, k_weight=None, eps: float = 1e-6, k_scales=None, v_scales=None,
+                   k_scale: float = 1.0, v_scale: float = 1.0, err_flag=None) -> None:
+    """Turn queries [T, Hq, D] into ``out_q`` (which may be ``query``) and keys
+    [T, Hkv, D] into the cache, values beside them, in one pass; with ``q_weight`` /
+    ``k_weight`` [D] the rows are RMS-normalised per head first.
+
+    Pair i of the first ``2 * inv_freq.numel()`` elements of a row is turned by
+    ``positions[t] * inv_freq[i]`` (``inv_freq`` float64 on the GPU, from
+    :func:`rope_frequencies`) and multiplied by ``factor``; a pair is the elements
+    (i, i + F), or (2i, 2i + 1) if ``interleaved``.  The caches are those of
+    :func:`reshape_and_cache` (16-bit, or e4m3 with ``k_scale`` / ``v_scale``), of
+    :func:`quant_reshape_and_cache` (with ``k_scales`` / ``v_scales``) or of
+    :func:`int4_reshape_and_cache`, told apart by dtype and shape.  query, key and value may be
+    slices of one projection's output."""
+    rt = _rt or _runtime()
+    dev, shape, kshape, cache = query.get_device(), query.shape, key.shape, k_cache.shape
+    if (dev != rt.current_device() or out_q.get_device() != dev or key.get_device() != dev or value.get_device() != dev or
+            k_cache.get_device() != dev or v_cache.get_device() != dev or slot_mapping.get_device() != dev or
+            positions.get_device() != dev or inv_freq.get_device() != dev or not out_q.is_contiguous() or
+            not k_cache.is_contiguous() or not v_cache.is_contiguous() or not slot_mapping.is_contiguous() or
+            not positions.is_contiguous() or not inv_freq.is_contiguous()):
+        _refuse((("out_q", out_q), ("k_cache", k_cache), ("v_cache", v_cache), ("slot_mapping", slot_mapping),
+                 ("positions", positions), ("inv_freq", inv_freq)), "query, key and value must be on the device of the caches")
+    if len(shape) != 3 or out_q.shape != shape or out_q.dtype != query.dtype:
+        raise ValueError("query/out_q must be [T, Hq, D] of one dtype")
+    T, hq, d = shape
+    if (len(kshape) != 3 or value.shape != kshape or kshape[0] != T or kshape[2] != d or key.dtype != query.dtype or
+            value.dtype != query.dtype):
+        raise ValueError("key/value must be [T, Hkv, D] of the query's dtype")
+    hkv = kshape[1]
+    if len(cache) != 4 or v_cache.shape != cache or v_cache.dtype != k_cache.dtype or cache[2] != hkv:
+        raise ValueError("caches must be [NB, bs, Hkv, ...] of one dtype, with the rows' heads")
+    nb, bs = cache[0], cache[1]
+    if (k_scales is None) != (v_scales is None):
+        raise ValueError("k_scales and v_scales go together")
+    four = k_scales is not None and k_scales.dtype == rt.b16
+    if four:
+        _int4_cache(rt, k_cache, v_cache, k_scales, v_scales, d)
+        code = PA_INT4
+    elif cache[3] != d:
+        raise ValueError("caches must be [NB, bs, Hkv, D]")
+    elif k_scales is not None:
+        rows = (nb, bs, hkv)
+        if k_scales.shape != rows or v_scales.shape != rows or k_scales.dtype != rt.f32 or v_scales.dtype != rt.f32:
+            raise ValueError("scales must be float32 [NB, bs, Hkv] (or bfloat16 for 4-bit codes)")
+        code = rt.codes[k_cache.dtype]
+    elif k_cache.dtype == query.dtype:
+        code = rt.half[k_cache.dtype]
+    elif rt.codes.get(k_cache.dtype) == PA_FP8_E4M3:
+        code = PA_FP8_E4M3
+    else:
+        raise TypeError("caches must have the query's dtype, or be e4m3 codes, or come with scales")
+    if k_scales is not None and (k_scales.get_device() != dev or v_scales.get_device() != dev or
+                                 not k_scales.is_contiguous() or not v_scales.is_contiguous()):
+        _refuse((("k_scales", k_scales), ("v_scales", v_scales)))
+    if slot_mapping.dtype != rt.i64 or slot_mapping.numel() != T or positions.dtype != rt.i64 or positions.numel() != T:
+        raise ValueError("slot_mapping and positions must be int64 [T]")
+    if inv_freq.dtype != rt.f64:
+        raise ValueError("inv_freq must be float64 [rot_dim / 2]")
+    for w in (q_weight, k_weight):
+        if w is not None and (w.dtype != query.dtype or w.numel() != d or w.get_device() != dev or not w.is_contiguous()):
+            raise ValueError("q_weight/k_weight must be [D] of the query's dtype, on its device")
+    qs, ks, vs = query.stride(), key.stride(), value.stride()
+    if (qs[2] != 1 or ks[2] != 1 or vs[2] != 1 or (hq != 1 and qs[1] != d) or
+            (hkv != 1 and (ks[1] != d or vs[1] != d))):
+        raise ValueError("query/key/value: the rows of one token must be dense")
+    one = T <= 1
+    st = rt.lib.pa_rope_and_cache(
+        out_q.data_ptr(), query.data_ptr(), key.data_ptr(), value.data_ptr(), hq * d if one else qs[0],
+        hkv * d if one else ks[0], hkv * d if one else vs[0], k_cache.data_ptr(), v_cache.data_ptr(), code,
+        None if k_scales is None else k_scales.data_ptr(), None if v_scales is None else v_scales.data_ptr(), k_scale,
+        v_scale, slot_mapping.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(), 2 * inv_freq.numel(), interleaved,
+        factor, None if q_weight is None else q_weight.data_ptr(), None if k_weight is None else k_weight.data_ptr(), eps,
+        T, hq, hkv, d, rt.half[query.dtype], nb, bs, None if err_flag is None else _flag(err_flag, dev), rt.stream(dev))
+    if st:
+        _lib.check(st, "pa_rope_and_cache")
 
 
 @functools.lru_cache(maxsize=1024)

@@ -11,13 +11,14 @@ import os
 from . import _build
 
 PA_OK, PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED, PA_ERR_CUDA, PA_ERR_WORKSPACE, PA_ERR_DEVICE_BOUNDS = range(6)
-PA_F16, PA_BF16, PA_F32, PA_FP8_E4M3, PA_INT8 = 0, 1, 2, 3, 4
+PA_F16, PA_BF16, PA_F32, PA_FP8_E4M3, PA_INT8, PA_INT4 = 0, 1, 2, 3, 4, 5
 
 FLAG_BAD_SLOT = 0x1
 FLAG_BAD_BLOCK_ID = 0x2
 FLAG_BAD_CONTEXT_LEN = 0x4
 FLAG_BAD_COPY_PAIR = 0x8
 FLAG_TIMEOUT = 0x10
+FLAG_NO_BLOCKS = 0x20
 
 # Every symbol include/pa.h declares, with (restype, argtypes).
 _P, _I, _I64, _SZ, _F = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
@@ -45,6 +46,9 @@ SIGNATURES = {
     "pa_int4_decode_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I, _I]),
     "pa_int4_decode": (_I, [_P, _I, _P, _I, _P, _P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _I64, _F, _I, _P, _SZ,
                             _P, _P]),
+    "pa_update_tables": (_I, [_P, _I, _P, _P, _P, _I, _P, _I64, _P, _P, _I64, _I, _P, _P, _P, _I64, _P, _P]),
+    "pa_rope_and_cache": (_I, [_P, _P, _P, _P, _I64, _I64, _I64, _P, _P, _I, _P, _P, _F, _F, _P, _P, _P, _I, _I, _F, _P, _P,
+                               _F, _I64, _I, _I, _I, _I, _I64, _I, _P, _P]),
     "pa_decode_shared_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I, _I, _I, _I, _I]),
     "pa_decode_shared": (_I, [_P, _I, _P, _P, _P, _I, _P, _I, _P, _I, _P, _I, _I, _P, _I, _I, _I, _I, _I, _I, _I64, _F,
                               _I, _P, _SZ, _P, _P]),

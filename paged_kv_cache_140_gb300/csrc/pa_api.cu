@@ -10,6 +10,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <initializer_list>
 #include <mutex>
 #include <numeric>
 
@@ -20,6 +21,7 @@
 #include "pa_shared_prefix.h"
 #include "pa_split.h"
 #include "pa_split_plan.h"
+#include "pa_step_ops.h"
 
 #define PA_EXPORT extern "C" __attribute__((visibility("default")))
 
@@ -1145,6 +1147,106 @@ PA_EXPORT pa_status pa_int4_decode(void *out, pa_dtype out_dtype, const void *qu
                         static_cast<const float *>(k_scales), static_cast<const float *>(v_scales), block_tables,
                         max_blocks_per_seq, context_lens, max_context_len, num_seqs, num_heads, num_kv_heads, head_dim,
                         block_size, num_blocks, scale, partition_size, workspace, workspace_bytes, err_flag, stream);
+}
+
+PA_EXPORT pa_status pa_update_tables(int32_t *block_tables, int max_blocks_per_seq, const int32_t *context_lens,
+                                     const int32_t *changes, int32_t *out_lens, int num_seqs, int32_t *free_blocks,
+                                     int64_t free_capacity, const int32_t *free_count, int32_t *out_free_count,
+                                     int64_t num_blocks, int block_size, int32_t *cu_seqlens, int64_t *slot_mapping,
+                                     int64_t *positions, int64_t num_tokens, int *err_flag, void *stream) {
+    if (num_seqs < 0 || max_blocks_per_seq <= 0 || free_capacity < 0 || num_blocks <= 0 || block_size <= 0 || num_tokens < 0)
+        return PA_ERR_INVALID_ARG;
+    if (num_seqs > pa::kTablesMaxSeqs || static_cast<int64_t>(max_blocks_per_seq) * block_size > (1 << 30) ||
+        num_tokens > (1 << 30) || free_capacity > INT32_MAX || num_blocks > INT32_MAX)
+        return PA_ERR_UNSUPPORTED;
+    if (!cu_seqlens || !free_count || !out_free_count) return PA_ERR_INVALID_ARG;
+    if (num_seqs > 0 && (!block_tables || !context_lens || !changes || !out_lens)) return PA_ERR_INVALID_ARG;
+    if ((num_tokens > 0 && (!slot_mapping || !positions)) || (free_capacity > 0 && !free_blocks)) return PA_ERR_INVALID_ARG;
+    const pa::TablesParams p{block_tables, max_blocks_per_seq, context_lens,   changes,    out_lens,
+                             num_seqs,     free_blocks,        free_capacity,  free_count, out_free_count,
+                             num_blocks,   block_size,         cu_seqlens,     slot_mapping, positions,
+                             num_tokens,   err_flag};
+    return pa::launch_update_tables(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+PA_EXPORT pa_status pa_rope_and_cache(void *out_q, const void *query, const void *key, const void *value, int64_t q_stride,
+                                      int64_t key_stride, int64_t value_stride, void *k_cache, void *v_cache,
+                                      pa_dtype cache_dtype, void *k_scales, void *v_scales, float k_scale, float v_scale,
+                                      const int64_t *slot_mapping, const int64_t *positions, const double *inv_freq,
+                                      int rot_dim, int interleaved, float factor, const void *q_weight,
+                                      const void *k_weight, float eps, int64_t num_tokens, int num_heads,
+                                      int num_kv_heads, int head_dim, pa_dtype dtype, int64_t num_blocks, int block_size,
+                                      int *err_flag, void *stream) {
+    if (num_tokens < 0 || num_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || num_blocks <= 0 || block_size <= 0 ||
+        !half_dtype(dtype))
+        return PA_ERR_INVALID_ARG;
+    if (!supported_head_dim(head_dim) || num_heads > (1 << 20) || num_kv_heads > (1 << 20) || num_tokens > INT32_MAX)
+        return PA_ERR_UNSUPPORTED;
+    if (rot_dim <= 0 || rot_dim > head_dim || rot_dim % 8 != 0) return PA_ERR_INVALID_ARG;
+    if (!(eps >= 0.f) || !(factor == factor)) return PA_ERR_INVALID_ARG;
+    // what the cache holds
+    int kind;
+    const bool scales = k_scales != nullptr && v_scales != nullptr;
+    if (cache_dtype == dtype) {
+        kind = pa::kRopeHalf;
+    } else if (cache_dtype == PA_FP8_E4M3 && !k_scales && !v_scales) {
+        if (!scale_ok(k_scale) || !scale_ok(v_scale)) return PA_ERR_INVALID_ARG;
+        kind = pa::kRopeE4M3;
+    } else if (quant_dtype(cache_dtype) || cache_dtype == PA_INT4) {
+        if (num_tokens > 0 && !scales) return PA_ERR_INVALID_ARG;
+        kind = cache_dtype == PA_INT4 ? pa::kRopeInt4 : cache_dtype == PA_INT8 ? pa::kRopeInt8 : pa::kRopeRows;
+        if (kind == pa::kRopeInt4 && !quant_slots_ok(pa::kCacheInt4, num_blocks, block_size, num_kv_heads))
+            return PA_ERR_UNSUPPORTED;
+    } else {
+        return half_dtype(cache_dtype) ? PA_ERR_UNSUPPORTED : PA_ERR_INVALID_ARG;
+    }
+    const int64_t q_row = static_cast<int64_t>(num_heads) * head_dim, kv_row = static_cast<int64_t>(num_kv_heads) * head_dim;
+    if (q_stride < q_row || key_stride < kv_row || value_stride < kv_row || q_stride % 8 != 0 || key_stride % 8 != 0 ||
+        value_stride % 8 != 0)
+        return PA_ERR_INVALID_ARG;
+    if (num_tokens == 0) return PA_OK;
+    if (!out_q || !query || !key || !value || !k_cache || !v_cache || !slot_mapping || !positions || !inv_freq)
+        return PA_ERR_INVALID_ARG;
+    for (const void *x : {static_cast<const void *>(out_q), query, key, value, static_cast<const void *>(k_cache),
+                          static_cast<const void *>(v_cache), q_weight, k_weight, static_cast<const void *>(k_scales),
+                          static_cast<const void *>(v_scales)})
+        if (!aligned16(x)) return PA_ERR_INVALID_ARG;
+    if (out_q == query && q_stride != q_row) return PA_ERR_INVALID_ARG;
+    DeviceInfo dev;
+    if (!device_info(dev)) return PA_ERR_CUDA;
+    pa::RopeParams p{};
+    p.src[0] = static_cast<const uint16_t *>(query);
+    p.src[1] = static_cast<const uint16_t *>(key);
+    p.src[2] = static_cast<const uint16_t *>(value);
+    p.stride[0] = q_stride;
+    p.stride[1] = key_stride;
+    p.stride[2] = value_stride;
+    p.out_q = static_cast<uint16_t *>(out_q);
+    p.cache[0] = k_cache;
+    p.cache[1] = v_cache;
+    p.scales[0] = k_scales;
+    p.scales[1] = v_scales;
+    p.scale[0] = k_scale;
+    p.scale[1] = v_scale;
+    p.slots = slot_mapping;
+    p.positions = positions;
+    p.inv_freq = inv_freq;
+    p.weight[0] = static_cast<const uint16_t *>(q_weight);
+    p.weight[1] = static_cast<const uint16_t *>(k_weight);
+    p.eps = eps;
+    p.factor = factor;
+    p.num_tokens = num_tokens;
+    p.hq = num_heads;
+    p.hkv = num_kv_heads;
+    p.rot = rot_dim;
+    p.interleaved = interleaved != 0;
+    p.num_slots = num_blocks * block_size;
+    p.bs = block_size;
+    p.err_flag = err_flag;
+    return pa::launch_rope_and_cache(p, head_dim, dtype == PA_BF16, kind, dev.sms, static_cast<cudaStream_t>(stream)) ==
+                   cudaSuccess
+               ? PA_OK
+               : PA_ERR_CUDA;
 }
 
 PA_EXPORT size_t pa_decode_shared_workspace_size(int num_seqs, int num_groups, int max_group_size, int num_heads,

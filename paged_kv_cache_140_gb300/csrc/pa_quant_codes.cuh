@@ -22,10 +22,16 @@ __device__ __forceinline__ uint32_t int8x4(float a, float b, float c, float d) {
     return __byte_perm(__byte_perm(ia, ib, 0x0040u), __byte_perm(ic, id, 0x0040u), 0x5410u);
 }
 
-// A group of 4-bit codes: x stands for s (u + z), s and z bfloat16 (the rounding
-// of s moves the grid by 2^-9 of itself, which the codes are then chosen for; that
-// of z, up to half a unit in 2^8, costs at most what the codes' own rounding does,
-// since s is at least 2^-8 of the largest magnitude).
+// Where the (scale, zero) words of a 4-bit row lie, in rows: [block][head][token][group].
+__device__ __forceinline__ int64_t word_row(int64_t block, int offset, int head, int hkv, int bs) {
+    return (block * hkv + head) * bs + offset;
+}
+
+// A group of 4-bit codes: x stands for s (u + z), s and z bfloat16.  The codes are
+// chosen for the rounded s and z: a range that s falls short of by its rounding, 2^-8,
+// costs a sixteenth of a code; z's rounding a thirty-second where a group is spread about
+// zero (|z| of 7.5), half a code where |z| is 2^8 and one just above.  |z| goes no
+// further, since s is at least 2^-8 of the largest magnitude.
 struct Group4 {
     float inv, zero;     // 1 / s and z
     uint32_t word;       // s in the low half, z in the high half

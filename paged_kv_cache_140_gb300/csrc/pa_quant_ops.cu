@@ -12,9 +12,9 @@
 // 4 bits: for a group x of 64 neighbouring elements of a row, in 32-bit arithmetic,
 //     s = bf16(max((max x / 2 - min x / 2) / 7.5, max |x| / 2^8, 2^-60)),  z = bf16(min x / s),
 //     code_i = rn(x_i (1 / s) - z), kept within 0 .. 15;
-// the group stands for s (code_i + z).  The term in max |x| keeps z within 2^8, where
-// bf16 holds it to half a code: values far from zero are then off by 2^-8 of
-// themselves at most.  A group that holds an infinity or NaN gets the scale NaN.
+// the group stands for s (code_i + z).  The term in max |x| keeps |z| to 2^8 or just
+// above, where bf16 holds it to one code: values far from zero are off by 3/2 of a code,
+// 1.5 2^-8 of the largest, at most.  A group that holds an infinity or NaN gets the scale NaN.
 // Codes lie two to a byte, the even element in the low half.  The scales of a block
 // are ordered [head][token][group], so that a block's 16 tokens of one head are 128
 // neighbouring bytes for the decode.
@@ -45,11 +45,6 @@ __device__ __forceinline__ void store32(void *dst, const uint32_t (&h)[8]) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(h[0]), "r"(h[1]), "r"(h[2]),
                  "r"(h[3]), "r"(h[4]), "r"(h[5]), "r"(h[6]), "r"(h[7])
                  : "memory");
-}
-
-// Where the (scale, zero) words of a 4-bit row start: [block][head][token][group].
-__device__ __forceinline__ int64_t word_row(int64_t block, int offset, int head, int hkv, int bs) {
-    return (block * hkv + head) * bs + offset;
 }
 
 struct QuantWrite {

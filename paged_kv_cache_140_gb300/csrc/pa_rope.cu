@@ -1,0 +1,328 @@
+// Norms of queries and keys, the rotation to their positions, and the write of keys
+// and values into the paged cache, in one pass.
+//
+// A row x of D elements (one token, one head):
+//     y = x w / sqrt(mean x^2 + eps)                  (queries and keys, where a weight is given)
+//     (a, b) -> m (a cos - b sin, b cos + a sin)      (queries and keys: pair i of the first 2F elements)
+// with the angle position * f_i, a pair being the elements (i, i + F) or, interleaved,
+// (2i, 2i + 1).  Nothing is rounded between the steps; rows come out in the inputs'
+// type, or as codes of the cache's (pa_quant_codes.cuh).
+//
+// The angle is taken in turns, as a 64-bit fraction: f_i / 2 pi = F_i 2^-64 to 64 bits
+// in integer arithmetic, and position * F_i modulo 2^64 is the fraction of a turn
+// without loss, at any position.  sincospif of it is good to a few 2^-24.
+//
+// Bound by memory: every row is read once and written once.  D / 8 lanes take a row,
+// 8 elements each; with the pairs half a row apart those are 4 and their 4 partners,
+// so that no element changes lanes.  A CTA takes one or four tokens' rows, its threads
+// first make the tokens' sines and cosines (once per token, not per head: 40 heads
+// share them), while each lane's first rows are on their way.
+#include "pa_decode_common.cuh"
+#include "pa_device.cuh"
+#include "pa_quant_codes.cuh"
+#include "pa_step_ops.h"
+
+namespace pa {
+
+namespace {
+
+using decode_common::launch_pdl;
+
+constexpr int kRopeThreads = 256;
+constexpr int kRopeTokens = 4;       // tokens of a CTA at most
+constexpr int kRopeAhead = 4;        // rows a lane has in flight
+
+// f / 2 pi, as a fraction of 2^64 (whole turns dropped).
+__device__ __forceinline__ uint64_t turn_fraction(double f) {
+    const uint64_t bits = static_cast<uint64_t>(__double_as_longlong(f));
+    const int e = static_cast<int>((bits >> 52) & 0x7ff);
+    // f = M 2^(e - 1086) with M's top bit set, and 1 / 2 pi = C 2^-66
+    const uint64_t M = ((bits & 0xfffffffffffffull) | 0x10000000000000ull) << 11;
+    const uint64_t h = __umul64hi(M, 0xa2f9836e4e44152aull);
+    const int sh = e - 1024;
+    uint64_t t = sh >= 0 ? (sh < 64 ? h << sh : 0) : (sh > -64 ? h >> -sh : 0);
+    if (e == 0) t = 0;
+    return bits >> 63 ? 0 - t : t;
+}
+
+__device__ __forceinline__ float2 cos_sin(int64_t position, double f, float factor) {
+    const int64_t t = static_cast<int64_t>(static_cast<uint64_t>(position) * turn_fraction(f));
+    float s, c;
+    sincospif(__ll2float_rn(t) * 0x1p-63f, &s, &c);
+    return make_float2(c * factor, s * factor);
+}
+
+// Eight elements of a row, four at each of two places.
+struct Piece {
+    uint2 a, b;
+};
+
+template <int D>
+__device__ __forceinline__ float group_sum(float v, uint32_t lanes) {
+#pragma unroll
+    for (int o = 1; o < D / 8; o <<= 1) v += __shfl_xor_sync(lanes, v, o);
+    return v;
+}
+
+// Codes of a row's eight values (four at elements oa, four at ob) into the cache.
+template <int D>
+__device__ __forceinline__ void write_codes(const RopeParams &p, int kind, int kv, const float (&y)[8], int oa, int ob, int l,
+                                            int head, int64_t slot, uint32_t lanes) {
+    const int64_t row = slot * p.hkv + head;
+    uint8_t *base = static_cast<uint8_t *>(p.cache[kv]);
+    if (kind == kRopeInt4) {
+        float lo[D / kGroup4], hi[D / kGroup4];
+        const int ga = oa / kGroup4, gb = ob / kGroup4;
+        uint32_t m = 0;
+#pragma unroll
+        for (int g = 0; g < D / kGroup4; ++g) {
+            lo[g] = INFINITY;
+            hi[g] = -INFINITY;
+            uint32_t mg = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if ((i < 4 ? ga : gb) == g) {
+                    lo[g] = fminf(lo[g], y[i]);
+                    hi[g] = fmaxf(hi[g], y[i]);
+                    mg = max(mg, __float_as_uint(y[i]) & 0x7fffffffu);
+                }
+            if (mg >= 0x7f800000u) m |= 1u << g;
+        }
+#pragma unroll
+        for (int o = 1; o < D / 8; o <<= 1) {
+            m |= __shfl_xor_sync(lanes, m, o);
+#pragma unroll
+            for (int g = 0; g < D / kGroup4; ++g) {
+                lo[g] = fminf(lo[g], __shfl_xor_sync(lanes, lo[g], o));
+                hi[g] = fmaxf(hi[g], __shfl_xor_sync(lanes, hi[g], o));
+            }
+        }
+        Group4 q[D / kGroup4];
+#pragma unroll
+        for (int g = 0; g < D / kGroup4; ++g) q[g] = group4(lo[g], hi[g], !((m >> g) & 1u));
+        auto of = [&](int g) {
+            const Group4 &a = q[0], &b = q[D / kGroup4 - 1];
+            return Group4{g ? b.inv : a.inv, g ? b.zero : a.zero, g ? b.word : a.word};
+        };
+        const Group4 qa = of(ga), qb = of(gb);
+        const bool fa = !((m >> ga) & 1u), fb = !((m >> gb) & 1u);
+        const uint32_t ca = __byte_perm(code4x2(y[0], y[1], qa), code4x2(y[2], y[3], qa), 0x0040u);
+        const uint32_t cb = __byte_perm(code4x2(y[4], y[5], qb), code4x2(y[6], y[7], qb), 0x0040u);
+        uint8_t *o = base + row * (D / 2);
+        *reinterpret_cast<uint16_t *>(o + oa / 2) = static_cast<uint16_t>(fa ? ca : 0u);
+        *reinterpret_cast<uint16_t *>(o + ob / 2) = static_cast<uint16_t>(fb ? cb : 0u);
+        if (l < D / kGroup4) {
+            const uint32_t s = static_cast<uint32_t>(slot), blk = s / p.bs;
+            static_cast<uint32_t *>(p.scales[kv])[word_row(blk, s - blk * p.bs, head, p.hkv, p.bs) * (D / kGroup4) + l] =
+                of(l).word;
+        }
+        return;
+    }
+    uint32_t code[2];
+    if (kind == kRopeE4M3) {
+        const float s = p.scale[kv];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            code[h] = f32x2_to_e4m3x2(__fdiv_rn(y[4 * h], s), __fdiv_rn(y[4 * h + 1], s)) |
+                      (f32x2_to_e4m3x2(__fdiv_rn(y[4 * h + 2], s), __fdiv_rn(y[4 * h + 3], s)) << 16);
+    } else {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(y[i]) & 0x7fffffffu);
+#pragma unroll
+        for (int o = 1; o < D / 8; o <<= 1) m = max(m, __shfl_xor_sync(lanes, m, o));
+        const bool finite = m < 0x7f800000u;      // (a NaN is above infinity)
+        const float top = kind == kRopeRows ? 448.f : 127.f;
+        const float amax = fmaxf(finite ? __uint_as_float(m) : 0.f, kAmaxFloor), inv = __fdiv_rn(top, amax);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float v0 = __fmul_rn(y[4 * h], inv), v1 = __fmul_rn(y[4 * h + 1], inv);
+            const float v2 = __fmul_rn(y[4 * h + 2], inv), v3 = __fmul_rn(y[4 * h + 3], inv);
+            code[h] = kind == kRopeRows ? f32x2_to_e4m3x2(v0, v1) | (f32x2_to_e4m3x2(v2, v3) << 16) : int8x4(v0, v1, v2, v3);
+            if (!finite) code[h] = 0u;
+        }
+        if (l == 0) static_cast<float *>(p.scales[kv])[row] = finite ? __fdiv_rn(amax, top) : __uint_as_float(kNanBits);
+    }
+    *reinterpret_cast<uint32_t *>(base + row * D + oa) = code[0];
+    *reinterpret_cast<uint32_t *>(base + row * D + ob) = code[1];
+}
+
+template <int D, bool BF16, bool QUANT>
+__global__ void __launch_bounds__(kRopeThreads)
+    rope_and_cache_kernel(const __grid_constant__ RopeParams p, int tokens, int rows_per, int kind) {
+    constexpr int LPR = D / 8, RG = kRopeThreads / LPR, U = kRopeAhead;
+    __shared__ __align__(16) float cos_t[kRopeTokens][D / 2], sin_t[kRopeTokens][D / 2];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int l = threadIdx.x % LPR, grp = threadIdx.x / LPR;
+    const uint32_t lanes = (LPR == 32 ? 0xffffffffu : ((1u << LPR) - 1u) << (threadIdx.x & 31 & ~(LPR - 1)));
+    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tokens;
+    const int nt = static_cast<int>(min(static_cast<int64_t>(tokens), p.num_tokens - t0));
+    const int R = p.hq + 2 * p.hkv, r0 = blockIdx.y * rows_per, rows = min(rows_per, R - r0);
+    if (rows <= 0) return;
+    const int n = nt * rows;                      // this CTA's rows; mine are grp, grp + RG, ...
+    const int step_t = RG / rows, step_r = RG % rows;
+    const int half = p.rot / 2;
+    const bool turns = 4 * l < half;              // my elements of a query or key are turned
+
+    // Row i of this CTA: its token, and which row of the token.
+    struct At {
+        int tok, row;
+    };
+    auto next = [&](At at) {
+        at.tok += step_t;
+        at.row += step_r;
+        if (at.row >= rows) {
+            at.row -= rows;
+            ++at.tok;
+        }
+        return at;
+    };
+    // 0 query, 1 key, 2 value, and the head
+    auto which = [&](int row, int &head) {
+        const int r = r0 + row;
+        const int w = r < p.hq ? 0 : r < p.hq + p.hkv ? 1 : 2;
+        head = w == 0 ? r : w == 1 ? r - p.hq : r - p.hq - p.hkv;
+        return w;
+    };
+    auto apart = [&](int w) { return w < 2 && turns && !p.interleaved; };
+    auto place_a = [&](int w) { return apart(w) ? 4 * l : 8 * l; };
+    auto place_b = [&](int w) { return apart(w) ? half + 4 * l : 8 * l + 4; };
+    auto load = [&](At at) {
+        int head;
+        const int w = which(at.row, head);
+        const uint16_t *x = p.src[w] + (t0 + at.tok) * p.stride[w] + static_cast<int64_t>(head) * D;
+        Piece v;
+        if (apart(w)) {
+            v.a = *reinterpret_cast<const uint2 *>(x + 4 * l);
+            v.b = *reinterpret_cast<const uint2 *>(x + half + 4 * l);
+        } else {
+            const uint4 u = *reinterpret_cast<const uint4 *>(x + 8 * l);
+            v.a = make_uint2(u.x, u.y);
+            v.b = make_uint2(u.z, u.w);
+        }
+        return v;
+    };
+
+    At at{grp / rows, grp % rows};
+    At ahead = at;
+    Piece v[U];
+    auto fetch = [&](int i0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (i0 + u * RG < n) v[u] = load(ahead);
+            ahead = next(ahead);
+        }
+    };
+    fetch(grp);
+    for (int i = threadIdx.x; i < nt * half; i += kRopeThreads) {
+        const int tok = i / half, k = i - tok * half;
+        const float2 cs = cos_sin(__ldg(p.positions + t0 + tok), __ldg(p.inv_freq + k), p.factor);
+        cos_t[tok][k] = cs.x;
+        sin_t[tok][k] = cs.y;
+    }
+    __syncthreads();
+    for (int i0 = grp; i0 < n; i0 += U * RG) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (i0 + u * RG >= n) break;
+            int head;
+            const int w = which(at.row, head);
+            const int64_t tok = t0 + at.tok;
+            const int oa = place_a(w), ob = place_b(w);
+            float y[8];
+            {
+                const uint32_t x[4] = {v[u].a.x, v[u].a.y, v[u].b.x, v[u].b.y};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float2 f = Half2x<BF16>::to_float2(x[k]);
+                    y[2 * k] = f.x;
+                    y[2 * k + 1] = f.y;
+                }
+            }
+            if (w < 2 && p.weight[w] != nullptr) {
+                float ss = 0.f;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) ss = fmaf(y[k], y[k], ss);
+                const float r = rsqrtf(group_sum<D>(ss, lanes) * (1.f / D) + p.eps);
+                const uint2 wa = __ldg(reinterpret_cast<const uint2 *>(p.weight[w] + oa));
+                const uint2 wb = __ldg(reinterpret_cast<const uint2 *>(p.weight[w] + ob));
+                const uint32_t ww[4] = {wa.x, wa.y, wb.x, wb.y};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float2 f = Half2x<BF16>::to_float2(ww[k]);
+                    y[2 * k] *= r * f.x;
+                    y[2 * k + 1] *= r * f.y;
+                }
+            }
+            if (w < 2 && turns) {
+                const float4 c = *reinterpret_cast<const float4 *>(&cos_t[at.tok][4 * l]);
+                const float4 s = *reinterpret_cast<const float4 *>(&sin_t[at.tok][4 * l]);
+                const float cc[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
+                float z[8];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float a = p.interleaved ? y[2 * k] : y[k], b = p.interleaved ? y[2 * k + 1] : y[k + 4];
+                    z[k] = a * cc[k] - b * sn[k];
+                    z[k + 4] = b * cc[k] + a * sn[k];
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    y[p.interleaved ? 2 * k : k] = z[k];
+                    y[p.interleaved ? 2 * k + 1 : k + 4] = z[k + 4];
+                }
+            }
+            uint16_t *out = nullptr;
+            int64_t slot = 0;
+            if (w == 0) {
+                out = p.out_q + (tok * p.hq + head) * D;
+            } else {
+                slot = __ldg(p.slots + tok);
+                if (slot >= p.num_slots) {
+                    if (l == 0) report(p.err_flag, 0x1 /* PA_FLAG_BAD_SLOT */);
+                    slot = -1;
+                }
+                if (!QUANT && slot >= 0) out = static_cast<uint16_t *>(p.cache[w - 1]) + (slot * p.hkv + head) * D;
+            }
+            if (QUANT && w > 0) {
+                if (slot >= 0) write_codes<D>(p, kind, w - 1, y, oa, ob, l, head, slot, lanes);
+            } else if (out != nullptr) {
+                const uint2 a = make_uint2(pack2<BF16>(y[0], y[1]), pack2<BF16>(y[2], y[3]));
+                const uint2 b = make_uint2(pack2<BF16>(y[4], y[5]), pack2<BF16>(y[6], y[7]));
+                if (apart(w)) {
+                    *reinterpret_cast<uint2 *>(out + oa) = a;
+                    *reinterpret_cast<uint2 *>(out + ob) = b;
+                } else {
+                    *reinterpret_cast<uint4 *>(out + oa) = make_uint4(a.x, a.y, b.x, b.y);
+                }
+            }
+            at = next(at);
+        }
+        fetch(i0 + U * RG);
+    }
+}
+
+template <int D, bool BF16>
+cudaError_t rope_t(const RopeParams &p, int kind, int sms, cudaStream_t stream) {
+    constexpr int RG = kRopeThreads / (D / 8);
+    const int R = p.hq + 2 * p.hkv;
+    // Four tokens to a CTA while that fills the GPU; few tokens are spread over CTAs by rows.
+    const int tokens = (p.num_tokens + kRopeTokens - 1) / kRopeTokens >= 4 * sms ? kRopeTokens : 1;
+    const int64_t blocks = (p.num_tokens + tokens - 1) / tokens;
+    int split = 1;
+    while (blocks * split < 4 * sms && R / (split * 2) >= RG) split *= 2;
+    const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(split));
+    const int rows = (R + split - 1) / split;
+    if (kind == kRopeHalf)
+        return launch_pdl(rope_and_cache_kernel<D, BF16, false>, grid, dim3(kRopeThreads), 0, stream, p, tokens, rows, kind);
+    return launch_pdl(rope_and_cache_kernel<D, BF16, true>, grid, dim3(kRopeThreads), 0, stream, p, tokens, rows, kind);
+}
+
+}  // namespace
+
+cudaError_t launch_rope_and_cache(const RopeParams &p, int head_dim, bool bf16, int kind, int sms, cudaStream_t stream) {
+    if (head_dim == 128) return bf16 ? rope_t<128, true>(p, kind, sms, stream) : rope_t<128, false>(p, kind, sms, stream);
+    return bf16 ? rope_t<64, true>(p, kind, sms, stream) : rope_t<64, false>(p, kind, sms, stream);
+}
+
+}  // namespace pa

@@ -74,3 +74,65 @@ def cache4(lens, bt, nb, bs, hkv, d, seed, vary=1.0, dtype="bf16", offset=0.0):
                 x = x * torch.exp(vary * torch.randn(L, hkv, 1, generator=g))
                 store4(c, n, Q.slots_of(bt, s, 0, L, bs), x.to(DT[dtype]))
     return c
+
+
+# ---------------------------------------------------- norm, rotation, write
+
+def turn(x, positions, freq, interleaved=False, factor=1.0, weight=None, eps=1e-6):
+    """Rows [T, H, D] normalised (weight given) and turned, in 64 bits."""
+    y = x.double()
+    if weight is not None:
+        y = y * weight.double() / torch.sqrt(y.square().mean(-1, keepdim=True) + eps)
+    n = freq.numel()
+    # the angle modulo a turn in exact arithmetic: freq as a fraction, positions as whole numbers
+    from fractions import Fraction
+    two_pi = Fraction(884279719003555, 140737488355328) + Fraction(9935515200043022, 2 ** 105)   # to 2^-105
+    turns = torch.empty(len(positions), n, dtype=torch.float64)
+    for i, f in enumerate(freq.tolist()):
+        per = Fraction(f) / two_pi
+        for t, p in enumerate(positions.tolist()):
+            turns[t, i] = float(p * per % 1)
+    angle = 2 * np.pi * turns[:, None]
+    i = torch.arange(n)
+    a, b = (2 * i, 2 * i + 1) if interleaved else (i, i + n)
+    out = y.clone()
+    c, s = factor * torch.cos(angle), factor * torch.sin(angle)
+    out[..., a] = y[..., a] * c - y[..., b] * s
+    out[..., b] = y[..., b] * c + y[..., a] * s
+    return out
+
+
+def turn_tolerance(x, d, dtype, factor=1.0, weight=None, eps=1e-6):
+    """Worst case of the 32-bit steps of turn(), as a bound per element from the pair's size.
+
+    The fraction of a turn and sincospi are off by 2^-24 and two units each, cos and sin by 4 x 2^-24
+    in all; the norm sums d squares (d half steps at most) and takes a root of 2 units; products and
+    the sum add 4 half steps: (d + 16) 2^-24 of |a| + |b|, then one rounding to dtype."""
+    y = x.double()
+    if weight is not None:
+        y = y * weight.double() / torch.sqrt(y.square().mean(-1, keepdim=True) + eps)
+    size = 2 * y.abs().amax(-1, keepdim=True) * max(1.0, abs(factor))
+    return size * (d + 16) * 2.0 ** -24, (torch.finfo(DT[dtype]).eps / 2 if dtype != "f32" else 2.0 ** -24)
+
+
+# ---------------------------------------------------------- block tables
+
+def update(bt, lens, changes, free, count, bs, room):
+    """The step on lists: (table, lengths, stack, count, cu, slots, positions)."""
+    bt, free = [list(r) for r in bt], list(free)
+    new = [max(0, n + c) for n, c in zip(lens, changes)]
+    blocks = lambda n: -(-n // bs)   # noqa: E731
+    for i in reversed(range(len(lens))):
+        for b in reversed(range(blocks(new[i]), blocks(lens[i]))):
+            free[count] = bt[i][b]
+            count += 1
+    cu, slots, pos = [0], [], []
+    for i in range(len(lens)):
+        for b in range(blocks(lens[i]), blocks(new[i])):
+            count -= 1
+            bt[i][b] = free[count]
+        for p in range(lens[i], new[i]):
+            slots.append(bt[i][p // bs] * bs + p % bs)
+            pos.append(p)
+        cu.append(len(pos))
+    return bt, new, free, count, cu, slots + [-1] * (room - len(pos)), pos + [0] * (room - len(pos))
