@@ -135,10 +135,13 @@ def test_plain_4bit_codes_are_within_half_a_step(dtype, offset):
     # half a code; s and z are rounded to bf16, each off by up to 2^-8 of itself (8 significant bits: half a last
     # place is 2^-8 of a number at the bottom of its binade): a range of 15 codes that falls short by 2^-8, and z; 32-bit steps
     bound = s * (0.5 + 15 * 2.0 ** -8 + z.abs() * 2.0 ** -8 + (z.abs() + 16) * 2.0 ** -22)
-    assert torch.all((back.unflatten(-1, (-1, 64)) - g).abs() <= bound[..., None])
+    # (some f16 rows come out infinite: their groups have the scale NaN, and no codes to look at)
+    ok = torch.isfinite(g).all(-1)
+    assert torch.equal(s.isnan(), ~ok) and torch.all(codes.unflatten(-1, (-1, 32))[~ok] == 0)
+    assert torch.all(((back.unflatten(-1, (-1, 64)) - g).abs() <= bound[..., None])[ok])
     # s is a fifteenth of the range, or 2^-8 of the largest value, to bf16, so |min / s| is at most
     # 2^8 (1 + 2^-8 + 2^-15) = 257.01, which bf16 (a last place of 2 there) rounds to 258 at most
-    assert torch.all((s * 15 >= (g.amax(-1) - g.amin(-1)) * (1 - 2.0 ** -8)) & (z.abs() <= 258))
+    assert torch.all(((s * 15 >= (g.amax(-1) - g.amin(-1)) * (1 - 2.0 ** -8)) & (z.abs() <= 258))[ok])
 
 
 def test_plain_turn_is_a_rotation():
