@@ -717,13 +717,16 @@ def update_tables(block_tables, context_lens, changes, free_blocks, free_count, 
         out_lens = context_lens
     if out_free_count is None:
         out_free_count = free_count
-    for t in (block_tables, context_lens, changes, free_blocks, free_count, slot_mapping, positions, cu_seqlens, out_lens,
-              out_free_count):
-        if t.get_device() != dev or not t.is_contiguous() or dev != rt.current_device():
-            _refuse((("block_tables", block_tables), ("context_lens", context_lens), ("changes", changes),
-                     ("free_blocks", free_blocks), ("free_count", free_count), ("slot_mapping", slot_mapping),
-                     ("positions", positions), ("cu_seqlens", cu_seqlens), ("out_lens", out_lens),
-                     ("out_free_count", out_free_count)))
+    if (dev != rt.current_device() or context_lens.get_device() != dev or changes.get_device() != dev or
+            free_blocks.get_device() != dev or free_count.get_device() != dev or slot_mapping.get_device() != dev or
+            positions.get_device() != dev or cu_seqlens.get_device() != dev or out_lens.get_device() != dev or
+            out_free_count.get_device() != dev or not block_tables.is_contiguous() or not context_lens.is_contiguous() or
+            not changes.is_contiguous() or not free_blocks.is_contiguous() or not slot_mapping.is_contiguous() or
+            not positions.is_contiguous() or not cu_seqlens.is_contiguous() or not out_lens.is_contiguous()):
+        _refuse((("block_tables", block_tables), ("context_lens", context_lens), ("changes", changes),
+                 ("free_blocks", free_blocks), ("free_count", free_count), ("slot_mapping", slot_mapping),
+                 ("positions", positions), ("cu_seqlens", cu_seqlens), ("out_lens", out_lens),
+                 ("out_free_count", out_free_count)))
     if len(table) != 2 or block_tables.dtype != rt.i32:
         raise ValueError("block_tables must be int32 [B, maxNB]")
     B = table[0]

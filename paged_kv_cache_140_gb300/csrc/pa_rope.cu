@@ -30,7 +30,6 @@ using decode_common::launch_pdl;
 
 constexpr int kRopeThreads = 256;
 constexpr int kRopeTokens = 4;       // tokens of a CTA at most
-constexpr int kRopeAhead = 4;        // rows a lane has in flight
 
 // f / 2 pi, as a fraction of 2^64 (whole turns dropped).
 __device__ __forceinline__ uint64_t turn_fraction(double f) {
@@ -51,11 +50,6 @@ __device__ __forceinline__ float2 cos_sin(int64_t position, double f, float fact
     sincospif(__ll2float_rn(t) * 0x1p-63f, &s, &c);
     return make_float2(c * factor, s * factor);
 }
-
-// Eight elements of a row, four at each of two places.
-struct Piece {
-    uint2 a, b;
-};
 
 template <int D>
 __device__ __forceinline__ float group_sum(float v, uint32_t lanes) {
@@ -147,175 +141,182 @@ __device__ __forceinline__ void write_codes(const RopeParams &p, int kind, int k
     *reinterpret_cast<uint32_t *>(base + row * D + ob) = code[1];
 }
 
-template <int D, bool BF16, bool QUANT>
+// (e0 e1)(e2 e3)(e4 e5)(e6 e7) -> (e0 e2)(e4 e6)(e1 e3)(e5 e7), and back.
+__device__ __forceinline__ void part_pairs(uint32_t (&x)[4]) {
+    const uint32_t a = __byte_perm(x[0], x[1], 0x5410u), b = __byte_perm(x[2], x[3], 0x5410u);
+    const uint32_t c = __byte_perm(x[0], x[1], 0x7632u), d = __byte_perm(x[2], x[3], 0x7632u);
+    x[0] = a;
+    x[1] = b;
+    x[2] = c;
+    x[3] = d;
+}
+__device__ __forceinline__ void join_pairs(uint32_t (&x)[4]) {
+    const uint32_t a = __byte_perm(x[0], x[2], 0x5410u), b = __byte_perm(x[0], x[2], 0x7632u);
+    const uint32_t c = __byte_perm(x[1], x[3], 0x5410u), d = __byte_perm(x[1], x[3], 0x7632u);
+    x[0] = a;
+    x[1] = b;
+    x[2] = c;
+    x[3] = d;
+}
+
+// A CTA takes TB tokens and rows_per of their rows: a group of lanes takes a row (query,
+// key or value of one head) of all TB tokens at a time, the next row's loads under way.
+template <int D, bool BF16, bool QUANT, int TB>
 __global__ void __launch_bounds__(kRopeThreads)
-    rope_and_cache_kernel(const __grid_constant__ RopeParams p, int tokens, int rows_per, int kind) {
-    constexpr int LPR = D / 8, RG = kRopeThreads / LPR, U = kRopeAhead;
-    __shared__ __align__(16) float cos_t[kRopeTokens][D / 2], sin_t[kRopeTokens][D / 2];
+    rope_and_cache_kernel(const __grid_constant__ RopeParams p, int rows_per, int kind) {
+    constexpr int LPR = D / 8, RG = kRopeThreads / LPR;
+    __shared__ __align__(16) float cos_t[TB][D / 2], sin_t[TB][D / 2];
+    __shared__ int64_t slot_t[TB];
     pdl_wait();
     pdl_launch_dependents();
     const int l = threadIdx.x % LPR, grp = threadIdx.x / LPR;
-    const uint32_t lanes = (LPR == 32 ? 0xffffffffu : ((1u << LPR) - 1u) << (threadIdx.x & 31 & ~(LPR - 1)));
-    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tokens;
-    const int nt = static_cast<int>(min(static_cast<int64_t>(tokens), p.num_tokens - t0));
-    const int R = p.hq + 2 * p.hkv, r0 = blockIdx.y * rows_per, rows = min(rows_per, R - r0);
-    if (rows <= 0) return;
-    const int n = nt * rows;                      // this CTA's rows; mine are grp, grp + RG, ...
-    const int step_t = RG / rows, step_r = RG % rows;
+    const uint32_t lanes = ((1u << LPR) - 1u) << (threadIdx.x & 31 & ~(LPR - 1));
+    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * TB;
+    const int nt = static_cast<int>(min(static_cast<int64_t>(TB), p.num_tokens - t0));
+    const int R = p.hq + 2 * p.hkv, r1 = min(R, static_cast<int>(blockIdx.y + 1) * rows_per);
     const int half = p.rot / 2;
-    const bool turns = 4 * l < half;              // my elements of a query or key are turned
+    const bool turned = 4 * l < half;             // my elements of a query or key are turned
 
-    // Row i of this CTA: its token, and which row of the token.
-    struct At {
-        int tok, row;
-    };
-    auto next = [&](At at) {
-        at.tok += step_t;
-        at.row += step_r;
-        if (at.row >= rows) {
-            at.row -= rows;
-            ++at.tok;
-        }
-        return at;
-    };
-    // 0 query, 1 key, 2 value, and the head
-    auto which = [&](int row, int &head) {
-        const int r = r0 + row;
-        const int w = r < p.hq ? 0 : r < p.hq + p.hkv ? 1 : 2;
-        head = w == 0 ? r : w == 1 ? r - p.hq : r - p.hq - p.hkv;
-        return w;
-    };
-    auto apart = [&](int w) { return w < 2 && turns && !p.interleaved; };
-    auto place_a = [&](int w) { return apart(w) ? 4 * l : 8 * l; };
-    auto place_b = [&](int w) { return apart(w) ? half + 4 * l : 8 * l + 4; };
-    auto load = [&](At at) {
-        int head;
-        const int w = which(at.row, head);
-        const uint16_t *x = p.src[w] + (t0 + at.tok) * p.stride[w] + static_cast<int64_t>(head) * D;
-        Piece v;
-        if (apart(w)) {
-            v.a = *reinterpret_cast<const uint2 *>(x + 4 * l);
-            v.b = *reinterpret_cast<const uint2 *>(x + half + 4 * l);
-        } else {
-            const uint4 u = *reinterpret_cast<const uint4 *>(x + 8 * l);
-            v.a = make_uint2(u.x, u.y);
-            v.b = make_uint2(u.z, u.w);
-        }
-        return v;
-    };
-
-    At at{grp / rows, grp % rows};
-    At ahead = at;
-    Piece v[U];
-    auto fetch = [&](int i0) {
+    // Row r of a token: 0 query, 1 key, 2 value, and the head; my elements' places in it.
+    auto which = [&](int r) { return r < p.hq ? 0 : r < p.hq + p.hkv ? 1 : 2; };
+    auto head_of = [&](int r, int w) { return w == 0 ? r : w == 1 ? r - p.hq : r - p.hq - p.hkv; };
+    auto apart = [&](int w) { return w < 2 && turned && !p.interleaved; };
+    uint32_t x[TB][4], nx[TB][4];
+    auto load = [&](int r, uint32_t (&v)[TB][4]) {
+        const int w = which(r);
+        const uint16_t *s = p.src[w] + t0 * p.stride[w] + static_cast<int64_t>(head_of(r, w)) * D;
+        const bool two = apart(w);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (i0 + u * RG < n) v[u] = load(ahead);
-            ahead = next(ahead);
+        for (int k = 0; k < TB; ++k) {
+            if (k < nt) {
+                if (two) {
+                    const uint2 a = *reinterpret_cast<const uint2 *>(s + 4 * l);
+                    const uint2 b = *reinterpret_cast<const uint2 *>(s + half + 4 * l);
+                    v[k][0] = a.x; v[k][1] = a.y; v[k][2] = b.x; v[k][3] = b.y;
+                } else {
+                    const uint4 u = *reinterpret_cast<const uint4 *>(s + 8 * l);
+                    v[k][0] = u.x; v[k][1] = u.y; v[k][2] = u.z; v[k][3] = u.w;
+                }
+            }
+            s += p.stride[w];
         }
     };
-    fetch(grp);
+    int r = blockIdx.y * rows_per + grp;
+    if (r < r1) load(r, x);
     for (int i = threadIdx.x; i < nt * half; i += kRopeThreads) {
-        const int tok = i / half, k = i - tok * half;
+        const int tok = TB == 1 ? 0 : i / half, k = i - tok * half;
         const float2 cs = cos_sin(__ldg(p.positions + t0 + tok), __ldg(p.inv_freq + k), p.factor);
         cos_t[tok][k] = cs.x;
         sin_t[tok][k] = cs.y;
     }
+    if (threadIdx.x < nt) {
+        int64_t s = __ldg(p.slots + t0 + threadIdx.x);
+        if (s >= p.num_slots) {
+            report(p.err_flag, 0x1 /* PA_FLAG_BAD_SLOT */);
+            s = -1;
+        }
+        slot_t[threadIdx.x] = s;
+    }
     __syncthreads();
-    for (int i0 = grp; i0 < n; i0 += U * RG) {
+    for (; r < r1; r += RG) {
+        if (r + RG < r1) load(r + RG, nx);
+        const int w = which(r), head = head_of(r, w);
+        const bool turns = w < 2 && turned, pairs = turns && p.interleaved, two = apart(w);
+        const int oa = two ? 4 * l : 8 * l, ob = two ? half + 4 * l : 8 * l + 4;
+        const bool norm = w < 2 && p.weight[w] != nullptr;
+        float wt[8];
+        if (norm) {
+            const uint2 wa = __ldg(reinterpret_cast<const uint2 *>(p.weight[w] + oa));
+            const uint2 wb = __ldg(reinterpret_cast<const uint2 *>(p.weight[w] + ob));
+            uint32_t u[4] = {wa.x, wa.y, wb.x, wb.y};
+            if (pairs) part_pairs(u);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (i0 + u * RG >= n) break;
-            int head;
-            const int w = which(at.row, head);
-            const int64_t tok = t0 + at.tok;
-            const int oa = place_a(w), ob = place_b(w);
-            float y[8];
-            {
-                const uint32_t x[4] = {v[u].a.x, v[u].a.y, v[u].b.x, v[u].b.y};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float2 f = Half2x<BF16>::to_float2(x[k]);
-                    y[2 * k] = f.x;
-                    y[2 * k + 1] = f.y;
-                }
+            for (int k = 0; k < 4; ++k) {
+                const float2 f = Half2x<BF16>::to_float2(u[k]);
+                wt[2 * k] = f.x;
+                wt[2 * k + 1] = f.y;
             }
-            if (w < 2 && p.weight[w] != nullptr) {
+        }
+#pragma unroll
+        for (int k = 0; k < TB; ++k) {
+            if (k >= nt) break;
+            if (pairs) part_pairs(x[k]);
+            float y[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 f = Half2x<BF16>::to_float2(x[k][j]);
+                y[2 * j] = f.x;
+                y[2 * j + 1] = f.y;
+            }
+            if (norm) {
                 float ss = 0.f;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) ss = fmaf(y[k], y[k], ss);
-                const float r = rsqrtf(group_sum<D>(ss, lanes) * (1.f / D) + p.eps);
-                const uint2 wa = __ldg(reinterpret_cast<const uint2 *>(p.weight[w] + oa));
-                const uint2 wb = __ldg(reinterpret_cast<const uint2 *>(p.weight[w] + ob));
-                const uint32_t ww[4] = {wa.x, wa.y, wb.x, wb.y};
+                for (int j = 0; j < 8; ++j) ss = fmaf(y[j], y[j], ss);
+                const float s = rsqrtf(group_sum<D>(ss, lanes) * (1.f / D) + p.eps);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float2 f = Half2x<BF16>::to_float2(ww[k]);
-                    y[2 * k] *= r * f.x;
-                    y[2 * k + 1] *= r * f.y;
-                }
+                for (int j = 0; j < 8; ++j) y[j] *= s * wt[j];
             }
-            if (w < 2 && turns) {
-                const float4 c = *reinterpret_cast<const float4 *>(&cos_t[at.tok][4 * l]);
-                const float4 s = *reinterpret_cast<const float4 *>(&sin_t[at.tok][4 * l]);
+            if (turns) {
+                const float4 c = *reinterpret_cast<const float4 *>(&cos_t[k][4 * l]);
+                const float4 s = *reinterpret_cast<const float4 *>(&sin_t[k][4 * l]);
                 const float cc[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
-                float z[8];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float a = p.interleaved ? y[2 * k] : y[k], b = p.interleaved ? y[2 * k + 1] : y[k + 4];
-                    z[k] = a * cc[k] - b * sn[k];
-                    z[k + 4] = b * cc[k] + a * sn[k];
-                }
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    y[p.interleaved ? 2 * k : k] = z[k];
-                    y[p.interleaved ? 2 * k + 1 : k + 4] = z[k + 4];
+                for (int j = 0; j < 4; ++j) {
+                    const float a = y[j], b = y[j + 4];
+                    y[j] = a * cc[j] - b * sn[j];
+                    y[j + 4] = b * cc[j] + a * sn[j];
                 }
             }
-            uint16_t *out = nullptr;
-            int64_t slot = 0;
-            if (w == 0) {
-                out = p.out_q + (tok * p.hq + head) * D;
-            } else {
-                slot = __ldg(p.slots + tok);
-                if (slot >= p.num_slots) {
-                    if (l == 0) report(p.err_flag, 0x1 /* PA_FLAG_BAD_SLOT */);
-                    slot = -1;
-                }
-                if (!QUANT && slot >= 0) out = static_cast<uint16_t *>(p.cache[w - 1]) + (slot * p.hkv + head) * D;
-            }
+            const int64_t slot = slot_t[k];
             if (QUANT && w > 0) {
+                if (pairs) {          // back into the row's order
+                    const float z[8] = {y[0], y[4], y[1], y[5], y[2], y[6], y[3], y[7]};
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) y[j] = z[j];
+                }
                 if (slot >= 0) write_codes<D>(p, kind, w - 1, y, oa, ob, l, head, slot, lanes);
-            } else if (out != nullptr) {
-                const uint2 a = make_uint2(pack2<BF16>(y[0], y[1]), pack2<BF16>(y[2], y[3]));
-                const uint2 b = make_uint2(pack2<BF16>(y[4], y[5]), pack2<BF16>(y[6], y[7]));
-                if (apart(w)) {
-                    *reinterpret_cast<uint2 *>(out + oa) = a;
-                    *reinterpret_cast<uint2 *>(out + ob) = b;
+                continue;
+            }
+            uint16_t *out = w == 0 ? p.out_q + ((t0 + k) * p.hq + head) * D
+                                   : static_cast<uint16_t *>(p.cache[w - 1]) + (slot * p.hkv + head) * D;
+            uint32_t h[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) h[j] = pack2<BF16>(y[2 * j], y[2 * j + 1]);
+            if (pairs) join_pairs(h);
+            if (w == 0 || slot >= 0) {
+                if (two) {
+                    *reinterpret_cast<uint2 *>(out + oa) = make_uint2(h[0], h[1]);
+                    *reinterpret_cast<uint2 *>(out + ob) = make_uint2(h[2], h[3]);
                 } else {
-                    *reinterpret_cast<uint4 *>(out + oa) = make_uint4(a.x, a.y, b.x, b.y);
+                    *reinterpret_cast<uint4 *>(out + oa) = make_uint4(h[0], h[1], h[2], h[3]);
                 }
             }
-            at = next(at);
         }
-        fetch(i0 + U * RG);
+#pragma unroll
+        for (int k = 0; k < TB; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[k][j] = nx[k][j];
     }
 }
 
-template <int D, bool BF16>
-cudaError_t rope_t(const RopeParams &p, int kind, int sms, cudaStream_t stream) {
+template <int D, bool BF16, bool QUANT>
+cudaError_t rope_q(const RopeParams &p, int kind, int sms, cudaStream_t stream) {
     constexpr int RG = kRopeThreads / (D / 8);
     const int R = p.hq + 2 * p.hkv;
     // Four tokens to a CTA while that fills the GPU; few tokens are spread over CTAs by rows.
-    const int tokens = (p.num_tokens + kRopeTokens - 1) / kRopeTokens >= 4 * sms ? kRopeTokens : 1;
-    const int64_t blocks = (p.num_tokens + tokens - 1) / tokens;
+    const bool many = (p.num_tokens + kRopeTokens - 1) / kRopeTokens >= 4 * sms;
+    const int64_t blocks = many ? (p.num_tokens + kRopeTokens - 1) / kRopeTokens : p.num_tokens;
     int split = 1;
     while (blocks * split < 4 * sms && R / (split * 2) >= RG) split *= 2;
     const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(split));
     const int rows = (R + split - 1) / split;
-    if (kind == kRopeHalf)
-        return launch_pdl(rope_and_cache_kernel<D, BF16, false>, grid, dim3(kRopeThreads), 0, stream, p, tokens, rows, kind);
-    return launch_pdl(rope_and_cache_kernel<D, BF16, true>, grid, dim3(kRopeThreads), 0, stream, p, tokens, rows, kind);
+    if (many) return launch_pdl(rope_and_cache_kernel<D, BF16, QUANT, kRopeTokens>, grid, dim3(kRopeThreads), 0, stream, p, rows, kind);
+    return launch_pdl(rope_and_cache_kernel<D, BF16, QUANT, 1>, grid, dim3(kRopeThreads), 0, stream, p, rows, kind);
+}
+
+template <int D, bool BF16>
+cudaError_t rope_t(const RopeParams &p, int kind, int sms, cudaStream_t stream) {
+    return kind == kRopeHalf ? rope_q<D, BF16, false>(p, kind, sms, stream) : rope_q<D, BF16, true>(p, kind, sms, stream);
 }
 
 }  // namespace
