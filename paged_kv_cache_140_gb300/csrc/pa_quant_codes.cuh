@@ -37,32 +37,56 @@ struct Group4 {
     uint32_t word;       // s in the low half, z in the high half
 };
 
+// Quotients correctly rounded by one step on an approximate one (P. Markstein, "Computation
+// of elementary functions on the IBM RISC System/6000 processor", 1990): with inv the
+// correctly rounded 1 / b, q = a inv and the exact remainder r = a - b q, the quotient is
+// q + r inv, rounded once.  (Checked against IEEE division: every s, 2^28 pairs (min, s), as
+// many d / 7.5.)
+__device__ __forceinline__ float quotient(float a, float b, float inv) {
+    const float q = __fmul_rn(a, inv);
+    return __fmaf_rn(__fmaf_rn(-b, q, a), inv, q);
+}
+// 1 / s for a bfloat16 s of 2^-60 to 2^125, correctly rounded: one step on an approximation.
+__device__ __forceinline__ float inverse(float s) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+    return __fmaf_rn(__fmaf_rn(-s, r, 1.f), r, r);
+}
+
 __device__ __forceinline__ Group4 group4(float lo, float hi, bool finite) {
     // (halves: the range of values of both signs may pass the largest float)
-    const float step = __fdiv_rn(__fsub_rn(__fmul_rn(0.5f, hi), __fmul_rn(0.5f, lo)), 7.5f);
+    const float step = quotient(__fsub_rn(__fmul_rn(0.5f, hi), __fmul_rn(0.5f, lo)), 7.5f, 0.13333333333f);
     const float s = fmaxf(fmaxf(step, __fmul_rn(fmaxf(hi, -lo), 0.00390625f)), kAmaxFloor);
     const uint32_t sb = float_to_bf16_bits(s);
     const float sf = __uint_as_float(sb << 16);
-    const uint32_t zb = float_to_bf16_bits(__fdiv_rn(lo, sf));
     Group4 g;
-    g.inv = __fdiv_rn(1.f, sf);
+    g.inv = inverse(sf);
+    const uint32_t zb = float_to_bf16_bits(quotient(lo, sf, g.inv));
     g.zero = __uint_as_float(zb << 16);
     g.word = finite ? sb | (zb << 16) : kNanBits >> 16;
     return g;
 }
 
-// The code of x in the low four bits (those above the low byte are not zero).
-__device__ __forceinline__ uint32_t code4(float x, const Group4 &g) {
-    const float y = __fsub_rn(__fmul_rn(x, g.inv), g.zero);
-    return __float_as_uint(__fadd_rn(fminf(fmaxf(y, 0.f), 15.f), 12582912.f));
+// The codes of x0 and x1 in the low and high half.  The roundings of s and z leave
+// x (1 / s) - z within a few codes of 0 and 15, so that the rounded value (in the low bits
+// once 1.5 2^23 is added) is cut off there as a 16-bit number.
+__device__ __forceinline__ uint32_t codes4_pair(float x0, float x1, const Group4 &g) {
+    constexpr float k = 12582912.f;
+    const uint32_t a = __float_as_uint(__fadd_rn(__fsub_rn(__fmul_rn(x0, g.inv), g.zero), k));
+    const uint32_t b = __float_as_uint(__fadd_rn(__fsub_rn(__fmul_rn(x1, g.inv), g.zero), k));
+    uint32_t v = __byte_perm(a, b, 0x5410u);
+    asm("max.s16x2 %0, %0, %1;" : "+r"(v) : "r"(0u));
+    asm("min.s16x2 %0, %0, %1;" : "+r"(v) : "r"(0x000f000fu));
+    return v;
 }
-// Two codes as one byte (the low byte of the result).
-__device__ __forceinline__ uint32_t code4x2(float x0, float x1, const Group4 &g) {
-    return code4(x0, g) + (code4(x1, g) << 4);
-}
+// Eight codes, the first in the lowest bits; four codes as two bytes.
 __device__ __forceinline__ uint32_t code4x8(const float *x, const Group4 &g) {
-    return __byte_perm(__byte_perm(code4x2(x[0], x[1], g), code4x2(x[2], x[3], g), 0x0040u),
-                       __byte_perm(code4x2(x[4], x[5], g), code4x2(x[6], x[7], g), 0x0040u), 0x5410u);
+    return codes4_pair(x[0], x[4], g) + codes4_pair(x[1], x[5], g) * 16u + codes4_pair(x[2], x[6], g) * 256u +
+           codes4_pair(x[3], x[7], g) * 4096u;
+}
+__device__ __forceinline__ uint32_t code4x4(float x0, float x1, float x2, float x3, const Group4 &g) {
+    const uint32_t v = codes4_pair(x0, x2, g) + codes4_pair(x1, x3, g) * 16u;     // bytes 0 and 2
+    return __byte_perm(v, 0u, 0x4420u);
 }
 
 // Packed minimum and maximum of 16-bit values, NaN where either is.

@@ -100,8 +100,7 @@ __device__ __forceinline__ void write_codes(const RopeParams &p, int kind, int k
         };
         const Group4 qa = of(ga), qb = of(gb);
         const bool fa = !((m >> ga) & 1u), fb = !((m >> gb) & 1u);
-        const uint32_t ca = __byte_perm(code4x2(y[0], y[1], qa), code4x2(y[2], y[3], qa), 0x0040u);
-        const uint32_t cb = __byte_perm(code4x2(y[4], y[5], qb), code4x2(y[6], y[7], qb), 0x0040u);
+        const uint32_t ca = code4x4(y[0], y[1], y[2], y[3], qa), cb = code4x4(y[4], y[5], y[6], y[7], qb);
         uint8_t *o = base + row * (D / 2);
         *reinterpret_cast<uint16_t *>(o + oa / 2) = static_cast<uint16_t>(fa ? ca : 0u);
         *reinterpret_cast<uint16_t *>(o + ob / 2) = static_cast<uint16_t>(fb ? cb : 0u);
