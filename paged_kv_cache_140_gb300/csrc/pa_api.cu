@@ -1157,14 +1157,14 @@ PA_EXPORT pa_status pa_update_tables(int32_t *block_tables, int max_blocks_per_s
     if (num_seqs < 0 || max_blocks_per_seq <= 0 || free_capacity < 0 || num_blocks <= 0 || block_size <= 0 || num_tokens < 0)
         return PA_ERR_INVALID_ARG;
     if (num_seqs > pa::kTablesMaxSeqs || static_cast<int64_t>(max_blocks_per_seq) * block_size > (1 << 30) ||
-        num_tokens > (1 << 30) || free_capacity > INT32_MAX || num_blocks > INT32_MAX)
+        num_tokens > (1 << 30) || free_capacity > (1 << 30) || num_blocks > INT32_MAX)
         return PA_ERR_UNSUPPORTED;
     if (!cu_seqlens || !free_count || !out_free_count) return PA_ERR_INVALID_ARG;
     if (num_seqs > 0 && (!block_tables || !context_lens || !changes || !out_lens)) return PA_ERR_INVALID_ARG;
     if ((num_tokens > 0 && (!slot_mapping || !positions)) || (free_capacity > 0 && !free_blocks)) return PA_ERR_INVALID_ARG;
     const pa::TablesParams p{block_tables, max_blocks_per_seq, context_lens,   changes,    out_lens,
                              num_seqs,     free_blocks,        free_capacity,  free_count, out_free_count,
-                             num_blocks,   block_size,         cu_seqlens,     slot_mapping, positions,
+                             num_blocks,   pa::divisor(block_size), cu_seqlens, slot_mapping, positions,
                              num_tokens,   err_flag};
     return pa::launch_update_tables(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

@@ -26,6 +26,7 @@
 // shared memory; each thread has several rows in flight.
 #include "pa_decode_common.cuh"
 #include "pa_device.cuh"
+#include "pa_divisor.cuh"
 #include "pa_quant_codes.cuh"
 #include "pa_split.h"
 
@@ -45,20 +46,6 @@ __device__ __forceinline__ void store32(void *dst, const uint32_t (&h)[8]) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(h[0]), "r"(h[1]), "r"(h[2]),
                  "r"(h[3]), "r"(h[4]), "r"(h[5]), "r"(h[6]), "r"(h[7])
                  : "memory");
-}
-
-// Division of numbers below 2^31 by a number known at the launch.
-struct Divisor {
-    uint32_t mul, shift, by;
-};
-Divisor divisor(uint32_t by) {
-    uint32_t k = 0;
-    while ((uint64_t{1} << k) < by) ++k;
-    // ceil(2^(31 + k) / by) <= 2^32 - 1 but for by = 1, where it is 2^31
-    return {static_cast<uint32_t>(((uint64_t{1} << (31 + k)) + by - 1) / by), k, by};
-}
-__device__ __forceinline__ uint32_t divided(uint32_t x, const Divisor &d) {
-    return static_cast<uint32_t>((static_cast<uint64_t>(x) * d.mul) >> (31 + d.shift));
 }
 
 struct QuantWrite {

@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "pa_divisor.cuh"
+
 namespace pa {
 
 // Sequences of one call: the kernel keeps 20 bytes for each in shared memory.
@@ -23,7 +25,7 @@ struct TablesParams {
     const int32_t *free_count;
     int32_t *out_free_count;     // may be free_count
     int64_t num_blocks;
-    int block_size;
+    Divisor block;               // the block size
     int32_t *cu_seqlens;         // [num_seqs + 1]
     int64_t *slots;              // [num_tokens]
     int64_t *positions;          // [num_tokens]
