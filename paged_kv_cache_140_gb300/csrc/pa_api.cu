@@ -1022,6 +1022,10 @@ pa_status quant_decode(void *out, pa_dtype out_dtype, const void *query, pa_dtyp
                                      num_kv_heads, head_dim, block_size, num_blocks, scale);
     if (st != PA_OK) return st;
     if (!quant_slots_ok(cache, num_blocks, block_size, num_kv_heads)) return PA_ERR_UNSUPPORTED;
+    // 4-bit caches: an item weighs up to two units more than its slots
+    if (cache == pa::kCacheInt4 && static_cast<int64_t>(num_kv_heads) * (max_context_len / 16 + 1) *
+                                           std::min(num_seqs, kSplitEntries) >= (int64_t{1} << 30))
+        return PA_ERR_UNSUPPORTED;
     SplitPlan w;
     if (!plan_split(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context_len, partition_size, cache,
                     false, 0, 0, 0, w))

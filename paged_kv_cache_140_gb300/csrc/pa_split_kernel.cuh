@@ -80,6 +80,10 @@ struct SplitLayout {
     // Teams of a producer and its consumers, each with a ring and a share of the slots of its
     // own.  4-bit codes: two, since one's warps are too few to hide their own latencies.
     static constexpr int kTeams = k4 ? 2 : 1;
+    // What an item's start and end cost, in slots: 4-bit slots are short enough for shares to
+    // be weighed with it (256 13B-shaped sequences: teams with 18 items of a few slots took
+    // 300,000 cycles, with 5 long ones 252,000).  It counts as lying before the item's slots.
+    static constexpr int kItemExtra = k4 ? 2 : 0;
     static constexpr int kThreads = kTeams * (kWarps + 1) * 32;
     static constexpr int kMT = D / 16;
     static constexpr int kStateRow = D + 4;              // floats per query row of a warp's state
@@ -286,11 +290,13 @@ __device__ __forceinline__ int item_slots(int len, int part, int P, int SW) {
 // Modes in which a list of one partition is the whole result.
 __device__ __forceinline__ bool final_mode(int mode) { return mode == kSplitDecode || mode == kSplitWhole; }
 
+// EX: what an item costs beyond its slots, in slots.
+template <int EX>
 __device__ __forceinline__ uint32_t entry_weight(int len, int mode, int ngroups, int P, int SW) {
-    if (len <= 0) return final_mode(mode) ? static_cast<uint32_t>(ngroups) : 0u;
+    if (len <= 0) return final_mode(mode) ? static_cast<uint32_t>(ngroups * (1 + EX)) : 0u;
     const int full = (len - 1) / P;   // partitions before the last
     return static_cast<uint32_t>(ngroups) *
-           static_cast<uint32_t>(full * ((P / kStageTokens + SW - 1) / SW) + item_slots(len, full, P, SW));
+           static_cast<uint32_t>(full * ((P / kStageTokens + SW - 1) / SW + EX) + item_slots(len, full, P, SW) + EX);
 }
 
 template <int D, int C, int CT>
@@ -301,7 +307,7 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
     using L = SplitLayout<D, C, CT>;
     constexpr bool k8 = L::k8;
     constexpr bool BF16 = CT == kCacheBF16;   // MMA operand type
-    constexpr int SUB = L::kSub, W = L::kWarps, TEAMS = L::kTeams, MT = L::kMT, KS = D / 16;
+    constexpr int SUB = L::kSub, W = L::kWarps, TEAMS = L::kTeams, EX = L::kItemExtra, MT = L::kMT, KS = D / 16;
     constexpr int NE = C == 1 ? 1 : 2;        // live columns per lane (columns 2t, 2t + 1)
     using Cvt = Half2x<BF16>;
     extern __shared__ uint8_t smem_raw[];
@@ -385,6 +391,13 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
     pdl_launch_dependents();
     // ---- the entries' lengths ----
     const bool tell = blockIdx.x == 0;
+    if constexpr (L::k4) {
+        // the tables on their way to L2 while the lengths are looked at
+        const int64_t bytes = static_cast<int64_t>(p.num_seqs) * p.max_blocks_per_seq * 4;
+        for (int64_t i = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) * 128; i < bytes;
+             i += static_cast<int64_t>(gridDim.x) * blockDim.x * 128)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const uint8_t *>(p.block_tables) + i));
+    }
     if (mode == kSplitWhole && tell)   // every group's bounds, the warps with the fewest entries first
         for (int g = blockDim.x - 1 - threadIdx.x; g < p.num_groups; g += blockDim.x)
             if (bad_group(p, g, __ldg(p.cu_groups + g), __ldg(p.cu_groups + g + 1)))
@@ -436,7 +449,7 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
         const int per = (E + nthr - 1) / nthr;
         const int beg = min(E, static_cast<int>(threadIdx.x) * per), end = min(E, beg + per);
         uint32_t local = 0;
-        for (int i = beg; i < end; ++i) local += entry_weight(len_s[i], mode, ngroups, P, SW);
+        for (int i = beg; i < end; ++i) local += entry_weight<EX>(len_s[i], mode, ngroups, P, SW);
         uint32_t incl = local;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -449,7 +462,7 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
         for (int w = 0; w < warp; ++w) run += warp_tot[w];
         for (int i = beg; i < end; ++i) {
             prefix[i] = run;
-            run += entry_weight(len_s[i], mode, ngroups, P, SW);
+            run += entry_weight<EX>(len_s[i], mode, ngroups, P, SW);
         }
         if (threadIdx.x == 0) {
             uint32_t tot = 0;
@@ -464,7 +477,7 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
     // result of its own, named in the item's.
     const uint32_t total = prefix[E];
     const uint32_t shares = gridDim.x * TEAMS, share = blockIdx.x * TEAMS + team;
-    const bool cut = p.cut && total >= shares * static_cast<uint32_t>((P / kStageTokens + SW - 1) / SW);
+    const bool cut = p.cut && total >= shares * static_cast<uint32_t>((P / kStageTokens + SW - 1) / SW + EX);
     const uint32_t lo = static_cast<uint32_t>(static_cast<uint64_t>(total) * share / shares);
     const uint32_t hi = static_cast<uint32_t>(static_cast<uint64_t>(total) * (share + 1) / shares);
 
@@ -483,7 +496,7 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
             ic.nslots = item_slots(ic.len, part, P, SW);
         };
         auto advance = [&]() {
-            ic.start += ic.nslots;
+            ic.start += ic.nslots + EX;
             if (++ic.grp < ngroups) return;
             ic.grp = 0;
             if (ic.part + 1 < ic.nparts) {
@@ -506,13 +519,14 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                 if (prefix[m] <= lo) a = m; else b = m;
             }
             set_entry(a);
-            const uint32_t pw = static_cast<uint32_t>(ngroups) * static_cast<uint32_t>((P / kStageTokens + SW - 1) / SW);
+            const uint32_t pw = static_cast<uint32_t>(ngroups) * static_cast<uint32_t>((P / kStageTokens + SW - 1) / SW + EX);
             const uint32_t off = lo - prefix[a];
             set_part(min(ic.nparts - 1, static_cast<int>(off / pw)));
             const uint32_t pstart = prefix[a] + static_cast<uint32_t>(ic.part) * pw;
-            const int grp = static_cast<int>((lo - pstart + (cut ? 0 : ic.nslots - 1)) / ic.nslots);
+            const int weight = ic.nslots + EX;
+            const int grp = static_cast<int>((lo - pstart + (cut ? 0 : weight - 1)) / weight);
             ic.grp = min(grp, ngroups - 1);
-            ic.start = pstart + static_cast<uint32_t>(ic.grp) * ic.nslots;
+            ic.start = pstart + static_cast<uint32_t>(ic.grp) * weight;
             if (grp >= ngroups) advance();
         }
         // An item's sequence, members, table row and first block; its tokens and
@@ -570,6 +584,10 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
         };
         while (ok && work && ic.start < hi) {
             const int kvh0 = ic.grp << p.log2_heads;
+            // this share's slots of the item
+            const int jb = cut ? max(0, static_cast<int>(lo - ic.start) - EX) : 0;
+            const int je = cut ? min(ic.nslots, static_cast<int>(hi - ic.start) - EX) : ic.nslots;
+            if (EX > 0 && je <= 0) break;      // the share ends before the item's first slot
             open_item();
             {
                 const int qi = static_cast<int>(items % kQueryRing);
@@ -592,9 +610,6 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                 ++items;
                 __syncwarp();
             }
-            // this CTA's slots of the item
-            const int jb = cut && ic.start < lo ? static_cast<int>(lo - ic.start) : 0;
-            const int je = cut ? min(ic.nslots, static_cast<int>(hi - ic.start)) : ic.nslots;
             const int kind = jb > 0               ? kContinued
                              : je < ic.nslots     ? kCut
                              : final_mode(mode) && ic.nparts == 1 ? kFinal
@@ -1248,8 +1263,8 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
             consume(std::true_type{});
         else if (mine > 0)
             consume(std::false_type{});
-        // my reads (and zeroing) of the slot are done
-        fence_proxy_async_smem();
+        // my reads (and zeroing: not of 4-bit slots) of the slot are done
+        if constexpr (!L::k4) fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) arrive(&empty[slot]);
 
