@@ -78,12 +78,14 @@ struct SplitLayout {
     static constexpr int kScaleBytes = k8 ? kTiles * kStageTokens * 4 * kGroups : 0;
     static constexpr int kSlotBytes = (2 * kKVBytes + 2 * kScaleBytes + 1023) / 1024 * 1024;
     // Teams of a producer and its consumers, each with a ring and a share of the slots of its
-    // own.  4-bit codes: two, since one's warps are too few to hide their own latencies.
-    static constexpr int kTeams = k4 ? 2 : 1;
+    // own.  4-bit codes: two, since one's warps are too few to hide their own latencies (with
+    // 8 query rows one with more registers is the faster: 138 us against 152 for 16 sequences
+    // of 16 K to 32 K tokens, 64 heads on 8).
+    static constexpr int kTeams = k4 && C < 8 ? 2 : 1;
     // What an item's start and end cost, in slots: 4-bit slots are short enough for shares to
     // be weighed with it (256 13B-shaped sequences: teams with 18 items of a few slots took
     // 300,000 cycles, with 5 long ones 252,000).  It counts as lying before the item's slots.
-    static constexpr int kItemExtra = k4 ? 2 : 0;
+    static constexpr int kItemExtra = k4 ? 1 : 0;
     static constexpr int kThreads = kTeams * (kWarps + 1) * 32;
     static constexpr int kMT = D / 16;
     static constexpr int kStateRow = D + 4;              // floats per query row of a warp's state
@@ -208,6 +210,13 @@ __device__ __forceinline__ void codes4(uint32_t (&low)[4], uint32_t (&high)[4], 
         high[k] = kBytes && second ? w : w & (kBytes ? 0x00ff00ffu : 0x00f000f0u);
     }
 }
+// An 8 x 8 matrix of 16-bit elements, lane (g, t) holding (g, 2t) and (g, 2t + 1), transposed.
+__device__ __forceinline__ uint32_t transposed(uint32_t a) {
+    uint32_t d;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    return d;
+}
+
 // N words of scale and zero, neighbours in shared memory.
 template <int N>
 struct Words {
@@ -327,12 +336,13 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
     // A team's part of shared memory: ring, queries, states, slots' descriptions, barriers.
     const int team = TEAMS == 1 ? 0 : warp / (W + 1), tw = TEAMS == 1 ? warp : warp % (W + 1);
     const size_t team_slots = static_cast<size_t>(S) * L::kSlotBytes;
-    const size_t team_rest = kQueryRing * kQEntry * H + (W - H) * L::kStateBytes + W * 8 * sizeof(float2) +
+    const int states = L::k4 && H < W ? W : W - H;
+    const size_t team_rest = kQueryRing * kQEntry * H + states * L::kStateBytes + W * 8 * sizeof(float2) +
                              S * (sizeof(SlotMeta) + 16) + (2 * kQueryRing + 16) * 8;
     uint8_t *slots = smem + team * team_slots;
     uint8_t *qbuf = smem + TEAMS * team_slots + team * team_rest;
-    uint8_t *xbuf = qbuf + kQueryRing * kQEntry * H;   // (W - H) warp states
-    float2 *xml = reinterpret_cast<float2 *>(xbuf + (W - H) * L::kStateBytes);   // [warp][8]
+    uint8_t *xbuf = qbuf + kQueryRing * kQEntry * H;   // warp states
+    float2 *xml = reinterpret_cast<float2 *>(xbuf + states * L::kStateBytes);    // [warp][8]
     SlotMeta *meta = reinterpret_cast<SlotMeta *>(xml + W * 8);
     uint64_t *full = reinterpret_cast<uint64_t *>(meta + S);
     uint64_t *empty = full + S;
@@ -369,8 +379,8 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
             mbar_init(&qempty[i], W);
         }
         for (int i = 0; i < H; ++i) {
-            mbar_init(&xfull[i], max(1, nsubs - 1));
-            mbar_init(&xfree[i], 1);
+            mbar_init(&xfull[i], L::k4 ? nsubs : max(1, nsubs - 1));
+            mbar_init(&xfree[i], L::k4 ? nsubs : 1);
         }
         fence_barrier_init();
         prefetch_tensormap(&tmap_k);
@@ -770,6 +780,9 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
     //   1 query row:  the slot's stage t & 1; its V weights for group t >> 1
     //   2 query rows: row t & 1, stage t >> 1
     //   4: row t; 8: rows 2t and 2t + 1 (both columns); one stage after the other.
+    // A lane's weights are the columns 2t and 2t + 1 of the V product too, as the high and
+    // low part of one (8 rows: of the two rows, the low parts in a product of their own), so
+    // that its sums, references and results are of the same rows throughout.
     constexpr int NX = C == 8 ? 2 : 1, ZG = C == 1 ? 1 : L::kGroups;
     const int my_stage = C == 1 ? t & 1 : t >> 1, my_group = t >> 1;
     float qsum[L::kGroups][2];    // the sum of a group's query elements, as large as the products have them
@@ -1183,19 +1196,15 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                     for (int gr = 0; gr < ZG; ++gr) zs[gr][e] *= al[e];
                 }
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {       // of column 2t + e of the V product
-                    const float a = C == 8 ? al[e % NX] : __shfl_sync(kFull, al[0], (2 * t + e) & (C - 1));
+                for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        acc[mt][e] *= a;
-                        acc[mt][2 + e] *= a;
-                    }
-                }
+                    for (int e = 0; e < 4; ++e) acc[mt][e] *= al[C == 8 ? e & (NX - 1) : 0];
                 weigh();
             }
             // ---- weights with their scales as binary16 parts: the high and low part of one
             // column (8 rows: the two columns' high parts, and their low ones) ----
-            uint32_t ph[2][ZG], pl[2][ZG];
+            uint32_t ph[2][ZG];
+            [[maybe_unused]] uint32_t pl[2][ZG];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
 #pragma unroll
@@ -1216,32 +1225,31 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                     }
                 }
             }
-            // ---- PV: the weights of tokens 2t, 2t + 1, 2t + 8, 2t + 9 for column g, from where they were made ----
-            const uint32_t pick = (L::kPaired ? g < 4 : (g & 1) == 0) ? 0x5410u : 0x7632u;
+            // ---- PV: the weights transposed to tokens 2t, 2t + 1, 2t + 8, 2t + 9 of column g ----
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int gr = 0; gr < ZG; ++gr) {
+                    ph[k][gr] = transposed(ph[k][gr]);
+                    if constexpr (!L::kPaired) pl[k][gr] = transposed(pl[k][gr]);
+                }
 #pragma unroll
             for (int hs = 0; hs < NS; ++hs) {
 #pragma unroll
                 for (int gr = 0; gr < L::kGroups; ++gr) {
-                    const int src = 8 * t + (C == 1   ? hs + 2 * gr
-                                             : C == 2 ? (g & 1) + 2 * hs
-                                             : C == 4 ? g & 3
-                                                      : g >> 1);
-                    auto fragment = [&](const uint32_t(&p)[2][ZG], uint32_t (&f)[2]) {
-#pragma unroll
-                        for (int k = 0; k < 2; ++k)
-                            f[k] = __byte_perm(__shfl_sync(kFull, p[k][ZG == 1 ? 0 : gr], src),
-                                               __shfl_sync(kFull, p[k][ZG == 1 ? 0 : gr], src + 4), pick);
-                    };
-                    uint32_t a[4], low[4], high[4], w[2], wl[2];
+                    // (up to 2 rows: the columns made for this stage and group)
+                    const bool of = C == 1 ? (g >> 1) == hs + 2 * gr : C == 2 ? (g >> 2) == hs : true;
+                    uint32_t a[4], low[4], high[4], w[2];
                     ldsm_x4_trans(a, (stage + hs * stage_off + off_v) ^ (gr << 5));
-                    fragment(ph, w);
-                    if constexpr (!L::kPaired) fragment(pl, wl);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) w[k] = of ? ph[k][ZG == 1 ? 0 : gr] : 0u;
 #pragma unroll
                     for (int i = 0; i < 4; i += 2) {
                         codes4<true>(low, high, a, i > 0);
                         mma_f16(acc[4 * gr + i], low, w);
                         mma_f16(acc[4 * gr + i + 1], high, w);
                         if constexpr (!L::kPaired) {
+                            const uint32_t wl[2] = {pl[0][gr], pl[1][gr]};
                             mma_f16(acc[4 * gr + i], low, wl);
                             mma_f16(acc[4 * gr + i + 1], high, wl);
                         }
@@ -1270,7 +1278,8 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
 
         if (!(m.flags & kLast)) continue;
         // ---- item end ----
-        if constexpr (L::k4) {      // sums over low codes and over bytes: their powers of two off, the bytes' low codes too
+        if constexpr (L::k4) {
+            // sums over low codes and over bytes: their powers of two off, the bytes' low codes too
 #pragma unroll
             for (int mt = 0; mt < MT; mt += 2)
 #pragma unroll
@@ -1278,195 +1287,255 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                     acc[mt + 1][e] = (acc[mt + 1][e] - acc[mt][e]) * 0x1p20f;
                     acc[mt][e] *= 0x1p24f;
                 }
-        }
-        if constexpr (L::kPaired) {   // the low parts' columns (c + 4: lane t + 2) onto the high parts'
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int e = 0; e < NE; ++e) {
-                    acc[mt][e] += __shfl_xor_sync(kFull, acc[mt][e], 2);
-                    acc[mt][2 + e] += __shfl_xor_sync(kFull, acc[mt][2 + e], 2);
-                }
-        }
-        if constexpr (L::k4) {
-            // sums over the lanes that weighed for one query row, then everything by the
-            // columns 2t, 2t + 1 of the V product, the zeros' share of each group added
-            constexpr int kFirstLane = C == 1 ? 1 : C == 2 ? 2 : 4;
-            auto total = [&](float v) {
+            // sums over the lanes that weighed for one row
+            auto total = [&](float v, int first) {
                 if constexpr (C == 1) v += __shfl_xor_sync(kFull, v, 1);
+                if constexpr (C == 2) v += __shfl_xor_sync(kFull, v, 2);
 #pragma unroll
-                for (int o = C == 1 ? 4 : kFirstLane; o < 32; o <<= 1) v += __shfl_xor_sync(kFull, v, o);
+                for (int o = 4; o < first; o <<= 1) v += __shfl_xor_sync(kFull, v, o);
                 return v;
             };
-            float mo[2], lo[2], lt[NX];
 #pragma unroll
-            for (int e = 0; e < NX; ++e) lt[e] = total(l_run[e]);
+            for (int e = 0; e < NX; ++e) {
+                l_run[e] = total(l_run[e], 32);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int row = (2 * t + e) & (C - 1);       // lane `row` of the first four holds it (C < 8)
-                mo[e] = C == 8 ? m_run[e] : __shfl_sync(kFull, m_run[0], row);
-                lo[e] = C == 8 ? lt[e % NX] : __shfl_sync(kFull, lt[0], row);
+                for (int gr = 0; gr < ZG; ++gr) zs[gr][e] = total(zs[gr][e], 32);    // the zeros' share of a group's elements
             }
+            // My results, quads of neighbouring elements 4g .. 4g + 3 of a group's halves:
+            // 1 row: those of group t >> 1, else of every group.
+            constexpr int NQ = C == 1 ? 2 : 2 * L::kGroups;
+            auto quad = [&](int e, int i) {
+                const int gr = i >> 1, r = 2 * (i & 1);
+                float q[4];
 #pragma unroll
-            for (int gr = 0; gr < L::kGroups; ++gr) {
-                float z[NX];
-#pragma unroll
-                for (int e = 0; e < NX; ++e) z[e] = total(zs[ZG == 1 ? 0 : gr][e]);
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float ze = C == 8 ? z[e % NX] : __shfl_sync(kFull, z[0], C == 1 ? 2 * gr : (2 * t + e) & (C - 1));
-#pragma unroll
-                    for (int mt = 4 * gr; mt < 4 * gr + 4; ++mt) {
-                        acc[mt][e] += ze;
-                        acc[mt][2 + e] += ze;
-                    }
+                for (int j = 0; j < 4; ++j) {
+                    auto part = [&](int mt) { return C == 8 ? acc[mt][r + e] : acc[mt][r] + acc[mt][r + 1]; };
+                    float v = part(4 * gr + j);
+                    if constexpr (C == 1 && L::kGroups == 2)
+                        if (my_group) v = part(4 + j);
+                    q[j] = total(v, 4) + zs[gr][e];
                 }
-            }
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                m_run[e] = mo[e];
-                l_run[e] = lo[e];
-            }
-        } else {
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1)
-#pragma unroll
-                for (int e = 0; e < NE; ++e) l_run[e] += __shfl_xor_sync(kFull, l_run[e], o);
-        }
-        if (nsubs > 1) {
-            // join the states of the head's warps: the others hand theirs to the first
-            const uint32_t par = (citems - 1) & 1u;      // of this item
-            if (sub > 0) {
-                if (citems > 1 && !mbar_try_wait(&xfree[head], par ^ 1u) && !mbar_wait_bounded(&xfree[head], par ^ 1u)) {
-                    if (lane == 0) report(p.err_flag, 0x10 /* PA_FLAG_TIMEOUT */);
+                return make_float4(q[0], q[1], q[2], q[3]);
+            };
+            auto element = [&](int i) { return (C == 1 ? 64 * my_group + 32 * i : 64 * (i >> 1) + 32 * (i & 1)) + 4 * g; };
+            const bool writes = C == 1 ? (t & 1) == 0 && my_group < L::kGroups : C == 2 ? t < 2 : true;
+            auto row_of = [&](int e) { return C == 8 ? 2 * t + e : t & (C - 1); };
+            const bool tells = g == 0 && (C == 1 ? t == 0 : writes);
+            const int kvh = m.kvh0 + head;
+            const bool fin = (m.flags & kFinal) != 0;
+            // A row's reference and sum, and quads of it, into the output or a row of the workspace.
+            auto row_at = [&](int c) -> int64_t {
+                return (m.flags & kContinued)
+                           ? p.cut_row + cut_row_of(p, share, head, c)
+                           : (((static_cast<int64_t>(m.seq) * Hkv + kvh) * p.max_parts + p.part_off + m.part) << lg) + c;
+            };
+            auto tell_row = [&](int c, float ref, float l) {
+                if (fin && p.ws_ml == nullptr) return;
+                const bool more = (m.flags & kCut) != 0;
+                st_global_hint(p.ws_ml + 4 * row_at(c),
+                               make_float4(ref, l, __int_as_float(fin ? kRowFinal : more ? kRowCut : 0),
+                                           __int_as_float(more ? cut_row_of(p, share + 1, head, c) : 0)),
+                               keep);
+            };
+            auto put = [&](int64_t at, float4 q, float sc) {
+                if (!fin) {
+                    st_global_hint(p.ws_acc + at, q, keep);
                     return;
                 }
-                float *xs = reinterpret_cast<float *>(xbuf + (tw - H) * L::kStateBytes);
+                q = make_float4(q.x * sc, q.y * sc, q.z * sc, q.w * sc);
+                if (p.out_dtype == 2)
+                    *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at) = q;
+                else
+                    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + at) =
+                        p.out_dtype == 1 ? make_uint2(pack2<true>(q.x, q.y), pack2<true>(q.z, q.w))
+                                         : make_uint2(pack2<false>(q.x, q.y), pack2<false>(q.z, q.w));
+            };
+            auto out_at = [&](int c) {
+                return fin ? (static_cast<int64_t>(m.seq) * Hq + (kvh << lg) + c) * D : row_at(c) * D;
+            };
+            if (nsubs == 1) {
 #pragma unroll
-                for (int e = 0; e < NE; ++e) {
-                    const int c = 2 * t + e;
-                    if (c >= C) continue;
+                for (int e = 0; e < NX; ++e) {
+                    const int c = row_of(e);
+                    const float l = l_run[e], sc = l == 0.f ? 0.f : 1.f / l;
+                    if (tells) tell_row(c, m_run[e], l);
+                    const int64_t at = out_at(c);
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        xs[c * L::kStateRow + 16 * mt + g] = acc[mt][e];
-                        xs[c * L::kStateRow + 16 * mt + 8 + g] = acc[mt][2 + e];
+                    for (int i = 0; i < NQ; ++i) {
+                        const float4 q = quad(e, i);
+                        if (writes) put(at + element(i), q, sc);
                     }
-                    if (g == 0) xml[tw * 8 + c] = make_float2(m_run[e], l_run[e]);
                 }
-                __syncwarp();
-                if (lane == 0) arrive(&xfull[head]);
                 continue;
             }
+            // Warps that share a head: all put their states into shared memory, and each joins its
+            // share of the rows' quads.
+            const uint32_t par = (citems - 1) & 1u;          // of this item
+            if (citems > 1 && !mbar_try_wait(&xfree[head], par ^ 1u) && !mbar_wait_bounded(&xfree[head], par ^ 1u)) {
+                if (lane == 0) report(p.err_flag, 0x10 /* PA_FLAG_TIMEOUT */);
+                return;
+            }
+            {
+                float *xs = reinterpret_cast<float *>(xbuf + tw * L::kStateBytes);
+#pragma unroll
+                for (int e = 0; e < NX; ++e) {
+#pragma unroll
+                    for (int i = 0; i < NQ; ++i) {
+                        const float4 q = quad(e, i);
+                        if (writes) *reinterpret_cast<float4 *>(xs + row_of(e) * L::kStateRow + element(i)) = q;
+                    }
+                    if (tells) xml[tw * 8 + row_of(e)] = make_float2(m_run[e], l_run[e]);
+                }
+            }
+            __syncwarp();
+            if (lane == 0) arrive(&xfull[head]);
             if (!mbar_try_wait(&xfull[head], par) && !mbar_wait_bounded(&xfull[head], par)) {
                 if (lane == 0) report(p.err_flag, 0x10 /* PA_FLAG_TIMEOUT */);
                 return;
             }
-#pragma unroll
-            for (int e = 0; e < NE; ++e) {
-                const int c = 2 * t + e;
-                if (c >= C) continue;
-                float mn = m_run[e];
-                for (int k = 1; k < nsubs; ++k) mn = fmaxf(mn, xml[(tw + k * H) * 8 + c].x);
-                const float al = m_run[e] == -INFINITY ? 1.f : fast_exp2(m_run[e] - mn);
-                m_run[e] = mn;
-                l_run[e] *= al;
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    acc[mt][e] *= al;
-                    acc[mt][2 + e] *= al;
+            for (int i = sub * 32 + lane; i < C * D / 4; i += nsubs * 32) {
+                const int c = i / (D / 4), d = i % (D / 4) * 4;
+                float ref = -INFINITY, l = 0.f;
+                for (int k = 0; k < nsubs; ++k) ref = fmaxf(ref, xml[(head + k * H) * 8 + c].x);
+                float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int k = 0; k < nsubs; ++k) {
+                    const float2 ml = xml[(head + k * H) * 8 + c];
+                    const float be = ml.x == -INFINITY ? 1.f : fast_exp2(ml.x - ref);
+                    const float4 x =
+                        *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(xbuf + (head + k * H) * L::kStateBytes) +
+                                                          c * L::kStateRow + d);
+                    l = fmaf(ml.y, be, l);
+                    q = make_float4(fmaf(x.x, be, q.x), fmaf(x.y, be, q.y), fmaf(x.z, be, q.z), fmaf(x.w, be, q.w));
                 }
-                for (int k = 1; k < nsubs; ++k) {
-                    const float *xs = reinterpret_cast<const float *>(xbuf + (tw + (k - 1) * H) * L::kStateBytes) +
-                                      c * L::kStateRow + g;
-                    const float2 ml = xml[(tw + k * H) * 8 + c];
-                    const float be = ml.x == -INFINITY ? 1.f : fast_exp2(ml.x - mn);
-                    l_run[e] = fmaf(ml.y, be, l_run[e]);
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        acc[mt][e] = fmaf(xs[16 * mt], be, acc[mt][e]);
-                        acc[mt][2 + e] = fmaf(xs[16 * mt + 8], be, acc[mt][2 + e]);
-                    }
-                }
+                if (d == 0) tell_row(c, ref, l);
+                put(out_at(c) + d, q, l == 0.f ? 0.f : 1.f / l);
             }
             __syncwarp();
             if (lane == 0) arrive(&xfree[head]);
+            continue;
         }
-        const int kvh = m.kvh0 + head;
-        const bool fin = (m.flags & kFinal) != 0;
+        if constexpr (!L::k4) {
+            if constexpr (L::kPaired) {   // the low parts' columns (c + 4: lane t + 2) onto the high parts'
 #pragma unroll
-        for (int e = 0; e < NE; ++e) {
-            const int c = 2 * t + e;
-            if (c >= (members << lg)) continue;
-            const int64_t sq = m.seq + (c >> lg);
-            const int hq = c & ((1 << lg) - 1);
-            const float sc = fin ? (l_run[e] == 0.f ? 0.f : 1.f / l_run[e]) : 1.f;
-            const int64_t r =
-                (m.flags & kContinued)
-                    ? p.cut_row + cut_row_of(p, share, head, c)
-                    : (((sq * Hkv + kvh) * p.max_parts + p.part_off + m.part) << lg) + hq;
-            if (g == 0 && !(fin && p.ws_ml == nullptr)) {
-                const bool more = (m.flags & kCut) != 0;
-                st_global_hint(p.ws_ml + 4 * r,
-                               make_float4(m_run[e], l_run[e], __int_as_float(fin ? kRowFinal : more ? kRowCut : 0),
-                                           __int_as_float(more ? cut_row_of(p, share + 1, head, c) : 0)),
-                               keep);
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int e = 0; e < NE; ++e) {
+                        acc[mt][e] += __shfl_xor_sync(kFull, acc[mt][e], 2);
+                        acc[mt][2 + e] += __shfl_xor_sync(kFull, acc[mt][2 + e], 2);
+                    }
             }
-            const int64_t orow = fin ? (sq * Hq + (kvh << lg) + hq) * D : r * D;
-            auto put2 = [&](int d, float a, float b) {   // two consecutive elements
-                if (!fin)
-                    st_global_hint(p.ws_acc + orow + d, make_float2(a, b), keep);
-                else if (p.out_dtype == 2)
-                    *reinterpret_cast<float2 *>(static_cast<float *>(p.out) + orow + d) = make_float2(a, b);
-                else
-                    *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.out) + orow + d) =
-                        p.out_dtype == 1 ? pack2<true>(a, b) : pack2<false>(a, b);
-            };
-            auto put1 = [&](int d, float a) {
-                if (!fin)
-                    p.ws_acc[orow + d] = a;
-                else if (p.out_dtype == 2)
-                    static_cast<float *>(p.out)[orow + d] = a;
-                else
-                    static_cast<uint16_t *>(p.out)[orow + d] = p.out_dtype == 1 ? float_to_bf16_bits(a) : float_to_f16_bits(a);
-            };
-            if constexpr (L::k4) {
-                // four neighbouring elements at a time: the two halves of each group
-                constexpr int kQuads = 2 * L::kGroups;
-                auto quad = [&](int i) {
-                    const int mt = 4 * (i >> 1), r = 2 * (i & 1) + e;
-                    return make_float4(acc[mt][r] * sc, acc[mt + 1][r] * sc, acc[mt + 2][r] * sc, acc[mt + 3][r] * sc);
-                };
-                const int64_t at = orow + 4 * g;
-                if (!fin || p.out_dtype == 2) {
-                    float *o = (fin ? static_cast<float *>(p.out) : p.ws_acc) + at;
 #pragma unroll
-                    for (int i = 0; i < kQuads; ++i) {
-                        if (fin)
-                            *reinterpret_cast<float4 *>(o + 32 * i) = quad(i);
-                        else
-                            st_global_hint(o + 32 * i, quad(i), keep);
+            for (int o = 4; o < 32; o <<= 1)
+#pragma unroll
+                for (int e = 0; e < NE; ++e) l_run[e] += __shfl_xor_sync(kFull, l_run[e], o);
+            if (nsubs > 1) {
+                // join the states of the head's warps: the others hand theirs to the first
+                const uint32_t par = (citems - 1) & 1u;      // of this item
+                if (sub > 0) {
+                    if (citems > 1 && !mbar_try_wait(&xfree[head], par ^ 1u) && !mbar_wait_bounded(&xfree[head], par ^ 1u)) {
+                        if (lane == 0) report(p.err_flag, 0x10 /* PA_FLAG_TIMEOUT */);
+                        return;
+                    }
+                    float *xs = reinterpret_cast<float *>(xbuf + (tw - H) * L::kStateBytes);
+#pragma unroll
+                    for (int e = 0; e < NE; ++e) {
+                        const int c = 2 * t + e;
+                        if (c >= C) continue;
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt) {
+                            xs[c * L::kStateRow + 16 * mt + g] = acc[mt][e];
+                            xs[c * L::kStateRow + 16 * mt + 8 + g] = acc[mt][2 + e];
+                        }
+                        if (g == 0) xml[tw * 8 + c] = make_float2(m_run[e], l_run[e]);
+                    }
+                    __syncwarp();
+                    if (lane == 0) arrive(&xfull[head]);
+                    continue;
+                }
+                if (!mbar_try_wait(&xfull[head], par) && !mbar_wait_bounded(&xfull[head], par)) {
+                    if (lane == 0) report(p.err_flag, 0x10 /* PA_FLAG_TIMEOUT */);
+                    return;
+                }
+#pragma unroll
+                for (int e = 0; e < NE; ++e) {
+                    const int c = 2 * t + e;
+                    if (c >= C) continue;
+                    float mn = m_run[e];
+                    for (int k = 1; k < nsubs; ++k) mn = fmaxf(mn, xml[(tw + k * H) * 8 + c].x);
+                    const float al = m_run[e] == -INFINITY ? 1.f : fast_exp2(m_run[e] - mn);
+                    m_run[e] = mn;
+                    l_run[e] *= al;
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        acc[mt][e] *= al;
+                        acc[mt][2 + e] *= al;
+                    }
+                    for (int k = 1; k < nsubs; ++k) {
+                        const float *xs = reinterpret_cast<const float *>(xbuf + (tw + (k - 1) * H) * L::kStateBytes) +
+                                          c * L::kStateRow + g;
+                        const float2 ml = xml[(tw + k * H) * 8 + c];
+                        const float be = ml.x == -INFINITY ? 1.f : fast_exp2(ml.x - mn);
+                        l_run[e] = fmaf(ml.y, be, l_run[e]);
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt) {
+                            acc[mt][e] = fmaf(xs[16 * mt], be, acc[mt][e]);
+                            acc[mt][2 + e] = fmaf(xs[16 * mt + 8], be, acc[mt][2 + e]);
+                        }
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) arrive(&xfree[head]);
+            }
+            const int kvh = m.kvh0 + head;
+            const bool fin = (m.flags & kFinal) != 0;
+#pragma unroll
+            for (int e = 0; e < NE; ++e) {
+                const int c = 2 * t + e;
+                if (c >= (members << lg)) continue;
+                const int64_t sq = m.seq + (c >> lg);
+                const int hq = c & ((1 << lg) - 1);
+                const float sc = fin ? (l_run[e] == 0.f ? 0.f : 1.f / l_run[e]) : 1.f;
+                const int64_t r =
+                    (m.flags & kContinued)
+                        ? p.cut_row + cut_row_of(p, share, head, c)
+                        : (((sq * Hkv + kvh) * p.max_parts + p.part_off + m.part) << lg) + hq;
+                if (g == 0 && !(fin && p.ws_ml == nullptr)) {
+                    const bool more = (m.flags & kCut) != 0;
+                    st_global_hint(p.ws_ml + 4 * r,
+                                   make_float4(m_run[e], l_run[e], __int_as_float(fin ? kRowFinal : more ? kRowCut : 0),
+                                               __int_as_float(more ? cut_row_of(p, share + 1, head, c) : 0)),
+                                   keep);
+                }
+                const int64_t orow = fin ? (sq * Hq + (kvh << lg) + hq) * D : r * D;
+                auto put2 = [&](int d, float a, float b) {   // two consecutive elements
+                    if (!fin)
+                        st_global_hint(p.ws_acc + orow + d, make_float2(a, b), keep);
+                    else if (p.out_dtype == 2)
+                        *reinterpret_cast<float2 *>(static_cast<float *>(p.out) + orow + d) = make_float2(a, b);
+                    else
+                        *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.out) + orow + d) =
+                            p.out_dtype == 1 ? pack2<true>(a, b) : pack2<false>(a, b);
+                };
+                auto put1 = [&](int d, float a) {
+                    if (!fin)
+                        p.ws_acc[orow + d] = a;
+                    else if (p.out_dtype == 2)
+                        static_cast<float *>(p.out)[orow + d] = a;
+                    else
+                        static_cast<uint16_t *>(p.out)[orow + d] = p.out_dtype == 1 ? float_to_bf16_bits(a) : float_to_f16_bits(a);
+                };
+                if constexpr (k8) {
+#pragma unroll
+                    for (int vc = 0; vc < D / 32; ++vc) {
+                        put2(32 * vc + 2 * g, acc[2 * vc][e] * sc, acc[2 * vc + 1][e] * sc);
+                        put2(32 * vc + 16 + 2 * g, acc[2 * vc][2 + e] * sc, acc[2 * vc + 1][2 + e] * sc);
                     }
                 } else {
-                    uint16_t *o = static_cast<uint16_t *>(p.out) + at;
 #pragma unroll
-                    for (int i = 0; i < kQuads; ++i) {
-                        const float4 v = quad(i);
-                        *reinterpret_cast<uint2 *>(o + 32 * i) =
-                            p.out_dtype == 1 ? make_uint2(pack2<true>(v.x, v.y), pack2<true>(v.z, v.w))
-                                             : make_uint2(pack2<false>(v.x, v.y), pack2<false>(v.z, v.w));
+                    for (int mt = 0; mt < MT; ++mt) {
+                        put1(16 * mt + g, acc[mt][e] * sc);
+                        put1(16 * mt + g + 8, acc[mt][2 + e] * sc);
                     }
-                }
-            } else if constexpr (k8) {
-#pragma unroll
-                for (int vc = 0; vc < D / 32; ++vc) {
-                    put2(32 * vc + 2 * g, acc[2 * vc][e] * sc, acc[2 * vc + 1][e] * sc);
-                    put2(32 * vc + 16 + 2 * g, acc[2 * vc][2 + e] * sc, acc[2 * vc + 1][2 + e] * sc);
-                }
-            } else {
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    put1(16 * mt + g, acc[mt][e] * sc);
-                    put1(16 * mt + g + 8, acc[mt][2 + e] * sc);
                 }
             }
         }

@@ -169,15 +169,15 @@ __global__ void __launch_bounds__(256)
 
 template <int D, int CT>
 SplitSmem smem_for(int cols, int log2_heads, int entries) {
-    using L = SplitLayout<D, 1, CT>;
-    const int H = 1 << log2_heads;
+    using L = SplitLayout<D, 1, CT>;         // (a state's size is by its rows; teams are told here)
+    const int H = 1 << log2_heads, teams = CT == kCacheInt4 && cols == 8 ? SplitLayout<D, 8, CT>::kTeams : L::kTeams;
+    const int states = L::k4 && H < L::kWarps ? L::kWarps : L::kWarps - H;
     SplitSmem s;
     s.fixed = 1024 +
-              L::kTeams * (static_cast<size_t>(kQueryRing) * cols * D * 2 * H +
-                           static_cast<size_t>(L::kWarps - H) * cols * L::kStateBytes + L::kWarps * 8 * sizeof(float2) +
-                           (2 * kQueryRing + 16) * 8) +
+              teams * (static_cast<size_t>(kQueryRing) * cols * D * 2 * H + static_cast<size_t>(states) * cols * L::kStateBytes +
+                       L::kWarps * 8 * sizeof(float2) + (2 * kQueryRing + 16) * 8) +
               32 * 4 + static_cast<size_t>(entries) * 12 + 16;
-    s.slot = L::kTeams * (L::kSlotBytes + sizeof(SlotMeta) + 16);
+    s.slot = teams * (L::kSlotBytes + sizeof(SlotMeta) + 16);
     return s;
 }
 
