@@ -364,7 +364,7 @@ class _Runtime:
         self.codes = _Codes({torch.int8: PA_INT8, torch.uint8: PA_FP8_E4M3, torch.float8_e4m3fn: PA_FP8_E4M3})
         self.b16, self.f64 = torch.bfloat16, torch.float64
         self.f32, self.i32, self.i64, self.u8 = torch.float32, torch.int32, torch.int64, torch.uint8
-        self.current_device = torch.cuda.current_device
+        self.current_device = torch._C._cuda_getDevice      # (without the first-use checks: the tensors exist)
         self.capturing = torch.cuda.is_current_stream_capturing
         self.stream = torch._C._cuda_getCurrentRawStream
         self.empty = torch.empty

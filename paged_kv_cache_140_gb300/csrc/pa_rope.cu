@@ -28,7 +28,7 @@ namespace {
 
 using decode_common::launch_pdl;
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 128;
 constexpr int kRopeTokens = 4;       // tokens of a CTA at most
 
 // f / 2 pi, as a fraction of 2^64 (whole turns dropped).
@@ -51,11 +51,28 @@ __device__ __forceinline__ float2 cos_sin(int64_t position, double f, float fact
     return make_float2(c * factor, s * factor);
 }
 
-template <int D>
-__device__ __forceinline__ float group_sum(float v, uint32_t lanes) {
+// Sums over the LPR lanes of a row, of one value or of four at once: with four, halves and
+// then quarters of the lanes go on with two and then one of them, and every lane looks up all
+// four at the end.  `then`: applied to a sum once per lane that holds it.
+template <int LPR, typename Then>
+__device__ __forceinline__ void row_sums(float (&v)[1], int, uint32_t lanes, Then then) {
 #pragma unroll
-    for (int o = 1; o < D / 8; o <<= 1) v += __shfl_xor_sync(lanes, v, o);
-    return v;
+    for (int o = 1; o < LPR; o <<= 1) v[0] += __shfl_xor_sync(lanes, v[0], o);
+    v[0] = then(v[0]);
+}
+template <int LPR, typename Then>
+__device__ __forceinline__ void row_sums(float (&v)[4], int l, uint32_t lanes, Then then) {
+    const bool upper = l & (LPR / 2), odd = l & (LPR / 4);
+    float a = upper ? v[2] : v[0], b = upper ? v[3] : v[1];
+    a += __shfl_xor_sync(lanes, upper ? v[0] : v[2], LPR / 2);
+    b += __shfl_xor_sync(lanes, upper ? v[1] : v[3], LPR / 2);
+    float c = odd ? b : a;
+    c += __shfl_xor_sync(lanes, odd ? a : b, LPR / 4);
+#pragma unroll
+    for (int o = LPR / 8; o > 0; o >>= 1) c += __shfl_xor_sync(lanes, c, o);
+    c = then(c);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = __shfl_sync(lanes, c, (k & 2 ? LPR / 2 : 0) + (k & 1 ? LPR / 4 : 0), LPR);
 }
 
 // Codes of a row's eight values (four at elements oa, four at ob) into the cache.
@@ -140,6 +157,31 @@ __device__ __forceinline__ void write_codes(const RopeParams &p, int kind, int k
     *reinterpret_cast<uint32_t *>(base + row * D + ob) = code[1];
 }
 
+// Two floats in a register pair, for instructions that take both at once.
+struct F2 {
+    uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 both(F2 x) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x.v));
+    return r;
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+
 // (e0 e1)(e2 e3)(e4 e5)(e6 e7) -> (e0 e2)(e4 e6)(e1 e3)(e5 e7), and back.
 __device__ __forceinline__ void part_pairs(uint32_t (&x)[4]) {
     const uint32_t a = __byte_perm(x[0], x[1], 0x5410u), b = __byte_perm(x[2], x[3], 0x5410u);
@@ -164,7 +206,7 @@ template <int D, bool BF16, bool QUANT, int TB>
 __global__ void __launch_bounds__(kRopeThreads)
     rope_and_cache_kernel(const __grid_constant__ RopeParams p, int rows_per, int kind) {
     constexpr int LPR = D / 8, RG = kRopeThreads / LPR;
-    __shared__ __align__(16) float cos_t[TB][D / 2], sin_t[TB][D / 2];
+    __shared__ __align__(16) float cos_t[TB][D / 2], sin_t[TB][D / 2], neg_t[TB][D / 2];   // (neg: less the sine)
     __shared__ int64_t slot_t[TB];
     pdl_wait();
     pdl_launch_dependents();
@@ -207,6 +249,7 @@ __global__ void __launch_bounds__(kRopeThreads)
         const float2 cs = cos_sin(__ldg(p.positions + t0 + tok), __ldg(p.inv_freq + k), p.factor);
         cos_t[tok][k] = cs.x;
         sin_t[tok][k] = cs.y;
+        neg_t[tok][k] = -cs.y;
     }
     if (threadIdx.x < nt) {
         int64_t s = __ldg(p.slots + t0 + threadIdx.x);
@@ -223,65 +266,89 @@ __global__ void __launch_bounds__(kRopeThreads)
         const bool turns = w < 2 && turned, pairs = turns && p.interleaved, two = apart(w);
         const int oa = two ? 4 * l : 8 * l, ob = two ? half + 4 * l : 8 * l + 4;
         const bool norm = w < 2 && p.weight[w] != nullptr;
-        float wt[8];
+        F2 wt[4];
         if (norm) {
             const uint2 wa = __ldg(reinterpret_cast<const uint2 *>(p.weight[w] + oa));
             const uint2 wb = __ldg(reinterpret_cast<const uint2 *>(p.weight[w] + ob));
             uint32_t u[4] = {wa.x, wa.y, wb.x, wb.y};
             if (pairs) part_pairs(u);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float2 f = Half2x<BF16>::to_float2(u[k]);
-                wt[2 * k] = f.x;
-                wt[2 * k + 1] = f.y;
+            for (int j = 0; j < 4; ++j) {
+                const float2 f = Half2x<BF16>::to_float2(u[j]);
+                wt[j] = f2(f.x, f.y);
             }
         }
+        float size[TB];               // 1 / sqrt(mean x^2 + eps)
+        if (norm) {
+#pragma unroll
+            for (int k = 0; k < TB; ++k) {
+                F2 s = f2(0.f, 0.f);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 f = Half2x<BF16>::to_float2(x[k][j]);
+                    const F2 y = f2(f.x, f.y);
+                    s = fma2(y, y, s);
+                }
+                const float2 ss = both(s);
+                size[k] = ss.x + ss.y;
+            }
+            row_sums<LPR>(size, l, lanes, [&](float s) { return rsqrtf(s * (1.f / D) + p.eps); });
+        }
+        // where the row goes: the query's output, or from where slots are counted in the cache
+        uint16_t *const base = w == 0 ? p.out_q + (t0 * p.hq + head) * D
+                                      : static_cast<uint16_t *>(p.cache[w - 1]) + static_cast<int64_t>(head) * D;
+        const int64_t row = static_cast<int64_t>(w == 0 ? p.hq : p.hkv) * D;
 #pragma unroll
         for (int k = 0; k < TB; ++k) {
             if (k >= nt) break;
             if (pairs) part_pairs(x[k]);
-            float y[8];
+            F2 y[4];                      // turned lanes: elements (a0 a1)(a2 a3) and their partners (b0 b1)(b2 b3)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const float2 f = Half2x<BF16>::to_float2(x[k][j]);
-                y[2 * j] = f.x;
-                y[2 * j + 1] = f.y;
+                y[j] = f2(f.x, f.y);
             }
             if (norm) {
-                float ss = 0.f;
+                const F2 s2 = f2(size[k], size[k]);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) ss = fmaf(y[j], y[j], ss);
-                const float s = rsqrtf(group_sum<D>(ss, lanes) * (1.f / D) + p.eps);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) y[j] *= s * wt[j];
+                for (int j = 0; j < 4; ++j) y[j] = y[j] * (s2 * wt[j]);
             }
             if (turns) {
                 const float4 c = *reinterpret_cast<const float4 *>(&cos_t[k][4 * l]);
                 const float4 s = *reinterpret_cast<const float4 *>(&sin_t[k][4 * l]);
-                const float cc[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
+                const float4 n = *reinterpret_cast<const float4 *>(&neg_t[k][4 * l]);
+                const F2 cc[2] = {f2(c.x, c.y), f2(c.z, c.w)}, sn[2] = {f2(s.x, s.y), f2(s.z, s.w)};
+                const F2 ng[2] = {f2(n.x, n.y), f2(n.z, n.w)};
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float a = y[j], b = y[j + 4];
-                    y[j] = a * cc[j] - b * sn[j];
-                    y[j + 4] = b * cc[j] + a * sn[j];
+                for (int j = 0; j < 2; ++j) {
+                    const F2 a = y[j], b = y[j + 2];
+                    y[j] = fma2(b, ng[j], a * cc[j]);
+                    y[j + 2] = fma2(a, sn[j], b * cc[j]);
                 }
             }
             const int64_t slot = slot_t[k];
             if (QUANT && w > 0) {
+                const float2 v0 = both(y[0]), v1 = both(y[1]), v2 = both(y[2]), v3 = both(y[3]);
+                float z[8] = {v0.x, v0.y, v1.x, v1.y, v2.x, v2.y, v3.x, v3.y};
                 if (pairs) {          // back into the row's order
-                    const float z[8] = {y[0], y[4], y[1], y[5], y[2], y[6], y[3], y[7]};
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) y[j] = z[j];
+                    z[1] = v2.x;
+                    z[2] = v0.y;
+                    z[3] = v2.y;
+                    z[4] = v1.x;
+                    z[5] = v3.x;
+                    z[6] = v1.y;
                 }
-                if (slot >= 0) write_codes<D>(p, kind, w - 1, y, oa, ob, l, head, slot, lanes);
+                if (slot >= 0) write_codes<D>(p, kind, w - 1, z, oa, ob, l, head, slot, lanes);
                 continue;
             }
-            uint16_t *out = w == 0 ? p.out_q + ((t0 + k) * p.hq + head) * D
-                                   : static_cast<uint16_t *>(p.cache[w - 1]) + (slot * p.hkv + head) * D;
             uint32_t h[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) h[j] = pack2<BF16>(y[2 * j], y[2 * j + 1]);
+            for (int j = 0; j < 4; ++j) {
+                const float2 f = both(y[j]);
+                h[j] = pack2<BF16>(f.x, f.y);
+            }
             if (pairs) join_pairs(h);
+            uint16_t *const out = base + (w == 0 ? k : slot) * row;
             if (w == 0 || slot >= 0) {
                 if (two) {
                     *reinterpret_cast<uint2 *>(out + oa) = make_uint2(h[0], h[1]);
