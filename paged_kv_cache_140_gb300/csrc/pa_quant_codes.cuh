@@ -4,6 +4,7 @@
 #pragma once
 
 #include "pa_device.cuh"
+#include "pa_f32x2.cuh"
 
 namespace pa {
 
@@ -72,9 +73,9 @@ __device__ __forceinline__ Group4 group4(float lo, float hi, bool finite) {
 // once 1.5 2^23 is added) is cut off there as a 16-bit number.
 __device__ __forceinline__ uint32_t codes4_pair(float x0, float x1, const Group4 &g) {
     constexpr float k = 12582912.f;
-    const uint32_t a = __float_as_uint(__fadd_rn(__fsub_rn(__fmul_rn(x0, g.inv), g.zero), k));
-    const uint32_t b = __float_as_uint(__fadd_rn(__fsub_rn(__fmul_rn(x1, g.inv), g.zero), k));
-    uint32_t v = __byte_perm(a, b, 0x5410u);
+    // (the products one by one: a packed one and the sum behind it come out as one rounding)
+    const float2 y = both(f2(__fmul_rn(x0, g.inv), __fmul_rn(x1, g.inv)) + f2(-g.zero, -g.zero) + f2(k, k));
+    uint32_t v = __byte_perm(__float_as_uint(y.x), __float_as_uint(y.y), 0x5410u);
     asm("max.s16x2 %0, %0, %1;" : "+r"(v) : "r"(0u));
     asm("min.s16x2 %0, %0, %1;" : "+r"(v) : "r"(0x000f000fu));
     return v;

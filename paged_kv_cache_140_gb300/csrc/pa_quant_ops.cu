@@ -387,9 +387,10 @@ cudaError_t write_t(const QuantWrite &p, int sms, cudaStream_t stream) {
 template <int D, bool BF16>
 cudaError_t write4_t(const QuantWrite &p, int sms, cudaStream_t stream) {
     constexpr int RPB = kThreads / (D / 16);
-    const uint32_t blocks4 = (p.rows + RPB * 4 - 1) / (RPB * 4);
-    if (blocks4 * 2 >= static_cast<uint32_t>(8 * sms))
-        return launch_pdl(quant4_write_kernel<D, BF16, 4>, dim3(blocks4, 2), dim3(kThreads), 0, stream, p);
+    // Two rows per thread once that still gives every SM 8 blocks (four are no faster).
+    const uint32_t blocks2 = (p.rows + RPB * 2 - 1) / (RPB * 2);
+    if (blocks2 * 2 >= static_cast<uint32_t>(8 * sms))
+        return launch_pdl(quant4_write_kernel<D, BF16, 2>, dim3(blocks2, 2), dim3(kThreads), 0, stream, p);
     return launch_pdl(quant4_write_kernel<D, BF16, 1>, dim3((p.rows + RPB - 1) / RPB, 2), dim3(kThreads), 0, stream, p);
 }
 

@@ -19,6 +19,7 @@
 // share them), while each lane's first rows are on their way.
 #include "pa_decode_common.cuh"
 #include "pa_device.cuh"
+#include "pa_f32x2.cuh"
 #include "pa_quant_codes.cuh"
 #include "pa_step_ops.h"
 
@@ -155,31 +156,6 @@ __device__ __forceinline__ void write_codes(const RopeParams &p, int kind, int k
     }
     *reinterpret_cast<uint32_t *>(base + row * D + oa) = code[0];
     *reinterpret_cast<uint32_t *>(base + row * D + ob) = code[1];
-}
-
-// Two floats in a register pair, for instructions that take both at once.
-struct F2 {
-    uint64_t v;
-};
-__device__ __forceinline__ F2 f2(float a, float b) {
-    F2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ float2 both(F2 x) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x.v));
-    return r;
-}
-__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
-    F2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-    F2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return r;
 }
 
 // (e0 e1)(e2 e3)(e4 e5)(e6 e7) -> (e0 e2)(e4 e6)(e1 e3)(e5 e7), and back.
