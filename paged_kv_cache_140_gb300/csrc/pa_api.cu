@@ -872,6 +872,9 @@ pa_status run_split(pa::SplitParams p, int cache, int head_dim, int cols, int en
         p.stages = static_cast<int>(std::min<size_t>(8, (room - need.fixed) / need.slot));
         const size_t smem = need.fixed + p.stages * need.slot;
         const int grid = static_cast<int>(std::min<int64_t>(std::min(dev.sms, pa::kSplitMaxCtas), p.entries * per_entry));
+        p.part_div = pa::divisor(p.partition_size);
+        p.block_div = pa::divisor(p.block_size);
+        p.share_div = pa::divisor(grid * pa::split_teams(cols, cache));
         auto launch = cache == pa::kCacheF16    ? pa::launch_split_f16
                       : cache == pa::kCacheBF16 ? pa::launch_split_bf16
                       : cache == pa::kCacheE4M3 ? pa::launch_split_e4m3
@@ -1022,9 +1025,9 @@ pa_status quant_decode(void *out, pa_dtype out_dtype, const void *query, pa_dtyp
                                      num_kv_heads, head_dim, block_size, num_blocks, scale);
     if (st != PA_OK) return st;
     if (!quant_slots_ok(cache, num_blocks, block_size, num_kv_heads)) return PA_ERR_UNSUPPORTED;
-    // 4-bit caches: an item weighs up to two units more than its slots
+    // 4-bit caches: an item weighs one unit more than its slots
     if (cache == pa::kCacheInt4 && static_cast<int64_t>(num_kv_heads) * (max_context_len / 16 + 1) *
-                                           std::min(num_seqs, kSplitEntries) >= (int64_t{1} << 30))
+                                           std::min(num_seqs, kSplitEntries) >= (int64_t{1} << 30))     // (so that their sum stays below 2^31)
         return PA_ERR_UNSUPPORTED;
     SplitPlan w;
     if (!plan_split(num_seqs, num_heads, num_kv_heads, head_dim, block_size, max_context_len, partition_size, cache,

@@ -8,6 +8,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "pa_divisor.cuh"
+
 namespace pa {
 
 // Cache element types of the split kernels.  The 8-bit ones carry one float
@@ -45,6 +47,7 @@ struct SplitParams {
     int64_t num_blocks;
     float scale_log2;            // softmax scale * log2(e)
     int partition_size;          // tokens per partition, a multiple of 16, at most 32 blocks
+    Divisor part_div, block_div, share_div;   // by the partition, the block, and the launch's shares (CTAs, teams of them)
     int max_parts;               // partial results per (sequence, KV head) in the workspace
     int part_off;                // where this launch's start among them
     // Workspace rows: one per (sequence, KV head, part, head of the group), then
@@ -87,6 +90,9 @@ inline int split_log2_heads(int num_kv_heads) {
     while (l < 3 && num_kv_heads % (2 << l) == 0) ++l;
     return l;
 }
+
+// Teams of a CTA, each with a share of a launch's work.
+int split_teams(int cols, int cache);
 
 // 16-token stages of one ring slot (a slot feeds every consumer warp once).
 int split_slot_stages(int cache, int log2_heads);

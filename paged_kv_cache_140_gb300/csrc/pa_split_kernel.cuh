@@ -290,10 +290,13 @@ struct ItemCursor {
     uint32_t start;
 };
 
-__device__ __forceinline__ int item_slots(int len, int part, int P, int SW) {
+// (Divisions by the partition's, the block's and the shares' number are products; slots
+// hold 2^lsw stages.  With the compiler's 32- and 64-bit divisions this bookkeeping took
+// 2 us of a call.)
+__device__ __forceinline__ int item_slots(int len, int part, int P, int lsw) {
     const int n = len - part * P;
-    const int st = n > 0 ? (min(P, n) + kStageTokens - 1) / kStageTokens : 1;
-    return (st + SW - 1) / SW;
+    const int st = n > 0 ? (min(P, n) + kStageTokens - 1) >> 4 : 1;
+    return (st + (1 << lsw) - 1) >> lsw;
 }
 
 // Modes in which a list of one partition is the whole result.
@@ -301,11 +304,12 @@ __device__ __forceinline__ bool final_mode(int mode) { return mode == kSplitDeco
 
 // EX: what an item costs beyond its slots, in slots.
 template <int EX>
-__device__ __forceinline__ uint32_t entry_weight(int len, int mode, int ngroups, int P, int SW) {
-    if (len <= 0) return final_mode(mode) ? static_cast<uint32_t>(ngroups * (1 + EX)) : 0u;
-    const int full = (len - 1) / P;   // partitions before the last
+__device__ __forceinline__ uint32_t entry_weight(const SplitParams &p, int len, int ngroups, int lsw) {
+    if (len <= 0) return final_mode(p.mode) ? static_cast<uint32_t>(ngroups * (1 + EX)) : 0u;
+    const int P = p.partition_size;
+    const int full = static_cast<int>(divided(static_cast<uint32_t>(len - 1), p.part_div));   // partitions before the last
     return static_cast<uint32_t>(ngroups) *
-           static_cast<uint32_t>(full * ((P / kStageTokens + SW - 1) / SW + EX) + item_slots(len, full, P, SW) + EX);
+           static_cast<uint32_t>(full * (item_slots(P, 0, P, lsw) + EX) + item_slots(len, full, P, lsw) + EX);
 }
 
 template <int D, int C, int CT>
@@ -327,6 +331,9 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
     const int P = p.partition_size, bs = p.block_size, mode = p.mode, lg = p.log2_group;
     const int H = 1 << p.log2_heads, ngroups = Hkv >> p.log2_heads;
     const int SW = L::kTiles >> p.log2_heads;          // stages per slot
+    constexpr int kLog2Tiles = L::kTiles == 8 ? 3 : 4;
+    static_assert(L::kTiles == 1 << kLog2Tiles && kStageTokens == 16, "");
+    const int lsw = kLog2Tiles - p.log2_heads;
     const int nsubs = W >> p.log2_heads;               // consumer warps per head
     const int RB = min(bs, kStageTokens);              // rows per box
     const int per_stage = kStageTokens / RB;           // boxes (blocks) per stage
@@ -369,22 +376,27 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
     const int log2_row_heads = L::k4 ? min(p.log2_heads, D == 128 ? 1 : 2) : 0;
     const uint32_t rowB = static_cast<uint32_t>(L::kRowB) << log2_row_heads;
 
-    if (lane == 0 && tw == 0) {
-        for (int i = 0; i < S; ++i) {
-            mbar_init(&full[i], lane_copies ? 33 : 1);
-            mbar_init(&empty[i], W);
-        }
-        for (int i = 0; i < kQueryRing; ++i) {
-            mbar_init(&qfull[i], 1);
-            mbar_init(&qempty[i], W);
-        }
-        for (int i = 0; i < H; ++i) {
+    if (tw == 0) {                 // the barriers, by the lanes of a team's first warp (8 of each kind at most)
+        const int i = lane & 7;
+        if (lane < 8) {
+            if (i < S) {
+                mbar_init(&full[i], lane_copies ? 33 : 1);
+                mbar_init(&empty[i], W);
+            }
+        } else if (lane < 16) {
+            if (i < kQueryRing) {
+                mbar_init(&qfull[i], 1);
+                mbar_init(&qempty[i], W);
+            }
+        } else if (lane < 24 && i < H) {
             mbar_init(&xfull[i], L::k4 ? nsubs : max(1, nsubs - 1));
             mbar_init(&xfree[i], L::k4 ? nsubs : 1);
         }
         fence_barrier_init();
-        prefetch_tensormap(&tmap_k);
-        prefetch_tensormap(&tmap_v);
+        if (lane == 0) prefetch_tensormap(&tmap_k);
+        if (lane == 1) prefetch_tensormap(&tmap_v);
+        if (scale_boxes && lane == 2) prefetch_tensormap(&tmap_ks);
+        if (scale_boxes && lane == 3) prefetch_tensormap(&tmap_vs);
     }
     // Launched with programmatic dependent launch.  late_wait: the previous kernel is
     // this call's prefix kernel (or an earlier launch of this one behind it), whose
@@ -459,7 +471,7 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
         const int per = (E + nthr - 1) / nthr;
         const int beg = min(E, static_cast<int>(threadIdx.x) * per), end = min(E, beg + per);
         uint32_t local = 0;
-        for (int i = beg; i < end; ++i) local += entry_weight<EX>(len_s[i], mode, ngroups, P, SW);
+        for (int i = beg; i < end; ++i) local += entry_weight<EX>(p, len_s[i], ngroups, lsw);
         uint32_t incl = local;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -472,7 +484,7 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
         for (int w = 0; w < warp; ++w) run += warp_tot[w];
         for (int i = beg; i < end; ++i) {
             prefix[i] = run;
-            run += entry_weight<EX>(len_s[i], mode, ngroups, P, SW);
+            run += entry_weight<EX>(p, len_s[i], ngroups, lsw);
         }
         if (threadIdx.x == 0) {
             uint32_t tot = 0;
@@ -487,9 +499,12 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
     // result of its own, named in the item's.
     const uint32_t total = prefix[E];
     const uint32_t shares = gridDim.x * TEAMS, share = blockIdx.x * TEAMS + team;
-    const bool cut = p.cut && total >= shares * static_cast<uint32_t>((P / kStageTokens + SW - 1) / SW + EX);
-    const uint32_t lo = static_cast<uint32_t>(static_cast<uint64_t>(total) * share / shares);
-    const uint32_t hi = static_cast<uint32_t>(static_cast<uint64_t>(total) * (share + 1) / shares);
+    const uint32_t full_slots = static_cast<uint32_t>(item_slots(P, 0, P, lsw) + EX);    // of a whole partition
+    const bool cut = p.cut && total >= shares * full_slots;
+    // total share / shares, rounded down
+    const uint32_t each = divided(total, p.share_div), left = total - each * shares;
+    const uint32_t lo = each * share + divided(left * share, p.share_div);
+    const uint32_t hi = each * (share + 1) + divided(left * (share + 1), p.share_div);
 
     if (tw == W) {
         // ------------------------------------------------------------ producer
@@ -499,11 +514,11 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
         auto set_entry = [&](int e) {
             ic.e = e;
             ic.len = len_s[e];
-            ic.nparts = ic.len > 0 ? (ic.len + P - 1) / P : 1;
+            ic.nparts = ic.len > 0 ? static_cast<int>(divided(static_cast<uint32_t>(ic.len + P - 1), p.part_div)) : 1;
         };
         auto set_part = [&](int part) {
             ic.part = part;
-            ic.nslots = item_slots(ic.len, part, P, SW);
+            ic.nslots = item_slots(ic.len, part, P, lsw);
         };
         auto advance = [&]() {
             ic.start += ic.nslots + EX;
@@ -529,7 +544,7 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                 if (prefix[m] <= lo) a = m; else b = m;
             }
             set_entry(a);
-            const uint32_t pw = static_cast<uint32_t>(ngroups) * static_cast<uint32_t>((P / kStageTokens + SW - 1) / SW + EX);
+            const uint32_t pw = static_cast<uint32_t>(ngroups) * full_slots;
             const uint32_t off = lo - prefix[a];
             set_part(min(ic.nparts - 1, static_cast<int>(off / pw)));
             const uint32_t pstart = prefix[a] + static_cast<uint32_t>(ic.part) * pw;
@@ -557,10 +572,10 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
             }
             t0 = ic.part * P;
             ntok = max(0, min(P, ic.len - t0));
-            fb = t0 / bs;
+            fb = static_cast<int>(divided(static_cast<uint32_t>(t0), p.block_div));
             if (mode == kSplitWhole && fb + lane < shared_blocks(p, seq, ic.len, false)) row = aux_s[ic.e];
             bid = -1;
-            if (ntok > 0 && lane <= (t0 + ntok - 1) / bs - fb)
+            if (ntok > 0 && lane <= static_cast<int>(divided(static_cast<uint32_t>(t0 + ntok - 1), p.block_div)) - fb)
                 bid = __ldg(p.block_tables + static_cast<int64_t>(row) * p.max_blocks_per_seq + blk0 + fb + lane);
         };
         // The slot's pieces are RB rows of one block (SW * per_stage of them, at most 32), one
@@ -569,7 +584,7 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
         const uint32_t box = static_cast<uint32_t>(RB * L::kRowB) << p.log2_heads;
         const uint32_t piece_off = per_stage == 1 ? lane * (box * L::kHalves)
                                                   : (lane >> 1) * (2 * box * L::kHalves) + (lane & 1) * box;
-        const int step_blocks = SW * kStageTokens / bs, step_rows = SW * kStageTokens % bs;
+        const int step_blocks = static_cast<int>(divided(SW * kStageTokens, p.block_div)), step_rows = SW * kStageTokens - step_blocks * bs;
         int islot = 0;
         uint32_t uses = 0, items = 0, phase = 1;       // phase: of the wait for a slot, once the ring has been gone round
         bool ok = true;
@@ -626,7 +641,7 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                                                                   : 0;
             // my piece's block (of the partition's) and its first row in it
             const int first = jb * SW * kStageTokens + (t0 - fb * bs) + lane * RB;
-            int pblk = first / bs, prow = first - pblk * bs;
+            int pblk = static_cast<int>(divided(static_cast<uint32_t>(first), p.block_div)), prow = first - pblk * bs;
             for (int j = jb; j < je; ++j) {
                 const int slot = take_slot();
                 if (!ok) break;

@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(256)
 template <int D, int CT>
 SplitSmem smem_for(int cols, int log2_heads, int entries) {
     using L = SplitLayout<D, 1, CT>;         // (a state's size is by its rows; teams are told here)
-    const int H = 1 << log2_heads, teams = CT == kCacheInt4 && cols == 8 ? SplitLayout<D, 8, CT>::kTeams : L::kTeams;
+    const int H = 1 << log2_heads, teams = split_teams(cols, CT);
     const int states = L::k4 && H < L::kWarps ? L::kWarps : L::kWarps - H;
     SplitSmem s;
     s.fixed = 1024 +
@@ -192,6 +192,11 @@ SplitSmem split_smem(int head_dim, int cols, int cache, int log2_heads, int entr
                                : smem_for<64, kCacheInt8>(cols, log2_heads, entries);
     return head_dim == 128 ? smem_for<128, kCacheF16>(cols, log2_heads, entries)
                            : smem_for<64, kCacheF16>(cols, log2_heads, entries);
+}
+
+int split_teams(int cols, int cache) {
+    if (cache != kCacheInt4) return 1;
+    return cols == 8 ? SplitLayout<128, 8, kCacheInt4>::kTeams : SplitLayout<128, 1, kCacheInt4>::kTeams;
 }
 
 int split_slot_stages(int cache, int log2_heads) {
