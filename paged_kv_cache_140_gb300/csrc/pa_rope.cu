@@ -17,6 +17,13 @@
 // so that no element changes lanes.  A CTA takes one or four tokens' rows, its threads
 // first make the tokens' sines and cosines (once per token, not per head: 40 heads
 // share them), while each lane's first rows are on their way.
+//
+// Measured (GB300, in a graph): 8,192 tokens of 32 query and 8 KV heads of 128, bf16, with
+// norms 37.6 us, 0.80 of the measured copy rate (35.0 without norms, 136 for four times the
+// tokens, 0.89; copying as many bytes takes 31); 256 tokens of 40 + 40 heads 5.6 us; 4 tokens
+// of 4 + 4 heads 1.9.  Steps: rows of any token to any lane 64 us; a row of four tokens at a
+// time 43; their four sums of squares reduced together (9 shuffles in place of 16) 41;
+// CTAs of 128 threads 38.  Eight tokens at a time take 52.
 #include "pa_decode_common.cuh"
 #include "pa_device.cuh"
 #include "pa_f32x2.cuh"

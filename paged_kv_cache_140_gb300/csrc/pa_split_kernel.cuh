@@ -1,5 +1,6 @@
-// Split decode attention over a paged cache: 16-bit caches, and 8-bit caches
-// (e4m3 or int8 codes) with one scale per token and KV head.
+// Split decode attention over a paged cache: 16-bit caches, 8-bit caches (e4m3 or
+// int8 codes) with one scale per token and KV head, and 4-bit caches (codes of 0 to 15)
+// with a scale and a zero per 64 elements of them.
 //
 // For query row q of an entry and the entry's tokens p, with code rows c_p and
 // scales k_p, v_p (1 for 16-bit caches):
@@ -25,6 +26,13 @@
 // scaled per row by a power of two to a largest element in [1, 2) (undone on
 // the logits), so that a bfloat16 query of any size fits.
 //
+// 4-bit codes u of group r stand for s_pr (u + z_pr), and everything but the codes is
+// taken out of the products, Q_r being the sum of q's elements in the group:
+//     x_p = scale sum_r s_pr (<q_r, u_pr> + z_pr Q_r),
+//     acc_r = sum (2^(s_p - m) s_pr) u_pr + sum (2^(s_p - m) s_pr) z_pr,
+// the reference following the larger of a token's V scales.  What the codes cost is
+// said at codes4, which lane weighs what where the consumers begin.
+//
 // What bounds it: reading the cache.  One producer warp brings ring slots in by
 // TMA (boxes of up to 8 KV heads: 16 rows of one physical block of each land as
 // one swizzled tile) and, for 8-bit caches, the scales, as boxes too where 4 or 8
@@ -42,6 +50,20 @@
 // that scales are cost 7 %, as 32-byte pieces.  Tried and slower: 16 consumer warps
 // (240 us against 221 at that time), one stage per slot (277), two ring slots instead
 // of three (241), a warp that prefetches slots into L2 (2 ahead 220, 8 ahead 296).
+//
+// 4-bit codes (in a graph, join included): the 13B-shaped batch 116 us, 0.83; the long
+// contexts 85, 0.81, of which 9 us pass before the first slot is there and 5 in the join.
+// Half the bytes of 8 bits for as many products: with the 8-bit consumer's shuffles and
+// conversions 198 and 129.  What it took: lanes that weigh logits of their own and codes that
+// enter the products unconverted (-9 and -5 %), two teams of 8 consumers in a CTA (-17 %, long
+// contexts none), three operations in place of five per eight codes (-5 %), the bookkeeping of
+// slots and shares without divisions (-5 %), shares weighed with items' ends (-4 %), weights
+// transposed by movmatrix (long contexts -2 %).  Tried and slower: three ring slots for each
+// team instead of two (150 us against 146 after a flush, long contexts 89 against 85 in a graph:
+// more requests in flight only queue), queries read from memory to make room for them, 16
+// consumers on one ring (250 against 226: 96 registers and a state each to join), two sets of
+// consumers that take one item's slots in turn (304 against 207).  Four producer warps for one
+// team took it from 207 to 191 before its bookkeeping was made shorter.
 // Waits are bounded (2 s) and report PA_FLAG_TIMEOUT.
 #pragma once
 
@@ -69,7 +91,7 @@ struct SplitLayout {
     static constexpr int kSub = k8 ? 2 : 1;              // stages per consumer warp and slot
     // Up to 4 query rows leave half of the products' 8 columns free: the weights'
     // high parts take columns 0-3 and their low parts columns 4-7 (the queries are
-    // repeated there), one product in place of two.
+    // repeated there), one product in place of two.  (4-bit codes: even and odd columns.)
     static constexpr bool kPaired = C <= 4;
     static constexpr int kTiles = kWarps * kSub;         // (stage, head) tiles of a slot
     static constexpr int kRowB = kRow < 128 ? kRow : 128;         // bytes of one box row

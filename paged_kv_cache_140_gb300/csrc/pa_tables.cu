@@ -18,6 +18,9 @@
 // neighbours at a time, which find their sequences together.  The tokens' slots and
 // positions follow from what this wrote: by the same CTA where there is one and few
 // tokens, else by a second kernel on all SMs.
+//
+// Measured (GB300, in a graph): 4 sequences 2.8 us, 256 that gain 6,561 tokens 7.0, 4,096 that
+// gain 54,240 14.7.  With the tokens on the cluster's 8 SMs too the last took 20 to 22.
 #include "pa_decode_common.cuh"
 #include "pa_device.cuh"
 #include "pa_step_ops.h"
@@ -274,7 +277,8 @@ __global__ void __launch_bounds__(256) token_slots_kernel(const __grid_constant_
 
 cudaError_t launch_update_tables(const TablesParams &p, cudaStream_t stream) {
     const size_t smem = static_cast<size_t>(p.num_seqs) * 5 * sizeof(int32_t);
-    // One CTA alone up to 1,024 sequences and 2,048 tokens; above, the tokens' kernel behind it,
+    // One CTA alone up to 1,024 sequences and 2,048 tokens (two rounds of its threads); above, the
+    // tokens' kernel behind it (256 sequences, 6,561 tokens: 7.0 us, all in a cluster of 8 9.3),
     // and 8 CTAs for more sequences than one has threads.
     const bool fused = p.num_seqs <= kTableThreads && p.num_tokens <= 2 * kTableThreads;
     const unsigned ctas = p.num_seqs <= kTableThreads ? 1 : 8;
