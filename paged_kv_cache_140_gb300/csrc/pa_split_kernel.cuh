@@ -51,14 +51,15 @@
 // (240 us against 221 at that time), one stage per slot (277), two ring slots instead
 // of three (241), a warp that prefetches slots into L2 (2 ahead 220, 8 ahead 296).
 //
-// 4-bit codes (in a graph, join included): the 13B-shaped batch 116 us, 0.83; the long
-// contexts 85, 0.81, of which 9 us pass before the first slot is there and 5 in the join.
+// 4-bit codes (in a graph, join included): the 13B-shaped batch 122 us, 0.79; the long
+// contexts 92, 0.75, of which 9 us pass before the first slot is there and 5 in the join.
 // Half the bytes of 8 bits for as many products: with the 8-bit consumer's shuffles and
 // conversions 198 and 129.  What it took: lanes that weigh logits of their own and codes that
 // enter the products unconverted (-9 and -5 %), two teams of 8 consumers in a CTA (-17 %, long
 // contexts none), three operations in place of five per eight codes (-5 %), the bookkeeping of
 // slots and shares without divisions (-5 %), shares weighed with items' ends (-4 %), weights
-// transposed by movmatrix (long contexts -2 %).  Tried and slower: three ring slots for each
+// transposed by movmatrix (long contexts -2 %); 116 and
+// 85 then, and V's sums kept small, for their accuracy, +5 and +9 %.  Tried and slower: three ring slots for each
 // team instead of two (150 us against 146 after a flush, long contexts 89 against 85 in a graph:
 // more requests in flight only queue), queries read from memory to make room for them, 16
 // consumers on one ring (250 against 226: 96 registers and a state each to join), two sets of
@@ -230,6 +231,20 @@ __device__ __forceinline__ void codes4(uint32_t (&low)[4], uint32_t (&high)[4], 
         const uint32_t w = second ? __byte_perm(a[k], 0u, 0x4341u) : a[k];
         low[k] = w & 0x000f000fu;
         high[k] = kBytes && second ? w : w & (kBytes ? 0x00ff00ffu : 0x00f000f0u);
+    }
+}
+// The same codes and bytes of V, 4 times up: a product's terms are aligned by their
+// exponents, which a denormal has as high as its format's lowest, and lose what lies 24 bits
+// below (whole calls' errors of 3e-6 to 4e-6 become 2e-6).  Inverted where turned has bits
+// (kTurned or 0): upper halves' codes n become 15 - n.
+constexpr uint32_t kTurned = 0x03fc0000u;
+__device__ __forceinline__ void value_codes4(uint32_t (&low)[4], uint32_t (&high)[4], const uint32_t (&a)[4], bool second,
+                                             uint32_t turned) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const uint32_t w = second ? a[k] >> 6 : a[k] << 2;
+        low[k] = (w & 0x003c003cu) ^ (turned & 0x003c003cu);
+        high[k] = (w & 0x03fc03fcu) ^ turned;
     }
 }
 // An 8 x 8 matrix of 16-bit elements, lane (g, t) holding (g, 2t) and (g, 2t + 1), transposed.
@@ -1172,6 +1187,7 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
             }
             // ---- logits, and the scales and zeros of the weights to come ----
             float x[2][NX], sv[2], vsc[2][ZG], vz[2][ZG];
+            bool below = false;
             const int st = first + (NS > 1 ? my_stage : 0);          // the stage I weigh
             const uint8_t *ks = sp + s4_off + st * s4_st + g * kScaleTok, *vs = ks + L::kScaleBytes;
 #pragma unroll
@@ -1202,8 +1218,20 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                     const uint32_t w = ZG == 1 && my_group ? vw.w[L::kGroups - 1] : vw.w[gr];
                     vsc[k][gr] = ok ? word_scale(w) : 0.f;
                     vz[k][gr] = ok ? word_zero(w) : 0.f;
+                    below = below || vz[k][gr] < 0.f;
                 }
             }
+            // Values on both sides of 0: every second token enters with its codes turned, 15 - n,
+            // and its weight negative: w (n + z) = -w (15 - n) + w (z + 15).  Sums over codes
+            // of one sign would grow far above the result, and the products cut off their
+            // accumulators' low bits every time: 7e-5 to 3e-4 of the result after 32 K tokens,
+            // 2e-6 with it at any length (13B-shaped 122 us against 116, long contexts 92 against
+            // 85; with the 8s' sum taken off by products of its own 121 and 99, with all codes as
+            // normal numbers 3e-7 to 2e-6, 151 and 116).  Rows of zeros have zeros of 0 and sum up
+            // to 0.
+            const bool turns = __any_sync(kFull, below);
+            const uint32_t turned = turns ? kTurned : 0u;
+            const float side = turns && (g & 1) ? -1.f : 1.f, top = turns && (g & 1) ? -15.f : 0.f;
             // ---- weights under the present reference, as for 8 bits ----
             float pw[2][NX];
             auto weigh = [&]() {
@@ -1251,8 +1279,8 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                     float w[NX];
 #pragma unroll
                     for (int e = 0; e < NX; ++e) {
-                        w[e] = pw[k][e] * vsc[k][gr];
-                        zs[gr][e] = fmaf(w[e], vz[k][gr], zs[gr][e]);
+                        w[e] = pw[k][e] * (vsc[k][gr] * side);
+                        zs[gr][e] = fmaf(w[e], fmaf(vz[k][gr], side, top), zs[gr][e]);
                     }
                     if constexpr (L::kPaired) {
                         ph[k][gr] = pack2_rz(w[0], w[0] - high_part(w[0]));
@@ -1282,7 +1310,7 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                     for (int k = 0; k < 2; ++k) w[k] = of ? ph[k][ZG == 1 ? 0 : gr] : 0u;
 #pragma unroll
                     for (int i = 0; i < 4; i += 2) {
-                        codes4<true>(low, high, a, i > 0);
+                        value_codes4(low, high, a, i > 0, turned);
                         mma_f16(acc[4 * gr + i], low, w);
                         mma_f16(acc[4 * gr + i + 1], high, w);
                         if constexpr (!L::kPaired) {
@@ -1321,8 +1349,8 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
             for (int mt = 0; mt < MT; mt += 2)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    acc[mt + 1][e] = (acc[mt + 1][e] - acc[mt][e]) * 0x1p20f;
-                    acc[mt][e] *= 0x1p24f;
+                    acc[mt + 1][e] = (acc[mt + 1][e] - acc[mt][e]) * 0x1p18f;
+                    acc[mt][e] *= 0x1p22f;
                 }
             // sums over the lanes that weighed for one row
             auto total = [&](float v, int first) {
