@@ -58,10 +58,10 @@
 // enter the products unconverted (-9 and -5 %), two teams of 8 consumers in a CTA (-17 %, long
 // contexts none), three operations in place of five per eight codes (-5 %), the bookkeeping of
 // slots and shares without divisions (-5 %), shares weighed with items' ends (-4 %), weights
-// transposed by movmatrix (long contexts -2 %); 116 and
-// 85 then, and V's sums kept small, for their accuracy, +5 and +9 %.  Tried and slower: three ring slots for each
-// team instead of two (150 us against 146 after a flush, long contexts 89 against 85 in a graph:
-// more requests in flight only queue), queries read from memory to make room for them, 16
+// transposed by movmatrix (long contexts -2 %): 116 and 85.  V's sums kept small for their
+// accuracy's sake took 5 and 9 % of it back.  Tried and slower: three ring slots for each team
+// instead of two (150 us against 146 after a flush, long contexts 89 against 85 in a graph: more
+// requests in flight only queue), queries read from memory to make room for them, 16
 // consumers on one ring (250 against 226: 96 registers and a state each to join), two sets of
 // consumers that take one item's slots in turn (304 against 207).  Four producer warps for one
 // team took it from 207 to 191 before its bookkeeping was made shorter.
