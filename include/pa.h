@@ -552,7 +552,8 @@ pa_status pa_int4_gather(void *out_k, void *out_v, pa_dtype out_dtype, const voi
  * pa_int4_decode -- pa_decode over a 4-bit cache, without the rows being widened in
  * memory.  Arguments, rules, workspace and reproducibility of pa_quant_decode
  * (head_dim 64 or 128, any number of KV heads, block_size 8 or a multiple of 16 up to
- * 256, 1, 2, 4 or 8 query heads per KV head).  Codes are exact in the products, each
+ * 256, 1, 2, 4 or 8 query heads per KV head), num_kv_heads * (max_context_len / 16 + 1) *
+ * num_seqs (of 2048 at most) below 2^30.  Codes are exact in the products, each
  * query row is first scaled by a power of two and taken in binary16, softmax weights
  * enter as two binary16 parts; sums and softmax are fp32.
  */

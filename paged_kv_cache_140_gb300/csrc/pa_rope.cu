@@ -20,7 +20,7 @@
 //
 // Measured (GB300, in a graph): 8,192 tokens of 32 query and 8 KV heads of 128, bf16, with
 // norms 37.6 us, 0.80 of the measured copy rate (35.0 without norms, 136 for four times the
-// tokens, 0.89; copying as many bytes takes 31); 256 tokens of 40 + 40 heads 5.6 us; 4 tokens
+// tokens, 0.89; copying as many bytes takes 31); 256 tokens of 40 + 40 heads 5.1 us; 4 tokens
 // of 4 + 4 heads 1.9.  Steps: rows of any token to any lane 64 us; a row of four tokens at a
 // time 43; their four sums of squares reduced together (9 shuffles in place of 16) 41;
 // CTAs of 128 threads 38.  Eight tokens at a time take 52.
@@ -352,13 +352,16 @@ template <int D, bool BF16, bool QUANT>
 cudaError_t rope_q(const RopeParams &p, int kind, int sms, cudaStream_t stream) {
     constexpr int RG = kRopeThreads / (D / 8);
     const int R = p.hq + 2 * p.hkv;
-    // Four tokens to a CTA while that fills the GPU; few tokens are spread over CTAs by rows.
-    const bool many = (p.num_tokens + kRopeTokens - 1) / kRopeTokens >= 4 * sms;
+    // Four tokens to a CTA from 128 rows an SM on (800 tokens of 32 + 8 heads 5.6 us, one by one
+    // 7.3; 256 tokens 3.6, one by one 3.4).  A token's rows are spread over CTAs while the GPU has
+    // fewer than four an SM, in whole rounds of a CTA's groups of lanes (64 + 8 heads, 800 tokens:
+    // 7.3 us, cut by halves 9.1).
+    const bool many = p.num_tokens * R >= static_cast<int64_t>(128) * sms;
     const int64_t blocks = many ? (p.num_tokens + kRopeTokens - 1) / kRopeTokens : p.num_tokens;
-    int split = 1;
-    while (blocks * split < 4 * sms && R / (split * 2) >= RG) split *= 2;
-    const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(split));
-    const int rows = (R + split - 1) / split;
+    const int rounds = (R + RG - 1) / RG;
+    const int64_t want = (4 * sms + blocks - 1) / blocks;
+    const int rows = (want < rounds ? static_cast<int>(rounds / want) : 1) * RG;
+    const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>((R + rows - 1) / rows));
     if (many) return launch_pdl(rope_and_cache_kernel<D, BF16, QUANT, kRopeTokens>, grid, dim3(kRopeThreads), 0, stream, p, rows, kind);
     return launch_pdl(rope_and_cache_kernel<D, BF16, QUANT, 1>, grid, dim3(kRopeThreads), 0, stream, p, rows, kind);
 }
