@@ -234,3 +234,35 @@ def test_turned_keys_as_codes(kind, interleaved, rot):
             inside = ref.abs() < 440 * sc
             got, ref, bound = torch.where(inside, got, ref), ref, bound
     assert torch.all((got - ref).abs() <= bound), ((got - ref).abs() / bound).max()
+
+
+@pytest.mark.parametrize("interleaved,rot,d", [(False, 64, 64), (True, 32, 128), (False, 128, 128)])
+@pytest.mark.parametrize("kind", KINDS + ["half"])
+def test_many_tokens_make_the_bytes_of_few(kind, interleaved, rot, d):
+    """One call of 163 tokens of 120 rows, four tokens at a time, and calls of 20 and less, one by one: the same
+    operations on every element, so the same bytes."""
+    T, hq, hkv, bs, nb = 163, 64, 28, 16, 12
+    _, dev, pos = inputs(T, hq, hkv, d, "bf16", seed=5)
+    dev[1][11, 3, 7] = float("inf")
+    dev[2][161, 27, d - 1] = float("nan")
+    slots = torch.randperm(nb * bs, generator=torch.Generator().manual_seed(0))[:T]
+    slots[::17] = -1
+    slots, pos = slots.cuda(), pos.cuda()
+    freq, _ = pa.rope_frequencies(rot)
+    made = []
+    for step in (T, 20):
+        if kind == "half":
+            c = {n: torch.full((nb, bs, hkv, d), 3.0, dtype=torch.bfloat16, device="cuda") for n in "kv"}
+        else:
+            c = caches(kind, nb, bs, hkv, d)
+        out = torch.empty(T, hq, d, dtype=torch.bfloat16, device="cuda")
+        for t in range(0, T, step):
+            part = [x[t:t + step] for x in dev]
+            if kind == "half":
+                pa.rope_and_cache(out[t:t + step], *part, c["k"], c["v"], slots[t:t + step], pos[t:t + step], freq,
+                                  interleaved=interleaved)
+            else:
+                rope_write(kind, out[t:t + step], part, c, slots[t:t + step], pos[t:t + step], freq, interleaved=interleaved)
+        made.append([out.view(torch.uint8)] + [x.view(torch.uint8) for x in c.values()])
+    for a, b in zip(*made):
+        assert torch.equal(a, b)
