@@ -29,8 +29,14 @@
 // 4-bit codes u of group r stand for s_pr (u + z_pr), and everything but the codes is
 // taken out of the products, Q_r being the sum of q's elements in the group:
 //     x_p = scale sum_r s_pr (<q_r, u_pr> + z_pr Q_r),
-//     acc_r = sum (2^(s_p - m) s_pr) u_pr + sum (2^(s_p - m) s_pr) z_pr,
-// the reference following the larger of a token's V scales.  What the codes cost is
+//     acc_r = sum (2^(s_p - m) s_pr) u_pr + sum (2^(s_p - m) s_pr) z_pr.
+// Each group of V has a reference of its own, so that its largest weight lies between
+// 2^6 and 2^15 however much smaller its values are than its neighbour's (under one
+// reference for both, codes of a group 2^-16 as large were off by 7e-5 of themselves and
+// from 2^-32 on lost, their zeros not): with one query row a lane weighs one group and m is
+// that group's, else a group's weights and sums are taken a power of two up (4 rows, long
+// contexts 94.9 us against 92.9; 8 rows 122.1 against 121.2).  Weights of 2^-76 and less of the
+// row's largest may count as none.  What the codes cost is
 // said at codes4, which lane weighs what where the consumers begin.
 //
 // What bounds it: reading the cache.  One producer warp brings ring slots in by
@@ -839,6 +845,9 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
     const int my_stage = C == 1 ? t & 1 : t >> 1, my_group = t >> 1;
     float qsum[L::kGroups][2];    // the sum of a group's query elements, as large as the products have them
     float zs[ZG][NX];             // the sum of weight, scale and zero
+    // both groups: the power of two that a group's weights are taken up by, in acc and zs too
+    constexpr bool kUp = ZG > 1;
+    [[maybe_unused]] float up[ZG][NX];
     float mu[2];                  // the reference that weights are taken under: m_run, or 0 while there is none
     int cslot = 0;
     uint32_t cphase = 0, citems = 0;
@@ -928,10 +937,13 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
 #pragma unroll
                 for (int gr = 0; gr < ZG; ++gr)
 #pragma unroll
-                    for (int e = 0; e < NX; ++e) zs[gr][e] = 0.f;
-                const float up = __uint_as_float(eb) * p.scale_log2 * (0x1p20f / kQ4);
-                qs[0] = __shfl_sync(kFull, up, 8 * t);
-                qs[1] = __shfl_sync(kFull, up, 8 * t + 4);
+                    for (int e = 0; e < NX; ++e) {
+                        zs[gr][e] = 0.f;
+                        up[gr][e] = 1.f;
+                    }
+                const float logits = __uint_as_float(eb) * p.scale_log2 * (0x1p20f / kQ4);
+                qs[0] = __shfl_sync(kFull, logits, 8 * t);
+                qs[1] = __shfl_sync(kFull, logits, 8 * t + 4);
             } else {
                 // Dims in the order the widened K fragments arrive: step
                 // 2kc + hl takes dims 32kc + 4t + 2hl (+1) and the same + 16.
@@ -1186,7 +1198,7 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                     }
             }
             // ---- logits, and the scales and zeros of the weights to come ----
-            float x[2][NX], sv[2], vsc[2][ZG], vz[2][ZG];
+            float x[2][NX], vsc[2][ZG], vz[2][ZG];
             bool below = false;
             const int st = first + (NS > 1 ? my_stage : 0);          // the stage I weigh
             const uint8_t *ks = sp + s4_off + st * s4_st + g * kScaleTok, *vs = ks + L::kScaleBytes;
@@ -1195,7 +1207,7 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                 // a masked token's scales may be anything: its V scales count as 0
                 const bool ok = kWhole || (g + 8 * k < mine - st * kStageTokens && !((m.bad >> (2 * (st0 + st) + k)) & 1u));
                 const Words<L::kGroups> kw = load_words<L::kGroups>(ks + k * s4_8), vw = load_words<L::kGroups>(vs + k * s4_8);
-                float sum[NX] = {}, big = kScaleFloor;
+                float sum[NX] = {};
 #pragma unroll
                 for (int gr = 0; gr < L::kGroups; ++gr) {
 #pragma unroll
@@ -1207,10 +1219,7 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                         const float one = NS > 1 && my_stage ? cv[NS - 1] : cv[0];
                         sum[e] = fmaf(word_scale(kw.w[gr]), fmaf(word_zero(kw.w[gr]), qsum[gr][e], one), sum[e]);
                     }
-                    // (a scale that is no number makes its own group's sums such, not the reference)
-                    big = fmaxf(big, word_scale(vw.w[gr]));
                 }
-                sv[k] = ok ? big : 0.f;
 #pragma unroll
                 for (int e = 0; e < NX; ++e) x[k][e] = ok ? sum[e] * qs[e] : -INFINITY;
 #pragma unroll
@@ -1232,42 +1241,73 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
             const bool turns = __any_sync(kFull, below);
             const uint32_t turned = turns ? kTurned : 0u;
             const float side = turns && (g & 1) ? -1.f : 1.f, top = turns && (g & 1) ? -15.f : 0.f;
-            // ---- weights under the present reference, as for 8 bits ----
-            float pw[2][NX];
+            // ---- weights under the present references, as for 8 bits; wt: with their scales, and where
+            // there is one group of them, their sides ----
+            float pw[2][NX], wt[2][ZG][NX];
             auto weigh = [&]() {
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
 #pragma unroll
-                    for (int e = 0; e < NX; ++e) pw[k][e] = fast_exp2(x[k][e] - mu[e]);
+                    for (int e = 0; e < NX; ++e) {
+                        pw[k][e] = fast_exp2(x[k][e] - mu[e]);
+#pragma unroll
+                        for (int gr = 0; gr < ZG; ++gr)
+                            wt[k][gr][e] = kUp ? pw[k][e] * vsc[k][gr] * up[gr][e] : pw[k][e] * (vsc[k][gr] * side);
+                    }
             };
             weigh();
             bool nd = false;
 #pragma unroll
-            for (int e = 0; e < NX; ++e)
-                nd = nd || m_run[e] == -INFINITY || fmaxf(pw[0][e] * sv[0], pw[1][e] * sv[1]) > kWeightMax;
+            for (int e = 0; e < NX; ++e) {
+                nd = nd || m_run[e] == -INFINITY;
+#pragma unroll
+                for (int gr = 0; gr < ZG; ++gr) {
+                    const float a = wt[0][gr][e], b = wt[1][gr][e];
+                    nd = nd || (kUp ? fmaxf(a, b) : fmaxf(fabsf(a), fabsf(b))) > kWeightMax;
+                }
+            }
             if (__any_sync(kFull, nd)) {
-                float al[NX];
+                float al[ZG][NX];
 #pragma unroll
                 for (int e = 0; e < NX; ++e) {
-                    float mx = fmaxf(x[0][e] + fast_log2(sv[0]), x[1][e] + fast_log2(sv[1]));
+                    float mx[ZG], mn = m_run[e];
 #pragma unroll
-                    for (int o = C == 1 ? 1 : C == 2 ? 2 : 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
-                    const float mn = fmaxf(m_run[e], mx - kWeightExp);
-                    al[e] = mn == -INFINITY ? 1.f : fast_exp2(m_run[e] - mn);
+                    for (int gr = 0; gr < ZG; ++gr) {
+                        // (a scale that is no number makes its own group's sums such, not the reference)
+                        mx[gr] = fmaxf(x[0][e] + fast_log2(fmaxf(vsc[0][gr], kScaleFloor)),
+                                       x[1][e] + fast_log2(fmaxf(vsc[1][gr], kScaleFloor)));
+#pragma unroll
+                        for (int o = C == 1 ? 1 : C == 2 ? 2 : 4; o < 32; o <<= 1)
+                            if (C != 1 || L::kGroups == 1 || o != 2) mx[gr] = fmaxf(mx[gr], __shfl_xor_sync(kFull, mx[gr], o));
+                        mn = fmaxf(mn, mx[gr] - kWeightExp);
+                    }
+                    const float fall = m_run[e] - mn;
+                    l_run[e] *= mn == -INFINITY ? 1.f : fast_exp2(fall);
+#pragma unroll
+                    for (int gr = 0; gr < ZG; ++gr) {
+                        float rise = 0.f;
+                        if constexpr (kUp) {
+                            // the group's own reference, m less the exponent it is taken up by, never falls
+                            const float had = static_cast<float>(static_cast<int>(__float_as_uint(up[gr][e]) >> 23) - 127);
+                            const float ref = fmaxf(m_run[e] - had, mx[gr] - kWeightExp);
+                            const float has = fminf(fmaxf(floorf(mn - ref), 0.f), 126.f);    // (0 while there is no reference)
+                            up[gr][e] = __uint_as_float(static_cast<uint32_t>(127 + static_cast<int>(has)) << 23);
+                            rise = has - had;
+                        }
+                        al[gr][e] = mn == -INFINITY ? 1.f : fast_exp2(fall + rise);
+                        zs[gr][e] *= al[gr][e];
+                    }
                     m_run[e] = mn;
                     mu[e] = mn == -INFINITY ? 0.f : mn;
-                    l_run[e] *= al[e];
-#pragma unroll
-                    for (int gr = 0; gr < ZG; ++gr) zs[gr][e] *= al[e];
                 }
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[mt][e] *= al[C == 8 ? e & (NX - 1) : 0];
+                    for (int e = 0; e < 4; ++e) acc[mt][e] *= al[kUp ? mt / 4 : 0][C == 8 ? e & (NX - 1) : 0];
                 weigh();
             }
-            // ---- weights with their scales as binary16 parts: the high and low part of one
-            // column (8 rows: the two columns' high parts, and their low ones) ----
+            // ---- those as binary16 parts: the high and low part of one column (8 rows: the two
+            // columns' high parts, and their low ones) ----
             uint32_t ph[2][ZG];
             [[maybe_unused]] uint32_t pl[2][ZG];
 #pragma unroll
@@ -1276,10 +1316,10 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                 for (int e = 0; e < NX; ++e) l_run[e] += pw[k][e];
 #pragma unroll
                 for (int gr = 0; gr < ZG; ++gr) {
-                    float w[NX];
+                    float(&w)[NX] = wt[k][gr];
 #pragma unroll
                     for (int e = 0; e < NX; ++e) {
-                        w[e] = pw[k][e] * (vsc[k][gr] * side);
+                        if constexpr (kUp) w[e] *= side;
                         zs[gr][e] = fmaf(w[e], fmaf(vz[k][gr], side, top), zs[gr][e]);
                     }
                     if constexpr (L::kPaired) {
@@ -1366,6 +1406,28 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
 #pragma unroll
                 for (int gr = 0; gr < ZG; ++gr) zs[gr][e] = total(zs[gr][e], 32);    // the zeros' share of a group's elements
             }
+            const bool fin = (m.flags & kFinal) != 0;
+            // What takes a group's sums back to the row's reference.  Two groups weighed by lanes
+            // apart: the larger reference and the sum under it, but for whole results, which
+            // need none in common.
+            [[maybe_unused]] float down[ZG][NX];
+            constexpr bool kApart = C == 1 && L::kGroups == 2;
+            if constexpr (kUp) {
+#pragma unroll
+                for (int gr = 0; gr < ZG; ++gr)
+#pragma unroll
+                    for (int e = 0; e < NX; ++e) down[gr][e] = __uint_as_float(0x7f000000u - __float_as_uint(up[gr][e]));
+            } else if constexpr (kApart) {
+                down[0][0] = 1.f;
+                if (!fin || nsubs > 1) {
+                    const float om = __shfl_xor_sync(kFull, m_run[0], 2), ol = __shfl_xor_sync(kFull, l_run[0], 2);
+                    if (om > m_run[0]) {
+                        down[0][0] = fast_exp2(m_run[0] - om);
+                        m_run[0] = om;
+                        l_run[0] = ol;
+                    }
+                }
+            }
             // My results, quads of neighbouring elements 4g .. 4g + 3 of a group's halves:
             // 1 row: those of group t >> 1, else of every group.
             constexpr int NQ = C == 1 ? 2 : 2 * L::kGroups;
@@ -1379,6 +1441,7 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
                     if constexpr (C == 1 && L::kGroups == 2)
                         if (my_group) v = part(4 + j);
                     q[j] = total(v, 4) + zs[gr][e];
+                    if constexpr (kUp || kApart) q[j] *= down[gr][e];
                 }
                 return make_float4(q[0], q[1], q[2], q[3]);
             };
@@ -1387,7 +1450,6 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
             auto row_of = [&](int e) { return C == 8 ? 2 * t + e : t & (C - 1); };
             const bool tells = g == 0 && (C == 1 ? t == 0 : writes);
             const int kvh = m.kvh0 + head;
-            const bool fin = (m.flags & kFinal) != 0;
             // A row's reference and sum, and quads of it, into the output or a row of the workspace.
             auto row_at = [&](int c) -> int64_t {
                 return (m.flags & kContinued)
