@@ -623,7 +623,8 @@ pa_status pa_update_tables(int32_t *block_tables, int max_blocks_per_seq, const 
  *     PA_FP8_E4M3, scales NULL     pa_reshape_and_cache with k_scale, v_scale (> 0)
  *     PA_FP8_E4M3 or PA_INT8       pa_quant_reshape_and_cache
  *     PA_INT4                      pa_int4_reshape_and_cache
- * (codes are made of the fp32 values, without a rounding to dtype before).
+ * (codes are made of the fp32 values, without a rounding to dtype before).  A token's bytes
+ * do not depend on how many others are in the call.
  *
  *   out_q        : [num_tokens, num_heads, head_dim], dtype; may be query where that is dense
  *   query, key, value : dtype (F16 or BF16), rows of one token dense, tokens q_stride,

@@ -61,11 +61,13 @@ __device__ __forceinline__ float2 cos_sin(int64_t position, double f, float fact
 
 // Sums over the LPR lanes of a row, of one value or of four at once: with four, halves and
 // then quarters of the lanes go on with two and then one of them, and every lane looks up all
-// four at the end.  `then`: applied to a sum once per lane that holds it.
+// four at the end.  Both add lanes LPR / 2 apart first, then LPR / 4 and so on to neighbours: a
+// token's bytes do not depend on how many others are in the call.  `then`: applied to a sum
+// once per lane that holds it.
 template <int LPR, typename Then>
 __device__ __forceinline__ void row_sums(float (&v)[1], int, uint32_t lanes, Then then) {
 #pragma unroll
-    for (int o = 1; o < LPR; o <<= 1) v[0] += __shfl_xor_sync(lanes, v[0], o);
+    for (int o = LPR / 2; o > 0; o >>= 1) v[0] += __shfl_xor_sync(lanes, v[0], o);
     v[0] = then(v[0]);
 }
 template <int LPR, typename Then>
