@@ -617,8 +617,8 @@ pa_status pa_update_tables(int32_t *block_tables, int max_blocks_per_seq, const 
  *     (a, b) <- factor * (a cos - b sin, b cos + a sin)   for pair i of the first rot_dim
  * elements, with the angle positions[t] * inv_freq[i]; a pair is the elements
  * (i, i + rot_dim / 2), or (2 i, 2 i + 1) if interleaved.  Angles are exact to a few
- * 2^-24 at any position.  Query rows go to out_q; key rows and (unchanged) value rows to
- * cache slots as by the write of the cache's own kind:
+ * 2^-24 at any position and any frequency allowed below.  Query rows go to out_q; key
+ * rows and (unchanged) value rows to cache slots as by the write of the cache's own kind:
  *     cache_dtype = dtype          pa_reshape_and_cache
  *     PA_FP8_E4M3, scales NULL     pa_reshape_and_cache with k_scale, v_scale (> 0)
  *     PA_FP8_E4M3 or PA_INT8       pa_quant_reshape_and_cache
