@@ -316,9 +316,16 @@ __global__ void __launch_bounds__(kRopeThreads)
         uint16_t *const base = w == 0 ? p.out_q + (t0 * p.hq + head) * D
                                       : static_cast<uint16_t *>(p.cache[w - 1]) + static_cast<int64_t>(head) * D;
         const int64_t row = static_cast<int64_t>(w == 0 ? p.hq : p.hkv) * D;
+        const bool as_it_is = !QUANT && w == 2;       // values: bits of a NaN too
+        if (as_it_is) {
+#pragma unroll
+            for (int k = 0; k < TB; ++k)
+                if (k < nt && slot_t[k] >= 0)
+                    *reinterpret_cast<uint4 *>(base + slot_t[k] * row + oa) = make_uint4(x[k][0], x[k][1], x[k][2], x[k][3]);
+        }
 #pragma unroll
         for (int k = 0; k < TB; ++k) {
-            if (k >= nt) break;
+            if (k >= nt || as_it_is) break;
             if (pairs) part_pairs(x[k]);
             F2 y[4];                      // turned lanes: elements (a0 a1)(a2 a3) and their partners (b0 b1)(b2 b3)
 #pragma unroll

@@ -9,7 +9,8 @@ torch = pytest.importorskip("torch")
 
 import paged_kv_cache_140_gb300 as pa
 
-from test_gpu_rope import KINDS, caches, inputs, rope_write
+import step_harness as S
+from test_gpu_rope import KINDS, caches, inputs, rope_write, slots_for
 
 pytestmark = pytest.mark.gpu
 
@@ -133,3 +134,26 @@ def test_near_and_far_positions_in_one_call(kind):
         made.append([out.view(torch.uint8)] + [x.view(torch.uint8) for x in c.values()])
     for a, b in zip(*made):
         assert torch.equal(a, b)
+
+
+# ------------------------------------------------------------ bytes as they are
+
+@pytest.mark.parametrize("T", [5, 1100])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_values_go_into_a_16_bit_cache_bit_for_bit(dtype, T):
+    """Every one of the 65,536 numbers of the type (of 5 tokens, some), NaNs of any bits among them."""
+    hkv, d, bs = 1, 64, 16
+    (q, k, v), dev, pos = inputs(T, 32, hkv, d, dtype, wide=False)
+    bits = torch.arange(T * d) if T * d >= 65536 else torch.arange(65536 - T * d, 65536)
+    dev[2] = (bits % 65536).to(torch.int32).to(torch.int16).view(S.DT[dtype]).view(T, hkv, d).cuda()
+    slots = slots_for(T, T // bs + 3, bs, skip=False).cuda()
+    freq, _ = pa.rope_frequencies(d)
+    made = []
+    for rope in (True, False):
+        kc, vc = (torch.full((T // bs + 3, bs, hkv, d), 3.0, dtype=S.DT[dtype], device="cuda") for _ in "kv")
+        if rope:
+            pa.rope_and_cache(torch.empty_like(dev[0]), *dev, kc, vc, slots, pos.cuda(), freq)
+        else:
+            pa.reshape_and_cache(dev[1], dev[2], kc, vc, slots)
+        made.append(vc.view(torch.int16))
+    assert torch.equal(*made)
