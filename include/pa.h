@@ -31,8 +31,9 @@
  *    infinities, largest value 448) with one scale per tensor: a K code c
  *    stands for value(c) * k_scale, V alike.  Writing quantises
  *    code = e4m3(fp32(x) / scale): the division in fp32 (IEEE), rounding to
- *    nearest-even, finite values saturating at +-448, NaN staying NaN.  The
- *    FP8 cache is supported for head_dim 128.
+ *    nearest-even, finite values saturating at +-448, NaN staying NaN.
+ *    Attention over the FP8 cache is supported for head_dim 128 (its rows are
+ *    written for 64 too).
  *  - Supported shapes: head_dim 64 or 128; block_size 8 or a multiple of 16
  *    up to 256; num_heads a multiple of num_kv_heads with
  *    num_heads / num_kv_heads in {1, 2, 4, 8}.

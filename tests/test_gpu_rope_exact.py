@@ -10,7 +10,7 @@ torch = pytest.importorskip("torch")
 import paged_kv_cache_140_gb300 as pa
 
 import step_harness as S
-from test_gpu_rope import KINDS, caches, inputs, rope_write, slots_for
+from test_gpu_rope import KINDS, caches, inputs, rope_write, slots_for, write
 
 pytestmark = pytest.mark.gpu
 
@@ -157,3 +157,21 @@ def test_values_go_into_a_16_bit_cache_bit_for_bit(dtype, T):
             pa.reshape_and_cache(dev[1], dev[2], kc, vc, slots)
         made.append(vc.view(torch.int16))
     assert torch.equal(*made)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_one_scale_per_tensor_makes_the_bytes_of_the_write(d):
+    """Keys at position 0 and values, saturated ones, infinities and NaN among them, for either head size."""
+    T, hq, hkv, bs = 70, 3, 5, 16
+    _, dev, pos = inputs(T, hq, hkv, d, "bf16")
+    for t in dev[1:]:      # (beyond the 16 elements that are turned: infinity times a sine of 0 is no number)
+        t[3, 1] = 0
+        t[4, 2, 37], t[5, 0, 39], t[6, 1, 32] = float("inf"), float("nan"), float("-inf")
+        t[7] *= 1000
+    slots = slots_for(T, 8, bs).cuda()
+    got, want = caches("tensor", 8, bs, hkv, d), caches("tensor", 8, bs, hkv, d)
+    freq, _ = pa.rope_frequencies(16)
+    rope_write("tensor", torch.empty(T, hq, d, dtype=torch.bfloat16, device="cuda"), dev, got, slots, 0 * pos.cuda(), freq)
+    write("tensor", dev[1].contiguous(), dev[2].contiguous(), want, slots)
+    for n in got:
+        assert torch.equal(got[n], want[n]), n
