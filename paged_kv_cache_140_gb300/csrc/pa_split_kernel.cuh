@@ -455,14 +455,8 @@ __global__ void __launch_bounds__((SplitLayout<D, C, CT>::kThreads), 1)
     if (!p.late_wait) pdl_wait();
     pdl_launch_dependents();
     // ---- the entries' lengths ----
+    // (Asking for the block tables' lines meanwhile gains nothing, tables in L2 or not.)
     const bool tell = blockIdx.x == 0;
-    if constexpr (L::k4) {
-        // the tables on their way to L2 while the lengths are looked at
-        const int64_t bytes = static_cast<int64_t>(p.num_seqs) * p.max_blocks_per_seq * 4;
-        for (int64_t i = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) * 128; i < bytes;
-             i += static_cast<int64_t>(gridDim.x) * blockDim.x * 128)
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const uint8_t *>(p.block_tables) + i));
-    }
     if (mode == kSplitWhole && tell)   // every group's bounds, the warps with the fewest entries first
         for (int g = blockDim.x - 1 - threadIdx.x; g < p.num_groups; g += blockDim.x)
             if (bad_group(p, g, __ldg(p.cu_groups + g), __ldg(p.cu_groups + g + 1)))

@@ -157,3 +157,14 @@ def test_a_group_that_is_no_number_leaves_its_neighbour_right(hq, hkv, group):
     ref = Q.attend(q[1], *(S.rows4(c, n, Q.slots_of(bt, 1, 0, 300, BS)) for n in "kv"), float(np.float32(D ** -0.5)))
     got[1, :r, a:a + 64] = ref[:r, a:a + 64]
     compare(got, bt, c, q, lens)
+
+
+@pytest.mark.parametrize("hq,hkv", [(8, 8), (32, 8), (2, 1)])
+def test_tables_wider_than_any_context(hq, hkv):
+    """A captured step's tables have room for the longest context there may be: the same bytes as of narrow ones."""
+    lens = [1, 0, 17, 300, 700]
+    bt, c, q = case(lens, hq, hkv, lambda x: x)
+    wide = torch.full((len(lens), 4096), -7, dtype=torch.int32)
+    wide[:, :bt.shape[1]] = bt
+    kw = dict(max_context_len=700, partition_size=64)
+    assert torch.equal(decode(bt, c, q, lens, **kw), decode(wide, c, q, lens, **kw))
