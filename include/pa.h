@@ -584,7 +584,12 @@ pa_status pa_int4_decode(void *out, pa_dtype out_dtype, const void *query, pa_dt
  *   - numbering all blocks that are taken the same way, number k is
  *     free_blocks[free_count + R - 1 - k]; the new count is free_count + R - (taken).
  * So a step and one that undoes it leave the stack as it was, and nothing depends on
- * timing.  Blocks must belong to one sequence only (shared ones are not to be dropped).
+ * timing.  A block that a step gives back must be in one table only, which is not checked
+ * (in two, it would be on the stack while the other reads it).  Sequences that share
+ * their first S blocks: one begins with the S ids written into its row and its length
+ * set to S * block_size; any but the last ends with the change S * block_size -
+ * context_lens[s], which gives back its own blocks, its length then set to 0; the last
+ * ends as any other and gives the shared ones back.
  *
  *   block_tables  : [num_seqs, max_blocks_per_seq] int32; entries past a sequence's
  *                   length are left as they were

@@ -709,7 +709,9 @@ def update_tables(block_tables, context_lens, changes, free_blocks, free_count, 
     left as they were.  Written too: ``slot_mapping`` and ``positions`` (int64 [T], T at
     least the tokens gained) of the gained tokens, then -1 and 0, and ``cu_seqlens``
     (int32 [B+1]), where each sequence's begin.  Where something does not fit, nothing
-    changes and the error flag says what (``include/pa.h`` has the order of blocks).
+    changes and the error flag says what (``include/pa.h`` has the order of blocks, and how
+    sequences that share their first blocks begin and end: a block must not be given back
+    while another table holds it).
     ``num_blocks`` (default: the capacity) bounds the block ids."""
     rt = _rt or _runtime()
     dev, table = block_tables.get_device(), block_tables.shape
