@@ -765,7 +765,11 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str | None = 
               is slowed by scale, the fastest not at all
     "parts"   pairs that turn at least ``fast_turns`` times in original_len positions as
               they are, those that turn at most ``slow_turns`` times slowed by scale, the
-              others in between; factor 0.1 ln(scale) + 1"""
+              others in between; factor 0.1 ln(scale) + 1
+
+    The ramp of "parts" goes by a pair's turns.  A model whose ramp goes by the pair's index
+    between two rounded borders brings an ``inv_freq`` of its own; one that has the ramp
+    without the factor passes ``factor=1.0``."""
     torch = _torch()
     _need(rot_dim >= 8 and rot_dim % 8 == 0, "rot_dim must be a multiple of 8")
     _need(base > 1.0 and scale >= 1.0 and math.isfinite(base) and math.isfinite(scale),
