@@ -279,12 +279,13 @@ cudaError_t launch_update_tables(const TablesParams &p, cudaStream_t stream) {
     const size_t smem = static_cast<size_t>(p.num_seqs) * 5 * sizeof(int32_t);
     // In a graph, us.  The tokens by the same CTA up to 2,048 of them, two rounds of its threads: 5.6
     // with 100 sequences and 989 tokens (by a kernel behind it 6.6), 11.8 with 1,000 and 1,689 (11.8); 128
-    // and 2,702 7.3 (7.0), 256 and 7,725 11.3 (7.6).  One CTA up to as many sequences as it has
-    // threads: 1,024 of a token each 8.2 (a cluster of 8: 9.5), 512 with 8,279 tokens 8.6 (9.0); above it 8: 1,500
-    // with 2,428 tokens 11.4 (one CTA 14.2), 4,096 with 53,583 14.8 (31.1), though 2,048 of a token each take
-    // 10.4 (9.9).  Fewer threads, whose barriers are shorter, for steps of up to 128 sequences and
-    // 256 tokens: 4 of a token each 2.9 (1,024 threads: 3.7), 128 4.2 (4.9), though 100 with 190 tokens and as
-    // many blocks to move take 5.8 (5.4); with more tokens 100 and 989 take 9.5 (5.6).
+    // and 2,702 7.3 (7.0), 256 and 7,725 11.3 (7.6).
+    // One CTA up to as many sequences as it has threads: 1,024 of a token each 8.2 (a cluster of 8: 9.5),
+    // 512 with 8,279 tokens 8.6 (9.0), though 1,000 with 15,680 11.0 (10.1); above it 8: 1,500 with
+    // 2,428 tokens 11.4 (one CTA 14.2), 4,096 with 53,583 14.8 (31.1), though 2,048 of a token each 10.4 (9.9).
+    // Fewer threads, whose barriers are shorter, for steps of up to 128 sequences and 256 tokens: 4
+    // of a token each 2.9 (1,024 threads: 3.7), 128 4.2 (4.9), though 100 with 190 tokens and as many blocks
+    // to move take 5.8 (5.4); with more tokens, 100 and 989, they take 9.5 (5.6).
     const bool fused = p.num_seqs <= kTableThreads && p.num_tokens <= 2 * kTableThreads;
     const unsigned ctas = p.num_seqs <= kTableThreads ? 1 : 8;
     const unsigned threads = fused && p.num_seqs <= 128 && p.num_tokens <= 256 ? 128 : kTableThreads;
