@@ -50,22 +50,28 @@
 // The SMs take equal shares of all slots; an item across a share's end is cut there.
 //
 // Measured (GB300, whole calls, join included; of the measured copy rate): 256
-// 13B-shaped sequences over e4m3 codes 217 us, 0.91; 64 7B-shaped over int8 99 us,
-// 0.85; 16 of 16 K to 32 K tokens, 32 heads on 8, e4m3, 127 us, 0.95.  With the math
-// left out the first took 216, without the scales' loads too 202: the 3 % of bytes
+// 13B-shaped sequences over e4m3 codes 212 us, 0.93; 64 7B-shaped over int8 96 us,
+// 0.88; 16 of 16 K to 32 K tokens, 32 heads on 8, e4m3, 126 us, 0.96.  (Before the bookkeeping
+// lost its divisions 217, 99 and 127.)  With the math
+// left out the first then took 216, without the scales' loads too 202: the 3 % of bytes
 // that scales are cost 7 %, as 32-byte pieces.  Tried and slower: 16 consumer warps
 // (240 us against 221 at that time), one stage per slot (277), two ring slots instead
 // of three (241), a warp that prefetches slots into L2 (2 ahead 220, 8 ahead 296).
 //
-// 4-bit codes (in a graph, join included): the 13B-shaped batch 122 us, 0.79; the long
-// contexts 92, 0.75, of which 9 us pass before the first slot is there and 5 in the join.
+// 4-bit codes (in a graph, join included): the 13B-shaped batch 120 us, 0.81; the long
+// contexts 94.5, 0.73 (8 query heads per KV head 121, 0.57; 2 86, 0.80; 1 80, 0.87), of which 9 us
+// pass before the first slot is there and 5 in the join.  Without the consumers' arithmetic, after a
+// flush: 126 us of 134, 90 of 104 and, 8 heads, 95 of 128.  96 registers are what 18 warps
+// leave (five on one sub-partition): at head_dim 128 the compiler spills 36, 100 and 120 bytes
+// a thread with 1, 2 and 4 query rows.
 // Half the bytes of 8 bits for as many products: with the 8-bit consumer's shuffles and
 // conversions 198 and 129.  What it took: lanes that weigh logits of their own and codes that
 // enter the products unconverted (-9 and -5 %), two teams of 8 consumers in a CTA (-17 %, long
 // contexts none), three operations in place of five per eight codes (-5 %), the bookkeeping of
 // slots and shares without divisions (-5 %), shares weighed with items' ends (-4 %), weights
 // transposed by movmatrix (long contexts -2 %): 116 and 85.  V's sums kept small for their
-// accuracy's sake took 5 and 9 % of it back.  Tried and slower: three ring slots for each team
+// accuracy's sake took 5 and 9 % of it back, references of the groups' own 2 % of the long
+// contexts'.  Tried and slower: three ring slots for each team
 // instead of two (150 us against 146 after a flush, long contexts 89 against 85 in a graph: more
 // requests in flight only queue), queries read from memory to make room for them, 16
 // consumers on one ring (250 against 226: 96 registers and a state each to join), two sets of
@@ -108,8 +114,8 @@ struct SplitLayout {
     static constexpr int kSlotBytes = (2 * kKVBytes + 2 * kScaleBytes + 1023) / 1024 * 1024;
     // Teams of a producer and its consumers, each with a ring and a share of the slots of its
     // own.  4-bit codes: two, since one's warps are too few to hide their own latencies (with
-    // 8 query rows one with more registers is the faster: 138 us against 152 for 16 sequences
-    // of 16 K to 32 K tokens, 64 heads on 8).
+    // 8 query rows one of 168 registers is the faster: 121 us against 165, whose 96 spill 208
+    // bytes, for 16 sequences of 16 K to 32 K tokens, 64 heads on 8).
     static constexpr int kTeams = k4 && C < 8 ? 2 : 1;
     // What an item's start and end cost, in slots: 4-bit slots are short enough for shares to
     // be weighed with it (256 13B-shaped sequences: teams with 18 items of a few slots took
