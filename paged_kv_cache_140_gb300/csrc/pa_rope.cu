@@ -54,10 +54,10 @@ __device__ __forceinline__ uint64_t mantissa(uint64_t bits) {
     return ((bits & 0xfffffffffffffull) | 0x10000000000000ull) << 11;
 }
 __device__ __forceinline__ int exponent(uint64_t bits) { return static_cast<int>((bits >> 52) & 0x7ff); }
-// |f| < 2
+// For |f| < 2 (others: some number).
 __device__ __forceinline__ uint64_t turn_fraction(uint64_t bits) {
     const int e = exponent(bits);
-    uint64_t t = __umul64hi(mantissa(bits), kTurnHigh + 1) >> (1024 - max(e, 961));      // (C's 64 bits, rounded)
+    uint64_t t = __umul64hi(mantissa(bits), kTurnHigh + 1) >> ((1024 - e) & 63);      // (C's 64 bits, rounded)
     if (e <= 960) t = 0;
     return bits >> 63 ? 0 - t : t;
 }
