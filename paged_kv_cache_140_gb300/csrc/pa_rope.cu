@@ -25,11 +25,12 @@
 // Measured (GB300, in a graph): 8,192 tokens of 32 query and 8 KV heads of 128, bf16, with
 // norms 37.2 us, 0.81 of the measured copy rate (34.6 without norms, 136 for four times the
 // tokens, 0.89; copying as many bytes takes 31); 256 tokens of 40 + 40 heads 5.1 us; 4 tokens
-// of 4 + 4 heads 1.9.  Into 8-bit caches the first takes 51.5 (0.54) and into a 4-bit one 72 (0.37), bound by
-// their operations: 37 and 52 M warp instructions against 28 M, at 122 registers, four CTAs an SM.  Steps: rows of any token to any lane 64 us; a row of four tokens at a
-// time 43; their four sums of squares reduced together (9 shuffles in place of 16) 41;
-// CTAs of 128 threads 38; value rows stored as they were read 37.2.  Eight tokens
-// at a time take 52.
+// of 4 + 4 heads 1.9.  Into 8-bit caches the first takes 51.5 (0.54) and into a 4-bit one 72
+// (0.37), bound by their operations: 37 and 52 M warp instructions against 28 M, at 122
+// registers, four CTAs an SM.  Steps: rows of any token to any lane 64 us; a row of four tokens
+// at a time 43; their four sums of squares reduced together (9 shuffles in place of 16) 41;
+// CTAs of 128 threads 38; value rows stored as they were read 37.2.  Eight tokens at a time
+// take 52.
 #include <type_traits>
 
 #include "pa_decode_common.cuh"
