@@ -557,7 +557,8 @@ pa_status pa_int4_gather(void *out_k, void *out_v, pa_dtype out_dtype, const voi
  * num_seqs (of 2048 at most) below 2^30.  Codes are exact in the products, each
  * query row is first scaled by a power of two and taken in binary16, softmax weights
  * enter as two binary16 parts; sums and softmax are fp32.  A group's elements are accurate
- * in proportion to the values of that group alone, however large the row's other group is.
+ * in proportion to the values of that group alone, however large the row's other group is
+ * (tokens whose softmax weight is below 2^-76 of the largest may count as none).
  */
 size_t pa_int4_decode_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size,
                                      int max_context_len, int partition_size);
